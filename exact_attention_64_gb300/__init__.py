@@ -30,6 +30,10 @@ __all__ = [
     "bwd_workspace_size",
     "device_status",
     "attention",
+    "paged_decode",
+    "cache_append",
+    "cache_evict",
+    "key_weights",
     "fwd_grid",
     "fwd_block_work",
     "fwd_schedule",
@@ -89,6 +93,13 @@ def load_library() -> ctypes.CDLL:
                               vp]),
         "fa2_bwd_atomic_timed": (i, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp,
                                      sz, vp, vp]),
+        "fa2_paged_decode": (i, [vp] * 9 + [i] * 7 + [f, i, vp, sz, vp]),
+        "fa2_paged_decode_workspace_size": (sz, [i] * 7),
+        "fa2_cache_append": (i, [vp] * 12 + [i] * 8 + [vp]),
+        "fa2_cache_evict": (i, [vp] * 10 + [i] * 9 + [vp, sz, vp]),
+        "fa2_cache_evict_workspace_size": (sz, [i] * 5),
+        "fa2_key_weights": (i, [vp] * 5 + [i] * 7 + [f, i, vp, sz, vp]),
+        "fa2_key_weights_workspace_size": (sz, []),
         "fa2_get_device_status": (i, [vp]),
         "fa2_status_string": (ctypes.c_char_p, [i]),
         "fa2_fwd_grid": (i, [i, i, i, _c_int_p, _c_int_p]),
@@ -440,3 +451,225 @@ class _FA2Function(torch.autograd.Function):
 def attention(q, k, v, causal: bool = False, scale: float | None = None):
     """Differentiable FlashAttention-2 (forward and backward in libfa2)."""
     return _FA2Function.apply(q, k, v, causal, scale)
+
+
+# ---------------------------------------------------------------------------
+# Paged key-value cache
+# ---------------------------------------------------------------------------
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """The library's entry points work on the current device."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        _check(name, fn(*args, _stream_ptr(dev)))
+        return
+    with torch.cuda.device(dev):
+        _check(name, fn(*args, _stream_ptr(dev)))
+
+
+def _workspace(workspace, need, func, dev):
+    """(tensor, bytes): the caller's scratch, or a new one."""
+    if need == 0:
+        raise FA2Error(func, 1)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _check_cache(k_cache, v_cache, table, lens):
+    """(num_pages, Hkv, page_size, d, B, max_pages) of a paged cache."""
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if k_cache.dim() != 4:
+        raise ValueError("expected a [num_pages, Hkv, page_size, d] cache")
+    if k_cache.dtype not in _DTYPES:
+        raise ValueError("k_cache must be float16 or bfloat16")
+    if table.dim() != 2:
+        raise ValueError("expected a [B, max_pages] table")
+    dev = k_cache.device
+    num_pages, Hkv, ps, d = k_cache.shape
+    B, max_pages = table.shape
+    _check_tensor("k_cache", k_cache, k_cache.shape, k_cache.dtype, dev)
+    _check_tensor("v_cache", v_cache, k_cache.shape, k_cache.dtype, dev)
+    _check_tensor("table", table, table.shape, torch.int32, dev)
+    _check_tensor("lens", lens, (B,), torch.int32, dev)
+    return num_pages, Hkv, ps, d, B, max_pages
+
+
+def paged_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, weights=None,
+                 weights_out=None, out=None, lse=None, workspace=None):
+    """Attention of one new token per sequence over a paged key-value cache.
+
+    q ``[B, Hq, d]``; k_cache, v_cache ``[num_pages, Hkv, page_size, d]``; table
+    int32 ``[B, max_pages]``, the pages of each sequence; lens int32 ``[B]``, its
+    slots in use (0: o = 0, lse = -inf). Query head x reads key head
+    x // (Hq // Hkv). With ``weights`` (float32 ``[B, Hkv, max_pages *
+    page_size]``) the token's attention weight on every slot, summed over the
+    query heads of a key head, is added to them: in place, or into
+    ``weights_out`` (slots past the length are left as they were). Returns
+    (o, lse): o like q, lse float32 [B, Hq].
+    """
+    num_pages, Hkv, ps, d, B, max_pages = _check_cache(k_cache, v_cache, table, lens)
+    dev, dt = k_cache.device, k_cache.dtype
+    if q.dim() != 3:
+        raise ValueError("expected a [B, Hq, d] query")
+    Hq = q.shape[1]
+    _check_tensor("q", q, (B, Hq, d), dt, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_tensor("out", out, (B, Hq, d), dt, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("lse", lse, (B, Hq), torch.float32, dev)
+    if weights is not None:
+        _check_tensor("weights", weights, (B, Hkv, max_pages * ps), torch.float32, dev)
+        if weights_out is None:
+            weights_out = weights
+        else:
+            _check_tensor("weights_out", weights_out, weights.shape, torch.float32, dev)
+    elif weights_out is not None:
+        raise ValueError("weights_out needs weights")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    need = load_library().fa2_paged_decode_workspace_size(B, Hq, Hkv, d, ps, max_pages,
+                                                          int(weights is not None))
+    ws, nbytes = _workspace(workspace, need, "fa2_paged_decode_workspace_size", dev)
+    _call("fa2_paged_decode", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          table.data_ptr(), lens.data_ptr(), _ptr(weights), _ptr(weights_out), out.data_ptr(),
+          lse.data_ptr(), B, Hq, Hkv, d, num_pages, ps, max_pages, float(scale), _DTYPES[dt],
+          ws.data_ptr(), nbytes)
+    return out, lse
+
+
+def cache_append(k, v, k_cache, v_cache, table, lens, num_new=None, weights=None,
+                 new_weights=None, positions=None, next_pos=None, lens_out=None):
+    """Writes new tokens into a paged cache, in place: token i of sequence b goes
+    to slot lens[b] + i. k, v ``[B, Hkv, T, d]`` (a prompt as ``forward`` takes
+    it, or one token); num_new int32 ``[B]`` counts the tokens of each sequence in
+    a padded batch (None: T). With ``weights`` the new slots' weights are set to
+    new_weights float32 ``[B, Hkv, T]`` (``key_weights`` of the prompt), or 0; with
+    ``positions`` (int32, like weights) to next_pos[b] + i. Returns the new
+    lengths, int32 [B] (lens itself is not changed).
+    """
+    num_pages, Hkv, ps, d, B, max_pages = _check_cache(k_cache, v_cache, table, lens)
+    dev, dt = k_cache.device, k_cache.dtype
+    if k.dim() != 4:
+        raise ValueError("expected [B, Hkv, T, d] keys")
+    T = k.shape[2]
+    _check_tensor("k", k, (B, Hkv, T, d), dt, dev)
+    _check_tensor("v", v, (B, Hkv, T, d), dt, dev)
+    slots = (B, Hkv, max_pages * ps)
+    if num_new is not None:
+        _check_tensor("num_new", num_new, (B,), torch.int32, dev)
+    if weights is not None:
+        _check_tensor("weights", weights, slots, torch.float32, dev)
+    if new_weights is not None:
+        if weights is None:
+            raise ValueError("new_weights needs weights")
+        _check_tensor("new_weights", new_weights, (B, Hkv, T), torch.float32, dev)
+    if (positions is None) != (next_pos is None):
+        raise ValueError("positions and next_pos go together")
+    if positions is not None:
+        _check_tensor("positions", positions, slots, torch.int32, dev)
+        _check_tensor("next_pos", next_pos, (B,), torch.int32, dev)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    else:
+        _check_tensor("lens_out", lens_out, (B,), torch.int32, dev)
+    _call("fa2_cache_append", dev, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(num_new), _ptr(weights),
+          _ptr(new_weights), _ptr(positions), _ptr(next_pos), lens_out.data_ptr(), B, Hkv, T, d,
+          num_pages, ps, max_pages, _DTYPES[dt])
+    return lens_out
+
+
+def cache_evict(k_cache, v_cache, table, lens, weights, budget: int, recent: int = 0,
+                positions=None, next_pos=None, weights_out=None, positions_out=None, lens_out=None,
+                workspace=None):
+    """Cuts a paged cache back to ``budget`` slots per sequence and key head, in
+    place, by accumulated attention weight.
+
+    Recent tokens stay first (position >= next_pos[b] - recent; without
+    positions the last ``recent`` slots), then those of the largest weight; NaN
+    counts as the smallest, and of equal ones the lower slot stays. Kept slots
+    below the budget do not move; the evicted ones take, in order, the kept slots
+    at or past it, with their weights and positions (updated in place, or into
+    ``weights_out`` / ``positions_out``). Each head keeps its own tokens. Returns
+    the new lengths, int32 [B]: min(lens, budget).
+    """
+    num_pages, Hkv, ps, d, B, max_pages = _check_cache(k_cache, v_cache, table, lens)
+    dev, dt = k_cache.device, k_cache.dtype
+    slots = (B, Hkv, max_pages * ps)
+    budget, recent = int(budget), int(recent)
+    if budget < 1 or not 0 <= recent <= budget:
+        raise ValueError("needs budget >= 1 and 0 <= recent <= budget")
+    budget, recent = min(budget, 2**31 - 1), min(recent, 2**31 - 1)
+    _check_tensor("weights", weights, slots, torch.float32, dev)
+    if weights_out is None:
+        weights_out = weights
+    else:
+        _check_tensor("weights_out", weights_out, slots, torch.float32, dev)
+    if (positions is None) != (next_pos is None):
+        raise ValueError("positions and next_pos go together")
+    if positions is not None:
+        _check_tensor("positions", positions, slots, torch.int32, dev)
+        _check_tensor("next_pos", next_pos, (B,), torch.int32, dev)
+        if positions_out is None:
+            positions_out = positions
+        else:
+            _check_tensor("positions_out", positions_out, slots, torch.int32, dev)
+    elif positions_out is not None:
+        raise ValueError("positions_out needs positions")
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    else:
+        _check_tensor("lens_out", lens_out, (B,), torch.int32, dev)
+    need = load_library().fa2_cache_evict_workspace_size(B, Hkv, ps, max_pages, budget)
+    ws, nbytes = _workspace(workspace, need, "fa2_cache_evict_workspace_size", dev)
+    _call("fa2_cache_evict", dev, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(),
+          lens.data_ptr(), weights.data_ptr(), weights_out.data_ptr(), _ptr(positions),
+          _ptr(positions_out), _ptr(next_pos), lens_out.data_ptr(), B, Hkv, d, num_pages, ps,
+          max_pages, budget, recent, _DTYPES[dt], ws.data_ptr(), nbytes)
+    return lens_out
+
+
+def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_lens=None, out=None,
+                workspace=None):
+    """Accumulated attention weight of a prompt's keys: the column sums of the
+    attention matrix of ``forward``, whose lse is given.
+
+    q ``[B, Hq, N, d]``, k ``[B, Hkv, N_k, d]`` (Hq a multiple of Hkv; the query
+    heads of a key head are added up), lse float32 ``[B, Hq, N]``. q_lens int32
+    ``[B]`` limits the queries of each sequence of a padded causal batch.
+    Returns float32 ``[B, Hkv, N_k]``: the weights that ``cache_append`` and
+    ``cache_evict`` take.
+    """
+    B, Hq, N, d = _shape(q)
+    Hkv, Nk = _shape(k)[1:3]
+    dt, dev = q.dtype, q.device
+    if dt not in _DTYPES:
+        raise ValueError("q must be float16 or bfloat16")
+    _check_tensor("q", q, (B, Hq, N, d), dt, dev)
+    _check_tensor("k", k, (B, Hkv, Nk, d), dt, dev)
+    _check_tensor("lse", lse, (B, Hq, N), torch.float32, dev)
+    if q_lens is not None:
+        _check_tensor("q_lens", q_lens, (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("out", out, (B, Hkv, Nk), torch.float32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    need = load_library().fa2_key_weights_workspace_size()
+    ws, nbytes = _workspace(workspace, need, "fa2_key_weights_workspace_size", dev)
+    _call("fa2_key_weights", dev, q.data_ptr(), k.data_ptr(), lse.data_ptr(), _ptr(q_lens),
+          out.data_ptr(), B, Hq, Hkv, N, Nk, d, int(bool(causal)), float(scale), _DTYPES[dt],
+          ws.data_ptr(), nbytes)
+    return out

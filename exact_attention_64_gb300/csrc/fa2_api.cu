@@ -16,6 +16,7 @@
 
 #include "../../include/fa2.h"
 #include "fa2_common.cuh"
+#include "fa2_host.h"
 
 namespace fa2 {
 cudaError_t launch_fwd(int d, bool bf16, bool causal, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -351,6 +352,20 @@ int num_splits_makespan(int BH, int N, int causal, int num_sms) {
 
 }  // namespace
 
+// The same set-up for the entry points of other translation units.
+namespace fa2 {
+int host_device_setup(int* num_sms, int** status) {
+  int dev = 0;
+  const int st = device_setup(&dev, status);
+  if (st == FA2_OK) *num_sms = g_num_sms[dev];
+  return st;
+}
+int host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+int host_map_16bit(CUtensorMap* m, const void* ptr, int BH, int N, int d, int dtype) {
+  return make_map_16bit(m, ptr, BH, N, d, dtype);
+}
+}  // namespace fa2
+
 extern "C" {
 
 int fa2_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N,
@@ -638,6 +653,7 @@ const char* fa2_status_string(int status) {
     case FA2_ERR_DEVICE_TIMEOUT: return "FA2_ERR_DEVICE_TIMEOUT";
     case FA2_ERR_WORKSPACE: return "FA2_ERR_WORKSPACE";
     case FA2_ERR_OVERLAP: return "FA2_ERR_OVERLAP";
+    case FA2_ERR_PAGE: return "FA2_ERR_PAGE";
     default: return "FA2_ERR_UNKNOWN";
   }
 }

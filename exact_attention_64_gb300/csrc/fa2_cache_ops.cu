@@ -1,0 +1,348 @@
+// Writes to the paged cache: appending new tokens, and eviction.
+#include "fa2_cache.cuh"
+
+namespace fa2 {
+
+// ---- Append ----------------------------------------------------------------
+// New token i of sequence b and key head h goes to slot lens[b] + i. A copy:
+// bound by HBM for prompts and by one launch for single tokens. One thread
+// moves 16 bytes of K and of V; consecutive threads walk a row, and a CTA takes
+// kAppendRows rows of [B][Hkv][T], several per thread so that their loads are
+// in flight together.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) fa2_cache_append_kernel(const AppendArgs a) {
+  constexpr int CH = D / 8;                     // 16-byte chunks of a row
+  constexpr int RPP = kAppendThreads / CH;      // rows per pass
+  const CacheView& c = a.c;
+  const int ch = threadIdx.x % CH;
+  const long long r0 = static_cast<long long>(blockIdx.x) * (RPP * kAppendUnroll) + threadIdx.x / CH;
+  uint4 kx[kAppendUnroll], vx[kAppendUnroll];
+  int row[kAppendUnroll], slot[kAppendUnroll], bh[kAppendUnroll], ti[kAppendUnroll];
+#pragma unroll
+  for (int x = 0; x < kAppendUnroll; ++x) {
+    const long long r = r0 + x * RPP;
+    row[x] = -1;
+    if (r >= a.rows) continue;
+    bh[x] = div_by(static_cast<int>(r), a.fT);
+    ti[x] = static_cast<int>(r) - bh[x] * a.T;
+    const int b = div_by(bh[x], a.fH), h = bh[x] - b * c.Hkv;
+    const int n = seq_len(c, b);
+    const int cnt = a.num_new != nullptr ? cut_len(__ldg(a.num_new + b), a.T) : a.T;
+    slot[x] = n + ti[x];
+    if (ti[x] >= cnt || slot[x] >= c.L) continue;  // padding, or no room in the table
+    row[x] = slot_row(c, b, h, slot[x]);
+    if (row[x] < 0) {
+      report_page(c.status);
+      continue;
+    }
+    kx[x] = __ldg(reinterpret_cast<const uint4*>(a.k + static_cast<size_t>(r) * D) + ch);
+    vx[x] = __ldg(reinterpret_cast<const uint4*>(a.v + static_cast<size_t>(r) * D) + ch);
+  }
+#pragma unroll
+  for (int x = 0; x < kAppendUnroll; ++x) {
+    if (row[x] < 0) continue;
+    reinterpret_cast<uint4*>(a.kc + static_cast<size_t>(row[x]) * D)[ch] = kx[x];
+    reinterpret_cast<uint4*>(a.vc + static_cast<size_t>(row[x]) * D)[ch] = vx[x];
+    if (ch != 0) continue;
+    const size_t at = static_cast<size_t>(bh[x]) * c.L + slot[x];
+    if (a.weights != nullptr)
+      a.weights[at] = a.new_weights != nullptr ? __ldg(a.new_weights + r0 + x * RPP) : 0.f;
+    if (a.positions != nullptr) a.positions[at] = __ldg(a.next_pos + div_by(bh[x], a.fH)) + ti[x];
+  }
+  // New lengths, by the first CTA. A length or a count outside its range is
+  // cut and reported.
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < c.B; b += kAppendThreads) {
+      const int n = seq_len(c, b);
+      const int want = a.num_new != nullptr ? __ldg(a.num_new + b) : a.T;
+      const int cnt = cut_len(want, a.T);
+      if (n != __ldg(c.lens + b) || cnt != want || n > c.L - cnt) report_page(c.status);
+      a.lens_out[b] = n > c.L - cnt ? c.L : n + cnt;
+    }
+  }
+}
+
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
+  const int per = kAppendThreads / (a.d / 8) * kAppendUnroll;
+  const long long grid = (a.rows + per - 1) / per;
+  if (a.d == 64)
+    fa2_cache_append_kernel<64><<<static_cast<unsigned>(grid), kAppendThreads, 0, stream>>>(a);
+  else
+    fa2_cache_append_kernel<128><<<static_cast<unsigned>(grid), kAppendThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// ---- Eviction --------------------------------------------------------------
+// Of a sequence and key head with more than `budget` slots the budget slots
+// with the largest keys stay. A key orders the slots: recent tokens first
+// (position >= next_pos - recent), then by weight, NaN last; equal keys by the
+// lower slot. Attention does not depend on the order of the slots, so the kept
+// slots below budget stay where they are, and the i-th evicted slot below
+// budget takes the i-th kept slot at or past budget: no row moves that does not
+// have to, and sources and destinations are disjoint.
+//
+// Selection: the key becomes a 32-bit integer of the same order, and the
+// budget-th largest is found digit by digit, 8 bits a pass, from histograms. A
+// (sequence, key head) is the work of one cluster: each CTA keeps the integer
+// keys of its share of the slots in shared memory, so that weights and
+// positions are read once, and the histograms of a pass are added up through
+// distributed shared memory. Integer counts: the result does not depend on any
+// order. Where the keys do not fit they are made again from global memory.
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictKeys = 49152;  // keys a CTA can hold: 192 KiB
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A 32-bit word of shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Integer of the same order as a weight: NaN 0, then -inf ... +inf.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 becomes +0
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+struct EvictShared {
+  uint32_t hist[4][256];
+  uint32_t total[256];
+  uint32_t warp_gt[kEvictWarps], warp_tie[kEvictWarps];  // per warp, then exclusive
+  uint32_t cta_gt, cta_tie, cta_gt_lo, cta_tie_lo;       // this CTA's counts
+  uint32_t digit, want;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const EvictArgs a, int C) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ EvictShared sh;
+  const CacheView& c = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = blockIdx.x / C;
+  const int rank = static_cast<int>(C > 1 ? cluster_rank() : 0u);
+  const int b = item / c.Hkv, h = item - b * c.Hkv;
+  const int n = seq_len(c, b);
+  const int k = min(n, a.budget);
+  const size_t base = static_cast<size_t>(item) * c.L;
+  const float* w_in = a.w_in + base;
+  float* w_out = a.w_out + base;
+  const int* p_in = a.p_in != nullptr ? a.p_in + base : nullptr;
+  int* p_out = a.p_in != nullptr ? a.p_out + base : nullptr;
+  const bool copy_w = a.w_out != a.w_in, copy_p = p_in != nullptr && a.p_out != a.p_in;
+  if (h == 0 && rank == 0 && tid == 0) {
+    if (n != __ldg(c.lens + b)) report_page(c.status);
+    a.lens_out[b] = k;
+  }
+  if (n <= a.budget) {  // nothing to evict
+    for (int j = rank * kEvictThreads + tid; j < n; j += C * kEvictThreads) {
+      if (copy_w) w_out[j] = w_in[j];
+      if (copy_p) p_out[j] = p_in[j];
+    }
+    return;  // the whole cluster
+  }
+  // This CTA's slots [j0, j1), of which each warp owns a run of whole 32s.
+  const int run = (((n + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;  // slots per warp
+  const int j0 = min(n, rank * run * kEvictWarps), j1 = min(n, j0 + run * kEvictWarps);
+  const long long first_recent =
+      p_in != nullptr ? static_cast<long long>(__ldg(a.next_pos + b)) - a.recent : 0;
+  auto make_key = [&](int j) -> uint32_t {
+    const uint32_t key = weight_key(w_in[j]);
+    // Without positions the slots are in the order of their tokens.
+    const bool is_recent = p_in != nullptr ? p_in[j] >= first_recent : j >= n - a.recent;
+    return is_recent && a.recent > 0 ? 0xffffffffu : key;
+  };
+  for (int i = tid; i < 4 * 256; i += kEvictThreads) (&sh.hist[0][0])[i] = 0u;
+  if (tid == 0) sh.cta_gt = sh.cta_tie = sh.cta_gt_lo = sh.cta_tie_lo = 0u;
+  if (a.cached)
+    for (int j = j0 + tid; j < j1; j += kEvictThreads) s_keys[j - j0] = make_key(j);
+  auto key_at = [&](int j) -> uint32_t { return a.cached ? s_keys[j - j0] : make_key(j); };
+  __syncthreads();
+  uint32_t prefix = 0, want = k;  // the want-th largest among the keys that start with prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int j = j0 + tid; j < j1; j += kEvictThreads) {
+      const uint32_t key = key_at(j);
+      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & 255u], 1u);
+    }
+    if (C > 1) cluster_sync(); else __syncthreads();
+    if (tid < 256) {
+      uint32_t t = 0;
+      if (C == 1) t = sh.hist[pass][tid];
+      else
+        for (int x = 0; x < C; ++x) t += cluster_load(&sh.hist[pass][tid], x);
+      sh.total[tid] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // Lane l has digits 255 - 8 l ... 248 - 8 l, the largest first.
+      uint32_t v[8], sum = 0;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sum += v[x] = sh.total[255 - 8 * lane - x];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      uint32_t above = incl - sum;
+      if (above < want && want <= incl) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          if (above < want && want <= above + v[x]) {
+            sh.digit = 255 - 8 * lane - x;
+            sh.want = want - above;
+          }
+          above += v[x];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | sh.digit;
+    want = sh.want;
+  }
+  // Slots with a key above `prefix` stay, and the first `want` of those equal to
+  // it. Counts before each warp's run, over the cluster in slot order.
+  const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
+  uint32_t gt = 0, tie = 0, gt_lo = 0, tie_lo = 0;
+  for (int j = w0 + lane; j < w1; j += 32) {
+    const uint32_t key = key_at(j);
+    const uint32_t g1 = key > prefix, t1 = key == prefix;
+    gt += g1;
+    tie += t1;
+    if (j < k) {
+      gt_lo += g1;
+      tie_lo += t1;
+    }
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  tie = __reduce_add_sync(0xffffffffu, tie);
+  gt_lo = __reduce_add_sync(0xffffffffu, gt_lo);
+  tie_lo = __reduce_add_sync(0xffffffffu, tie_lo);
+  if (lane == 0) {
+    sh.warp_gt[warp] = gt;
+    sh.warp_tie[warp] = tie;
+    atomicAdd(&sh.cta_gt, gt);
+    atomicAdd(&sh.cta_tie, tie);
+    atomicAdd(&sh.cta_gt_lo, gt_lo);
+    atomicAdd(&sh.cta_tie_lo, tie_lo);
+  }
+  if (C > 1) cluster_sync(); else __syncthreads();
+  uint32_t gt_before = 0, tie_before = 0, lo_gt = 0, lo_tie = 0;
+  if (C == 1) {
+    lo_gt = sh.cta_gt_lo;
+    lo_tie = sh.cta_tie_lo;
+  } else {
+    for (int x = 0; x < C; ++x) {
+      if (x < rank) {
+        gt_before += cluster_load(&sh.cta_gt, x);
+        tie_before += cluster_load(&sh.cta_tie, x);
+      }
+      lo_gt += cluster_load(&sh.cta_gt_lo, x);
+      lo_tie += cluster_load(&sh.cta_tie_lo, x);
+    }
+  }
+  for (int x = 0; x < warp; ++x) {
+    gt_before += sh.warp_gt[x];
+    tie_before += sh.warp_tie[x];
+  }
+  const uint32_t kept_lo = lo_gt + min(lo_tie, want);  // kept slots below k
+  const int moves = k - static_cast<int>(kept_lo);
+  int* holes = a.holes + static_cast<size_t>(item) * a.list;
+  int* movers = a.movers + static_cast<size_t>(item) * a.list;
+  for (int jb = w0; jb < w1; jb += 32) {
+    const int j = jb + lane;
+    const uint32_t key = j < w1 ? key_at(j) : 0u;
+    const bool g1 = j < w1 && key > prefix, t1 = j < w1 && key == prefix;
+    const uint32_t gm = __ballot_sync(0xffffffffu, g1), tm = __ballot_sync(0xffffffffu, t1);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t tb = tie_before + __popc(tm & below);
+    const uint32_t kept = gt_before + __popc(gm & below) + min(tb, want);  // kept slots before j
+    const bool keep = g1 || (t1 && tb < want);
+    if (j < w1) {
+      if (j < k && !keep) {
+        holes[j - kept] = j;
+      } else if (j < k) {
+        if (copy_w) w_out[j] = w_in[j];
+        if (copy_p) p_out[j] = p_in[j];
+      } else if (keep) {
+        movers[kept - kept_lo] = j;
+      }
+    }
+    gt_before += __popc(gm);
+    tie_before += __popc(tm);
+  }
+  if (C > 1) cluster_sync(); else __syncthreads();
+  // The moves, 32 at a time per warp of the cluster: a lane looks up one
+  // move's rows, then the warp copies them, 16 bytes of K and of V per lane.
+  constexpr int CH = D / 8, RPI = 32 / CH;
+  const int ch = lane % CH, sub = lane / CH;
+  for (int m0 = (rank * kEvictWarps + warp) * 32; m0 < moves; m0 += C * kEvictThreads) {
+    int src = -1, dst = -1;
+    if (m0 + lane < moves) {
+      const int sj = __ldcg(movers + m0 + lane), dj = __ldcg(holes + m0 + lane);
+      src = slot_row(c, b, h, sj);
+      dst = slot_row(c, b, h, dj);
+      if (src < 0 || dst < 0) report_page(c.status);
+      w_out[dj] = w_in[sj];
+      if (p_in != nullptr) p_out[dj] = p_in[sj];
+    }
+    const int cnt = min(32, moves - m0);
+#pragma unroll 4
+    for (int i = 0; i < 32; i += RPI) {
+      if (i >= cnt) break;
+      const int s = __shfl_sync(0xffffffffu, src, i + sub), d = __shfl_sync(0xffffffffu, dst, i + sub);
+      if (s >= 0 && d >= 0) {
+        const uint4 x = *(reinterpret_cast<const uint4*>(a.kc + static_cast<size_t>(s) * D) + ch);
+        const uint4 y = *(reinterpret_cast<const uint4*>(a.vc + static_cast<size_t>(s) * D) + ch);
+        reinterpret_cast<uint4*>(a.kc + static_cast<size_t>(d) * D)[ch] = x;
+        reinterpret_cast<uint4*>(a.vc + static_cast<size_t>(d) * D)[ch] = y;
+      }
+    }
+  }
+  // No CTA leaves while another may still read its counts: the last cluster
+  // barrier above is past every distributed read.
+}
+
+cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
+  EvictArgs a = a0;
+  // CTAs per (sequence, key head). Up to 4096 slots one CTA does it without
+  // cluster barriers; longer tables are shared by 8.
+  const int C = a.c.L <= 4096 ? 1 : 8;
+  const long long items = static_cast<long long>(a.c.B) * a.c.Hkv;
+  const long long per = ((static_cast<long long>(a.c.L) + C - 1) / C + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+  a.cached = per <= kEvictKeys;
+  const size_t smem = a.cached ? static_cast<size_t>(per) * 4 : 0;
+  auto kern = a.d == 64 ? fa2_cache_evict_kernel<64> : fa2_cache_evict_kernel<128>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items * C));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, C);
+}
+
+}  // namespace fa2

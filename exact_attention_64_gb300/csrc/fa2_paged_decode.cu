@@ -1,0 +1,577 @@
+// Attention of one new token over a paged key-value cache.
+//
+//   s_j = scale q . k_j, L = ln sum_j e^(s_j), o = sum_j e^(s_j - L) v_j over the
+//   lens[b] slots of a sequence; with weights also
+//   w_out[j] = w_in[j] + sum over the query heads of a key head of e^(s_j - L).
+//
+// What bounds it: every cached K and V byte is read once for 4 g flop per
+// element (g query heads share a key head), so HBM. What a design has to give
+// is bytes in flight and an even share of the cache for every SM whatever the
+// lengths; the arithmetic only has to stay out of the way.
+//
+// Split. The cache's slots are cut into units of 64 (sequence, then key head,
+// then slot) and CTA c of G takes units [c T / G, (c+1) T / G) of the T units
+// that the lengths in device memory amount to: every CTA reads the same share
+// of the cache, with one long sequence or many uneven ones, and the same launch
+// serves a captured graph whose lengths change. A (sequence, key head) inside
+// one CTA's range is finished there; one that is cut leaves its unnormalised
+// O, m and l in the workspace, two per CTA at most, and a second launch joins them.
+//
+// A CTA has 4 warps; warp w owns slots 16 w .. 16 w + 15 of every unit and
+// feeds itself: cp.async copies of 16 bytes into its own ring of shared memory
+// (rows XOR-swizzled by 16-byte chunk), no CTA-wide barrier until a segment
+// ends. 16-byte copies follow any page size, a page per slot included, which a
+// bulk copy of a page's run cannot.
+//
+// Products. S^T = K Q^T and O^T += V^T P^T with m16n8k16 matrix instructions:
+// the 16 slots (or 16 columns of V) are the long side and 8 query heads the
+// short one. At 8 heads a slot costs 512 bytes (d = 128) and 2 x 16/16 of these
+// instructions, far below what they can do at the memory's pace, so tcgen05
+// (M = 128 rows of which g would be used) would gain nothing here. P is split
+// into a 16-bit value and a 16-bit remainder, two products, so that the output
+// carries the one rounding at the end and no rounding of P.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa2_cache.cuh"
+
+namespace fa2 {
+
+constexpr int kUnit = 64;       // slots per unit
+constexpr int kDecWarps = 4;    // 16 slots of a unit each
+constexpr float kLn2f = 0.6931471805599453f;
+constexpr float kLog2ef = 1.4426950408889634f;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+  const int n = full ? 16 : 0;  // 0: the 16 bytes are filled with zeros, src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// Transpose of an 8 x 8 matrix of 16-bit values held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8)
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---- Units ---------------------------------------------------------------
+// HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
+__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit - 1) / kUnit; }
+
+// T, by a whole warp.
+__device__ __forceinline__ long long total_units(const CacheView& c, int HH, int lane) {
+  long long t = 0;
+  for (int b = lane; b < c.B; b += 32) t += static_cast<long long>(tiles_of(seq_len(c, b))) * HH;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+struct UnitCursor {
+  int b, hh, tile;  // sequence, item of the sequence, unit of the item
+  int n, ntiles;    // slots of the sequence, units of the item
+};
+
+// Cursor of unit u < T, by a whole warp.
+__device__ __forceinline__ UnitCursor unit_cursor(const CacheView& c, int HH, long long u, int lane) {
+  long long base = 0;
+  UnitCursor k{};
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < c.B ? seq_len(c, b) : 0;
+    const long long mine = static_cast<long long>(tiles_of(n)) * HH;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, u < base + incl);
+    if (hit != 0u) {
+      const int src = __ffs(hit) - 1;
+      const long long r = u - (base + __shfl_sync(0xffffffffu, incl - mine, src));
+      k.b = b0 + src;
+      k.n = __shfl_sync(0xffffffffu, n, src);
+      k.ntiles = tiles_of(k.n);
+      k.hh = static_cast<int>(r / k.ntiles);
+      k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
+      return k;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return k;
+}
+
+__device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k) {
+  if (++k.tile < k.ntiles) return;
+  k.tile = 0;
+  if (++k.hh < HH) return;
+  k.hh = 0;
+  do {
+    if (++k.b >= c.B) {
+      k.n = k.ntiles = 0;
+      return;
+    }
+    k.n = seq_len(c, k.b);
+  } while (k.n == 0);
+  k.ntiles = tiles_of(k.n);
+}
+
+// Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer
+// units than CTAs, T CTAs take one each.
+__device__ __forceinline__ long long unit_begin(long long x, long long G, long long T) { return x * T / G; }
+__device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
+  return static_cast<int>(((u + 1) * G - 1) / T);
+}
+
+template <int D, int NT>
+struct DecCfg {
+  static constexpr int ROW = D * 2;                        // bytes of a row
+  static constexpr int STAGE = 2 * 16 * ROW;               // a warp's K and V of one unit
+  static constexpr int STAGES = D == 128 ? 3 : 6;          // 96 KiB of ring per CTA either way
+  static constexpr int RING = kDecWarps * STAGES * STAGE;
+  static constexpr int HS = D + 4;                         // merge: floats per head (4: no bank conflicts)
+  static constexpr int SMEM = RING + kDecWarps * 8 * HS * 4;
+  static constexpr int HEADS = 8 * NT;                     // query heads of a tile
+};
+
+template <int D, bool BF16, int NT, bool WEIGHTS>
+__global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
+  using C = DecCfg<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kDecWarps][C::HEADS];
+  __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheView& c = a.c;
+  const int HH = c.Hkv * a.HG;
+  const long long T = total_units(c, HH, lane);
+  const long long G = min(static_cast<long long>(gridDim.x), T);
+  const int cta = blockIdx.x;
+  if (cta == 0 && warp == 0)
+    for (int b = lane; b < c.B; b += 32)
+      if (__ldg(c.lens + b) != seq_len(c, b)) report_page(c.status);
+  if (cta >= G) return;
+  const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
+  UnitCursor cc = unit_cursor(c, HH, u0, lane);
+  UnitCursor ic = cc;  // next unit to copy
+  const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
+  float* merge = reinterpret_cast<float*>(smem + C::RING);
+
+  // Page of this lane's slot (lane % 16 of the warp's 16) in the next unit to
+  // copy, looked up one unit ahead of its use.
+  long long left = u1 - u0;  // units not yet copied
+  int pg = 0, off = 0, hk = 0;
+  bool in = false;
+  auto look_up = [&]() {
+    const int slot = ic.tile * kUnit + warp * 16 + (lane & 15);
+    in = left > 0 && slot < ic.n;
+    hk = a.HG == 1 ? ic.hh : ic.hh / a.HG;
+    if (in) {
+      const int p = div_by(slot, c.ps);
+      off = slot - p * c.ps.d;
+      pg = __ldg(c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
+    }
+  };
+  auto copy_next = [&](int st) {
+    if (left > 0) {
+      const int row = in ? page_row(c, pg, hk, off) : -1;
+      if (in && row < 0) report_page(c.status);
+      const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+      if (lane == 0) s_mask[warp][st] = mask;
+      if (__any_sync(0xffffffffu, in)) {
+        constexpr int CH = D / 8;            // 16-byte chunks per row
+        constexpr int RPI = 32 / CH;         // rows per warp-wide copy
+        const uint32_t base = ring + st * C::STAGE;
+        const int ch = lane % CH;
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = i * RPI + lane / CH;
+          const int rr = __shfl_sync(0xffffffffu, row, r);
+          const size_t e = static_cast<size_t>(max(rr, 0)) * D + ch * 8;
+          const uint32_t dst = base + r * C::ROW + ((ch ^ (r & 7)) * 16);
+          cp_async16(dst, a.k + e, rr >= 0);
+          cp_async16(dst + 16 * C::ROW, a.v + e, rr >= 0);
+        }
+      }
+      unit_advance(c, HH, ic);
+      --left;
+      look_up();
+    }
+    cp_async_commit();
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < C::STAGES; ++s) copy_next(s);
+
+  uint32_t qf[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+  int st = 0;
+  const int t = lane & 3, r8 = lane >> 2;
+#pragma unroll 1
+  for (long long u = u0; u < u1; ++u) {
+    const bool first = u == u0 || cc.tile == 0;
+    const int h = a.HG == 1 ? cc.hh : cc.hh / a.HG;
+    const int head0 = (cc.hh - h * a.HG) * C::HEADS;  // first head of the tile inside its group
+    if (first) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hd = head0 + nt * 8 + r8;
+        const uint32_t* qp = reinterpret_cast<const uint32_t*>(
+            a.q + (static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + (hd < a.g ? hd : 0)) * D);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qf[nt][kk][0] = hd < a.g ? __ldg(qp + kk * 8 + t) : 0u;
+          qf[nt][kk][1] = hd < a.g ? __ldg(qp + kk * 8 + 4 + t) : 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[nt][x][y] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+    }
+    cp_async_wait<C::STAGES - 1>();
+    __syncwarp();
+    const int slot0 = cc.tile * kUnit + warp * 16;
+    if (slot0 < cc.n) {
+      const uint32_t mask = s_mask[warp][st];
+      const uint32_t kb = ring + st * C::STAGE, vb = kb + 16 * C::ROW;
+      const int lr = lane & 15, lc = lane >> 4;  // ldmatrix row and chunk of this lane
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t ka[4];
+        ldsm4(ka, kb + lr * C::ROW + (((2 * kk + lc) ^ (lr & 7)) * 16));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(s[nt], ka, qf[nt][kk][0], qf[nt][kk][1]);
+      }
+      const bool ok0 = (mask >> r8) & 1u, ok1 = (mask >> (r8 + 8)) & 1u;
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) x[y] = (y < 2 ? ok0 : ok1) ? s[nt][y] * a.scale_log2 : -INFINITY;
+        if constexpr (WEIGHTS) {
+          // Logits of slots r8 and r8 + 8, heads 2t and 2t + 1 of the tile.
+          const int hd = head0 + nt * 8 + 2 * t;
+          float* lg = a.logits +
+                      ((static_cast<size_t>(cc.b) * c.Hkv + h) * c.L + slot0 + r8) * a.g + hd;
+          if (slot0 + r8 < cc.n) {
+            if (hd < a.g) lg[0] = x[0];
+            if (hd + 1 < a.g) lg[1] = x[1];
+          }
+          if (slot0 + r8 + 8 < cc.n) {
+            if (hd < a.g) lg[8 * static_cast<size_t>(a.g)] = x[2];
+            if (hd + 1 < a.g) lg[8 * static_cast<size_t>(a.g) + 1] = x[3];
+          }
+        }
+        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+        for (int of = 4; of < 32; of <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, of));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, of));
+        }
+        // The reference moves only when the maximum grows by more than 8 (log2
+        // units): exact, since O and l share it, and p stays below 2^8.
+        if (__any_sync(0xffffffffu, mx0 > m[nt][0] + 8.f || mx1 > m[nt][1] + 8.f)) {
+          const float n0 = fmaxf(m[nt][0], mx0), n1 = fmaxf(m[nt][1], mx1);
+          const float f0 = m[nt][0] == n0 ? 1.f : ex2_approx(m[nt][0] - n0);
+          const float f1 = m[nt][1] == n1 ? 1.f : ex2_approx(m[nt][1] - n1);
+          m[nt][0] = n0;
+          m[nt][1] = n1;
+          l[nt][0] *= f0;
+          l[nt][1] *= f1;
+#pragma unroll
+          for (int y = 0; y < D / 16; ++y) {
+            o[nt][y][0] *= f0;
+            o[nt][y][1] *= f1;
+            o[nt][y][2] *= f0;
+            o[nt][y][3] *= f1;
+          }
+        }
+        const float z0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        float p[4];
+        p[0] = ex2_approx(x[0] - z0);
+        p[1] = ex2_approx(x[1] - z1);
+        p[2] = ex2_approx(x[2] - z0);
+        p[3] = ex2_approx(x[3] - z1);
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        const uint32_t h0 = pack_x2<BF16>(p[0], p[1]), h1 = pack_x2<BF16>(p[2], p[3]);
+        const float2 b0 = unpack_x2<BF16>(h0), b1 = unpack_x2<BF16>(h1);
+        ph[nt][0] = transpose8(h0);
+        ph[nt][1] = transpose8(h1);
+        pl[nt][0] = transpose8(pack_x2<BF16>(p[0] - b0.x, p[1] - b0.y));
+        pl[nt][1] = transpose8(pack_x2<BF16>(p[2] - b1.x, p[3] - b1.y));
+      }
+      const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        uint32_t va[4];
+        ldsm4_t(va, vb + vr * C::ROW + (((2 * dt + vc) ^ (vr & 7)) * 16));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816<BF16>(o[nt][dt], va, ph[nt][0], ph[nt][1]);
+          mma16816<BF16>(o[nt][dt], va, pl[nt][0], pl[nt][1]);
+        }
+      }
+    }
+    __syncwarp();
+    copy_next(st);
+    st = st + 1 == C::STAGES ? 0 : st + 1;
+
+    if (u + 1 == u1 || cc.tile + 1 == cc.ntiles) {
+      // End of a segment: the four warps' (m, l, O) are merged.
+      const bool from_start = cc.tile - (u - u0) <= 0;  // the segment begins with its item
+      const bool whole = from_start && cc.tile + 1 == cc.ntiles;
+      const int slot = 2 * cta + (from_start ? 1 : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float x = l[nt][y];
+#pragma unroll
+          for (int of = 4; of < 32; of <<= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
+          if (r8 == 0) s_ml[warp][nt * 8 + 2 * t + y] = make_float2(m[nt][y], x);
+        }
+        float* mg = merge + warp * 8 * C::HS;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          mg[(2 * t) * C::HS + x * 16 + r8] = o[nt][x][0];
+          mg[(2 * t + 1) * C::HS + x * 16 + r8] = o[nt][x][1];
+          mg[(2 * t) * C::HS + x * 16 + r8 + 8] = o[nt][x][2];
+          mg[(2 * t + 1) * C::HS + x * 16 + r8 + 8] = o[nt][x][3];
+        }
+        __syncthreads();
+        const int hd = threadIdx.x >> 4;              // head of the tile of 8
+        const int e0 = (threadIdx.x & 15) * (D / 16); // its first element here
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, s_ml[w][nt * 8 + hd].x);
+        float S = 0.f, acc[D / 16];
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) acc[x] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float2 ml = s_ml[w][nt * 8 + hd];
+          const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+          S += ml.y * f;
+          const float4* src = reinterpret_cast<const float4*>(merge + (w * 8 + hd) * C::HS + e0);
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            const float4 y = src[x];
+            acc[4 * x] += y.x * f;
+            acc[4 * x + 1] += y.y * f;
+            acc[4 * x + 2] += y.z * f;
+            acc[4 * x + 3] += y.w * f;
+          }
+        }
+        const int gh = head0 + nt * 8 + hd;
+        if (gh < a.g) {
+          if (whole) {
+            const size_t row = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + gh;
+            const float inv = S > 0.f ? 1.f / S : 0.f;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + e0);
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) dst[x] = pack_x2<BF16>(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+            if (e0 == 0) a.lse[row] = S > 0.f ? (M + log2f(S)) * kLn2f : -INFINITY;
+          } else {
+            float4* dst = reinterpret_cast<float4*>(
+                a.part_o + (static_cast<size_t>(slot) * C::HEADS + nt * 8 + hd) * D + e0);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              dst[x] = make_float4(acc[4 * x], acc[4 * x + 1], acc[4 * x + 2], acc[4 * x + 3]);
+            if (e0 == 0) a.part_ml[static_cast<size_t>(slot) * C::HEADS + nt * 8 + hd] = make_float2(M, S);
+          }
+        }
+        __syncthreads();
+      }
+    }
+    unit_advance(c, HH, cc);
+  }
+}
+
+// ---- Join ------------------------------------------------------------------
+// The same CTAs over the same units. The parts of a cut item are joined by the
+// CTAs that hold them, part x taking heads x, x + P, ... of the tile; then, with
+// weights, every CTA adds its own slots' weights, e^(s - L) summed over the
+// group's heads, from the logits that it wrote.
+
+// Parts [c0, c1] of the item of units [ub, ub + ntiles).
+struct ItemParts {
+  int c0, c1;
+};
+__device__ __forceinline__ ItemParts item_parts(long long ub, int ntiles, long long G, long long T) {
+  return ItemParts{unit_cta(ub, G, T), unit_cta(ub + ntiles - 1, G, T)};
+}
+// Workspace slot of CTA x's part of an item whose first part is CTA c0's.
+__device__ __forceinline__ int part_slot(int x, int c0) { return 2 * x + (x == c0 ? 1 : 0); }
+
+// (M, S) of one head over an item's parts, by a whole warp.
+__device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int hd, ItemParts p, int lane) {
+  float M = -INFINITY;
+  for (int x = p.c0 + lane; x <= p.c1; x += 32)
+    M = fmaxf(M, part_ml[static_cast<size_t>(part_slot(x, p.c0)) * heads + hd].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float S = 0.f;
+  for (int x = p.c0 + lane; x <= p.c1; x += 32) {
+    const float2 ml = part_ml[static_cast<size_t>(part_slot(x, p.c0)) * heads + hd];
+    S += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - M);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+  return make_float2(M, S);
+}
+
+template <int D, bool BF16, int NT, bool WEIGHTS>
+__global__ void __launch_bounds__(128) fa2_paged_join_kernel(const DecodeArgs a) {
+  constexpr int HEADS = 8 * NT;
+  extern __shared__ float s_lse[];  // [g], log2 units (weights)
+  __shared__ float2 s_ml[HEADS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheView& c = a.c;
+  const int HH = c.Hkv * a.HG;
+  const long long T = total_units(c, HH, lane);
+  const long long G = min(static_cast<long long>(gridDim.x), T);
+  const int cta = blockIdx.x;
+  grid_dependency_wait();
+  // Sequences without a token: o = 0, L = -inf.
+  for (int b = cta; b < c.B; b += gridDim.x) {
+    if (seq_len(c, b) > 0) continue;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
+    for (int x = threadIdx.x; x < a.Hq * D / 2; x += 128) dst[x] = 0u;
+    for (int x = threadIdx.x; x < a.Hq; x += 128) a.lse[static_cast<size_t>(b) * a.Hq + x] = -INFINITY;
+  }
+  if (cta >= G) return;
+  const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
+  UnitCursor cc = unit_cursor(c, HH, u0, lane);
+  for (long long u = u0; u < u1;) {
+    const long long ub = u - cc.tile;  // first unit of the item
+    const int cnt = static_cast<int>(min(static_cast<long long>(cc.ntiles - cc.tile), u1 - u));
+    const int h = cc.hh / a.HG, hg = cc.hh - h * a.HG;
+    const ItemParts p = item_parts(ub, cc.ntiles, G, T);
+    const int P = p.c1 - p.c0 + 1;
+    const size_t row0 = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g;
+    if (P > 1) {
+      for (int hd = warp; hd < HEADS; hd += 4) {
+        if (hg * HEADS + hd >= a.g) break;
+        const float2 x = join_ml(a.part_ml, HEADS, hd, p, lane);
+        if (lane == 0) s_ml[hd] = x;
+      }
+      __syncthreads();
+      for (int hd = cta - p.c0; hd < HEADS && hg * HEADS + hd < a.g; hd += P) {
+        const float2 ml = s_ml[hd];
+        const size_t row = row0 + hg * HEADS + hd;
+        for (int e = threadIdx.x; e < D; e += 128) {
+          float acc = 0.f;
+#pragma unroll 4
+          for (int x = p.c0; x <= p.c1; ++x) {
+            const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
+            const float px = a.part_ml[at].x;
+            acc += (px == -INFINITY ? 0.f : ex2_approx(px - ml.x)) * a.part_o[at * D + e];
+          }
+          acc = ml.y > 0.f ? acc / ml.y : 0.f;
+          a.o[row * D + e] = static_cast<uint16_t>(pack_x2<BF16>(acc, 0.f) & 0xffffu);
+        }
+        if (threadIdx.x == 0) a.lse[row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
+      }
+    }
+    if constexpr (WEIGHTS) {
+      if (hg == 0) {
+        // L of every head of the group, whatever its tile's parts are.
+        for (int hd = warp; hd < a.g; hd += 4) {
+          const int x = hd / HEADS;
+          const ItemParts px = item_parts(ub + static_cast<long long>(x) * cc.ntiles, cc.ntiles, G, T);
+          float v;
+          if (px.c0 == px.c1) {
+            v = a.lse[row0 + hd] * kLog2ef;
+          } else {
+            const float2 ml = join_ml(a.part_ml, HEADS, hd - x * HEADS, px, lane);
+            v = ml.y > 0.f ? ml.x + log2f(ml.y) : -INFINITY;
+          }
+          if (lane == 0) s_lse[hd] = v;
+        }
+        __syncthreads();
+        const size_t base = (static_cast<size_t>(cc.b) * c.Hkv + h) * c.L;
+        const int j1 = min((cc.tile + cnt) * kUnit, cc.n);
+        for (int j = cc.tile * kUnit + threadIdx.x; j < j1; j += 128) {
+          const float* lg = a.logits + (base + j) * a.g;
+          float w = 0.f;
+          for (int hd = 0; hd < a.g; ++hd) {
+            const float x = lg[hd];
+            w += x == -INFINITY ? 0.f : ex2_approx(x - s_lse[hd]);
+          }
+          a.w_out[base + j] = a.w_in[base + j] + w;
+        }
+      }
+    }
+    __syncthreads();  // s_ml, s_lse are rewritten by the next item
+    cc.tile += cnt - 1;
+    unit_advance(c, HH, cc);
+    u += cnt;
+  }
+}
+
+template <int D, bool BF16, int NT, bool WEIGHTS>
+static cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
+  using C = DecCfg<D, NT>;
+  auto kern = fa2_paged_decode_kernel<D, BF16, NT, WEIGHTS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kDecWarps * 32, C::SMEM, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas), dim3(128),
+                          WEIGHTS ? a.g * sizeof(float) : 0, stream, a);
+}
+
+cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas,
+                                cudaStream_t stream) {
+  const bool w = a.w_out != nullptr;
+#define FA2_DEC_CASE(DD, BB, NN, WW) \
+  if (d == DD && bf16 == BB && head_tile == 8 * NN && w == WW) \
+    return launch_decode_t<DD, BB, NN, WW>(a, ctas, stream);
+#define FA2_DEC_CASES(DD, BB) \
+  FA2_DEC_CASE(DD, BB, 1, false) FA2_DEC_CASE(DD, BB, 1, true) \
+  FA2_DEC_CASE(DD, BB, 2, false) FA2_DEC_CASE(DD, BB, 2, true)
+  FA2_DEC_CASES(64, true)
+  FA2_DEC_CASES(64, false)
+  FA2_DEC_CASES(128, true)
+  FA2_DEC_CASES(128, false)
+#undef FA2_DEC_CASES
+#undef FA2_DEC_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa2

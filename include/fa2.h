@@ -33,8 +33,9 @@
  * Errors: every entry point returns an fa2_status (int). Arguments are checked
  * before anything is launched; on an error nothing is launched and no output
  * is touched. A kernel never traps: a bounded wait that runs out writes
- * FA2_ERR_DEVICE_TIMEOUT into the device status word, which
- * fa2_get_device_status() reports.
+ * FA2_ERR_DEVICE_TIMEOUT into the device status word, and a value in device
+ * memory that a paged-cache kernel cannot follow writes FA2_ERR_PAGE;
+ * fa2_get_device_status() reports them.
  */
 #ifndef FA2_H_
 #define FA2_H_
@@ -54,7 +55,9 @@ typedef enum fa2_status {
   FA2_ERR_CUDA = 5,           /* a CUDA runtime / driver call or kernel launch failed */
   FA2_ERR_DEVICE_TIMEOUT = 6, /* a kernel gave up on a bounded wait (see fa2_get_device_status) */
   FA2_ERR_WORKSPACE = 7,      /* backward workspace missing or smaller than fa2_bwd_workspace_size */
-  FA2_ERR_OVERLAP = 8         /* an output buffer overlaps an input buffer */
+  FA2_ERR_OVERLAP = 8,        /* an output buffer overlaps an input buffer */
+  FA2_ERR_PAGE = 9            /* device status only: a paged-cache call met a page number, a length or a
+                                 count outside the cache (see "Paged key-value cache") */
 } fa2_status;
 
 typedef enum fa2_dtype { FA2_FP16 = 0, FA2_BF16 = 1 } fa2_dtype;
@@ -278,9 +281,126 @@ int fa2_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, 
                     const void* dO, void* dq, void* dk, void* dv, int B, int H, int N, int d,
                     int causal, float scale, int dtype, void* stream);
 
+/* ---- Paged key-value cache ------------------------------------------------
+ * Generation after a prompt: the keys and values of earlier tokens live in a
+ * cache of pages, a new token attends to them, and a cache that may not grow
+ * is cut back by the attention weight that its tokens have gathered.
+ *
+ *   k_cache, v_cache : device [num_pages][Hkv][page_size][d] dtype, 16-byte
+ *                      aligned. Any page_size >= 1.
+ *   table            : device int32 [B][max_pages]: the pages of each sequence.
+ *                      Slot j of sequence b lies in page table[b][j / page_size].
+ *                      Entries past the slots in use are not read.
+ *   lens             : device int32 [B]: slots in use, 0 .. L, with
+ *                      L = max_pages * page_size.
+ *   weights          : device fp32 [B][Hkv][L]: the attention weight gathered by
+ *                      the token of each slot. They belong to the sequence, not
+ *                      to the page: sequences may share the pages of a common
+ *                      prefix and still be counted apart.
+ *   positions        : device int32 [B][Hkv][L]: the position in the text of the
+ *                      token of each slot (after an eviction slots are in no
+ *                      order, and each head has kept other tokens).
+ *   d, dtype         : as in fa2_fwd. Query heads: Hq = g * Hkv, g <= 128; query
+ *                      head x reads key head x / g. B, Hq, Hkv <= 65535;
+ *                      num_pages * Hkv * page_size < 2^31; L <= 2^30.
+ *
+ * Lengths, counts and pages are read on the device, so a captured graph follows
+ * them. A page number outside 0 .. num_pages - 1 is not followed: its slots
+ * count as masked (decode), are not written (append) or not moved (evict). A
+ * length or count outside its range is cut to it. Either sets FA2_ERR_PAGE in
+ * the device status word. */
+
+/* Attention of one new token per sequence, whose own key and value are in the
+ * cache (fa2_cache_append first):
+ *   s_j = scale q . k_j for the slots j < lens[b], L = ln sum_j e^(s_j),
+ *   o = sum_j e^(s_j - L) v_j;  lens[b] = 0: o = 0, L = -inf.
+ * With weights (both or neither pointer):
+ *   weights_out[j] = weights[j] + sum over the g query heads of e^(s_j - L)
+ * for j < lens[b]; slots past that are left as they were.
+ *   q, o        : device [B][Hq][d] dtype, 16-byte aligned; o is written.
+ *   lse         : device [B][Hq] fp32, written.
+ *   weights_out : may be weights itself.
+ *   workspace   : device, >= fa2_paged_decode_workspace_size(...) bytes,
+ *                 256-byte aligned, scratch owned by the caller.
+ * The result does not depend on timing: repeated calls give the same bits. */
+int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int* table,
+                     const int* lens, const float* weights, float* weights_out, void* o, float* lse,
+                     int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                     float scale, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fa2_paged_decode: the partial results of a fixed number of CTAs
+ * and, with weights (nonzero), the fp32 logits [B][Hq][L]. 0 for invalid sizes. */
+size_t fa2_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages,
+                                       int weights);
+
+/* Appends new tokens: token i < num_new[b] of sequence b goes to slot
+ * lens[b] + i; lens_out[b] = lens[b] + num_new[b]. Tokens past L are dropped
+ * (FA2_ERR_PAGE).
+ *   k, v        : device [B][Hkv][T][d] dtype, 16-byte aligned (a prompt as
+ *                 fa2_fwd takes it, or T = 1).
+ *   num_new     : device int32 [B], 0 .. T (a padded batch), or NULL: T each.
+ *   weights     : or NULL; the new slots get new_weights[B][Hkv][T] (fp32; for a
+ *                 prompt, fa2_key_weights), or 0 if that is NULL.
+ *   positions   : or NULL; the new slots get next_pos[b] + i (int32 [B]).
+ *   lens_out    : device int32 [B], not lens itself.
+ * Pages that several sequences name must not be appended to. */
+int fa2_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int* table,
+                     const int* lens, const int* num_new, float* weights, const float* new_weights,
+                     int* positions, const int* next_pos, int* lens_out, int B, int Hkv, int T, int d,
+                     int num_pages, int page_size, int max_pages, int dtype, void* stream);
+
+/* Eviction: every (sequence, key head) with lens[b] > budget keeps budget slots,
+ * in place, in slots 0 .. budget - 1; lens_out[b] = min(lens[b], budget). Kept
+ * are, in this order, recent tokens (position >= next_pos[b] - recent; without
+ * positions the last `recent` slots) and those of the largest weight; NaN counts
+ * as the smallest, -0 as 0; of equal ones the lower slot stays. Kept slots below
+ * budget stay where they are; the i-th evicted slot below budget (ascending)
+ * takes the row, weight and position of the i-th kept slot at or past it.
+ * Pages past the new length may be given to other sequences afterwards.
+ *   weights_out, positions_out : slots below lens_out[b] are written, the others
+ *                 left as they were; each may be its input itself.
+ *   positions, positions_out, next_pos : all or none. next_pos[b] is the
+ *                 position that the next token will get.
+ *   budget      : >= 1.  recent: 0 .. budget.
+ *   lens_out    : device int32 [B], not lens itself.
+ *   workspace   : device, >= fa2_cache_evict_workspace_size(...) bytes,
+ *                 256-byte aligned, scratch owned by the caller.
+ * Pages that several sequences name must not be evicted from. After
+ * FA2_ERR_PAGE the contents of the sequence concerned are undefined. */
+int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* lens, const float* weights,
+                    float* weights_out, const int* positions, int* positions_out, const int* next_pos,
+                    int* lens_out, int B, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                    int budget, int recent, int dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Workspace of fa2_cache_evict: two int32 lists of at most min(budget,
+ * L - budget) moves per (sequence, key head). 0 for invalid sizes. */
+size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pages, int budget);
+
+/* Accumulated attention weight of a prompt's keys, after fa2_fwd / fa2_fwd_qk:
+ *   out[b][h][j] = sum over the g = Hq / Hkv query heads x of key head h and the
+ *   queries i < q_lens[b] that see key j of e^(scale q_i . k_j - lse_i).
+ *   q           : device [B][Hq][N][d] dtype; lse: device fp32 [B][Hq][N], the
+ *                 forward's (over keys repeated g times where g > 1).
+ *   k           : device [B][Hkv][Nk][d] dtype.
+ *   q_lens      : device int32 [B], 0 .. N (cut to it), or NULL: N each. A causal
+ *                 batch padded on the right counts only its real queries, and
+ *                 padded keys get 0; padded rows of q, k and lse may hold anything.
+ *   out         : device fp32 [B][Hkv][Nk], written.
+ *   causal      : top-left, as in fa2_fwd_qk. Keys that no query sees get 0.
+ *   workspace   : device, >= fa2_key_weights_workspace_size() bytes, 256-byte
+ *                 aligned, scratch owned by the caller.
+ * Sizes as in fa2_fwd, g <= 128. Repeated calls give the same bits. */
+int fa2_key_weights(const void* q, const void* k, const float* lse, const int* q_lens, float* out, int B,
+                    int Hq, int Hkv, int N, int Nk, int d, int causal, float scale, int dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+size_t fa2_key_weights_workspace_size(void);
+
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: FA2_OK, or FA2_ERR_DEVICE_TIMEOUT if any kernel since the last call
- * gave up on a bounded wait, or FA2_ERR_CUDA if the synchronisation failed. */
+ * gave up on a bounded wait, FA2_ERR_PAGE if a paged-cache kernel met a bad
+ * page, length or count, or FA2_ERR_CUDA if the synchronisation failed. */
 int fa2_get_device_status(void* stream);
 
 /* Static, human-readable name of a status code. */
