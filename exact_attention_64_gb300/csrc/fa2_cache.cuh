@@ -9,6 +9,7 @@
 // page_size * d * 2 bytes. A sequence has lens[b] slots in use, of at most
 // L = max_pages * page_size.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include "sm103_ptx.cuh"
@@ -81,6 +82,20 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Raises a kernel's shared-memory limit on the current device, once per device
+// (`done`: a mask of devices, one per kernel).
+template <class K>
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Launch of a kernel that calls grid_dependency_wait before it reads what the
@@ -160,7 +175,7 @@ struct KeyWeightArgs {
   float* part;            // workspace [2 G][256]
   int B, Hq, Hkv, g, N, Nk;
   int nkb;                // key blocks of 256
-  float scale_log2;
+  float scale_log2;       // scale * log2(e)
   int* status;
   unsigned long long timeout_ns;
 };

@@ -168,7 +168,7 @@ int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, co
   a.g = Hq / Hkv;
   const int ht = head_tile(a.g);
   a.HG = (a.g + ht - 1) / ht;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const int ctas = 2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas;
   (void)cudaGetLastError();  // a non-sticky error of another caller is not ours
   const cudaError_t e =
@@ -323,7 +323,7 @@ int fa2_key_weights(const void* q, const void* k, const float* lse, const int* q
   a.N = N;
   a.Nk = Nk;
   a.nkb = (Nk + 255) / 256;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.timeout_ns = fa2::kDefaultWaitTimeoutNs;
   const int ctas = sms < kKwCtas ? sms : kKwCtas;
   (void)cudaGetLastError();

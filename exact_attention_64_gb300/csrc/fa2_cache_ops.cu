@@ -328,7 +328,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   a.cached = per <= kEvictKeys;
   const size_t smem = a.cached ? static_cast<size_t>(per) * 4 : 0;
   auto kern = a.d == 64 ? fa2_cache_evict_kernel<64> : fa2_cache_evict_kernel<128>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictKeys * 4);
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = allow_smem(kern, kEvictKeys * 4, done[a.d == 64]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * C));

@@ -6,17 +6,23 @@
 // with L the forward's logsumexp: the column sums of the attention matrix,
 // which the forward cannot form itself, L being known only after its last tile.
 //
-// What bounds it: one product, S^T = K Q^T, 2 d flop per (key, query), and one
-// exponential for it. A 128 x 128 tile takes 512 clocks of tensor core at
-// d = 128 (256 at d = 64) and 512 clocks of the SM's 32 exponentials per clock.
+// What bounds it: one product, S = Q K^T, 2 d flop per (query, key), and one
+// exponential for it. 128 queries x 256 keys take 1024 clocks of tensor core at
+// d = 128 (512 at d = 64) and 1024 clocks of the SM's 32 exponentials per clock.
 //
-// S^T and not S: TMEM lane = key, so a thread owns a key and its sum over the
-// queries is a chain of additions in a register, without shuffles or atomics;
-// what varies along the columns, L, is one broadcast shared-memory load for
-// four columns. A work item is 256 keys (tiles A and B, a warpgroup each), so
-// that a Q tile fetched from L2 feeds two products; each tile has two S^T
-// buffers, all of TMEM, so the tensor core fills one while the warpgroup
-// reads the other.
+// Layout: TMEM lane = query, column = key, and a thread keeps the running sums
+// of its 64 columns in registers over all query tiles of an item. So L is one
+// scalar per thread and tile, nothing is read from shared memory between the
+// product and the sums (its bandwidth belongs to the product's operands), and
+// the sum over lanes happens once per item. The transposed form (lane = key)
+// needs no such sum but a broadcast read of L per column: 290 us against
+// %KW8192% us at B=2 H=16 N=8192 d=128 causal.
+//
+// A work item is 256 keys, so that a Q tile fetched from L2 feeds a product
+// 256 wide (which also reads less shared memory per flop than two of 128); the
+// four groups of compute warps own 64 columns each (64 sums a thread; 128, on
+// two groups, left no registers to overlap exponentials: 382 us). All of TMEM is two S buffers: the tensor
+// core fills one while the groups read the other.
 //
 // Split: the (item, query head, query tile) units of all items, in that order,
 // are cut into one run per SM of equal length. An item inside one run is
@@ -29,9 +35,9 @@
 namespace fa2 {
 
 constexpr int kKwKeys = 256;  // keys per item
+constexpr int kKwThreads = 384;  // 4 control warps, 2 groups of 4 compute warps
+constexpr float kLog2eRest = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 
-struct BoolTrue { static constexpr bool value = true; };
-struct BoolFalse { static constexpr bool value = false; };
 
 // Query tiles [i0, nq) of item kb; none: no query sees its keys.
 struct KwShape {
@@ -160,29 +166,166 @@ __device__ __forceinline__ bool kw_active(const KeyWeightArgs& a, const KwShape&
   return kt * kTileRows < a.Nk && (!s.causal || k.i >= kt);
 }
 
+// Shared memory: two K buffers of 256 rows (the next item's keys arrive while
+// this one's are in use) and a ring of Q tiles.
 template <int D>
 struct KwCfg {
   static constexpr int TILE = kTileRows * D * 2;
-  static constexpr int NQ = D == 128 ? 4 : 8;  // Q tiles in flight: 128 KiB
+  static constexpr int NQ = D == 128 ? 2 : 8;  // Q tiles in flight: 64 KiB, 128 KiB
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_L = OFF_Q + NQ * TILE;
-  static constexpr int SMEM = OFF_L + NQ * kTileRows * 4 + 1024;
+  static constexpr int OFF_Q = 4 * TILE;
+  static constexpr int SMEM = OFF_Q + NQ * TILE + 1024;
+};
+
+// What the compute warps need to know of a unit, written ahead by a warp of its
+// own: it keeps the unit arithmetic out of registers that hold sums.
+constexpr int kKwInfos = 4;
+struct KwInfo {
+  float2 row[kTileRows];  // (nl, f) of each query, see kw_chunk
+  float* dst;             // where the 256 sums go when the unit ends a run of its item
+  int keys;               // how many of them there are
+  int flags;              // 1, 2: tile A, B active; 4, 8: masked; 16: ends the run
+  int d0;                 // first query minus first key (not causal: past every key)
+  int rows;               // queries of the tile below the sequence's end
 };
 
 template <int D>
 struct KwShared {
-  uint64_t k_full, k_free;
+  uint64_t k_full[2], k_free[2];
   uint64_t q_full[KwCfg<D>::NQ], q_free[KwCfg<D>::NQ];
-  uint64_t l_full[KwCfg<D>::NQ], l_free[KwCfg<D>::NQ];
-  uint64_t s_full[2][2], s_free[2][2];  // [tile][buffer]
+  uint64_t s_full[2], s_free[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  float4 sums[2][32];  // per tile: sums of its 128 keys handed from warp to warp
+  uint64_t i_full[kKwInfos], i_free[kKwInfos];
+  KwInfo info[kKwInfos];
 };
 
+// S = Q K^T of one unit: M = 128 queries, N = 256 keys, or 128 if tile B has
+// nothing to see.
+template <int D, bool BF16, int N>
+__device__ __forceinline__ void kw_issue(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
+  constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t ad = make_sdesc_sw128(q_smem + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024);
+    const uint64_t bd = make_sdesc_sw128(k_smem + (kk / 4) * (kKwKeys * 128) + (kk % 4) * 32, 16, 1024);
+    umma_ss_warp(d_tmem, ad, bd, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+// 16 columns (keys) of one query row: acc += e^(score - L), as
+// 2^(s c + nl) f with nl an integer and f in 2^-0.5 .. 2^0.5. With MASK only
+// keys below lim count.
+template <bool MASK>
+__device__ __forceinline__ void kw_chunk(const uint32_t (&v)[16], float2* acc, float c, float nl, float f,
+                                         int lim) {
+  const float2 c2 = make_float2(c, c), n2 = make_float2(nl, nl), f2 = make_float2(f, f);
+#pragma unroll
+  for (int x = 0; x < 16; x += 2) {
+    const float2 e = f2_fma(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c2, n2);
+    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+    if constexpr (MASK) {
+      p.x = x < lim ? p.x : 0.f;
+      p.y = x + 1 < lim ? p.y : 0.f;
+    }
+    acc[x / 2] = f2_fma(p, f2, acc[x / 2]);
+  }
+}
+
+// The compute warps: group t = tile t, a thread = one query row (TMEM lane),
+// with the sums of the tile's 128 keys in registers.
+template <int D>
+__device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float c, long long units, int warp,
+                                           int lane, const WaitCtx& wc) {
+  const int t = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kTileRows;
+  float2 acc[64];
+#pragma unroll
+  for (int x = 0; x < 64; ++x) acc[x] = make_float2(0.f, 0.f);
+  uint32_t va[16], vb[16];
+  int n = 0, st = 0;  // unit (of this CTA), its info slot
+  for (; units > 0; --units, ++n, st = (st + 1) % kKwInfos) {
+    const int buf = n & 1;
+    const uint32_t ts = t_lane + buf * kKwKeys;
+    if (!mbar_wait_warp(&sh.i_full[st], (n / kKwInfos) & 1, wc)) return;
+    const int flags = sh.info[st].flags;
+    const float2 row = sh.info[st].row[r];
+    if (!mbar_wait_warp(&sh.s_full[buf], (n >> 1) & 1, wc)) return;
+    tc_fence_after();
+    if (flags & (1 << t)) {
+      tmem_ld_32x32b_x16(ts, va);
+      if (flags & (4 << t)) {
+        // Visible keys of this row, from the tile's first one.
+        const int lim0 = min(sh.info[st].d0 + r - t * kTileRows + 1, kTileRows);
+        const int lim = r < sh.info[st].rows ? lim0 : 0;
+#pragma unroll
+        for (int x = 0; x < 128; x += 16) {
+          tmem_wait_ld();
+          reg_fence(va);
+          kw_chunk<true>(va, acc + x / 2, c, row.x, row.y, lim - x);
+          if (x < 112) tmem_ld_32x32b_x16(ts + x + 16, va);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 128; x += 32) {
+          tmem_wait_ld();
+          reg_fence(va);
+          tmem_ld_32x32b_x16(ts + x + 16, vb);
+          kw_chunk<false>(va, acc + x / 2, c, row.x, row.y, 0);
+          tmem_wait_ld();
+          reg_fence(vb);
+          if (x < 96) tmem_ld_32x32b_x16(ts + x + 32, va);
+          kw_chunk<false>(vb, acc + x / 2 + 8, c, row.x, row.y, 0);
+        }
+      }
+    }
+    tc_fence_before();  // the buffer has been read
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.s_free[buf]);
+    if (flags & 16) {
+      // Sums over the warp's 32 rows by halving: lane l ends with keys 4 l ..
+      // 4 l + 3; then over the group's four warps, in order.
+#pragma unroll
+      for (int o = 16, m = 32; o > 0; o >>= 1, m >>= 1) {
+#pragma unroll
+        for (int x = 0; x < m; ++x) {
+          const bool up = lane & o;
+          const float2 keep = up ? acc[x + m] : acc[x], give = up ? acc[x] : acc[x + m];
+          acc[x] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, give.x, o),
+                               keep.y + __shfl_xor_sync(0xffffffffu, give.y, o));
+        }
+      }
+      float4 sum = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
+#pragma unroll
+      for (int x = 3; x > 0; --x) {
+        if (quad == x) sh.sums[t][lane] = sum;
+        named_bar_sync(1 + t, 128);
+        if (quad == x - 1) {
+          const float4 y = sh.sums[t][lane];
+          sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
+        }
+      }
+      named_bar_sync(1 + t, 128);  // read by warp 0 before the next run's warp 3 writes
+      if (quad == 0) {
+        const int key = t * kTileRows + 4 * lane, keys = sh.info[st].keys;
+        float* dst = sh.info[st].dst + key;
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (key + x < keys) dst[x] = v[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 64; ++x) acc[x] = make_float2(0.f, 0.f);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.i_free[st]);
+  }
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kKwThreads, 1)
     fa2_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const KeyWeightArgs a, const KwShape s) {
   using C = KwCfg<D>;
@@ -192,19 +335,20 @@ __global__ void __launch_bounds__(384, 1)
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&sh.k_full, 1);
-    mbar_init(&sh.k_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 8);  // one arrival per compute warp
+    }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
-      mbar_init(&sh.l_full[i], 1);
-      mbar_init(&sh.l_free[i], 8);
     }
-    for (int t = 0; t < 2; ++t)
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&sh.s_full[t][x], 1);
-        mbar_init(&sh.s_free[t][x], 4);
-      }
+    for (int i = 0; i < kKwInfos; ++i) {
+      mbar_init(&sh.i_full[i], 1);
+      mbar_init(&sh.i_free[i], 8);
+    }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -224,178 +368,137 @@ __global__ void __launch_bounds__(384, 1)
   const long long u0 = cta < G ? cta * T / G : 0, u1 = cta < G ? (cta + 1) * T / G : 0;
   KwCursor cu{};
   if (u0 < u1) cu = kw_cursor(a, s, u0, lane);
-  float* lsm = reinterpret_cast<float*>(smem + C::OFF_L);
 
-  if (warp == 0 && lane == 0 && u0 < u1) {
-    // Producer: K of each item, then its Q tiles.
-    int items = 0, qs = 0, qph = 0, last_k = -1;
-    int used = 0;  // Q stages issued
-    bool ok = true, fresh = true;
-    for (long long u = u0; u < u1 && ok; ++u) {
-      if (fresh) {
-        if (items > 0) ok = mbar_wait(&sh.k_free, (items - 1) & 1, wc);
+  if (warp < 4) {
+    // 4 x 32 x 72 + 8 x 32 x 216 = 64,512 = the launch's 384 x 168 registers.
+    setmaxnreg_dec<72>();
+    if (warp == 0 && lane == 0 && u0 < u1) {
+      // Producer: the Q tiles of the units, K of each item before its first.
+      int items = 0, qs = 0, qph = 0, used = 0;
+      bool ok = true, fresh = true;
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      for (long long u = u0; u < u1 && ok; ++u) {
+        if (fresh) {
+          const int kb = items & 1;
+          if (items > 1) ok = mbar_wait(&sh.k_free[kb], ((items >> 1) - 1) & 1, wc);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&sh.k_full[kb], 2 * C::TILE);
+          uint8_t* dst = smem + C::OFF_K + kb * 2 * C::TILE;
+#pragma unroll
+          for (int sl = 0; sl < D / 64; ++sl)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              tma_load_3d(dst + sl * (kKwKeys * 128) + t * (kTileRows * 128), &tm_k, &sh.k_full[kb], sl * 64,
+                          cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
+          ++items;
+        }
+        if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
         if (!ok) break;
-        const int bk = cu.b * a.Hkv + cu.h;
-        mbar_arrive_expect_tx(&sh.k_full, 2 * C::TILE);
-        load_tile<D>(smem + C::OFF_K, &tm_k, &sh.k_full, cu.kb * kKwKeys, bk);
-        load_tile<D>(smem + C::OFF_K + C::TILE, &tm_k, &sh.k_full, cu.kb * kKwKeys + kTileRows, bk);
-        last_k = items++;
+        mbar_arrive_expect_tx(&sh.q_full[qs], C::TILE);
+        load_tile<D>(smem + C::OFF_Q + qs * C::TILE, &tm_q, &sh.q_full[qs], cu.i * kTileRows,
+                     cu.b * a.Hq + cu.h * a.g + cu.gh);
+        ++used;
+        if (++qs == C::NQ) {
+          qs = 0;
+          qph ^= 1;
+        }
+        fresh = kw_advance(a, s, cu);
       }
-      if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
-      if (!ok) break;
-      mbar_arrive_expect_tx(&sh.q_full[qs], C::TILE);
-      load_tile<D>(smem + C::OFF_Q + qs * C::TILE, &tm_q, &sh.q_full[qs], cu.i * kTileRows,
-                   cu.b * a.Hq + cu.h * a.g + cu.gh);
-      ++used;
-      if (++qs == C::NQ) {
-        qs = 0;
-        qph ^= 1;
+      if (!ok) {  // copies in flight land before the CTA ends
+        for (int x = 0; x < 2; ++x) {
+          const int uses = (items + 1 - x) / 2;
+          if (uses > 0) mbar_wait_drain(&sh.k_full[x], (uses - 1) & 1, a.timeout_ns);
+        }
+        for (int x = 0; x < C::NQ; ++x) {
+          const int uses = used / C::NQ + (x < used % C::NQ ? 1 : 0);
+          if (uses > 0) mbar_wait_drain(&sh.q_full[x], (uses - 1) & 1, a.timeout_ns);
+        }
       }
-      fresh = kw_advance(a, s, cu);
-    }
-    if (!ok) {  // copies in flight land before the CTA ends
-      if (last_k >= 0) mbar_wait_drain(&sh.k_full, last_k & 1, a.timeout_ns);
-      for (int x = 0; x < C::NQ; ++x) {
-        const int uses = used / C::NQ + (x < used % C::NQ ? 1 : 0);
-        if (uses > 0) mbar_wait_drain(&sh.q_full[x], (uses - 1) & 1, a.timeout_ns);
-      }
-    }
-  } else if (warp == 2 && u0 < u1) {
-    // -L log2(e) of each query tile.
-    int st = 0, ph = 0;
-    bool ok = true;
-    for (long long u = u0; u < u1 && ok; ++u) {
-      const float* src = a.lse + (static_cast<size_t>(cu.b) * a.Hq + static_cast<size_t>(cu.h) * a.g + cu.gh) * a.N;
-      float v[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int q = cu.i * kTileRows + x * 32 + lane;
-        v[x] = q < cu.qlen ? -__ldg(src + q) * kLog2e : 0.f;
-      }
-      if (u - u0 >= C::NQ) ok = mbar_wait_warp(&sh.l_free[st], ph ^ 1, wc);
-      if (!ok) break;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) lsm[st * kTileRows + x * 32 + lane] = v[x];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.l_full[st]);
-      if (++st == C::NQ) {
-        st = 0;
-        ph ^= 1;
-      }
-      kw_advance(a, s, cu);
-    }
-  } else if (warp == 1 && u0 < u1) {
-    // Issuer: S^T of tiles A and B into buffer (use of the tile) % 2.
-    int items = 0, qs = 0, qph = 0, cnt[2] = {0, 0};
-    bool ok = true, fresh = true;
-    const uint32_t k_base = smem_u32(smem + C::OFF_K), q_base = smem_u32(smem + C::OFF_Q);
-    for (long long u = u0; u < u1 && ok; ++u) {
-      if (fresh) {
-        ok = mbar_wait_warp(&sh.k_full, items & 1, wc);
-        if (!ok) break;
-        ++items;
-      }
-      ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
-      if (!ok) break;
-      const bool act0 = kw_active(a, s, cu, 0), act1 = kw_active(a, s, cu, 1);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!(t == 0 ? act0 : act1)) continue;
-        const int buf = cnt[t] & 1, use = cnt[t] >> 1;
-        if (use > 0) ok = ok && mbar_wait_warp(&sh.s_free[t][buf], (use - 1) & 1, wc);
+    } else if (warp == 1 && u0 < u1) {
+      // Issuer: S of unit n into buffer n % 2.
+      int items = 0, qs = 0, qph = 0, n = 0;
+      bool ok = true, fresh = true;
+      const uint32_t k_base = smem_u32(smem + C::OFF_K), q_base = smem_u32(smem + C::OFF_Q);
+      for (long long u = u0; u < u1; ++u, ++n) {
+        if (fresh) {
+          ok = mbar_wait_warp(&sh.k_full[items & 1], (items >> 1) & 1, wc);
+          if (!ok) break;
+          ++items;
+        }
+        const int buf = n & 1, kb = (items - 1) & 1;
+        if (n > 1)
+          ok = mbar_wait2_warp(&sh.q_full[qs], qph, &sh.s_free[buf], ((n >> 1) - 1) & 1, wc);
+        else
+          ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
         if (!ok) break;
         tc_fence_after();
-        mma_rows_x_rows<D, BF16>(tmem + (t * 2 + buf) * 128, k_base + t * C::TILE, q_base + qs * C::TILE);
-        umma_commit_warp(&sh.s_full[t][buf]);
-        ++cnt[t];
+        const uint32_t d = tmem + buf * kKwKeys, q = q_base + qs * C::TILE, k = k_base + kb * 2 * C::TILE;
+        if (kw_active(a, s, cu, 1)) kw_issue<D, BF16, 256>(d, q, k);
+        else kw_issue<D, BF16, 128>(d, q, k);
+        umma_commit_warp(&sh.s_full[buf]);
+        umma_commit_warp(&sh.q_free[qs]);
+        if (++qs == C::NQ) {
+          qs = 0;
+          qph ^= 1;
+        }
+        fresh = kw_advance(a, s, cu);
+        if (fresh) umma_commit_warp(&sh.k_free[kb]);
       }
-      if (!ok) break;
-      umma_commit_warp(&sh.q_free[qs]);
-      if (++qs == C::NQ) {
-        qs = 0;
-        qph ^= 1;
-      }
-      fresh = kw_advance(a, s, cu);
-      if (fresh) umma_commit_warp(&sh.k_free);
-    }
-    umma_commit_warp(&sh.mma_done);
-    mbar_wait_drain(&sh.mma_done, 0, a.timeout_ns);
-  } else if (warp >= 4 && u0 < u1) {
-    const int t = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * 256;
-    const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    int st = 0, ph = 0, cnt = 0;
-    bool ok = true;
-    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-    bool from_start = cu.to_end == static_cast<long long>(cu.nq - s.i0(cu.kb)) * s.g;
-    for (long long u = u0; u < u1; ++u) {
-      ok = mbar_wait_warp(&sh.l_full[st], ph, wc);
-      if (!ok) break;
-      const int key = cu.kb * kKwKeys + t * kTileRows + r;
-      if (kw_active(a, s, cu, t)) {
-        const int buf = cnt & 1;
-        ok = mbar_wait_warp(&sh.s_full[t][buf], (cnt >> 1) & 1, wc);
-        if (!ok) break;
-        ++cnt;
-        tc_fence_after();
-        const float4* nl = reinterpret_cast<const float4*>(lsm + st * kTileRows);
+      umma_commit_warp(&sh.mma_done);
+      mbar_wait_drain(&sh.mma_done, 0, a.timeout_ns);
+    } else if (warp == 2 && u0 < u1) {
+      int st = 0, ph = 0;
+      bool from_start = cu.to_end == static_cast<long long>(cu.nq - s.i0(cu.kb)) * s.g;
+      for (long long u = u0; u < u1; ++u) {
+        const float* lse = a.lse + (static_cast<size_t>(cu.b) * a.Hq + static_cast<size_t>(cu.h) * a.g + cu.gh) * a.N;
         const int q0 = cu.i * kTileRows;
-        const bool mask = (s.causal && cu.i == 2 * cu.kb + t) || q0 + kTileRows > cu.qlen;
-        const uint32_t ts = t_lane + buf * 128;
+        float2 row[4];
 #pragma unroll
-        for (int cb = 0; cb < 128; cb += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(ts + cb, v);
-          tmem_wait_ld();
-          reg_fence(v);
-          if (cb == 96) {  // the buffer has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
+        for (int x = 0; x < 4; ++x) {
+          const int q = q0 + x * 32 + lane;
+          const float l = q < cu.qlen ? __ldg(lse + q) : 0.f;
+          // 2^(s c - L log2 e) with the integer part of L log2 e in the exponent
+          // and the rest as a factor: neither is rounded against the large
+          // exponents of s and L.
+          const float hi = l * kLog2e;
+          const float lo = fmaf(l, kLog2e, -hi) + l * kLog2eRest;
+          const float whole = rintf(hi);
+          row[x] = make_float2(-whole, ex2_approx(-((hi - whole) + lo)));
+        }
+        if (u - u0 >= kKwInfos && !mbar_wait_warp(&sh.i_free[st], ph ^ 1, wc)) break;
+        KwInfo& w = sh.info[st];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w.row[x * 32 + lane] = row[x];
+        if (lane == 0) {
+          const bool item_end = cu.to_end == 1, flush = item_end || u + 1 == u1;
+          const bool tail = q0 + kTileRows > cu.qlen;
+          w.flags = 1 | (kw_active(a, s, cu, 1) ? 2 : 0) | (tail || (s.causal && cu.i == 2 * cu.kb) ? 4 : 0) |
+                    (tail || (s.causal && cu.i == 2 * cu.kb + 1) ? 8 : 0) | (flush ? 16 : 0);
+          w.d0 = s.causal ? q0 - cu.kb * kKwKeys : 2 * kKwKeys;
+          w.rows = cu.qlen - q0;
+          if (from_start && item_end) {
+            w.dst = a.out + (static_cast<size_t>(cu.b) * a.Hkv + cu.h) * a.Nk + cu.kb * kKwKeys;
+            w.keys = a.Nk - cu.kb * kKwKeys;
+          } else {
+            w.dst = a.part + (static_cast<size_t>(2) * cta + (from_start ? 1 : 0)) * kKwKeys;
+            w.keys = kKwKeys;
           }
-          auto body = [&](auto masked) {
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 n4 = nl[(cb + x) / 4];
-              const float2 x0 = f2_fma(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl2,
-                                       make_float2(n4.x, n4.y));
-              const float2 x1 = f2_fma(make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl2,
-                                       make_float2(n4.z, n4.w));
-              float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-              float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-              if constexpr (decltype(masked)::value) {
-                const int q = q0 + cb + x;
-                auto seen = [&](int qq) { return qq < cu.qlen && (!s.causal || qq >= key); };
-                p0.x = seen(q) ? p0.x : 0.f;
-                p0.y = seen(q + 1) ? p0.y : 0.f;
-                p1.x = seen(q + 2) ? p1.x : 0.f;
-                p1.y = seen(q + 3) ? p1.y : 0.f;
-              }
-              acc0 = f2_add(acc0, p0);
-              acc1 = f2_add(acc1, p1);
-            }
-          };
-          if (mask) body(BoolTrue{}); else body(BoolFalse{});
         }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.l_free[st]);
-      if (++st == C::NQ) {
-        st = 0;
-        ph ^= 1;
-      }
-      const bool item_end = cu.to_end == 1;
-      if (item_end || u + 1 == u1) {
-        const float w = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-        if (from_start && item_end) {
-          if (key < a.Nk) a.out[(static_cast<size_t>(cu.b) * a.Hkv + cu.h) * a.Nk + key] = w;
-        } else {
-          a.part[(static_cast<size_t>(2) * cta + (from_start ? 1 : 0)) * kKwKeys + t * kTileRows + r] = w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.i_full[st]);
+        if (++st == kKwInfos) {
+          st = 0;
+          ph ^= 1;
         }
-        acc0 = acc1 = make_float2(0.f, 0.f);
+        if (kw_advance(a, s, cu)) from_start = true;
       }
-      if (kw_advance(a, s, cu)) from_start = true;
     }
+  } else if (u0 < u1) {
+    setmaxnreg_inc<216>();
+    kw_compute<D>(sh, tmem, a.scale_log2, u1 - u0, warp, lane, wc);
+  } else {
+    setmaxnreg_inc<216>();
   }
   __syncwarp();
   tc_fence_before();
@@ -438,9 +541,10 @@ template <int D, bool BF16>
 static cudaError_t launch_key_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const KeyWeightArgs& a,
                                         const KwShape& s, int ctas, cudaStream_t stream) {
   auto kern = fa2_key_weights_kernel<D, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KwCfg<D>::SMEM);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, KwCfg<D>::SMEM, done);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, 384, KwCfg<D>::SMEM, stream>>>(tq, tk, a, s);
+  kern<<<ctas, kKwThreads, KwCfg<D>::SMEM, stream>>>(tq, tk, a, s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_key_weights_join_kernel, dim3(static_cast<unsigned>(a.B * a.Hkv) * a.nkb),

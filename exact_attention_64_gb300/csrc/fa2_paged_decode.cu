@@ -547,7 +547,8 @@ template <int D, bool BF16, int NT, bool WEIGHTS>
 static cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
   using C = DecCfg<D, NT>;
   auto kern = fa2_paged_decode_kernel<D, BF16, NT, WEIGHTS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kDecWarps * 32, C::SMEM, stream>>>(a);
   e = cudaGetLastError();
