@@ -18,11 +18,11 @@
 // needs no such sum but a broadcast read of L per column: 290 us against
 // %KW8192% us at B=2 H=16 N=8192 d=128 causal.
 //
-// A work item is 256 keys, so that a Q tile fetched from L2 feeds a product
-// 256 wide (which also reads less shared memory per flop than two of 128); the
-// four groups of compute warps own 64 columns each (64 sums a thread; 128, on
-// two groups, left no registers to overlap exponentials: 382 us). All of TMEM is two S buffers: the tensor
-// core fills one while the groups read the other.
+// A work item is 256 keys, tiles A and B, so that a Q tile fetched from L2
+// feeds two products; two groups of four compute warps own 64 columns of each.
+// All of TMEM is two S buffers per tile. (Two groups of 128 columns, 254 us,
+// leave two warps per scheduler to hide each other's waits; one barrier pair
+// for both tiles and a barrier of its own for the facts of a unit, 260 us.)
 //
 // Split: the (item, query head, query tile) units of all items, in that order,
 // are cut into one run per SM of equal length. An item inside one run is
@@ -35,7 +35,7 @@
 namespace fa2 {
 
 constexpr int kKwKeys = 256;  // keys per item
-constexpr int kKwThreads = 384;  // 4 control warps, 2 groups of 4 compute warps
+constexpr int kKwThreads = 640;  // 4 control warps, 4 groups of 4 compute warps
 constexpr float kLog2eRest = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 
 
@@ -177,9 +177,9 @@ struct KwCfg {
   static constexpr int SMEM = OFF_Q + NQ * TILE + 1024;
 };
 
-// What the compute warps need to know of a unit, written ahead by a warp of its
-// own: it keeps the unit arithmetic out of registers that hold sums.
-constexpr int kKwInfos = 4;
+// What the compute warps need to know of a unit, written by a warp of its own:
+// it keeps the unit arithmetic out of registers that hold sums. One slot per S
+// buffer.
 struct KwInfo {
   float2 row[kTileRows];  // (nl, f) of each query, see kw_chunk
   float* dst;             // where the 256 sums go when the unit ends a run of its item
@@ -193,27 +193,13 @@ template <int D>
 struct KwShared {
   uint64_t k_full[2], k_free[2];
   uint64_t q_full[KwCfg<D>::NQ], q_free[KwCfg<D>::NQ];
-  uint64_t s_full[2], s_free[2];
+  uint64_t s_full[2][2], s_free[2][2];  // [tile][buffer]
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  float4 sums[2][32];  // per tile: sums of its 128 keys handed from warp to warp
-  uint64_t i_full[kKwInfos], i_free[kKwInfos];
-  KwInfo info[kKwInfos];
+  float2 sums[4][32];  // per group: sums of its 64 keys handed from warp to warp
+  KwInfo info[2];
 };
-
-// S = Q K^T of one unit: M = 128 queries, N = 256 keys, or 128 if tile B has
-// nothing to see.
-template <int D, bool BF16, int N>
-__device__ __forceinline__ void kw_issue(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
-  constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, false, false);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint64_t ad = make_sdesc_sw128(q_smem + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024);
-    const uint64_t bd = make_sdesc_sw128(k_smem + (kk / 4) * (kKwKeys * 128) + (kk % 4) * 32, 16, 1024);
-    umma_ss_warp(d_tmem, ad, bd, idesc, kk > 0 ? 1u : 0u);
-  }
-}
 
 // 16 columns (keys) of one query row: acc += e^(score - L), as
 // 2^(s c + nl) f with nl an integer and f in 2^-0.5 .. 2^0.5. With MASK only
@@ -234,61 +220,72 @@ __device__ __forceinline__ void kw_chunk(const uint32_t (&v)[16], float2* acc, f
   }
 }
 
-// The compute warps: group t = tile t, a thread = one query row (TMEM lane),
-// with the sums of the tile's 128 keys in registers.
+// The compute warps: group cg has columns 64 cg .. 64 cg + 63 (half of tile
+// cg / 2), a thread one query row (TMEM lane), with the sums of its 64 keys in
+// registers.
 template <int D>
 __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float c, long long units, int warp,
                                            int lane, const WaitCtx& wc) {
-  const int t = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * kTileRows;
-  float2 acc[64];
+  const int cg = (warp - 4) >> 2, t = cg >> 1, quad = warp & 3, r = quad * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * t * kTileRows + (cg & 1) * 64;
+  float2 acc[32];
 #pragma unroll
-  for (int x = 0; x < 64; ++x) acc[x] = make_float2(0.f, 0.f);
-  uint32_t va[16], vb[16];
-  int n = 0, st = 0;  // unit (of this CTA), its info slot
-  for (; units > 0; --units, ++n, st = (st + 1) % kKwInfos) {
+  for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
+  int n = 0;
+  for (; units > 0; --units, ++n) {
     const int buf = n & 1;
-    const uint32_t ts = t_lane + buf * kKwKeys;
-    if (!mbar_wait_warp(&sh.i_full[st], (n / kKwInfos) & 1, wc)) return;
-    const int flags = sh.info[st].flags;
-    const float2 row = sh.info[st].row[r];
-    if (!mbar_wait_warp(&sh.s_full[buf], (n >> 1) & 1, wc)) return;
+    const uint32_t ts = t_lane + buf * kTileRows;
+    if (!mbar_wait_warp(&sh.s_full[t][buf], (n >> 1) & 1, wc)) return;
     tc_fence_after();
-    if (flags & (1 << t)) {
+    const KwInfo& w = sh.info[buf];
+    const int flags = w.flags;
+    const float2 row = w.row[r];
+    float* dst = w.dst;
+    const int keys = w.keys;
+    if ((flags & (1 << t)) && !(flags & (4 << t))) {
+      uint32_t va[16], vb[16];
       tmem_ld_32x32b_x16(ts, va);
-      if (flags & (4 << t)) {
-        // Visible keys of this row, from the tile's first one.
-        const int lim0 = min(sh.info[st].d0 + r - t * kTileRows + 1, kTileRows);
-        const int lim = r < sh.info[st].rows ? lim0 : 0;
+      tmem_wait_ld();
+      reg_fence(va);
+      tmem_ld_32x32b_x16(ts + 16, vb);
+      kw_chunk<false>(va, acc, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(vb);
+      tmem_ld_32x32b_x16(ts + 32, va);
+      kw_chunk<false>(vb, acc + 8, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(va);
+      tmem_ld_32x32b_x16(ts + 48, vb);
+      kw_chunk<false>(va, acc + 16, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(vb);
+      tc_fence_before();  // the buffer and the facts have been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
+      kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+    } else {
+      if (flags & (1 << t)) {
+        // Visible keys of this row, from the group's first one.
+        const int lim0 = min(w.d0 + r - cg * 64 + 1, 64);
+        const int lim = r < w.rows ? lim0 : 0;
 #pragma unroll
-        for (int x = 0; x < 128; x += 16) {
+        for (int x = 0; x < 64; x += 16) {
+          uint32_t va[16];
+          tmem_ld_32x32b_x16(ts + x, va);
           tmem_wait_ld();
           reg_fence(va);
           kw_chunk<true>(va, acc + x / 2, c, row.x, row.y, lim - x);
-          if (x < 112) tmem_ld_32x32b_x16(ts + x + 16, va);
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < 128; x += 32) {
-          tmem_wait_ld();
-          reg_fence(va);
-          tmem_ld_32x32b_x16(ts + x + 16, vb);
-          kw_chunk<false>(va, acc + x / 2, c, row.x, row.y, 0);
-          tmem_wait_ld();
-          reg_fence(vb);
-          if (x < 96) tmem_ld_32x32b_x16(ts + x + 32, va);
-          kw_chunk<false>(vb, acc + x / 2 + 8, c, row.x, row.y, 0);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
     }
-    tc_fence_before();  // the buffer has been read
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.s_free[buf]);
     if (flags & 16) {
-      // Sums over the warp's 32 rows by halving: lane l ends with keys 4 l ..
-      // 4 l + 3; then over the group's four warps, in order.
+      // Sums over the warp's 32 rows by halving: lane l ends with keys 2 l and
+      // 2 l + 1; then over the group's four warps, in order.
 #pragma unroll
-      for (int o = 16, m = 32; o > 0; o >>= 1, m >>= 1) {
+      for (int o = 16, m = 16; o > 0; o >>= 1, m >>= 1) {
 #pragma unroll
         for (int x = 0; x < m; ++x) {
           const bool up = lane & o;
@@ -297,30 +294,25 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
                                keep.y + __shfl_xor_sync(0xffffffffu, give.y, o));
         }
       }
-      float4 sum = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
+      float2 sum = acc[0];
 #pragma unroll
       for (int x = 3; x > 0; --x) {
-        if (quad == x) sh.sums[t][lane] = sum;
-        named_bar_sync(1 + t, 128);
+        if (quad == x) sh.sums[cg][lane] = sum;
+        named_bar_sync(1 + cg, 128);
         if (quad == x - 1) {
-          const float4 y = sh.sums[t][lane];
-          sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
+          const float2 y = sh.sums[cg][lane];
+          sum = make_float2(sum.x + y.x, sum.y + y.y);
         }
       }
-      named_bar_sync(1 + t, 128);  // read by warp 0 before the next run's warp 3 writes
+      named_bar_sync(1 + cg, 128);  // read by warp 0 before the next run's warp 3 writes
       if (quad == 0) {
-        const int key = t * kTileRows + 4 * lane, keys = sh.info[st].keys;
-        float* dst = sh.info[st].dst + key;
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (key + x < keys) dst[x] = v[x];
+        const int key = cg * 64 + 2 * lane;
+        if (key < keys) dst[key] = sum.x;
+        if (key + 1 < keys) dst[key + 1] = sum.y;
       }
 #pragma unroll
-      for (int x = 0; x < 64; ++x) acc[x] = make_float2(0.f, 0.f);
+      for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.i_free[st]);
   }
 }
 
@@ -338,16 +330,14 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_free[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 8);  // one arrival per compute warp
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&sh.s_full[t][i], 2);  // the product and the unit's facts
+        mbar_init(&sh.s_free[t][i], 8);  // one arrival per compute warp of the tile
+      }
     }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
-    }
-    for (int i = 0; i < kKwInfos; ++i) {
-      mbar_init(&sh.i_full[i], 1);
-      mbar_init(&sh.i_free[i], 8);
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
@@ -370,8 +360,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   if (u0 < u1) cu = kw_cursor(a, s, u0, lane);
 
   if (warp < 4) {
-    // 4 x 32 x 72 + 8 x 32 x 216 = 64,512 = the launch's 384 x 168 registers.
-    setmaxnreg_dec<72>();
+    // 4 x 32 x 64 + 16 x 32 x 104 = 61,440 = the launch's 640 x 96 registers.
+    setmaxnreg_dec<64>();
     if (warp == 0 && lane == 0 && u0 < u1) {
       // Producer: the Q tiles of the units, K of each item before its first.
       int items = 0, qs = 0, qph = 0, used = 0;
@@ -384,13 +374,10 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           if (items > 1) ok = mbar_wait(&sh.k_free[kb], ((items >> 1) - 1) & 1, wc);
           if (!ok) break;
           mbar_arrive_expect_tx(&sh.k_full[kb], 2 * C::TILE);
-          uint8_t* dst = smem + C::OFF_K + kb * 2 * C::TILE;
 #pragma unroll
-          for (int sl = 0; sl < D / 64; ++sl)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              tma_load_3d(dst + sl * (kKwKeys * 128) + t * (kTileRows * 128), &tm_k, &sh.k_full[kb], sl * 64,
-                          cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
+          for (int t = 0; t < 2; ++t)
+            load_tile<D>(smem + C::OFF_K + (2 * kb + t) * C::TILE, &tm_k, &sh.k_full[kb],
+                         cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
           ++items;
         }
         if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
@@ -427,16 +414,22 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           ++items;
         }
         const int buf = n & 1, kb = (items - 1) & 1;
-        if (n > 1)
-          ok = mbar_wait2_warp(&sh.q_full[qs], qph, &sh.s_free[buf], ((n >> 1) - 1) & 1, wc);
-        else
-          ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
+        ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
+        const bool act_b = kw_active(a, s, cu, 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && n > 1) ok = mbar_wait_warp(&sh.s_free[t][buf], ((n >> 1) - 1) & 1, wc);
+          if (!ok) break;
+          if (t == 0 || act_b) {
+            tc_fence_after();
+            mma_rows_x_rows<D, BF16>(tmem + (2 * t + buf) * kTileRows, q_base + qs * C::TILE,
+                                     k_base + (2 * kb + t) * C::TILE);
+            umma_commit_warp(&sh.s_full[t][buf]);
+          } else if (lane == 0) {
+            mbar_arrive(&sh.s_full[t][buf]);
+          }
+        }
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kKwKeys, q = q_base + qs * C::TILE, k = k_base + kb * 2 * C::TILE;
-        if (kw_active(a, s, cu, 1)) kw_issue<D, BF16, 256>(d, q, k);
-        else kw_issue<D, BF16, 128>(d, q, k);
-        umma_commit_warp(&sh.s_full[buf]);
         umma_commit_warp(&sh.q_free[qs]);
         if (++qs == C::NQ) {
           qs = 0;
@@ -448,9 +441,9 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       umma_commit_warp(&sh.mma_done);
       mbar_wait_drain(&sh.mma_done, 0, a.timeout_ns);
     } else if (warp == 2 && u0 < u1) {
-      int st = 0, ph = 0;
+      int n = 0;
       bool from_start = cu.to_end == static_cast<long long>(cu.nq - s.i0(cu.kb)) * s.g;
-      for (long long u = u0; u < u1; ++u) {
+      for (long long u = u0; u < u1; ++u, ++n) {
         const float* lse = a.lse + (static_cast<size_t>(cu.b) * a.Hq + static_cast<size_t>(cu.h) * a.g + cu.gh) * a.N;
         const int q0 = cu.i * kTileRows;
         float2 row[4];
@@ -466,8 +459,9 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           const float whole = rintf(hi);
           row[x] = make_float2(-whole, ex2_approx(-((hi - whole) + lo)));
         }
-        if (u - u0 >= kKwInfos && !mbar_wait_warp(&sh.i_free[st], ph ^ 1, wc)) break;
-        KwInfo& w = sh.info[st];
+        const int buf = n & 1, par = ((n >> 1) - 1) & 1;
+        if (n > 1 && !mbar_wait2_warp(&sh.s_free[0][buf], par, &sh.s_free[1][buf], par, wc)) break;
+        KwInfo& w = sh.info[buf];
 #pragma unroll
         for (int x = 0; x < 4; ++x) w.row[x * 32 + lane] = row[x];
         if (lane == 0) {
@@ -486,19 +480,15 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.i_full[st]);
-        if (++st == kKwInfos) {
-          st = 0;
-          ph ^= 1;
-        }
+        if (lane < 2) mbar_arrive(&sh.s_full[lane][buf]);
         if (kw_advance(a, s, cu)) from_start = true;
       }
     }
   } else if (u0 < u1) {
-    setmaxnreg_inc<216>();
+    setmaxnreg_inc<104>();
     kw_compute<D>(sh, tmem, a.scale_log2, u1 - u0, warp, lane, wc);
   } else {
-    setmaxnreg_inc<216>();
+    setmaxnreg_inc<104>();
   }
   __syncwarp();
   tc_fence_before();
