@@ -163,6 +163,7 @@ struct EvictArgs {
   int* lens_out;          // [B]
   int* holes;             // workspace [B*Hkv][list]
   int* movers;            // workspace [B*Hkv][list]
+  int* counts;            // workspace [B*Hkv]: moves of each item
   int list;               // longest list of moves: min(budget, L - budget)
   int budget, recent, d;
   int cached;             // keys of a CTA's slots fit in its shared memory

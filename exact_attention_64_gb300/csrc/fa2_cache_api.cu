@@ -226,7 +226,7 @@ size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pag
   if (check_cache(B, Hkv, 64, 1, page_size, max_pages, FA2_BF16) != FA2_OK || budget < 1) return 0;
   const long long L = static_cast<long long>(max_pages) * page_size;
   const long long list = budget < L ? (budget < L - budget ? budget : L - budget) : 0;
-  return 2 * align_up(static_cast<size_t>(B) * Hkv * list * 4, 256) + 256;
+  return 2 * align_up(static_cast<size_t>(B) * Hkv * list * 4, 256) + align_up(static_cast<size_t>(B) * Hkv * 4, 256);
 }
 
 int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* lens, const float* weights,
@@ -269,9 +269,10 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
   a.next_pos = next_pos;
   a.lens_out = lens_out;
   a.list = budget < a.c.L ? (budget < a.c.L - budget ? budget : a.c.L - budget) : 0;
+  const size_t lists = align_up(static_cast<size_t>(B) * Hkv * a.list * 4, 256);
   a.holes = static_cast<int*>(workspace);
-  a.movers = reinterpret_cast<int*>(static_cast<char*>(workspace) +
-                                    align_up(static_cast<size_t>(B) * Hkv * a.list * 4, 256));
+  a.movers = reinterpret_cast<int*>(static_cast<char*>(workspace) + lists);
+  a.counts = reinterpret_cast<int*>(static_cast<char*>(workspace) + 2 * lists);
   a.budget = budget;
   a.recent = recent;
   a.d = d;

@@ -91,9 +91,18 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // positions are read once, and the histograms of a pass are added up through
 // distributed shared memory. Integer counts: the result does not depend on any
 // order. Where the keys do not fit they are made again from global memory.
+//
+// Moves: a warp takes 8 at a time, so that 4 KiB per warp are in flight. A few
+// moves per row (a cache that is one token over) are made by the cluster that
+// found them; many are left as lists to a second launch whose grid is cut by
+// moves, because the clusters of a wave find theirs at the same time and would
+// leave the memory idle until then.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictKeys = 49152;  // keys a CTA can hold: 192 KiB
+constexpr int kMoveThreads = 256;
+constexpr int kMovesPerWarp = 8;
+constexpr int kInlineMoves = 256;  // longest list that the selecting cluster works off itself
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -119,17 +128,59 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 struct EvictShared {
-  uint32_t hist[4][256];
-  uint32_t total[256];
+  __align__(16) uint32_t hist[4][256];
+  __align__(16) uint32_t total[256];
   uint32_t warp_gt[kEvictWarps], warp_tie[kEvictWarps];  // per warp, then exclusive
   uint32_t cta_gt, cta_tie, cta_gt_lo, cta_tie_lo;       // this CTA's counts
-  uint32_t digit, want;
 };
+
+// Moves m0 .. m0 + 7 of an item with `moves` of them, by a whole warp: lanes 0 ..
+// 7 look up the sources, 8 .. 15 the destinations, then all copy, 16 bytes of K
+// and of V per lane and row.
+template <int D>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int item, int m0, int moves, int lane) {
+  const CacheView& c = a.c;
+  const int b = item / c.Hkv, h = item - b * c.Hkv;
+  const size_t list = static_cast<size_t>(item) * a.list, base = static_cast<size_t>(item) * c.L;
+  const int m = m0 + (lane & 7);
+  int slot = 0, row = -1;
+  if (lane < 16 && m < moves) {
+    slot = __ldcg((lane < 8 ? a.movers : a.holes) + list + m);
+    row = slot_row(c, b, h, slot);
+    if (row < 0) report_page(c.status);
+  }
+  const int to = __shfl_down_sync(0xffffffffu, slot, 8);
+  if (lane < 8 && m < moves) {
+    a.w_out[base + to] = a.w_in[base + slot];
+    if (a.p_in != nullptr) a.p_out[base + to] = a.p_in[base + slot];
+  }
+  constexpr int CH = D / 8, RPI = 32 / CH, IT = kMovesPerWarp / RPI;
+  const int ch = lane % CH, sub = lane / CH;
+  uint4 kx[IT], vx[IT];
+  int dst[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int s = __shfl_sync(0xffffffffu, row, i * RPI + sub);
+    dst[i] = __shfl_sync(0xffffffffu, row, 8 + i * RPI + sub);
+    if (s < 0) dst[i] = -1;
+    if (dst[i] >= 0) {
+      kx[i] = reinterpret_cast<const uint4*>(a.kc + static_cast<size_t>(s) * D)[ch];
+      vx[i] = reinterpret_cast<const uint4*>(a.vc + static_cast<size_t>(s) * D)[ch];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    if (dst[i] < 0) continue;
+    reinterpret_cast<uint4*>(a.kc + static_cast<size_t>(dst[i]) * D)[ch] = kx[i];
+    reinterpret_cast<uint4*>(a.vc + static_cast<size_t>(dst[i]) * D)[ch] = vx[i];
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const EvictArgs a, int C) {
   extern __shared__ uint32_t s_keys[];
   __shared__ EvictShared sh;
+  grid_launch_dependents();
   const CacheView& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = blockIdx.x / C;
@@ -147,6 +198,7 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
     if (n != __ldg(c.lens + b)) report_page(c.status);
     a.lens_out[b] = k;
   }
+  if (rank == 0 && tid == 0 && n <= a.budget) a.counts[item] = 0;
   if (n <= a.budget) {  // nothing to evict
     for (int j = rank * kEvictThreads + tid; j < n; j += C * kEvictThreads) {
       if (copy_w) w_out[j] = w_in[j];
@@ -179,41 +231,44 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
       const uint32_t key = key_at(j);
       if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & 255u], 1u);
     }
-    if (C > 1) cluster_sync(); else __syncthreads();
-    if (tid < 256) {
-      uint32_t t = 0;
-      if (C == 1) t = sh.hist[pass][tid];
-      else
+    const uint32_t* total = sh.hist[pass];
+    if (C > 1) {
+      cluster_sync();
+      if (tid < 256) {
+        uint32_t t = 0;
         for (int x = 0; x < C; ++x) t += cluster_load(&sh.hist[pass][tid], x);
-      sh.total[tid] = t;
+        sh.total[tid] = t;
+      }
+      total = sh.total;
     }
     __syncthreads();
-    if (warp == 0) {
-      // Lane l has digits 255 - 8 l ... 248 - 8 l, the largest first.
-      uint32_t v[8], sum = 0;
+    // Every warp finds the digit for itself: lane l has digits 255 - 8 l ...
+    // 248 - 8 l, the largest first.
+    uint32_t v[8], sum = 0;
+    *reinterpret_cast<uint4*>(&v[0]) = *reinterpret_cast<const uint4*>(total + 248 - 8 * lane);
+    *reinterpret_cast<uint4*>(&v[4]) = *reinterpret_cast<const uint4*>(total + 252 - 8 * lane);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) sum += v[x] = sh.total[255 - 8 * lane - x];
-      uint32_t incl = sum;
+    for (int x = 0; x < 8; ++x) sum += v[x];
+    uint32_t incl = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      uint32_t above = incl - sum;
-      if (above < want && want <= incl) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          if (above < want && want <= above + v[x]) {
-            sh.digit = 255 - 8 * lane - x;
-            sh.want = want - above;
-          }
-          above += v[x];
-        }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
     }
-    __syncthreads();
-    prefix = (prefix << 8) | sh.digit;
-    want = sh.want;
+    uint32_t above = incl - sum, digit = 0, left = 0;
+    const unsigned hit = __ballot_sync(0xffffffffu, above < want && want <= incl);
+#pragma unroll
+    for (int x = 7; x >= 0; --x) {
+      if (above < want && want <= above + v[x]) {
+        digit = 248 - 8 * lane + x;
+        left = want - above;
+      }
+      above += v[x];
+    }
+    const int src = __ffs(hit) - 1;
+    prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, src);
+    want = __shfl_sync(0xffffffffu, left, src);
+    if (C > 1) __syncthreads();  // sh.total is rewritten by the next pass
   }
   // Slots with a key above `prefix` stay, and the first `want` of those equal to
   // it. Counts before each warp's run, over the cluster in slot order.
@@ -286,44 +341,34 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
     gt_before += __popc(gm);
     tie_before += __popc(tm);
   }
+  if (rank == 0 && tid == 0) a.counts[item] = moves;
+  // No CTA leaves while another may still read its counts, and the lists are
+  // complete after this.
   if (C > 1) cluster_sync(); else __syncthreads();
-  // The moves, 32 at a time per warp of the cluster: a lane looks up one
-  // move's rows, then the warp copies them, 16 bytes of K and of V per lane.
-  constexpr int CH = D / 8, RPI = 32 / CH;
-  const int ch = lane % CH, sub = lane / CH;
-  for (int m0 = (rank * kEvictWarps + warp) * 32; m0 < moves; m0 += C * kEvictThreads) {
-    int src = -1, dst = -1;
-    if (m0 + lane < moves) {
-      const int sj = __ldcg(movers + m0 + lane), dj = __ldcg(holes + m0 + lane);
-      src = slot_row(c, b, h, sj);
-      dst = slot_row(c, b, h, dj);
-      if (src < 0 || dst < 0) report_page(c.status);
-      w_out[dj] = w_in[sj];
-      if (p_in != nullptr) p_out[dj] = p_in[sj];
-    }
-    const int cnt = min(32, moves - m0);
-#pragma unroll 4
-    for (int i = 0; i < 32; i += RPI) {
-      if (i >= cnt) break;
-      const int s = __shfl_sync(0xffffffffu, src, i + sub), d = __shfl_sync(0xffffffffu, dst, i + sub);
-      if (s >= 0 && d >= 0) {
-        const uint4 x = *(reinterpret_cast<const uint4*>(a.kc + static_cast<size_t>(s) * D) + ch);
-        const uint4 y = *(reinterpret_cast<const uint4*>(a.vc + static_cast<size_t>(s) * D) + ch);
-        reinterpret_cast<uint4*>(a.kc + static_cast<size_t>(d) * D)[ch] = x;
-        reinterpret_cast<uint4*>(a.vc + static_cast<size_t>(d) * D)[ch] = y;
-      }
-    }
-  }
-  // No CTA leaves while another may still read its counts: the last cluster
-  // barrier above is past every distributed read.
+  if (a.list <= kInlineMoves)
+    for (int m0 = (rank * kEvictWarps + warp) * kMovesPerWarp; m0 < moves; m0 += C * kEvictWarps * kMovesPerWarp)
+      move_rows<D>(a, item, m0, moves, lane);
+}
+
+// The moves of all items, kMoveThreads / 32 * 8 per CTA.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) fa2_cache_move_kernel(const EvictArgs a, int chunks) {
+  const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  const int moves = a.counts[item];
+  const int m0 = (chunk * (kMoveThreads / 32) + warp) * kMovesPerWarp;
+  if (m0 < moves) move_rows<D>(a, item, m0, moves, lane);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   EvictArgs a = a0;
-  // CTAs per (sequence, key head). Up to 4096 slots one CTA does it without
-  // cluster barriers; longer tables are shared by 8.
-  const int C = a.c.L <= 4096 ? 1 : 8;
   const long long items = static_cast<long long>(a.c.B) * a.c.Hkv;
+  // CTAs per (sequence, key head): doubled from 1 to 8 while a CTA has more
+  // than 2048 slots and two CTAs per SM still hold all items at once, or while
+  // it has more than its shared memory takes keys for.
+  int C = 1;
+  while (C < 8 && ((a.c.L / C > 2048 && items * C * 2 <= 304) || a.c.L / C > kEvictKeys)) C *= 2;
   const long long per = ((static_cast<long long>(a.c.L) + C - 1) / C + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
   a.cached = per <= kEvictKeys;
   const size_t smem = a.cached ? static_cast<size_t>(per) * 4 : 0;
@@ -343,7 +388,13 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, C);
+  e = cudaLaunchKernelEx(&cfg, kern, a, C);
+  if (e != cudaSuccess || a.list <= kInlineMoves) return e;
+  constexpr int per_cta = kMoveThreads / 32 * kMovesPerWarp;
+  const int chunks = (a.list + per_cta - 1) / per_cta;
+  if (items * chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_dependent(a.d == 64 ? fa2_cache_move_kernel<64> : fa2_cache_move_kernel<128>,
+                          dim3(static_cast<unsigned>(items * chunks)), dim3(kMoveThreads), 0, stream, a, chunks);
 }
 
 }  // namespace fa2

@@ -373,8 +373,8 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
                     int budget, int recent, int dtype, void* workspace, size_t workspace_bytes,
                     void* stream);
 
-/* Workspace of fa2_cache_evict: two int32 lists of at most min(budget,
- * L - budget) moves per (sequence, key head). 0 for invalid sizes. */
+/* Workspace of fa2_cache_evict: per (sequence, key head) two int32 lists of at
+ * most min(budget, L - budget) moves and their count. 0 for invalid sizes. */
 size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pages, int budget);
 
 /* Accumulated attention weight of a prompt's keys, after fa2_fwd / fa2_fwd_qk:
