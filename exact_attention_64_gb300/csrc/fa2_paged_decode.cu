@@ -37,8 +37,13 @@
 
 namespace fa2 {
 
-constexpr int kUnit = 64;       // slots per unit
-constexpr int kDecWarps = 4;    // 16 slots of a unit each
+constexpr int kDecWarps = 4;
+// Slots per unit: 32 KiB of K and V. A warp has 16 (d = 128) or 32 (d = 64) of
+// them, so that its fixed cost per unit (maximum, ring, cursor) is spread over
+// the same bytes at both head sizes.
+template <int D>
+constexpr int kUnit = 64 * (128 / D);
+constexpr int kMaxGroup = 128;  // query heads per key head
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr float kLog2ef = 1.4426950408889634f;
 
@@ -80,12 +85,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // ---- Units ---------------------------------------------------------------
 // HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
-__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit - 1) / kUnit; }
+template <int D>
+__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
 
 // T, by a whole warp.
+template <int D>
 __device__ __forceinline__ long long total_units(const CacheView& c, int HH, int lane) {
   long long t = 0;
-  for (int b = lane; b < c.B; b += 32) t += static_cast<long long>(tiles_of(seq_len(c, b))) * HH;
+  for (int b = lane; b < c.B; b += 32) t += static_cast<long long>(tiles_of<D>(seq_len(c, b))) * HH;
 #pragma unroll
   for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
@@ -97,13 +104,14 @@ struct UnitCursor {
 };
 
 // Cursor of unit u < T, by a whole warp.
+template <int D>
 __device__ __forceinline__ UnitCursor unit_cursor(const CacheView& c, int HH, long long u, int lane) {
   long long base = 0;
   UnitCursor k{};
   for (int b0 = 0; b0 < c.B; b0 += 32) {
     const int b = b0 + lane;
     const int n = b < c.B ? seq_len(c, b) : 0;
-    const long long mine = static_cast<long long>(tiles_of(n)) * HH;
+    const long long mine = static_cast<long long>(tiles_of<D>(n)) * HH;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -116,7 +124,7 @@ __device__ __forceinline__ UnitCursor unit_cursor(const CacheView& c, int HH, lo
       const long long r = u - (base + __shfl_sync(0xffffffffu, incl - mine, src));
       k.b = b0 + src;
       k.n = __shfl_sync(0xffffffffu, n, src);
-      k.ntiles = tiles_of(k.n);
+      k.ntiles = tiles_of<D>(k.n);
       k.hh = static_cast<int>(r / k.ntiles);
       k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
       return k;
@@ -126,6 +134,7 @@ __device__ __forceinline__ UnitCursor unit_cursor(const CacheView& c, int HH, lo
   return k;
 }
 
+template <int D>
 __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k) {
   if (++k.tile < k.ntiles) return;
   k.tile = 0;
@@ -138,7 +147,7 @@ __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCur
     }
     k.n = seq_len(c, k.b);
   } while (k.n == 0);
-  k.ntiles = tiles_of(k.n);
+  k.ntiles = tiles_of<D>(k.n);
 }
 
 // Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer
@@ -151,9 +160,11 @@ __device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
 template <int D, int NT>
 struct DecCfg {
   static constexpr int ROW = D * 2;                        // bytes of a row
-  static constexpr int STAGE = 2 * 16 * ROW;               // a warp's K and V of one unit
-  static constexpr int STAGES = D == 128 ? 3 : 6;          // 96 KiB of ring per CTA either way
-  static constexpr int RING = kDecWarps * STAGES * STAGE;
+  static constexpr int RB = 128 / D;                       // blocks of 16 slots per warp and unit
+  static constexpr int ROWS = 16 * RB;                     // slots per warp and unit
+  static constexpr int STAGE = 2 * ROWS * ROW;             // a warp's K and V of one unit: 8 KiB
+  static constexpr int STAGES = 3;
+  static constexpr int RING = kDecWarps * STAGES * STAGE;  // 96 KiB per CTA
   static constexpr int HS = D + 4;                         // merge: floats per head (4: no bank conflicts)
   static constexpr int SMEM = RING + kDecWarps * 8 * HS * 4;
   static constexpr int HEADS = 8 * NT;                     // query heads of a tile
@@ -163,13 +174,13 @@ template <int D, bool BF16, int NT, bool WEIGHTS>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
   using C = DecCfg<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_ml[kDecWarps][C::HEADS];
+  __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const long long T = total_units(c, HH, lane);
+  const long long T = total_units<D>(c, HH, lane);
   const long long G = min(static_cast<long long>(gridDim.x), T);
   const int cta = blockIdx.x;
   if (cta == 0 && warp == 0)
@@ -177,18 +188,18 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       if (__ldg(c.lens + b) != seq_len(c, b)) report_page(c.status);
   if (cta >= G) return;
   const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
-  UnitCursor cc = unit_cursor(c, HH, u0, lane);
+  UnitCursor cc = unit_cursor<D>(c, HH, u0, lane);
   UnitCursor ic = cc;  // next unit to copy
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
   float* merge = reinterpret_cast<float*>(smem + C::RING);
 
-  // Page of this lane's slot (lane % 16 of the warp's 16) in the next unit to
+  // Page of this lane's slot (lane mod the warp's slots) in the next unit to
   // copy, looked up one unit ahead of its use.
   long long left = u1 - u0;  // units not yet copied
   int pg = 0, off = 0, hk = 0;
   bool in = false;
   auto look_up = [&]() {
-    const int slot = ic.tile * kUnit + warp * 16 + (lane & 15);
+    const int slot = ic.tile * kUnit<D> + warp * C::ROWS + (lane & (C::ROWS - 1));
     in = left > 0 && slot < ic.n;
     hk = a.HG == 1 ? ic.hh : ic.hh / a.HG;
     if (in) {
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     if (left > 0) {
       const int row = in ? page_row(c, pg, hk, off) : -1;
       if (in && row < 0) report_page(c.status);
-      const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+      const uint32_t mask = __ballot_sync(0xffffffffu, row >= 0);
       if (lane == 0) s_mask[warp][st] = mask;
       if (__any_sync(0xffffffffu, in)) {
         constexpr int CH = D / 8;            // 16-byte chunks per row
@@ -209,16 +220,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         const uint32_t base = ring + st * C::STAGE;
         const int ch = lane % CH;
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
+        for (int i = 0; i < C::ROWS / RPI; ++i) {
           const int r = i * RPI + lane / CH;
           const int rr = __shfl_sync(0xffffffffu, row, r);
           const size_t e = static_cast<size_t>(max(rr, 0)) * D + ch * 8;
           const uint32_t dst = base + r * C::ROW + ((ch ^ (r & 7)) * 16);
           cp_async16(dst, a.k + e, rr >= 0);
-          cp_async16(dst + 16 * C::ROW, a.v + e, rr >= 0);
+          cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0);
         }
       }
-      unit_advance(c, HH, ic);
+      unit_advance<D>(c, HH, ic);
       --left;
       look_up();
     }
@@ -259,43 +270,52 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     }
     cp_async_wait<C::STAGES - 1>();
     __syncwarp();
-    const int slot0 = cc.tile * kUnit + warp * 16;
+    const int slot0 = cc.tile * kUnit<D> + warp * C::ROWS;
     if (slot0 < cc.n) {
       const uint32_t mask = s_mask[warp][st];
-      const uint32_t kb = ring + st * C::STAGE, vb = kb + 16 * C::ROW;
+      const uint32_t kb = ring + st * C::STAGE, vb = kb + C::ROWS * C::ROW;
       const int lr = lane & 15, lc = lane >> 4;  // ldmatrix row and chunk of this lane
-      float s[NT][4];
+      float s[C::RB][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      for (int rb = 0; rb < C::RB; ++rb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[rb][nt][0] = s[rb][nt][1] = s[rb][nt][2] = s[rb][nt][3] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t ka[4];
-        ldsm4(ka, kb + lr * C::ROW + (((2 * kk + lc) ^ (lr & 7)) * 16));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(s[nt], ka, qf[nt][kk][0], qf[nt][kk][1]);
+        for (int rb = 0; rb < C::RB; ++rb) {
+          uint32_t ka[4];
+          ldsm4(ka, kb + (rb * 16 + lr) * C::ROW + (((2 * kk + lc) ^ (lr & 7)) * 16));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(s[rb][nt], ka, qf[nt][kk][0], qf[nt][kk][1]);
+        }
       }
-      const bool ok0 = (mask >> r8) & 1u, ok1 = (mask >> (r8 + 8)) & 1u;
-      uint32_t ph[NT][2], pl[NT][2];
+      uint32_t ph[C::RB][NT][2], pl[C::RB][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float x[C::RB][4];
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = (y < 2 ? ok0 : ok1) ? s[nt][y] * a.scale_log2 : -INFINITY;
-        if constexpr (WEIGHTS) {
-          // Logits of slots r8 and r8 + 8, heads 2t and 2t + 1 of the tile.
-          const int hd = head0 + nt * 8 + 2 * t;
-          float* lg = a.logits +
-                      ((static_cast<size_t>(cc.b) * c.Hkv + h) * c.L + slot0 + r8) * a.g + hd;
-          if (slot0 + r8 < cc.n) {
-            if (hd < a.g) lg[0] = x[0];
-            if (hd + 1 < a.g) lg[1] = x[1];
+        for (int rb = 0; rb < C::RB; ++rb) {
+          const bool ok0 = (mask >> (rb * 16 + r8)) & 1u, ok1 = (mask >> (rb * 16 + r8 + 8)) & 1u;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) x[rb][y] = (y < 2 ? ok0 : ok1) ? s[rb][nt][y] * a.scale_log2 : -INFINITY;
+          if constexpr (WEIGHTS) {
+            // Logits of slots r8 and r8 + 8, heads 2t and 2t + 1 of the tile.
+            const int hd = head0 + nt * 8 + 2 * t, j = slot0 + rb * 16 + r8;
+            float* lg = a.logits + ((static_cast<size_t>(cc.b) * c.Hkv + h) * c.L + j) * a.g + hd;
+            if (j < cc.n) {
+              if (hd < a.g) lg[0] = x[rb][0];
+              if (hd + 1 < a.g) lg[1] = x[rb][1];
+            }
+            if (j + 8 < cc.n) {
+              if (hd < a.g) lg[8 * static_cast<size_t>(a.g)] = x[rb][2];
+              if (hd + 1 < a.g) lg[8 * static_cast<size_t>(a.g) + 1] = x[rb][3];
+            }
           }
-          if (slot0 + r8 + 8 < cc.n) {
-            if (hd < a.g) lg[8 * static_cast<size_t>(a.g)] = x[2];
-            if (hd + 1 < a.g) lg[8 * static_cast<size_t>(a.g) + 1] = x[3];
-          }
+          mx0 = fmaxf(mx0, fmaxf(x[rb][0], x[rb][2]));
+          mx1 = fmaxf(mx1, fmaxf(x[rb][1], x[rb][3]));
         }
-        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
 #pragma unroll
         for (int of = 4; of < 32; of <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, of));
@@ -320,29 +340,35 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           }
         }
         const float z0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-        float p[4];
-        p[0] = ex2_approx(x[0] - z0);
-        p[1] = ex2_approx(x[1] - z1);
-        p[2] = ex2_approx(x[2] - z0);
-        p[3] = ex2_approx(x[3] - z1);
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        const uint32_t h0 = pack_x2<BF16>(p[0], p[1]), h1 = pack_x2<BF16>(p[2], p[3]);
-        const float2 b0 = unpack_x2<BF16>(h0), b1 = unpack_x2<BF16>(h1);
-        ph[nt][0] = transpose8(h0);
-        ph[nt][1] = transpose8(h1);
-        pl[nt][0] = transpose8(pack_x2<BF16>(p[0] - b0.x, p[1] - b0.y));
-        pl[nt][1] = transpose8(pack_x2<BF16>(p[2] - b1.x, p[3] - b1.y));
+#pragma unroll
+        for (int rb = 0; rb < C::RB; ++rb) {
+          float p[4];
+          p[0] = ex2_approx(x[rb][0] - z0);
+          p[1] = ex2_approx(x[rb][1] - z1);
+          p[2] = ex2_approx(x[rb][2] - z0);
+          p[3] = ex2_approx(x[rb][3] - z1);
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          const uint32_t h0 = pack_x2<BF16>(p[0], p[1]), h1 = pack_x2<BF16>(p[2], p[3]);
+          const float2 b0 = unpack_x2<BF16>(h0), b1 = unpack_x2<BF16>(h1);
+          ph[rb][nt][0] = transpose8(h0);
+          ph[rb][nt][1] = transpose8(h1);
+          pl[rb][nt][0] = transpose8(pack_x2<BF16>(p[0] - b0.x, p[1] - b0.y));
+          pl[rb][nt][1] = transpose8(pack_x2<BF16>(p[2] - b1.x, p[3] - b1.y));
+        }
       }
       const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
-        uint32_t va[4];
-        ldsm4_t(va, vb + vr * C::ROW + (((2 * dt + vc) ^ (vr & 7)) * 16));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816<BF16>(o[nt][dt], va, ph[nt][0], ph[nt][1]);
-          mma16816<BF16>(o[nt][dt], va, pl[nt][0], pl[nt][1]);
+        for (int rb = 0; rb < C::RB; ++rb) {
+          uint32_t va[4];
+          ldsm4_t(va, vb + (rb * 16 + vr) * C::ROW + (((2 * dt + vc) ^ (vr & 7)) * 16));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<BF16>(o[nt][dt], va, ph[rb][nt][0], ph[rb][nt][1]);
+            mma16816<BF16>(o[nt][dt], va, pl[rb][nt][0], pl[rb][nt][1]);
+          }
         }
       }
     }
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           float x = l[nt][y];
 #pragma unroll
           for (int of = 4; of < 32; of <<= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
-          if (r8 == 0) s_ml[warp][nt * 8 + 2 * t + y] = make_float2(m[nt][y], x);
+          if (r8 == 0) s_ml[warp][2 * t + y] = make_float2(m[nt][y], x);
         }
         float* mg = merge + warp * 8 * C::HS;
 #pragma unroll
@@ -377,13 +403,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         const int e0 = (threadIdx.x & 15) * (D / 16); // its first element here
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, s_ml[w][nt * 8 + hd].x);
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, s_ml[w][hd].x);
         float S = 0.f, acc[D / 16];
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) acc[x] = 0.f;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-          const float2 ml = s_ml[w][nt * 8 + hd];
+          const float2 ml = s_ml[w][hd];
           const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
           S += ml.y * f;
           const float4* src = reinterpret_cast<const float4*>(merge + (w * 8 + hd) * C::HS + e0);
@@ -417,7 +443,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         __syncthreads();
       }
     }
-    unit_advance(c, HH, cc);
+    unit_advance<D>(c, HH, cc);
   }
 }
 
@@ -439,43 +465,91 @@ __device__ __forceinline__ int part_slot(int x, int c0) { return 2 * x + (x == c
 
 // (M, S) of one head over an item's parts, by a whole warp.
 __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int hd, ItemParts p, int lane) {
-  float M = -INFINITY;
-  for (int x = p.c0 + lane; x <= p.c1; x += 32)
-    M = fmaxf(M, part_ml[static_cast<size_t>(part_slot(x, p.c0)) * heads + hd].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float S = 0.f;
+  float M = -INFINITY, S = 0.f;
+#pragma unroll 4
   for (int x = p.c0 + lane; x <= p.c1; x += 32) {
     const float2 ml = part_ml[static_cast<size_t>(part_slot(x, p.c0)) * heads + hd];
-    S += ml.x == -INFINITY ? 0.f : ml.y * ex2_approx(ml.x - M);
+    const float n = fmaxf(M, ml.x);
+    if (n != -INFINITY) S = S * ex2_approx(M - n) + ml.y * ex2_approx(ml.x - n);
+    M = n;
   }
+  float top = M;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  S = top == -INFINITY ? 0.f : S * ex2_approx(M - top);
 #pragma unroll
   for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-  return make_float2(M, S);
+  return make_float2(top, S);
+}
+
+// What bounds the join: the latency of a few dependent reads, and with weights
+// the logits, which come from L2. Hence many threads, and several independent
+// loads per thread.
+constexpr int kJoinThreads = 512;
+
+// w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
+// slot are read at a time.
+template <int VEC>
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, int j0, int j1, const float* s_lse) {
+  constexpr int U = 4;  // slots per thread in flight
+  const int g = a.g;
+  for (int j = j0 + threadIdx.x; j < j1; j += U * kJoinThreads) {
+    float w[U], add[U];
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int jj = j + y * kJoinThreads;
+      w[y] = jj < j1 ? a.w_in[base + jj] : 0.f;
+      add[y] = 0.f;
+    }
+    for (int hd = 0; hd < g; hd += VEC) {
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        const int jj = j + y * kJoinThreads;
+        if (jj >= j1) continue;
+        const float* lg = a.logits + (base + jj) * g + hd;
+        float x[VEC];
+        if constexpr (VEC == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(lg);
+        else if constexpr (VEC == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(lg);
+        else x[0] = *lg;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) add[y] += x[e] == -INFINITY ? 0.f : ex2_approx(x[e] - s_lse[hd + e]);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int jj = j + y * kJoinThreads;
+      if (jj < j1) a.w_out[base + jj] = w[y] + add[y];
+    }
+  }
 }
 
 template <int D, bool BF16, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(128) fa2_paged_join_kernel(const DecodeArgs a) {
-  constexpr int HEADS = 8 * NT;
-  extern __shared__ float s_lse[];  // [g], log2 units (weights)
+__global__ void __launch_bounds__(kJoinThreads) fa2_paged_join_kernel(const DecodeArgs a) {
+  constexpr int HEADS = 8 * NT, WARPS = kJoinThreads / 32;
   __shared__ float2 s_ml[HEADS];
+  __shared__ float4 s_acc[WARPS][8];
+  __shared__ float s_lse[kMaxGroup];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const long long T = total_units(c, HH, lane);
+  const long long T = total_units<D>(c, HH, lane);
   const long long G = min(static_cast<long long>(gridDim.x), T);
   const int cta = blockIdx.x;
+  long long u0 = 0, u1 = 0;
+  UnitCursor cc{};
+  if (cta < G) {
+    u0 = unit_begin(cta, G, T);
+    u1 = unit_begin(cta + 1, G, T);
+    cc = unit_cursor<D>(c, HH, u0, lane);
+  }
   grid_dependency_wait();
   // Sequences without a token: o = 0, L = -inf.
   for (int b = cta; b < c.B; b += gridDim.x) {
     if (seq_len(c, b) > 0) continue;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
-    for (int x = threadIdx.x; x < a.Hq * D / 2; x += 128) dst[x] = 0u;
-    for (int x = threadIdx.x; x < a.Hq; x += 128) a.lse[static_cast<size_t>(b) * a.Hq + x] = -INFINITY;
+    for (int x = threadIdx.x; x < a.Hq * D / 2; x += kJoinThreads) dst[x] = 0u;
+    for (int x = threadIdx.x; x < a.Hq; x += kJoinThreads) a.lse[static_cast<size_t>(b) * a.Hq + x] = -INFINITY;
   }
-  if (cta >= G) return;
-  const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
-  UnitCursor cc = unit_cursor(c, HH, u0, lane);
   for (long long u = u0; u < u1;) {
     const long long ub = u - cc.tile;  // first unit of the item
     const int cnt = static_cast<int>(min(static_cast<long long>(cc.ntiles - cc.tile), u1 - u));
@@ -483,62 +557,84 @@ __global__ void __launch_bounds__(128) fa2_paged_join_kernel(const DecodeArgs a)
     const ItemParts p = item_parts(ub, cc.ntiles, G, T);
     const int P = p.c1 - p.c0 + 1;
     const size_t row0 = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g;
+    const int heads = min(HEADS, a.g - hg * HEADS);  // of this tile
     if (P > 1) {
-      for (int hd = warp; hd < HEADS; hd += 4) {
-        if (hg * HEADS + hd >= a.g) break;
+      for (int hd = warp; hd < heads; hd += WARPS) {
         const float2 x = join_ml(a.part_ml, HEADS, hd, p, lane);
         if (lane == 0) s_ml[hd] = x;
       }
       __syncthreads();
-      for (int hd = cta - p.c0; hd < HEADS && hg * HEADS + hd < a.g; hd += P) {
+      // Pieces of 32 elements of one head, dealt to the parts' CTAs; 8 threads
+      // read a part's piece.
+      constexpr int PC = D / 32;
+      for (int y = cta - p.c0; y < heads * PC; y += P) {
+        const int hd = y / PC, e0 = (y - hd * PC) * 32 + (lane & 7) * 4;
         const float2 ml = s_ml[hd];
-        const size_t row = row0 + hg * HEADS + hd;
-        for (int e = threadIdx.x; e < D; e += 128) {
-          float acc = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-          for (int x = p.c0; x <= p.c1; ++x) {
-            const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
-            const float px = a.part_ml[at].x;
-            acc += (px == -INFINITY ? 0.f : ex2_approx(px - ml.x)) * a.part_o[at * D + e];
-          }
-          acc = ml.y > 0.f ? acc / ml.y : 0.f;
-          a.o[row * D + e] = static_cast<uint16_t>(pack_x2<BF16>(acc, 0.f) & 0xffffu);
+        for (int x = p.c0 + (threadIdx.x >> 3); x <= p.c1; x += kJoinThreads / 8) {
+          const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
+          const float px = a.part_ml[at].x;
+          const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + e0);
+          const float f = px == -INFINITY ? 0.f : ex2_approx(px - ml.x);
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
         }
-        if (threadIdx.x == 0) a.lse[row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+        }
+        if (lane < 8) s_acc[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0 && lane < 8) {
+#pragma unroll
+          for (int x = 1; x < WARPS; ++x) {
+            const float4 v = s_acc[x][lane];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+          }
+          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+          const size_t row = row0 + hg * HEADS + hd;
+          *reinterpret_cast<uint2*>(a.o + row * D + e0) =
+              make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+          if (e0 == 0) a.lse[row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
+        }
+        __syncthreads();
       }
     }
     if constexpr (WEIGHTS) {
       if (hg == 0) {
         // L of every head of the group, whatever its tile's parts are.
-        for (int hd = warp; hd < a.g; hd += 4) {
+        for (int hd = warp; hd < a.g; hd += WARPS) {
           const int x = hd / HEADS;
-          const ItemParts px = item_parts(ub + static_cast<long long>(x) * cc.ntiles, cc.ntiles, G, T);
+          const ItemParts px = x == 0 ? p : item_parts(ub + static_cast<long long>(x) * cc.ntiles, cc.ntiles, G, T);
           float v;
           if (px.c0 == px.c1) {
             v = a.lse[row0 + hd] * kLog2ef;
           } else {
-            const float2 ml = join_ml(a.part_ml, HEADS, hd - x * HEADS, px, lane);
+            const float2 ml = x == 0 ? s_ml[hd] : join_ml(a.part_ml, HEADS, hd - x * HEADS, px, lane);
             v = ml.y > 0.f ? ml.x + log2f(ml.y) : -INFINITY;
           }
           if (lane == 0) s_lse[hd] = v;
         }
         __syncthreads();
         const size_t base = (static_cast<size_t>(cc.b) * c.Hkv + h) * c.L;
-        const int j1 = min((cc.tile + cnt) * kUnit, cc.n);
-        for (int j = cc.tile * kUnit + threadIdx.x; j < j1; j += 128) {
-          const float* lg = a.logits + (base + j) * a.g;
-          float w = 0.f;
-          for (int hd = 0; hd < a.g; ++hd) {
-            const float x = lg[hd];
-            w += x == -INFINITY ? 0.f : ex2_approx(x - s_lse[hd]);
-          }
-          a.w_out[base + j] = a.w_in[base + j] + w;
-        }
+        const int j0 = cc.tile * kUnit<D>, j1 = min((cc.tile + cnt) * kUnit<D>, cc.n);
+        if (a.g % 4 == 0) add_weights<4>(a, base, j0, j1, s_lse);
+        else if (a.g % 2 == 0) add_weights<2>(a, base, j0, j1, s_lse);
+        else add_weights<1>(a, base, j0, j1, s_lse);
       }
     }
     __syncthreads();  // s_ml, s_lse are rewritten by the next item
     cc.tile += cnt - 1;
-    unit_advance(c, HH, cc);
+    unit_advance<D>(c, HH, cc);
     u += cnt;
   }
 }
@@ -553,8 +649,8 @@ static cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, cudaStream_t s
   kern<<<ctas, kDecWarps * 32, C::SMEM, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas), dim3(128),
-                          WEIGHTS ? a.g * sizeof(float) : 0, stream, a);
+  return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas), dim3(kJoinThreads), 0,
+                          stream, a);
 }
 
 cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas,
