@@ -14,6 +14,7 @@ bfloat16 (``d`` in {64, 128}); the logsumexp is float32 ``[B, H, N]``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from pathlib import Path
 
@@ -471,9 +472,23 @@ def _need(name, t, shape, dtype, index):
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
+def _space(name, *sizes):
+    """A workspace size of the library; a pure function of the sizes."""
+    need = getattr(load_library(), name)(*sizes)
+    if need == 0:
+        raise FA2Error(name, 1)
+    return need
+
+
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(load_library(), name)
+
+
 def _call(name, index, *args):
     """The library's entry points work on the current device."""
-    fn = getattr(load_library(), name)
+    fn = _entry(name)
     if _current_device() == index:
         code = fn(*args, _raw_stream(index))
     else:
@@ -483,10 +498,8 @@ def _call(name, index, *args):
         raise FA2Error(name, code)
 
 
-def _workspace(workspace, need, func, dev):
+def _workspace(workspace, need, dev):
     """(tensor, bytes): the caller's scratch, or a new one."""
-    if need == 0:
-        raise FA2Error(func, 1)
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev), need
     if workspace.device != dev or not workspace.is_contiguous():
@@ -549,9 +562,8 @@ def paged_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, w
         raise ValueError("weights_out needs weights")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = load_library().fa2_paged_decode_workspace_size(B, Hq, Hkv, d, ps, max_pages,
-                                                          int(weights is not None))
-    ws, nbytes = _workspace(workspace, need, "fa2_paged_decode_workspace_size", q.device)
+    need = _space("fa2_paged_decode_workspace_size", B, Hq, Hkv, d, ps, max_pages, int(weights is not None))
+    ws, nbytes = _workspace(workspace, need, q.device)
     _call("fa2_paged_decode", index, qp, *cache, wp, wop, op, lp, B, Hq, Hkv, d, num_pages, ps,
           max_pages, float(scale), _DTYPES[dt], ws.data_ptr(), nbytes)
     return out, lse
@@ -627,8 +639,8 @@ def cache_evict(k_cache, v_cache, table, lens, weights, budget: int, recent: int
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     lp = _need("lens_out", lens_out, (B,), torch.int32, index)
-    need = load_library().fa2_cache_evict_workspace_size(B, Hkv, ps, max_pages, budget)
-    ws, nbytes = _workspace(workspace, need, "fa2_cache_evict_workspace_size", lens.device)
+    need = _space("fa2_cache_evict_workspace_size", B, Hkv, ps, max_pages, budget)
+    ws, nbytes = _workspace(workspace, need, lens.device)
     _call("fa2_cache_evict", index, *cache, wp, wop, pp, pop, xp, lp, B, Hkv, d, num_pages, ps,
           max_pages, budget, recent, _DTYPES[k_cache.dtype], ws.data_ptr(), nbytes)
     return lens_out
@@ -660,8 +672,7 @@ def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_l
     op = _need("out", out, (B, Hkv, Nk), torch.float32, index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = load_library().fa2_key_weights_workspace_size()
-    ws, nbytes = _workspace(workspace, need, "fa2_key_weights_workspace_size", q.device)
+    ws, nbytes = _workspace(workspace, _space("fa2_key_weights_workspace_size"), q.device)
     _call("fa2_key_weights", index, qp, kp, sp, np_, op, B, Hq, Hkv, N, Nk, d, int(bool(causal)), float(scale),
           _DTYPES[dt], ws.data_ptr(), nbytes)
     return out

@@ -116,6 +116,9 @@ inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
+// Slots per unit of the decode: 32 KiB of K and V.
+__host__ __device__ constexpr int decode_unit(int d) { return 64 * (128 / d); }
+
 // ---- Arguments ------------------------------------------------------------
 struct DecodeArgs {
   CacheView c;
@@ -131,6 +134,7 @@ struct DecodeArgs {
   float2* part_ml;        // workspace [2 G][heads of a tile]: its (m, l), m in log2 units
   int Hq, g;              // query heads; query heads per key head
   int HG;                 // head tiles per key head
+  int join_split;         // blocks of the join per CTA of the decode
   float scale_log2;       // scale * log2(e)
 };
 

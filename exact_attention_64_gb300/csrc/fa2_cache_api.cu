@@ -92,13 +92,21 @@ size_t slot_bytes(int B, int Hkv, int page_size, int max_pages) {
 // its products; 16 read a group's keys half as often.
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
 
+// Most CTAs that a decode can use: one per unit of a full table.
+int decode_ctas(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
+  const int g = Hq / Hkv, unit = fa2::decode_unit(d);
+  const long long L = static_cast<long long>(page_size) * max_pages;
+  const long long units = static_cast<long long>(B) * Hkv * ((g + head_tile(g) - 1) / head_tile(g)) * ((L + unit - 1) / unit);
+  return units < kDecodeCtas ? static_cast<int>(units) : kDecodeCtas;
+}
+
 // Workspace of the decode: partial O and (m, l) of cut items, then the logits.
 struct DecodeSpace {
   size_t o, ml, logits, total;
 };
 DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_pages, bool weights) {
   DecodeSpace s{};
-  const size_t parts = static_cast<size_t>(2) * kDecodeCtas * head_tile(Hq / Hkv);
+  const size_t parts = static_cast<size_t>(2) * decode_ctas(B, Hq, Hkv, d, page_size, max_pages) * head_tile(Hq / Hkv);
   s.o = 0;
   s.ml = align_up(parts * d * 4, 256);
   s.logits = s.ml + align_up(parts * 8, 256);
@@ -169,7 +177,7 @@ int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, co
   const int ht = head_tile(a.g);
   a.HG = (a.g + ht - 1) / ht;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const int ctas = 2 * sms < kDecodeCtas ? 2 * sms : kDecodeCtas;
+  const int most = decode_ctas(B, Hq, Hkv, d, page_size, max_pages), ctas = 2 * sms < most ? 2 * sms : most;
   (void)cudaGetLastError();  // a non-sticky error of another caller is not ours
   const cudaError_t e =
       fa2::launch_paged_decode(d, dtype == FA2_BF16, ht, a, ctas, static_cast<cudaStream_t>(stream));

@@ -42,14 +42,23 @@ constexpr int kDecWarps = 4;
 // them, so that its fixed cost per unit (maximum, ring, cursor) is spread over
 // the same bytes at both head sizes.
 template <int D>
-constexpr int kUnit = 64 * (128 / D);
+constexpr int kUnit = decode_unit(D);
 constexpr int kMaxGroup = 128;  // query heads per key head
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr float kLog2ef = 1.4426950408889634f;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+// `pol`: the cache is read once, so its lines leave L2 first; what the join
+// reads again (logits, partial results) stays.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full, uint64_t pol) {
   const int n = full ? 16 : 0;  // 0: the 16 bytes are filled with zeros, src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(n),
+               "l"(pol)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -190,6 +199,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
   UnitCursor cc = unit_cursor<D>(c, HH, u0, lane);
   UnitCursor ic = cc;  // next unit to copy
+  const uint64_t pol = read_once_policy();
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
   float* merge = reinterpret_cast<float*>(smem + C::RING);
 
@@ -225,8 +235,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           const int rr = __shfl_sync(0xffffffffu, row, r);
           const size_t e = static_cast<size_t>(max(rr, 0)) * D + ch * 8;
           const uint32_t dst = base + r * C::ROW + ((ch ^ (r & 7)) * 16);
-          cp_async16(dst, a.k + e, rr >= 0);
-          cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0);
+          cp_async16(dst, a.k + e, rr >= 0, pol);
+          cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0, pol);
         }
       }
       unit_advance<D>(c, HH, ic);
@@ -304,13 +314,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
             // Logits of slots r8 and r8 + 8, heads 2t and 2t + 1 of the tile.
             const int hd = head0 + nt * 8 + 2 * t, j = slot0 + rb * 16 + r8;
             float* lg = a.logits + ((static_cast<size_t>(cc.b) * c.Hkv + h) * c.L + j) * a.g + hd;
-            if (j < cc.n) {
-              if (hd < a.g) lg[0] = x[rb][0];
-              if (hd + 1 < a.g) lg[1] = x[rb][1];
-            }
-            if (j + 8 < cc.n) {
-              if (hd < a.g) lg[8 * static_cast<size_t>(a.g)] = x[rb][2];
-              if (hd + 1 < a.g) lg[8 * static_cast<size_t>(a.g) + 1] = x[rb][3];
+            const bool in0 = j < cc.n, in1 = j + 8 < cc.n;
+            if (a.g % 2 == 0) {
+              if (hd < a.g && in0) *reinterpret_cast<float2*>(lg) = make_float2(x[rb][0], x[rb][1]);
+              if (hd < a.g && in1)
+                *reinterpret_cast<float2*>(lg + 8 * static_cast<size_t>(a.g)) = make_float2(x[rb][2], x[rb][3]);
+            } else {
+              if (hd < a.g && in0) lg[0] = x[rb][0];
+              if (hd + 1 < a.g && in0) lg[1] = x[rb][1];
+              if (hd < a.g && in1) lg[8 * static_cast<size_t>(a.g)] = x[rb][2];
+              if (hd + 1 < a.g && in1) lg[8 * static_cast<size_t>(a.g) + 1] = x[rb][3];
             }
           }
           mx0 = fmaxf(mx0, fmaxf(x[rb][0], x[rb][2]));
@@ -483,9 +496,12 @@ __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int 
 }
 
 // What bounds the join: the latency of a few dependent reads, and with weights
-// the logits, which come from L2. Hence many threads, and several independent
-// loads per thread.
-constexpr int kJoinThreads = 512;
+// the logits, which come from L2. So a CTA's range is shared by up to
+// kJoinSplit blocks when there are logits, one per kJoinUnits units, and a
+// thread has several loads in flight.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 4;
+constexpr int kJoinUnits = 8;
 
 // w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
 // slot are read at a time.
@@ -523,105 +539,148 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, in
   }
 }
 
+// O and L of the heads of one cut item, by block `sub` of `subs` of CTA `cta`.
+// Pieces of 32 elements of a head are dealt to the blocks of all its parts.
+template <int D, bool BF16, int NT>
+__device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int cta, int sub,
+                                          int subs, int warp, int lane, bool need_ml, float2* s_ml, float4 (*s_acc)[8]) {
+  constexpr int HEADS = 8 * NT, WARPS = kJoinThreads / 32, PC = D / 32;
+  const int P = p.c1 - p.c0 + 1;
+  const int h = k.hh / a.HG, hg = k.hh - h * a.HG;
+  const int heads = min(HEADS, a.g - hg * HEADS);
+  const size_t row0 = static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + hg * HEADS;
+  if (!need_ml && (cta - p.c0) * subs + sub >= heads * PC) return;  // nothing dealt to this block
+  for (int hd = warp; hd < heads; hd += WARPS) {
+    const float2 x = join_ml(a.part_ml, HEADS, hd, p, lane);
+    if (lane == 0) s_ml[hd] = x;
+  }
+  __syncthreads();
+  // Few parts: a warp per piece, four parts at a time. Many: the block.
+  const bool wide = P > 32;
+  const int rank = (cta - p.c0) * subs + sub, ranks = P * subs;
+  const int step = wide ? kJoinThreads / 8 : 4, first = wide ? threadIdx.x >> 3 : lane >> 3;
+  for (int y = wide ? rank : rank + ranks * warp; y < heads * PC; y += wide ? ranks : ranks * WARPS) {
+    const int hd = y / PC, e0 = (y - hd * PC) * 32 + (lane & 7) * 4;
+    const float2 ml = s_ml[hd];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = p.c0 + first; x <= p.c1; x += step) {
+      const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
+      const float px = a.part_ml[at].x;
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + e0);
+      const float f = px == -INFINITY ? 0.f : ex2_approx(px - ml.x);
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+    }
+    if (wide) {
+      if (lane < 8) s_acc[warp][lane] = acc;
+      __syncthreads();
+      if (warp == 0 && lane < 8) {
+#pragma unroll
+        for (int x = 1; x < WARPS; ++x) {
+          const float4 v = s_acc[x][lane];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (lane < 8 && (!wide || warp == 0)) {
+      const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+      *reinterpret_cast<uint2*>(a.o + (row0 + hd) * D + e0) =
+          make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+      if (e0 == 0) a.lse[row0 + hd] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
+    }
+  }
+  __syncthreads();
+}
+
 template <int D, bool BF16, int NT, bool WEIGHTS>
 __global__ void __launch_bounds__(kJoinThreads) fa2_paged_join_kernel(const DecodeArgs a) {
   constexpr int HEADS = 8 * NT, WARPS = kJoinThreads / 32;
-  __shared__ float2 s_ml[HEADS];
+  const int split = a.join_split;
+  __shared__ float2 s_ml[2][HEADS];  // of the CTA's first and last item, if cut
   __shared__ float4 s_acc[WARPS][8];
   __shared__ float s_lse[kMaxGroup];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
   const long long T = total_units<D>(c, HH, lane);
-  const long long G = min(static_cast<long long>(gridDim.x), T);
-  const int cta = blockIdx.x;
-  long long u0 = 0, u1 = 0;
-  UnitCursor cc{};
+  const long long G = min(static_cast<long long>(gridDim.x / split), T);
+  const int cta = blockIdx.x / split, sub = blockIdx.x - cta * split;
+  long long u0 = 0, u1 = 0, v0 = 0, v1 = 0;  // units of the CTA, and this block's share of them
+  int subs = 1;
+  UnitCursor first{}, last{}, cc{};
   if (cta < G) {
     u0 = unit_begin(cta, G, T);
     u1 = unit_begin(cta + 1, G, T);
-    cc = unit_cursor<D>(c, HH, u0, lane);
+    subs = static_cast<int>(max(1LL, min(static_cast<long long>(split), (u1 - u0) / kJoinUnits)));
+    if (sub < subs) {
+      v0 = u0 + (u1 - u0) * sub / subs;
+      v1 = u0 + (u1 - u0) * (sub + 1) / subs;
+      first = last = cc = unit_cursor<D>(c, HH, u0, lane);
+      last.tile += static_cast<int>(u1 - 1 - u0);
+      if (first.tile + (u1 - 1 - u0) >= first.ntiles) last = unit_cursor<D>(c, HH, u1 - 1, lane);
+      if (sub > 0) cc = unit_cursor<D>(c, HH, v0, lane);
+    }
   }
   grid_dependency_wait();
   // Sequences without a token: o = 0, L = -inf.
-  for (int b = cta; b < c.B; b += gridDim.x) {
+  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     if (seq_len(c, b) > 0) continue;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
     for (int x = threadIdx.x; x < a.Hq * D / 2; x += kJoinThreads) dst[x] = 0u;
     for (int x = threadIdx.x; x < a.Hq; x += kJoinThreads) a.lse[static_cast<size_t>(b) * a.Hq + x] = -INFINITY;
   }
-  for (long long u = u0; u < u1;) {
-    const long long ub = u - cc.tile;  // first unit of the item
-    const int cnt = static_cast<int>(min(static_cast<long long>(cc.ntiles - cc.tile), u1 - u));
-    const int h = cc.hh / a.HG, hg = cc.hh - h * a.HG;
-    const ItemParts p = item_parts(ub, cc.ntiles, G, T);
-    const int P = p.c1 - p.c0 + 1;
-    const size_t row0 = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g;
-    const int heads = min(HEADS, a.g - hg * HEADS);  // of this tile
-    if (P > 1) {
-      for (int hd = warp; hd < heads; hd += WARPS) {
-        const float2 x = join_ml(a.part_ml, HEADS, hd, p, lane);
-        if (lane == 0) s_ml[hd] = x;
-      }
-      __syncthreads();
-      // Pieces of 32 elements of one head, dealt to the parts' CTAs; 8 threads
-      // read a part's piece.
-      constexpr int PC = D / 32;
-      for (int y = cta - p.c0; y < heads * PC; y += P) {
-        const int hd = y / PC, e0 = (y - hd * PC) * 32 + (lane & 7) * 4;
-        const float2 ml = s_ml[hd];
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int x = p.c0 + (threadIdx.x >> 3); x <= p.c1; x += kJoinThreads / 8) {
-          const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
-          const float px = a.part_ml[at].x;
-          const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + e0);
-          const float f = px == -INFINITY ? 0.f : ex2_approx(px - ml.x);
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
-        }
-#pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-        }
-        if (lane < 8) s_acc[warp][lane] = acc;
-        __syncthreads();
-        if (warp == 0 && lane < 8) {
-#pragma unroll
-          for (int x = 1; x < WARPS; ++x) {
-            const float4 v = s_acc[x][lane];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-          }
-          const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
-          const size_t row = row0 + hg * HEADS + hd;
-          *reinterpret_cast<uint2*>(a.o + row * D + e0) =
-              make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
-          if (e0 == 0) a.lse[row] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
-        }
-        __syncthreads();
-      }
-    }
-    if constexpr (WEIGHTS) {
-      if (hg == 0) {
+  if (cta >= G || sub >= subs) return;
+  // Only the first and the last item of a CTA can be cut.
+  const long long b_first = u0 - first.tile, b_last = u1 - 1 - last.tile;  // their first units
+  const ItemParts pf = item_parts(b_first, first.ntiles, G, T);
+  const bool cut_first = pf.c0 != pf.c1;
+  if (cut_first)
+    join_item<D, BF16, NT>(a, first, pf, cta, sub, subs, warp, lane, WEIGHTS && v0 < b_first + first.ntiles, s_ml[0],
+                           s_acc);
+  bool cut_last = false;
+  if (b_last > b_first) {
+    const ItemParts pl = item_parts(b_last, last.ntiles, G, T);
+    cut_last = pl.c0 != pl.c1;
+    if (cut_last)
+      join_item<D, BF16, NT>(a, last, pl, cta, sub, subs, warp, lane, WEIGHTS && v1 > b_last, s_ml[1], s_acc);
+  }
+  if constexpr (WEIGHTS) {
+    for (long long u = v0; u < v1;) {
+      const int cnt = static_cast<int>(min(static_cast<long long>(cc.ntiles - cc.tile), v1 - u));
+      const int h = cc.hh / a.HG;
+      if (cc.hh == h * a.HG) {  // one head tile of a group adds for all
+        const long long ub = u - cc.tile;
         // L of every head of the group, whatever its tile's parts are.
         for (int hd = warp; hd < a.g; hd += WARPS) {
           const int x = hd / HEADS;
-          const ItemParts px = x == 0 ? p : item_parts(ub + static_cast<long long>(x) * cc.ntiles, cc.ntiles, G, T);
-          float v;
-          if (px.c0 == px.c1) {
-            v = a.lse[row0 + hd] * kLog2ef;
+          float2 ml;
+          bool whole = false;
+          if (x == 0 && ub == b_first && cut_first) {
+            ml = s_ml[0][hd];
+          } else if (x == 0 && ub == b_last && cut_last) {
+            ml = s_ml[1][hd];
           } else {
-            const float2 ml = x == 0 ? s_ml[hd] : join_ml(a.part_ml, HEADS, hd - x * HEADS, px, lane);
-            v = ml.y > 0.f ? ml.x + log2f(ml.y) : -INFINITY;
+            const ItemParts p = item_parts(ub + static_cast<long long>(x) * cc.ntiles, cc.ntiles, G, T);
+            whole = p.c0 == p.c1;
+            if (!whole) ml = join_ml(a.part_ml, HEADS, hd - x * HEADS, p, lane);
           }
+          float v;
+          if (whole) v = a.lse[static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + hd] * kLog2ef;
+          else v = ml.y > 0.f ? ml.x + log2f(ml.y) : -INFINITY;
           if (lane == 0) s_lse[hd] = v;
         }
         __syncthreads();
@@ -630,17 +689,20 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_paged_join_kernel(const Deco
         if (a.g % 4 == 0) add_weights<4>(a, base, j0, j1, s_lse);
         else if (a.g % 2 == 0) add_weights<2>(a, base, j0, j1, s_lse);
         else add_weights<1>(a, base, j0, j1, s_lse);
+        __syncthreads();  // s_lse is rewritten by the next item
       }
+      cc.tile += cnt - 1;
+      unit_advance<D>(c, HH, cc);
+      u += cnt;
     }
-    __syncthreads();  // s_ml, s_lse are rewritten by the next item
-    cc.tile += cnt - 1;
-    unit_advance<D>(c, HH, cc);
-    u += cnt;
   }
 }
 
 template <int D, bool BF16, int NT, bool WEIGHTS>
-static cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
+static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) {
+  // A full table gives each CTA this many units; the lengths may give fewer.
+  const long long per = static_cast<long long>(a.c.B) * a.c.Hkv * a.HG * ((a.c.L + kUnit<D> - 1) / kUnit<D>) / ctas;
+  a.join_split = WEIGHTS && per >= 2 * kJoinUnits ? kJoinSplit : 1;
   using C = DecCfg<D, NT>;
   auto kern = fa2_paged_decode_kernel<D, BF16, NT, WEIGHTS>;
   static std::atomic<unsigned long long> done{0};
@@ -649,8 +711,8 @@ static cudaError_t launch_decode_t(const DecodeArgs& a, int ctas, cudaStream_t s
   kern<<<ctas, kDecWarps * 32, C::SMEM, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas), dim3(kJoinThreads), 0,
-                          stream, a);
+  return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas * a.join_split),
+                          dim3(kJoinThreads), 0, stream, a);
 }
 
 cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas,
