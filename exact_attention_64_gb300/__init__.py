@@ -14,7 +14,6 @@ bfloat16 (``d`` in {64, 128}); the logsumexp is float32 ``[B, H, N]``.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 from pathlib import Path
 
@@ -457,74 +456,21 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None):
 # ---------------------------------------------------------------------------
 # Paged key-value cache
 # ---------------------------------------------------------------------------
-# These calls run once per token, often in microseconds, so their checks are
-# kept to a few attribute reads.
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_native_mod = None
 
 
-def _need(name, t, shape, dtype, index):
-    """A contiguous tensor of this shape and type on CUDA device ``index``; its
-    address."""
-    if (t.get_device() != index or t.shape != shape or t.dtype is not dtype
-            or not t.is_contiguous()):
-        _check_tensor(name, t, shape, dtype, torch.device("cuda", max(index, 0)))
-    return t.data_ptr()
-
-
-@functools.lru_cache(maxsize=4096)
-def _space(name, *sizes):
-    """A workspace size of the library; a pure function of the sizes."""
-    need = getattr(load_library(), name)(*sizes)
-    if need == 0:
-        raise FA2Error(name, 1)
-    return need
-
-
-@functools.lru_cache(maxsize=None)
-def _entry(name):
-    return getattr(load_library(), name)
-
-
-def _call(name, index, *args):
-    """The library's entry points work on the current device."""
-    fn = _entry(name)
-    if _current_device() == index:
-        code = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            code = fn(*args, _raw_stream(index))
-    if code != 0:
-        raise FA2Error(name, code)
-
-
-def _workspace(workspace, need, dev):
-    """(tensor, bytes): the caller's scratch, or a new one."""
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev), need
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _check_cache(k_cache, v_cache, table, lens):
-    """Of a paged cache: (num_pages, Hkv, page_size, d, B, max_pages), the device
-    index, and the addresses of the four tensors."""
-    index = k_cache.get_device()
-    if index < 0:
-        raise ValueError("k_cache must be a CUDA tensor")
-    shape, width = k_cache.shape, table.shape
-    if len(shape) != 4:
-        raise ValueError("expected a [num_pages, Hkv, page_size, d] cache")
-    if k_cache.dtype not in _DTYPES:
-        raise ValueError("k_cache must be float16 or bfloat16")
-    if len(width) != 2:
-        raise ValueError("expected a [B, max_pages] table")
-    dt = k_cache.dtype
-    ptrs = (_need("k_cache", k_cache, shape, dt, index), _need("v_cache", v_cache, shape, dt, index),
-            _need("table", table, width, torch.int32, index),
-            _need("lens", lens, width[:1], torch.int32, index))
-    return (*shape, *width), index, ptrs
+def _native():
+    """The native entry points of the per-token calls (csrc/binding.cpp)."""
+    global _native_mod
+    if _native_mod is None:
+        load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the native binding is not built; run "
+                               "`python -m exact_attention_64_gb300.build`") from e
+        _native_mod = _binding
+    return _native_mod
 
 
 def paged_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, weights=None,
@@ -540,33 +486,8 @@ def paged_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, w
     ``weights_out`` (slots past the length are left as they were). Returns
     (o, lse): o like q, lse float32 [B, Hq].
     """
-    (num_pages, Hkv, ps, d, B, max_pages), index, cache = _check_cache(k_cache, v_cache, table, lens)
-    dt = k_cache.dtype
-    if q.dim() != 3:
-        raise ValueError("expected a [B, Hq, d] query")
-    Hq = q.shape[1]
-    rows = (B, Hq, d)
-    qp = _need("q", q, rows, dt, index)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    op, lp = _need("out", out, rows, dt, index), _need("lse", lse, rows[:2], torch.float32, index)
-    wp = wop = None
-    if weights is not None:
-        slots = (B, Hkv, max_pages * ps)
-        wp = wop = _need("weights", weights, slots, torch.float32, index)
-        if weights_out is not None:
-            wop = _need("weights_out", weights_out, slots, torch.float32, index)
-    elif weights_out is not None:
-        raise ValueError("weights_out needs weights")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    need = _space("fa2_paged_decode_workspace_size", B, Hq, Hkv, d, ps, max_pages, int(weights is not None))
-    ws, nbytes = _workspace(workspace, need, q.device)
-    _call("fa2_paged_decode", index, qp, *cache, wp, wop, op, lp, B, Hq, Hkv, d, num_pages, ps,
-          max_pages, float(scale), _DTYPES[dt], ws.data_ptr(), nbytes)
-    return out, lse
+    return (_native_mod or _native()).paged_decode(q, k_cache, v_cache, table, lens, scale, weights,
+                                                   weights_out, out, lse, workspace)
 
 
 def cache_append(k, v, k_cache, v_cache, table, lens, num_new=None, weights=None,
@@ -579,28 +500,8 @@ def cache_append(k, v, k_cache, v_cache, table, lens, num_new=None, weights=None
     ``positions`` (int32, like weights) to next_pos[b] + i. Returns the new
     lengths, int32 [B] (lens itself is not changed).
     """
-    (num_pages, Hkv, ps, d, B, max_pages), index, cache = _check_cache(k_cache, v_cache, table, lens)
-    dt = k_cache.dtype
-    if k.dim() != 4:
-        raise ValueError("expected [B, Hkv, T, d] keys")
-    T = k.shape[2]
-    new, slots = (B, Hkv, T, d), (B, Hkv, max_pages * ps)
-    kp, vp = _need("k", k, new, dt, index), _need("v", v, new, dt, index)
-    if new_weights is not None and weights is None:
-        raise ValueError("new_weights needs weights")
-    if (positions is None) != (next_pos is None):
-        raise ValueError("positions and next_pos go together")
-    np_ = None if num_new is None else _need("num_new", num_new, (B,), torch.int32, index)
-    wp = None if weights is None else _need("weights", weights, slots, torch.float32, index)
-    nwp = None if new_weights is None else _need("new_weights", new_weights, new[:3], torch.float32, index)
-    pp = None if positions is None else _need("positions", positions, slots, torch.int32, index)
-    xp = None if next_pos is None else _need("next_pos", next_pos, (B,), torch.int32, index)
-    if lens_out is None:
-        lens_out = torch.empty_like(lens)
-    lp = _need("lens_out", lens_out, (B,), torch.int32, index)
-    _call("fa2_cache_append", index, kp, vp, *cache, np_, wp, nwp, pp, xp, lp, B, Hkv, T, d, num_pages,
-          ps, max_pages, _DTYPES[dt])
-    return lens_out
+    return (_native_mod or _native()).cache_append(k, v, k_cache, v_cache, table, lens, num_new, weights,
+                                                   new_weights, positions, next_pos, lens_out)
 
 
 def cache_evict(k_cache, v_cache, table, lens, weights, budget: int, recent: int = 0,
@@ -617,33 +518,9 @@ def cache_evict(k_cache, v_cache, table, lens, weights, budget: int, recent: int
     ``weights_out`` / ``positions_out``). Each head keeps its own tokens. Returns
     the new lengths, int32 [B]: min(lens, budget).
     """
-    (num_pages, Hkv, ps, d, B, max_pages), index, cache = _check_cache(k_cache, v_cache, table, lens)
-    slots = (B, Hkv, max_pages * ps)
-    budget, recent = int(budget), int(recent)
-    if budget < 1 or not 0 <= recent <= budget:
-        raise ValueError("needs budget >= 1 and 0 <= recent <= budget")
-    budget, recent = min(budget, 2**31 - 1), min(recent, 2**31 - 1)
-    wp = wop = _need("weights", weights, slots, torch.float32, index)
-    if weights_out is not None:
-        wop = _need("weights_out", weights_out, slots, torch.float32, index)
-    if (positions is None) != (next_pos is None):
-        raise ValueError("positions and next_pos go together")
-    pp = pop = xp = None
-    if positions is not None:
-        pp = pop = _need("positions", positions, slots, torch.int32, index)
-        xp = _need("next_pos", next_pos, (B,), torch.int32, index)
-        if positions_out is not None:
-            pop = _need("positions_out", positions_out, slots, torch.int32, index)
-    elif positions_out is not None:
-        raise ValueError("positions_out needs positions")
-    if lens_out is None:
-        lens_out = torch.empty_like(lens)
-    lp = _need("lens_out", lens_out, (B,), torch.int32, index)
-    need = _space("fa2_cache_evict_workspace_size", B, Hkv, ps, max_pages, budget)
-    ws, nbytes = _workspace(workspace, need, lens.device)
-    _call("fa2_cache_evict", index, *cache, wp, wop, pp, pop, xp, lp, B, Hkv, d, num_pages, ps,
-          max_pages, budget, recent, _DTYPES[k_cache.dtype], ws.data_ptr(), nbytes)
-    return lens_out
+    return (_native_mod or _native()).cache_evict(k_cache, v_cache, table, lens, weights, budget, recent,
+                                                  positions, next_pos, weights_out, positions_out,
+                                                  lens_out, workspace)
 
 
 def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_lens=None, out=None,
@@ -657,22 +534,4 @@ def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_l
     Returns float32 ``[B, Hkv, N_k]``: the weights that ``cache_append`` and
     ``cache_evict`` take.
     """
-    B, Hq, N, d = q.shape if q.dim() == 4 else _shape(q)
-    Hkv, Nk = (k.shape if k.dim() == 4 else _shape(k))[1:3]
-    dt, index = q.dtype, q.get_device()
-    if dt not in _DTYPES:
-        raise ValueError("q must be float16 or bfloat16")
-    qp, kp = _need("q", q, (B, Hq, N, d), dt, index), _need("k", k, (B, Hkv, Nk, d), dt, index)
-    sp = _need("lse", lse, (B, Hq, N), torch.float32, index)
-    np_ = None if q_lens is None else _need("q_lens", q_lens, (B,), torch.int32, index)
-    if index < 0:
-        raise ValueError("q must be a CUDA tensor")
-    if out is None:
-        out = torch.empty((B, Hkv, Nk), dtype=torch.float32, device=q.device)
-    op = _need("out", out, (B, Hkv, Nk), torch.float32, index)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    ws, nbytes = _workspace(workspace, _space("fa2_key_weights_workspace_size"), q.device)
-    _call("fa2_key_weights", index, qp, kp, sp, np_, op, B, Hq, Hkv, N, Nk, d, int(bool(causal)), float(scale),
-          _DTYPES[dt], ws.data_ptr(), nbytes)
-    return out
+    return (_native_mod or _native()).key_weights(q, k, lse, causal, scale, q_lens, out, workspace)

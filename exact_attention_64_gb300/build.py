@@ -1,8 +1,11 @@
 """Builds libfa2.so (the sm_103a CUDA library behind include/fa2.h) in-tree.
 
-Every translation unit under csrc/ is compiled by nvcc for sm_103a in
-parallel, then linked into exact_attention_64_gb300/libfa2.so. A rebuild only
-happens when a source or header is newer than the library.
+Every CUDA translation unit under csrc/ is compiled by nvcc for sm_103a in
+parallel, then linked into exact_attention_64_gb300/libfa2.so; csrc/binding.cpp,
+the native Python entry points of the per-token calls, is compiled by g++ beside
+them and linked against it as exact_attention_64_gb300/_binding.so. A rebuild
+only happens when a source or header is newer than the libraries, or when the
+binding was built for another PyTorch or Python.
 """
 
 from __future__ import annotations
@@ -10,6 +13,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -18,6 +22,8 @@ CSRC = PKG / "csrc"
 ROOT = PKG.parent
 BUILD = ROOT / "_build"
 LIB = PKG / "libfa2.so"
+BINDING = PKG / "_binding.so"
+BINDING_FOR = BUILD / "binding_for.txt"  # the PyTorch and Python it was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
@@ -33,18 +39,62 @@ def _sources():
 
 
 def _deps():
-    return sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + [ROOT / "include" / "fa2.h"]
+    return (sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) +
+            sorted(CSRC.glob("*.cpp")) + [ROOT / "include" / "fa2.h"])
+
+
+def _torch_tag() -> str:
+    import torch
+
+    return f"{torch.__version__} {sys.version}"
 
 
 def needs_build() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not BINDING.exists() or not BINDING_FOR.exists():
         return True
-    t = LIB.stat().st_mtime
+    if BINDING_FOR.read_text() != _torch_tag():
+        return True
+    t = min(LIB.stat().st_mtime, BINDING.stat().st_mtime)
     return any(p.stat().st_mtime > t for p in _deps())
 
 
+def _run(cmd, what, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(verbose: bool) -> Path:
+    import torch
+
+    inc = Path(torch.__file__).resolve().parent / "include"
+    obj = BUILD / "binding.o"
+    cuda = Path(_nvcc()).resolve().parent.parent / "include"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-isystem", str(inc), "-isystem", str(inc / "torch" / "csrc" / "api" / "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", str(cuda),
+          "-c", str(CSRC / "binding.cpp"), "-o", str(obj)], "g++ failed on binding.cpp", verbose)
+    return obj
+
+
+def _link_binding(obj: Path, verbose: bool) -> None:
+    import torch
+
+    lib = Path(torch.__file__).resolve().parent / "lib"
+    tmp = BINDING.with_suffix(".so.tmp")
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", str(tmp), str(obj), f"-L{PKG}", "-lfa2",
+          f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link of the binding failed", verbose)
+    os.replace(tmp, BINDING)
+    BINDING_FOR.write_text(_torch_tag())
+
+
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile and link libfa2.so; returns its path. Raises on failure."""
+    """Compile and link libfa2.so and the native binding; returns the library's
+    path. Raises on failure."""
     if not force and not needs_build():
         return LIB
     BUILD.mkdir(exist_ok=True)
@@ -53,24 +103,19 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     def compile_one(src: Path) -> Path:
         obj = BUILD / (src.stem + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", str(src), "-o", str(obj)]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src.name}:\n{r.stdout}\n{r.stderr}")
+        _run(cmd, f"nvcc failed on {src.name}", verbose)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(compile_one, _sources()))
+        binding_obj = binding.result()
     tmp = LIB.with_suffix(".so.tmp")
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", str(tmp), *map(str, objs),
            "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link failed", verbose)
     os.replace(tmp, LIB)
+    _link_binding(binding_obj, verbose)
     return LIB
 
 
