@@ -85,12 +85,19 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // have to, and sources and destinations are disjoint.
 //
 // Selection: the key becomes a 32-bit integer of the same order, and the
-// budget-th largest is found digit by digit, 8 bits a pass, from histograms. A
-// (sequence, key head) is the work of one cluster: each CTA keeps the integer
-// keys of its share of the slots in shared memory, so that weights and
-// positions are read once, and the histograms of a pass are added up through
-// distributed shared memory. Integer counts: the result does not depend on any
-// order. Where the keys do not fit they are made again from global memory.
+// budget-th largest is found digit by digit, 8 bits a pass, from histograms.
+// (Three passes of 11 bits and fewer collisions: no faster in one CTA, and 17
+// against 12 us in a cluster of 8, whose CTAs read each other's counters.) A
+// (sequence, key head) is the work of one cluster, a warp has a run of its
+// slots, and the keys stay in registers, so that weights and positions are
+// read once; the histograms of a pass are added up through distributed shared
+// memory. Integer counts: the result does not depend on any order. Rows too
+// long for the registers of a cluster keep their keys in its shared memory
+// (keys in shared memory throughout: 19 us for 128 heads of 8192 slots, against
+// %SELREG%), and past that make them again from global memory. One slot too
+// many, the steady state of a bounded cache, needs no histogram: the smallest
+// key goes, of equal ones the highest slot (5.8 us for 256 heads of 2049 slots,
+// against 12.3).
 //
 // Moves: a warp takes 8 at a time, so that 4 KiB per warp are in flight. A few
 // moves per row (a cache that is one token over) are made by the cluster that
@@ -99,7 +106,8 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // leave the memory idle until then.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictKeys = 49152;  // keys a CTA can hold: 192 KiB
+constexpr int kEvictRegs = 8;      // keys a thread can hold: 4096 slots per CTA
+constexpr int kEvictKeys = 49152;  // keys a CTA's shared memory can hold: 192 KiB
 constexpr int kMoveThreads = 256;
 constexpr int kMovesPerWarp = 8;
 constexpr int kInlineMoves = 256;  // longest list that the selecting cluster works off itself
@@ -112,11 +120,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// A 32-bit word of shared memory of CTA `rank` of the cluster.
+// Words of shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t rank) {
   uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ unsigned long long cluster_load64(const unsigned long long* p, uint32_t rank) {
+  uint32_t a;
+  unsigned long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
 
@@ -130,6 +146,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 struct EvictShared {
   __align__(16) uint32_t hist[4][256];
   __align__(16) uint32_t total[256];
+  unsigned long long least[kEvictWarps], cta_least;
+  int one[2];  // source and destination of a single move
   uint32_t warp_gt[kEvictWarps], warp_tie[kEvictWarps];  // per warp, then exclusive
   uint32_t cta_gt, cta_tie, cta_gt_lo, cta_tie_lo;       // this CTA's counts
 };
@@ -138,14 +156,15 @@ struct EvictShared {
 // 7 look up the sources, 8 .. 15 the destinations, then all copy, 16 bytes of K
 // and of V per lane and row.
 template <int D>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, int item, int m0, int moves, int lane) {
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int item, const int* movers, const int* holes, int m0,
+                                          int moves, int lane) {
   const CacheView& c = a.c;
   const int b = item / c.Hkv, h = item - b * c.Hkv;
-  const size_t list = static_cast<size_t>(item) * a.list, base = static_cast<size_t>(item) * c.L;
+  const size_t base = static_cast<size_t>(item) * c.L;
   const int m = m0 + (lane & 7);
   int slot = 0, row = -1;
   if (lane < 16 && m < moves) {
-    slot = __ldcg((lane < 8 ? a.movers : a.holes) + list + m);
+    slot = (lane < 8 ? movers : holes)[m];
     row = slot_row(c, b, h, slot);
     if (row < 0) report_page(c.status);
   }
@@ -176,7 +195,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int item, int m0, 
   }
 }
 
-template <int D>
+template <int D, bool REG>
 __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const EvictArgs a, int C) {
   extern __shared__ uint32_t s_keys[];
   __shared__ EvictShared sh;
@@ -194,11 +213,13 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
   const int* p_in = a.p_in != nullptr ? a.p_in + base : nullptr;
   int* p_out = a.p_in != nullptr ? a.p_out + base : nullptr;
   const bool copy_w = a.w_out != a.w_in, copy_p = p_in != nullptr && a.p_out != a.p_in;
-  if (h == 0 && rank == 0 && tid == 0) {
-    if (n != __ldg(c.lens + b)) report_page(c.status);
-    a.lens_out[b] = k;
+  if (rank == 0 && tid == 0) {
+    if (h == 0) {
+      if (n != __ldg(c.lens + b)) report_page(c.status);
+      a.lens_out[b] = k;
+    }
+    if (n <= a.budget) a.counts[item] = 0;
   }
-  if (rank == 0 && tid == 0 && n <= a.budget) a.counts[item] = 0;
   if (n <= a.budget) {  // nothing to evict
     for (int j = rank * kEvictThreads + tid; j < n; j += C * kEvictThreads) {
       if (copy_w) w_out[j] = w_in[j];
@@ -206,37 +227,129 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
     }
     return;  // the whole cluster
   }
-  // This CTA's slots [j0, j1), of which each warp owns a run of whole 32s.
-  const int run = (((n + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;  // slots per warp
+  // This CTA's slots are kEvictWarps runs of whole 32s, one per warp; this
+  // warp's are [w0, w1), of which a lane has w0 + lane, w0 + 32 + lane, ...
+  const int run = (((n + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
   const int j0 = min(n, rank * run * kEvictWarps), j1 = min(n, j0 + run * kEvictWarps);
+  const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
   const long long first_recent =
       p_in != nullptr ? static_cast<long long>(__ldg(a.next_pos + b)) - a.recent : 0;
-  auto make_key = [&](int j) -> uint32_t {
-    const uint32_t key = weight_key(w_in[j]);
+  auto key_of = [&](int j, float w, int pos) -> uint32_t {
     // Without positions the slots are in the order of their tokens.
-    const bool is_recent = p_in != nullptr ? p_in[j] >= first_recent : j >= n - a.recent;
-    return is_recent && a.recent > 0 ? 0xffffffffu : key;
+    const bool is_recent = p_in != nullptr ? pos >= first_recent : j >= n - a.recent;
+    return is_recent && a.recent > 0 ? 0xffffffffu : weight_key(w);
   };
+  // Each of the warp's slots in order of i, `f(i, j)`: i-th 32 of the run.
+  uint32_t key[REG ? kEvictRegs : 1];
+  auto each = [&](auto f) {
+    if constexpr (REG) {
+#pragma unroll
+      for (int i = 0; i < kEvictRegs; ++i) f(i, w0 + 32 * i + lane);
+    } else {
+      for (int i = 0; w0 + 32 * i < w1; ++i) f(i, w0 + 32 * i + lane);
+    }
+  };
+  // Keys, and the copies of the slots below budget: evicted ones are written
+  // again when a kept slot takes their place.
+  auto load_key = [&](int j) -> uint32_t {
+    const float w = w_in[j];
+    const int pos = p_in != nullptr ? p_in[j] : 0;
+    return key_of(j, w, pos);
+  };
+  if constexpr (REG) {
+    float w[kEvictRegs];
+    int pos[kEvictRegs];
+    each([&](int i, int j) {
+      w[i] = j < w1 ? w_in[j] : 0.f;
+      pos[i] = j < w1 && p_in != nullptr ? p_in[j] : 0;
+    });
+    each([&](int i, int j) {
+      key[i] = key_of(j, w[i], pos[i]);
+      if (j < w1 && j < k) {
+        if (copy_w) w_out[j] = w[i];
+        if (copy_p) p_out[j] = pos[i];
+      }
+    });
+  } else {
+    each([&](int, int j) {
+      if (j >= w1) return;
+      if (a.cached) s_keys[j - j0] = load_key(j);
+      if (j < k) {
+        if (copy_w) w_out[j] = w_in[j];
+        if (copy_p) p_out[j] = p_in[j];
+      }
+    });
+  }
+  auto key_at = [&](int i, int j) -> uint32_t {
+    if constexpr (REG) return key[i];
+    else return a.cached ? s_keys[j - j0] : load_key(j);
+  };
+  if (n - k == 1) {
+    // The smallest key, of equal ones the highest slot, as one number to
+    // minimise: key, then the slot's complement.
+    unsigned long long least = ~0ull;
+    each([&](int i, int j) {
+      if (j >= w1) return;
+      const unsigned long long x = (static_cast<unsigned long long>(key_at(i, j)) << 32) | ~static_cast<uint32_t>(j);
+      least = x < least ? x : least;
+    });
+    auto warp_least = [&](unsigned long long x) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const unsigned long long y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = y < x ? y : x;
+      }
+      return x;
+    };
+    least = warp_least(least);
+    if (lane == 0) sh.least[warp] = least;
+    __syncthreads();
+    if (C > 1) {
+      if (warp == 0) {
+        least = warp_least(lane < kEvictWarps ? sh.least[lane] : ~0ull);
+        if (lane == 0) sh.cta_least = least;
+      }
+      cluster_sync();
+    }
+    if (rank == 0 && warp == 0) {
+      unsigned long long x = ~0ull;
+      if (C > 1) {
+        if (lane < C) x = cluster_load64(&sh.cta_least, lane);
+      } else if (lane < kEvictWarps) {
+        x = sh.least[lane];
+      }
+      const int gone = static_cast<int>(~static_cast<uint32_t>(warp_least(x)));
+      if (lane == 0) {
+        a.counts[item] = 0;
+        sh.one[0] = k;
+        sh.one[1] = gone;
+      }
+      __syncwarp();
+      if (gone < k) move_rows<D>(a, item, &sh.one[0], &sh.one[1], 0, 1, lane);
+    }
+    if (C > 1) cluster_sync();  // the others' shared memory has been read
+    return;
+  }
   for (int i = tid; i < 4 * 256; i += kEvictThreads) (&sh.hist[0][0])[i] = 0u;
   if (tid == 0) sh.cta_gt = sh.cta_tie = sh.cta_gt_lo = sh.cta_tie_lo = 0u;
-  if (a.cached)
-    for (int j = j0 + tid; j < j1; j += kEvictThreads) s_keys[j - j0] = make_key(j);
-  auto key_at = [&](int j) -> uint32_t { return a.cached ? s_keys[j - j0] : make_key(j); };
   __syncthreads();
   uint32_t prefix = 0, want = k;  // the want-th largest among the keys that start with prefix
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    for (int j = j0 + tid; j < j1; j += kEvictThreads) {
-      const uint32_t key = key_at(j);
-      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&sh.hist[pass][(key >> shift) & 255u], 1u);
-    }
+    each([&](int i, int j) {
+      if (j >= w1) return;
+      const uint32_t x = key_at(i, j);
+      if (pass == 0 || (x >> (shift + 8)) == prefix) atomicAdd(&sh.hist[pass][(x >> shift) & 255u], 1u);
+    });
     const uint32_t* total = sh.hist[pass];
     if (C > 1) {
       cluster_sync();
       if (tid < 256) {
         uint32_t t = 0;
-        for (int x = 0; x < C; ++x) t += cluster_load(&sh.hist[pass][tid], x);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x < C) t += cluster_load(&sh.hist[pass][tid], x);
         sh.total[tid] = t;
       }
       total = sh.total;
@@ -272,18 +385,18 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
   }
   // Slots with a key above `prefix` stay, and the first `want` of those equal to
   // it. Counts before each warp's run, over the cluster in slot order.
-  const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
   uint32_t gt = 0, tie = 0, gt_lo = 0, tie_lo = 0;
-  for (int j = w0 + lane; j < w1; j += 32) {
-    const uint32_t key = key_at(j);
-    const uint32_t g1 = key > prefix, t1 = key == prefix;
+  each([&](int i, int j) {
+    if (j >= w1) return;
+    const uint32_t x = key_at(i, j);
+    const uint32_t g1 = x > prefix, t1 = x == prefix;
     gt += g1;
     tie += t1;
     if (j < k) {
       gt_lo += g1;
       tie_lo += t1;
     }
-  }
+  });
   gt = __reduce_add_sync(0xffffffffu, gt);
   tie = __reduce_add_sync(0xffffffffu, tie);
   gt_lo = __reduce_add_sync(0xffffffffu, gt_lo);
@@ -302,11 +415,12 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
     lo_gt = sh.cta_gt_lo;
     lo_tie = sh.cta_tie_lo;
   } else {
-    for (int x = 0; x < C; ++x) {
-      if (x < rank) {
-        gt_before += cluster_load(&sh.cta_gt, x);
-        tie_before += cluster_load(&sh.cta_tie, x);
-      }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (x >= C) break;
+      const uint32_t g1 = cluster_load(&sh.cta_gt, x), t1 = cluster_load(&sh.cta_tie, x);
+      gt_before += x < rank ? g1 : 0u;
+      tie_before += x < rank ? t1 : 0u;
       lo_gt += cluster_load(&sh.cta_gt_lo, x);
       lo_tie += cluster_load(&sh.cta_tie_lo, x);
     }
@@ -319,35 +433,28 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
   const int moves = k - static_cast<int>(kept_lo);
   int* holes = a.holes + static_cast<size_t>(item) * a.list;
   int* movers = a.movers + static_cast<size_t>(item) * a.list;
-  for (int jb = w0; jb < w1; jb += 32) {
-    const int j = jb + lane;
-    const uint32_t key = j < w1 ? key_at(j) : 0u;
-    const bool g1 = j < w1 && key > prefix, t1 = j < w1 && key == prefix;
+  each([&](int i, int j) {
+    const uint32_t x = j < w1 ? key_at(i, j) : 0u;
+    const bool g1 = j < w1 && x > prefix, t1 = j < w1 && x == prefix;
     const uint32_t gm = __ballot_sync(0xffffffffu, g1), tm = __ballot_sync(0xffffffffu, t1);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t tb = tie_before + __popc(tm & below);
     const uint32_t kept = gt_before + __popc(gm & below) + min(tb, want);  // kept slots before j
     const bool keep = g1 || (t1 && tb < want);
     if (j < w1) {
-      if (j < k && !keep) {
-        holes[j - kept] = j;
-      } else if (j < k) {
-        if (copy_w) w_out[j] = w_in[j];
-        if (copy_p) p_out[j] = p_in[j];
-      } else if (keep) {
-        movers[kept - kept_lo] = j;
-      }
+      if (j < k && !keep) holes[j - kept] = j;
+      if (j >= k && keep) movers[kept - kept_lo] = j;
     }
     gt_before += __popc(gm);
     tie_before += __popc(tm);
-  }
+  });
   if (rank == 0 && tid == 0) a.counts[item] = moves;
   // No CTA leaves while another may still read its counts, and the lists are
   // complete after this.
   if (C > 1) cluster_sync(); else __syncthreads();
   if (a.list <= kInlineMoves)
     for (int m0 = (rank * kEvictWarps + warp) * kMovesPerWarp; m0 < moves; m0 += C * kEvictWarps * kMovesPerWarp)
-      move_rows<D>(a, item, m0, moves, lane);
+      move_rows<D>(a, item, movers, holes, m0, moves, lane);
 }
 
 // The moves of all items, kMoveThreads / 32 * 8 per CTA.
@@ -358,24 +465,34 @@ __global__ void __launch_bounds__(kMoveThreads) fa2_cache_move_kernel(const Evic
   grid_dependency_wait();
   const int moves = a.counts[item];
   const int m0 = (chunk * (kMoveThreads / 32) + warp) * kMovesPerWarp;
-  if (m0 < moves) move_rows<D>(a, item, m0, moves, lane);
+  const size_t list = static_cast<size_t>(item) * a.list;
+  if (m0 < moves) move_rows<D>(a, item, a.movers + list, a.holes + list, m0, moves, lane);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   EvictArgs a = a0;
   const long long items = static_cast<long long>(a.c.B) * a.c.Hkv;
   // CTAs per (sequence, key head): doubled from 1 to 8 while a CTA has more
-  // than 2048 slots and two CTAs per SM still hold all items at once, or while
-  // it has more than its shared memory takes keys for.
+  // slots than its registers take, or more than 2048 and two CTAs per SM still
+  // hold all items at once.
+  constexpr int kReg = kEvictThreads * kEvictRegs;
+  const auto share = [&](int C) {  // slots of a CTA
+    const int run = (((a.c.L + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
+    return static_cast<long long>(run) * kEvictWarps;
+  };
   int C = 1;
-  while (C < 8 && ((a.c.L / C > 2048 && items * C * 2 <= 304) || a.c.L / C > kEvictKeys)) C *= 2;
-  const long long per = ((static_cast<long long>(a.c.L) + C - 1) / C + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
-  a.cached = per <= kEvictKeys;
-  const size_t smem = a.cached ? static_cast<size_t>(per) * 4 : 0;
-  auto kern = a.d == 64 ? fa2_cache_evict_kernel<64> : fa2_cache_evict_kernel<128>;
-  static std::atomic<unsigned long long> done[2];
-  cudaError_t e = allow_smem(kern, kEvictKeys * 4, done[a.d == 64]);
-  if (e != cudaSuccess) return e;
+  while (C < 8 && (share(C) > kReg || (share(C) > 2048 && items * C * 2 <= 304))) C *= 2;
+  const bool reg = share(C) <= kReg;
+  a.cached = !reg && share(C) <= kEvictKeys;
+  const size_t smem = a.cached ? static_cast<size_t>(share(C)) * 4 : 0;
+  auto kern = a.d == 64 ? (reg ? fa2_cache_evict_kernel<64, true> : fa2_cache_evict_kernel<64, false>)
+                        : (reg ? fa2_cache_evict_kernel<128, true> : fa2_cache_evict_kernel<128, false>);
+  cudaError_t e = cudaSuccess;
+  if (!reg) {
+    static std::atomic<unsigned long long> done[2];
+    e = allow_smem(kern, kEvictKeys * 4, done[a.d == 64]);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(items * C));
   cfg.blockDim = dim3(kEvictThreads);
