@@ -94,7 +94,7 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // memory. Integer counts: the result does not depend on any order. Rows too
 // long for the registers of a cluster keep their keys in its shared memory
 // (keys in shared memory throughout: 19 us for 128 heads of 8192 slots, against
-// %SELREG%), and past that make them again from global memory. One slot too
+// 15), and past that make them again from global memory. One slot too
 // many, the steady state of a bounded cache, needs no histogram: the smallest
 // key goes, of equal ones the highest slot (5.8 us for 256 heads of 2049 slots,
 // against 12.3).
@@ -473,15 +473,15 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   EvictArgs a = a0;
   const long long items = static_cast<long long>(a.c.B) * a.c.Hkv;
   // CTAs per (sequence, key head): doubled from 1 to 8 while a CTA has more
-  // slots than its registers take, or more than 2048 and two CTAs per SM still
-  // hold all items at once.
+  // slots than its registers take. More CTAs than that cost more in cluster
+  // barriers than they save: 2 heads of 16384 slots 13.0 us with 4, 13.7 with 8.
   constexpr int kReg = kEvictThreads * kEvictRegs;
   const auto share = [&](int C) {  // slots of a CTA
     const int run = (((a.c.L + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
     return static_cast<long long>(run) * kEvictWarps;
   };
   int C = 1;
-  while (C < 8 && (share(C) > kReg || (share(C) > 2048 && items * C * 2 <= 304))) C *= 2;
+  while (C < 8 && share(C) > kReg) C *= 2;
   const bool reg = share(C) <= kReg;
   a.cached = !reg && share(C) <= kEvictKeys;
   const size_t smem = a.cached ? static_cast<size_t>(share(C)) * 4 : 0;

@@ -16,7 +16,7 @@
 // product and the sums (its bandwidth belongs to the product's operands), and
 // the sum over lanes happens once per item. The transposed form (lane = key)
 // needs no such sum but a broadcast read of L per column: 290 us against
-// %KW8192% us at B=2 H=16 N=8192 d=128 causal.
+// 236 us at B=2 H=16 N=8192 d=128 causal.
 //
 // A work item is 256 keys, tiles A and B, so that a Q tile fetched from L2
 // feeds two products; two groups of four compute warps own 64 columns of each.
