@@ -197,7 +197,8 @@ struct KwShared {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  float2 sums[4][32];  // per group: sums of its 64 keys handed from warp to warp
+  uint64_t sum_full[4], sum_free[4];  // per group
+  float2 sums[4][3][32];  // per group: the sums of 64 keys of its warps 1 .. 3
   KwInfo info[2];
 };
 
@@ -231,18 +232,23 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
   float2 acc[32];
 #pragma unroll
   for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
-  int n = 0;
-  for (; units > 0; --units, ++n) {
+  auto release = [&](int buf) {  // the buffer and its unit's facts have been read
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
+  };
+  int n = 0, flushes = 0;
+  while (units > 0) {
     const int buf = n & 1;
     const uint32_t ts = t_lane + buf * kTileRows;
     if (!mbar_wait_warp(&sh.s_full[t][buf], (n >> 1) & 1, wc)) return;
     tc_fence_after();
-    const KwInfo& w = sh.info[buf];
-    const int flags = w.flags;
-    const float2 row = w.row[r];
-    float* dst = w.dst;
-    const int keys = w.keys;
-    if ((flags & (1 << t)) && !(flags & (4 << t))) {
+    int flags = sh.info[buf].flags;
+    float* dst = sh.info[buf].dst;
+    int keys = sh.info[buf].keys;
+    const float2 row = sh.info[buf].row[r];
+    const int plain = 1 << t, kind = 5 << t;  // active, not masked
+    if ((flags & kind) == plain) {
       uint32_t va[16], vb[16];
       tmem_ld_32x32b_x16(ts, va);
       tmem_wait_ld();
@@ -259,15 +265,55 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
       kw_chunk<false>(va, acc + 16, c, row.x, row.y, 0);
       tmem_wait_ld();
       reg_fence(vb);
-      tc_fence_before();  // the buffer and the facts have been read
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
-      kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+      release(buf);
+      ++n;
+      --units;
+      if (D == 64 && !(flags & 16)) {
+        // The same item goes on: its next unit's first columns are asked for
+        // before this one's last are worked on, so that every other wait for a
+        // product and for TMEM is hidden. (Always doing so carries loads across
+        // the loop's back edge, which costs spills: twice the time.) Worth it
+        // where the products are short: 214 against 227 us at d = 64, 239
+        // against 237 at d = 128 (B = 2, H = 16, N = 8192, causal).
+        if (!mbar_wait_warp(&sh.s_full[t][buf ^ 1], (n >> 1) & 1, wc)) return;
+        tc_fence_after();
+        const int f1 = sh.info[buf ^ 1].flags;
+        if ((f1 & kind) == plain) {
+          const float2 row1 = sh.info[buf ^ 1].row[r];
+          const uint32_t t1 = t_lane + (buf ^ 1) * kTileRows;
+          tmem_ld_32x32b_x16(t1, va);
+          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+          tmem_wait_ld();
+          reg_fence(va);
+          tmem_ld_32x32b_x16(t1 + 16, vb);
+          kw_chunk<false>(va, acc, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(vb);
+          tmem_ld_32x32b_x16(t1 + 32, va);
+          kw_chunk<false>(vb, acc + 8, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(va);
+          tmem_ld_32x32b_x16(t1 + 48, vb);
+          kw_chunk<false>(va, acc + 16, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(vb);
+          flags = f1;
+          dst = sh.info[buf ^ 1].dst;
+          keys = sh.info[buf ^ 1].keys;
+          release(buf ^ 1);
+          kw_chunk<false>(vb, acc + 24, c, row1.x, row1.y, 0);
+          ++n;
+          --units;
+        } else {
+          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+        }
+      } else {
+        kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+      }
     } else {
-      if (flags & (1 << t)) {
+      if (flags & plain) {
         // Visible keys of this row, from the group's first one.
-        const int lim0 = min(w.d0 + r - cg * 64 + 1, 64);
-        const int lim = r < w.rows ? lim0 : 0;
+        const int lim = r < sh.info[buf].rows ? sh.info[buf].d0 + r - cg * 64 + 1 : 0;
 #pragma unroll
         for (int x = 0; x < 64; x += 16) {
           uint32_t va[16];
@@ -277,13 +323,13 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
           kw_chunk<true>(va, acc + x / 2, c, row.x, row.y, lim - x);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
+      release(buf);
+      ++n;
+      --units;
     }
     if (flags & 16) {
       // Sums over the warp's 32 rows by halving: lane l ends with keys 2 l and
-      // 2 l + 1; then over the group's four warps, in order.
+      // 2 l + 1; the group's first warp adds the four warps' in order.
 #pragma unroll
       for (int o = 16, m = 16; o > 0; o >>= 1, m >>= 1) {
 #pragma unroll
@@ -294,22 +340,26 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
                                keep.y + __shfl_xor_sync(0xffffffffu, give.y, o));
         }
       }
-      float2 sum = acc[0];
+      if (quad > 0) {
+        if (flushes > 0 && !mbar_wait_warp(&sh.sum_free[cg], (flushes - 1) & 1, wc)) return;
+        sh.sums[cg][quad - 1][lane] = acc[0];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sum_full[cg]);
+      } else {
+        if (!mbar_wait_warp(&sh.sum_full[cg], flushes & 1, wc)) return;
+        float2 sum = acc[0];
 #pragma unroll
-      for (int x = 3; x > 0; --x) {
-        if (quad == x) sh.sums[cg][lane] = sum;
-        named_bar_sync(1 + cg, 128);
-        if (quad == x - 1) {
-          const float2 y = sh.sums[cg][lane];
+        for (int x = 0; x < 3; ++x) {
+          const float2 y = sh.sums[cg][x][lane];
           sum = make_float2(sum.x + y.x, sum.y + y.y);
         }
-      }
-      named_bar_sync(1 + cg, 128);  // read by warp 0 before the next run's warp 3 writes
-      if (quad == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.sum_free[cg]);
         const int key = cg * 64 + 2 * lane;
         if (key < keys) dst[key] = sum.x;
         if (key + 1 < keys) dst[key + 1] = sum.y;
       }
+      ++flushes;
 #pragma unroll
       for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
     }
@@ -338,6 +388,10 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.sum_full[i], 3);
+      mbar_init(&sh.sum_free[i], 1);
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
