@@ -376,42 +376,53 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   __shared__ KwShared<D> sh;
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_free[i], 1);
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(&sh.s_full[t][i], 2);  // the product and the unit's facts
-        mbar_init(&sh.s_free[t][i], 8);  // one arrival per compute warp of the tile
+  // Barriers are set up by one lane of three warps, TMEM by a fourth, while the
+  // others already look for their first unit.
+  if (lane == 0) {
+    if (warp == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      for (int i = 0; i < C::NQ; ++i) {
+        mbar_init(&sh.q_full[i], 1);
+        mbar_init(&sh.q_free[i], 1);
       }
+      sh.abort_flag = 0;
+      fence_mbar_init();
+    } else if (warp == 2) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.k_full[i], 1);
+        mbar_init(&sh.k_free[i], 1);
+        for (int t = 0; t < 2; ++t) {
+          mbar_init(&sh.s_full[t][i], 2);  // the product and the unit's facts
+          mbar_init(&sh.s_free[t][i], 8);  // one arrival per compute warp of the tile
+        }
+      }
+      mbar_init(&sh.mma_done, 1);
+      fence_mbar_init();
+    } else if (warp == 3) {
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&sh.sum_full[i], 3);
+        mbar_init(&sh.sum_free[i], 1);
+      }
+      fence_mbar_init();
     }
-    for (int i = 0; i < C::NQ; ++i) {
-      mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_free[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.sum_full[i], 3);
-      mbar_init(&sh.sum_free[i], 1);
-    }
-    mbar_init(&sh.mma_done, 1);
-    sh.abort_flag = 0;
-    fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem_base;
-  const WaitCtx wc{a.status, &sh.abort_flag, a.timeout_ns};
   const long long T = kw_total(a, s, lane);
   const long long G = T < gridDim.x ? T : gridDim.x;
   const int cta = blockIdx.x;
   const long long u0 = cta < G ? cta * T / G : 0, u1 = cta < G ? (cta + 1) * T / G : 0;
   KwCursor cu{};
-  if (u0 < u1) cu = kw_cursor(a, s, u0, lane);
+  if (u0 < u1 && warp < 4) cu = kw_cursor(a, s, u0, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  const WaitCtx wc{a.status, &sh.abort_flag, a.timeout_ns};
 
   if (warp < 4) {
     // 4 x 32 x 64 + 16 x 32 x 104 = 61,440 = the launch's 640 x 96 registers.
@@ -420,8 +431,6 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       // Producer: the Q tiles of the units, K of each item before its first.
       int items = 0, qs = 0, qph = 0, used = 0;
       bool ok = true, fresh = true;
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
       for (long long u = u0; u < u1 && ok; ++u) {
         if (fresh) {
           const int kb = items & 1;
