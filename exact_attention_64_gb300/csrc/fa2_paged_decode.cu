@@ -498,9 +498,12 @@ __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int 
 // What bounds the join: the latency of a few dependent reads, and with weights
 // the logits, which come from L2. So a CTA's range is shared by up to
 // kJoinSplit blocks when there are logits, one per kJoinUnits units, and a
-// thread has several loads in flight.
+// thread has several loads in flight. All blocks have to be resident at once:
+// 2 x 304 blocks of 256 threads with 64 registers fill the SMs; with 4 x 304
+// those waiting for the decode to end kept the rest out (118 us against 110 for
+// the decode of 32 sequences, 613 MB, with weights).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSplit = 4;
+constexpr int kJoinSplit = 2;
 constexpr int kJoinUnits = 8;
 
 // w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
@@ -607,7 +610,7 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
 }
 
 template <int D, bool BF16, int NT, bool WEIGHTS>
-__global__ void __launch_bounds__(kJoinThreads) fa2_paged_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const DecodeArgs a) {
   constexpr int HEADS = 8 * NT, WARPS = kJoinThreads / 32;
   const int split = a.join_split;
   __shared__ float2 s_ml[2][HEADS];  // of the CTA's first and last item, if cut
