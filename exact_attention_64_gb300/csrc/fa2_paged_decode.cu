@@ -97,14 +97,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D>
 __device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
 
-// T, by a whole warp.
-template <int D>
-__device__ __forceinline__ long long total_units(const CacheView& c, int HH, int lane) {
-  long long t = 0;
-  for (int b = lane; b < c.B; b += 32) t += static_cast<long long>(tiles_of<D>(seq_len(c, b))) * HH;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
+// Quotient of 0 <= a and b > 0; 32 bits when they do, which is nearly always.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 struct UnitCursor {
@@ -112,36 +108,54 @@ struct UnitCursor {
   int n, ntiles;    // slots of the sequence, units of the item
 };
 
-// Cursor of unit u < T, by a whole warp.
+// The units of all sequences, by a whole warp: T, and where a unit lies. Up to
+// 32 sequences are read once and their running sums stay with the lanes.
 template <int D>
-__device__ __forceinline__ UnitCursor unit_cursor(const CacheView& c, int HH, long long u, int lane) {
-  long long base = 0;
-  UnitCursor k{};
-  for (int b0 = 0; b0 < c.B; b0 += 32) {
-    const int b = b0 + lane;
-    const int n = b < c.B ? seq_len(c, b) : 0;
-    const long long mine = static_cast<long long>(tiles_of<D>(n)) * HH;
-    long long incl = mine;
+struct UnitMap {
+  const CacheView& c;
+  int HH, lane, n;
+  long long incl, T;
+
+  __device__ UnitMap(const CacheView& view, int hh, int l) : c(view), HH(hh), lane(l) {
+    n = length(lane);
+    incl = scan(n);
+    T = __shfl_sync(0xffffffffu, incl, 31);
+    for (int b0 = 32; b0 < c.B; b0 += 32) T += __shfl_sync(0xffffffffu, scan(length(b0 + lane)), 31);
+  }
+  __device__ int length(int b) const { return b < c.B ? seq_len(c, b) : 0; }
+  __device__ long long scan(int slots) const {
+    long long t = static_cast<long long>(tiles_of<D>(slots)) * HH;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      const long long y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, u < base + incl);
-    if (hit != 0u) {
-      const int src = __ffs(hit) - 1;
-      const long long r = u - (base + __shfl_sync(0xffffffffu, incl - mine, src));
-      k.b = b0 + src;
-      k.n = __shfl_sync(0xffffffffu, n, src);
-      k.ntiles = tiles_of<D>(k.n);
-      k.hh = static_cast<int>(r / k.ntiles);
-      k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
-      return k;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    return t;
   }
-  return k;
-}
+  // Cursor of unit u < T.
+  __device__ UnitCursor at(long long u) const {
+    long long base = 0, sum = incl;
+    int len = n;
+    for (int b0 = 0;; b0 += 32) {
+      const unsigned hit = __ballot_sync(0xffffffffu, u < base + sum);
+      if (hit != 0u) {
+        const int src = __ffs(hit) - 1;
+        UnitCursor k;
+        k.b = b0 + src;
+        k.n = __shfl_sync(0xffffffffu, len, src);
+        k.ntiles = tiles_of<D>(k.n);
+        const long long r = u - (base + __shfl_sync(0xffffffffu, sum, src) - static_cast<long long>(k.ntiles) * HH);
+        k.hh = static_cast<int>(div_pos(r, k.ntiles));
+        k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
+        return k;
+      }
+      if (b0 + 32 >= c.B) return UnitCursor{};
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      len = length(b0 + 32 + lane);
+      sum = scan(len);
+    }
+  }
+};
 
 template <int D>
 __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k) {
@@ -161,9 +175,9 @@ __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCur
 
 // Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer
 // units than CTAs, T CTAs take one each.
-__device__ __forceinline__ long long unit_begin(long long x, long long G, long long T) { return x * T / G; }
+__device__ __forceinline__ long long unit_begin(long long x, long long G, long long T) { return div_pos(x * T, G); }
 __device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
-  return static_cast<int>(((u + 1) * G - 1) / T);
+  return static_cast<int>(div_pos((u + 1) * G - 1, T));
 }
 
 template <int D, int NT>
@@ -189,7 +203,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const long long T = total_units<D>(c, HH, lane);
+  const UnitMap<D> map(c, HH, lane);
+  const long long T = map.T;
   const long long G = min(static_cast<long long>(gridDim.x), T);
   const int cta = blockIdx.x;
   if (cta == 0 && warp == 0)
@@ -197,7 +212,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       if (__ldg(c.lens + b) != seq_len(c, b)) report_page(c.status);
   if (cta >= G) return;
   const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
-  UnitCursor cc = unit_cursor<D>(c, HH, u0, lane);
+  UnitCursor cc = map.at(u0);
   UnitCursor ic = cc;  // next unit to copy
   const uint64_t pol = read_once_policy();
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
@@ -619,7 +634,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const long long T = total_units<D>(c, HH, lane);
+  const UnitMap<D> map(c, HH, lane);
+  const long long T = map.T;
   const long long G = min(static_cast<long long>(gridDim.x / split), T);
   const int cta = blockIdx.x / split, sub = blockIdx.x - cta * split;
   long long u0 = 0, u1 = 0, v0 = 0, v1 = 0;  // units of the CTA, and this block's share of them
@@ -628,14 +644,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
   if (cta < G) {
     u0 = unit_begin(cta, G, T);
     u1 = unit_begin(cta + 1, G, T);
-    subs = static_cast<int>(max(1LL, min(static_cast<long long>(split), (u1 - u0) / kJoinUnits)));
+    subs = static_cast<int>(max(1LL, min(static_cast<long long>(split), div_pos(u1 - u0, kJoinUnits))));
     if (sub < subs) {
-      v0 = u0 + (u1 - u0) * sub / subs;
-      v1 = u0 + (u1 - u0) * (sub + 1) / subs;
-      first = last = cc = unit_cursor<D>(c, HH, u0, lane);
+      v0 = u0 + div_pos((u1 - u0) * sub, subs);
+      v1 = u0 + div_pos((u1 - u0) * (sub + 1), subs);
+      first = last = cc = map.at(u0);
       last.tile += static_cast<int>(u1 - 1 - u0);
-      if (first.tile + (u1 - 1 - u0) >= first.ntiles) last = unit_cursor<D>(c, HH, u1 - 1, lane);
-      if (sub > 0) cc = unit_cursor<D>(c, HH, v0, lane);
+      if (first.tile + (u1 - 1 - u0) >= first.ntiles) last = map.at(u1 - 1);
+      if (sub > 0) cc = map.at(v0);
     }
   }
   grid_dependency_wait();
