@@ -11,7 +11,7 @@
 // tensor core at d = 128 (512 at d = 64) and 1220 of the exponentials: a loop of
 // the same arithmetic alone reaches 26.8 per clock and SM. The kernel takes
 // about 1800: with the products taken out 1710, with the arithmetic taken out
-// 1580, so neither alone holds it up. Each warp also waits for its product, for
+// 1780, so neither alone holds it up. Each warp also waits for its product, for
 // TMEM (slow to answer while the tensor core accumulates there) and at each 16
 // columns for the tail of its own arithmetic, and four warps per scheduler hide
 // two thirds of that.
@@ -21,15 +21,17 @@
 // scalar per thread and tile, nothing is read from shared memory between the
 // product and the sums (its bandwidth belongs to the product's operands), and
 // the sum over lanes happens once per item. The transposed form (lane = key)
-// needs no such sum but a broadcast read of L per column: 290 us against 231 at
+// needs no such sum but a broadcast read of L per column: 290 us against 236 at
 // B = 2, H = 16, N = 8192, d = 128, causal.
 //
 // A work item is 256 keys, tiles A and B, so that a Q tile fetched from L2
-// feeds a product 256 wide. All of TMEM is two S buffers: the tensor core fills
-// one while four groups of four compute warps, 64 columns each, read the other.
-// (Two groups of 128 columns, 254 us, leave two warps per scheduler. Two products
-// 128 wide with barriers of their own, 237. A part of the exponentials as a
-// polynomial on the FMA pipes: 248 with one pair of eight, 265 with two.)
+// feeds two products; two groups of four compute warps own 64 columns of each.
+// All of TMEM is two S buffers per tile. Not kept: two groups of 128 columns
+// (254 us, two warps per scheduler); one product 256 wide with one barrier for
+// both tiles (231 us there, but 56 against 51 on B = 8, 16/4 heads, N = 2048,
+// where more tiles are masked); a part of the exponentials as a polynomial on the
+// FMA pipes (248 with one pair of eight, 265 with two); four units in a row
+// without a break at d = 128 (279: spills).
 //
 // Split: the (item, query head, query tile) units of all items, in that order,
 // are cut into one run per SM of equal length. An item inside one run is
@@ -185,11 +187,8 @@ struct KwCfg {
 };
 
 // What the compute warps need to know of a unit, written by a warp of its own:
-// it keeps the unit arithmetic out of registers that hold sums. The facts of
-// unit n + 1 are there when S of unit n is, so that reading them hides behind
-// unit n's work (shared memory answers slowly while products stream through it).
-constexpr int kKwInfos = 4;
-constexpr int kKwRun = 2;  // units worked on without a break, see kw_plain_units
+// it keeps the unit arithmetic out of registers that hold sums. One slot per S
+// buffer.
 struct KwInfo {
   float2 row[kTileRows];  // (nl, f) of each query, see kw_chunk
   float* dst;             // where the 256 sums go when the unit ends a run of its item
@@ -203,28 +202,14 @@ template <int D>
 struct KwShared {
   uint64_t k_full[2], k_free[2];
   uint64_t q_full[KwCfg<D>::NQ], q_free[KwCfg<D>::NQ];
-  uint64_t s_full[2], s_free[2];
-  uint64_t info0;  // the facts of unit 0
+  uint64_t s_full[2][2], s_free[2][2];  // [tile][buffer]
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
   uint64_t sum_full[4], sum_free[4];  // per group
   float2 sums[4][3][32];  // per group: the sums of 64 keys of its warps 1 .. 3
-  KwInfo info[kKwInfos];
+  KwInfo info[2];
 };
-
-// S = Q K^T of one unit: M = 128 queries, N = 256 keys, or 128 if tile B has
-// nothing to see. Both K tiles lie in one slab of 256 rows per 64 columns.
-template <int D, bool BF16, int N>
-__device__ __forceinline__ void kw_issue(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
-  constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, false, false);
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint64_t ad = make_sdesc_sw128(q_smem + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024);
-    const uint64_t bd = make_sdesc_sw128(k_smem + (kk / 4) * (kKwKeys * 128) + (kk % 4) * 32, 16, 1024);
-    umma_ss_warp(d_tmem, ad, bd, idesc, kk > 0 ? 1u : 0u);
-  }
-}
 
 // 16 columns (keys) of one query row: acc += e^(score - L), as
 // 2^(s c + nl) f with nl an integer and f in 2^-0.5 .. 2^0.5. With MASK only
@@ -245,139 +230,114 @@ __device__ __forceinline__ void kw_chunk(const uint32_t (&v)[16], float2* acc, f
   }
 }
 
-// A compute warp: group cg has columns 64 cg .. 64 cg + 63 (half of tile cg / 2),
-// a thread one query row (TMEM lane), with the sums of its 64 keys in registers.
-struct KwWarp {
-  int cg, t, quad, r, lane;
-  uint32_t t_lane;     // TMEM address of its lanes and columns, buffer 0
-  float c;
-  int n;               // unit of this CTA that is being worked on
-  long long units;     // left, this one included
-  int flags, next_flags;
-  float2 row, next_row;
-  bool ready;          // S of unit n has been waited for, its facts are in flags and row
-};
-
-// Takes over the facts of unit n, whose S is there, and asks for the next's.
-template <int D>
-__device__ __forceinline__ void kw_begin(KwShared<D>& sh, KwWarp& x) {
-  tc_fence_after();
-  x.flags = x.next_flags;
-  x.row = x.next_row;
-  const KwInfo& w = sh.info[(x.n + 1) % kKwInfos];  // past the last unit: not used
-  x.next_flags = w.flags;
-  x.next_row = w.row[x.r];
-}
-__device__ __forceinline__ bool kw_plain(const KwWarp& x) { return (x.flags & (5 << x.t)) == (1 << x.t); }
-
-// The buffer of unit n and the facts of unit n + 1 have been read.
-template <int D>
-__device__ __forceinline__ void kw_release(KwShared<D>& sh, const KwWarp& x) {
-  tc_fence_before();
-  __syncwarp();
-  if (x.lane == 0) mbar_arrive(&sh.s_free[x.n & 1]);
-}
-
-// Up to LEFT plain units (active, not masked) of one item in a row; the first
-// 16 columns of unit n have been asked for, into va. Before the last columns of
-// a unit are worked on, the first of the next one are asked for, so that the
-// waits for its product and for TMEM hide behind them: 231 us against 236 without
-// at d = 128, 214 against 227 at d = 64 (B = 2, H = 16, N = 8192, causal). Four
-// units in a row spill, 279 us, and so does a loop, which carries the loads across
-// its back edge. False if a wait ran out.
-template <int D, int LEFT>
-__device__ __forceinline__ bool kw_plain_units(KwShared<D>& sh, KwWarp& x, float2* acc, uint32_t (&va)[16],
-                                               uint32_t (&vb)[16], const WaitCtx& wc) {
-  const uint32_t ts = x.t_lane + (x.n & 1) * kKwKeys;
-  const float2 row = x.row;
-  tmem_wait_ld();
-  reg_fence(va);
-  tmem_ld_32x32b_x16(ts + 16, vb);
-  kw_chunk<false>(va, acc, x.c, row.x, row.y, 0);
-  tmem_wait_ld();
-  reg_fence(vb);
-  tmem_ld_32x32b_x16(ts + 32, va);
-  kw_chunk<false>(vb, acc + 8, x.c, row.x, row.y, 0);
-  tmem_wait_ld();
-  reg_fence(va);
-  tmem_ld_32x32b_x16(ts + 48, vb);
-  const bool more = LEFT > 1 && !(x.flags & 16);
-  bool there = false;
-  if (more) there = mbar_test_wait(smem_u32(&sh.s_full[(x.n + 1) & 1]), ((x.n + 1) >> 1) & 1);
-  kw_chunk<false>(va, acc + 16, x.c, row.x, row.y, 0);
-  tmem_wait_ld();
-  reg_fence(vb);
-  kw_release(sh, x);
-  ++x.n;
-  --x.units;
-  if constexpr (LEFT > 1) {
-    if (more) {
-      if (!__all_sync(0xffffffffu, there) && !mbar_wait_warp(&sh.s_full[x.n & 1], (x.n >> 1) & 1, wc)) return false;
-      kw_begin(sh, x);
-      if (kw_plain(x)) {
-        tmem_ld_32x32b_x16(x.t_lane + (x.n & 1) * kKwKeys, va);
-        kw_chunk<false>(vb, acc + 24, x.c, row.x, row.y, 0);
-        return kw_plain_units<D, LEFT - 1>(sh, x, acc, va, vb, wc);
-      }
-      x.ready = true;
-    }
-  }
-  kw_chunk<false>(vb, acc + 24, x.c, row.x, row.y, 0);
-  return true;
-}
-
+// The compute warps: group cg has columns 64 cg .. 64 cg + 63 (half of tile
+// cg / 2), a thread one query row (TMEM lane), with the sums of its 64 keys in
+// registers.
 template <int D>
 __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float c, long long units, int warp,
                                            int lane, const WaitCtx& wc) {
-  KwWarp x;
-  x.cg = (warp - 4) >> 2;
-  x.t = x.cg >> 1;
-  x.quad = warp & 3;
-  x.r = x.quad * 32 + lane;
-  x.lane = lane;
-  x.t_lane = tmem + (static_cast<uint32_t>(x.quad * 32) << 16) + x.cg * 64;
-  x.c = c;
-  x.n = 0;
-  x.units = units;
-  x.ready = false;
-  const int cg = x.cg, quad = x.quad;
+  const int cg = (warp - 4) >> 2, t = cg >> 1, quad = warp & 3, r = quad * 32 + lane;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * t * kTileRows + (cg & 1) * 64;
   float2 acc[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.f, 0.f);
-  int flushes = 0;
-  if (units == 0 || !mbar_wait_warp(&sh.info0, 0, wc)) return;
-  x.next_flags = sh.info[0].flags;
-  x.next_row = sh.info[0].row[x.r];
-  while (x.units > 0) {
-    if (!x.ready) {
-      if (!mbar_wait_warp(&sh.s_full[x.n & 1], (x.n >> 1) & 1, wc)) return;
-      kw_begin(sh, x);
-    }
-    x.ready = false;
-    if (kw_plain(x)) {
+  for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
+  auto release = [&](int buf) {  // the buffer and its unit's facts have been read
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
+  };
+  int n = 0, flushes = 0;
+  while (units > 0) {
+    const int buf = n & 1;
+    const uint32_t ts = t_lane + buf * kTileRows;
+    if (!mbar_wait_warp(&sh.s_full[t][buf], (n >> 1) & 1, wc)) return;
+    tc_fence_after();
+    int flags = sh.info[buf].flags;
+    float* dst = sh.info[buf].dst;
+    int keys = sh.info[buf].keys;
+    const float2 row = sh.info[buf].row[r];
+    const int plain = 1 << t, kind = 5 << t;  // active, not masked
+    if ((flags & kind) == plain) {
       uint32_t va[16], vb[16];
-      tmem_ld_32x32b_x16(x.t_lane + (x.n & 1) * kKwKeys, va);
-      if (!kw_plain_units<D, kKwRun>(sh, x, acc, va, vb, wc)) return;
-    } else {
-      if (x.flags & (1 << x.t)) {
-        // Visible keys of this row, from the group's first one.
-        const KwInfo& w = sh.info[x.n % kKwInfos];
-        const int lim = x.r < w.rows ? w.d0 + x.r - cg * 64 + 1 : 0;
-#pragma unroll
-        for (int i = 0; i < 64; i += 16) {
-          uint32_t va[16];
-          tmem_ld_32x32b_x16(x.t_lane + (x.n & 1) * kKwKeys + i, va);
+      tmem_ld_32x32b_x16(ts, va);
+      tmem_wait_ld();
+      reg_fence(va);
+      tmem_ld_32x32b_x16(ts + 16, vb);
+      kw_chunk<false>(va, acc, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(vb);
+      tmem_ld_32x32b_x16(ts + 32, va);
+      kw_chunk<false>(vb, acc + 8, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(va);
+      tmem_ld_32x32b_x16(ts + 48, vb);
+      kw_chunk<false>(va, acc + 16, c, row.x, row.y, 0);
+      tmem_wait_ld();
+      reg_fence(vb);
+      release(buf);
+      ++n;
+      --units;
+      if (D == 64 && !(flags & 16)) {
+        // The same item goes on: its next unit's first columns are asked for
+        // before this one's last are worked on, so that every other wait for a
+        // product and for TMEM is hidden. (Always doing so carries loads across
+        // the loop's back edge, which costs spills: twice the time.) Worth it
+        // where the products are short: 214 against 227 us at d = 64, 239
+        // against 237 at d = 128 (B = 2, H = 16, N = 8192, causal).
+        if (!mbar_wait_warp(&sh.s_full[t][buf ^ 1], (n >> 1) & 1, wc)) return;
+        tc_fence_after();
+        const int f1 = sh.info[buf ^ 1].flags;
+        if ((f1 & kind) == plain) {
+          const float2 row1 = sh.info[buf ^ 1].row[r];
+          const uint32_t t1 = t_lane + (buf ^ 1) * kTileRows;
+          tmem_ld_32x32b_x16(t1, va);
+          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
           tmem_wait_ld();
           reg_fence(va);
-          kw_chunk<true>(va, acc + i / 2, c, x.row.x, x.row.y, lim - i);
+          tmem_ld_32x32b_x16(t1 + 16, vb);
+          kw_chunk<false>(va, acc, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(vb);
+          tmem_ld_32x32b_x16(t1 + 32, va);
+          kw_chunk<false>(vb, acc + 8, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(va);
+          tmem_ld_32x32b_x16(t1 + 48, vb);
+          kw_chunk<false>(va, acc + 16, c, row1.x, row1.y, 0);
+          tmem_wait_ld();
+          reg_fence(vb);
+          flags = f1;
+          dst = sh.info[buf ^ 1].dst;
+          keys = sh.info[buf ^ 1].keys;
+          release(buf ^ 1);
+          kw_chunk<false>(vb, acc + 24, c, row1.x, row1.y, 0);
+          ++n;
+          --units;
+        } else {
+          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+        }
+      } else {
+        kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+      }
+    } else {
+      if (flags & plain) {
+        // Visible keys of this row, from the group's first one.
+        const int lim = r < sh.info[buf].rows ? sh.info[buf].d0 + r - cg * 64 + 1 : 0;
+#pragma unroll
+        for (int x = 0; x < 64; x += 16) {
+          if (__all_sync(0xffffffffu, lim <= x)) break;  // the warp's rows see none of the rest
+          uint32_t va[16];
+          tmem_ld_32x32b_x16(ts + x, va);
+          tmem_wait_ld();
+          reg_fence(va);
+          kw_chunk<true>(va, acc + x / 2, c, row.x, row.y, lim - x);
         }
       }
-      kw_release(sh, x);
-      ++x.n;
-      --x.units;
+      release(buf);
+      ++n;
+      --units;
     }
-    if (!x.ready && (x.flags & 16)) {
-      const KwInfo& w = sh.info[(x.n - 1) % kKwInfos];  // stays until unit n has been released
+    if (flags & 16) {
       // Sums over the warp's 32 rows by halving: lane l ends with keys 2 l and
       // 2 l + 1; the group's first warp adds the four warps' in order.
 #pragma unroll
@@ -406,8 +366,8 @@ __device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_free[cg]);
         const int key = cg * 64 + 2 * lane;
-        if (key < w.keys) w.dst[key] = sum.x;
-        if (key + 1 < w.keys) w.dst[key + 1] = sum.y;
+        if (key < keys) dst[key] = sum.x;
+        if (key + 1 < keys) dst[key + 1] = sum.y;
       }
       ++flushes;
 #pragma unroll
@@ -442,11 +402,12 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.k_full[i], 1);
         mbar_init(&sh.k_free[i], 1);
-        mbar_init(&sh.s_full[i], 2);   // the product, and the facts of the next unit
-        mbar_init(&sh.s_free[i], 16);  // one arrival per compute warp
+        for (int t = 0; t < 2; ++t) {
+          mbar_init(&sh.s_full[t][i], 2);  // the product and the unit's facts
+          mbar_init(&sh.s_free[t][i], 8);  // one arrival per compute warp of the tile
+        }
       }
       mbar_init(&sh.mma_done, 1);
-      mbar_init(&sh.info0, 1);
       fence_mbar_init();
     } else if (warp == 3) {
       for (int i = 0; i < 4; ++i) {
@@ -486,13 +447,10 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           if (items > 1) ok = mbar_wait(&sh.k_free[kb], ((items >> 1) - 1) & 1, wc);
           if (!ok) break;
           mbar_arrive_expect_tx(&sh.k_full[kb], 2 * C::TILE);
-          uint8_t* dst = smem + C::OFF_K + kb * 2 * C::TILE;
 #pragma unroll
-          for (int sl = 0; sl < D / 64; ++sl)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              tma_load_3d(dst + sl * (kKwKeys * 128) + t * (kTileRows * 128), &tm_k, &sh.k_full[kb], sl * 64,
-                          cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
+          for (int t = 0; t < 2; ++t)
+            load_tile<D>(smem + C::OFF_K + (2 * kb + t) * C::TILE, &tm_k, &sh.k_full[kb],
+                         cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
           ++items;
         }
         if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
@@ -529,14 +487,22 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           ++items;
         }
         const int buf = n & 1, kb = (items - 1) & 1;
-        ok = n > 1 ? mbar_wait2_warp(&sh.q_full[qs], qph, &sh.s_free[buf], ((n >> 1) - 1) & 1, wc)
-                   : mbar_wait_warp(&sh.q_full[qs], qph, wc);
+        ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
+        const bool act_b = kw_active(a, s, cu, 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && n > 1) ok = mbar_wait_warp(&sh.s_free[t][buf], ((n >> 1) - 1) & 1, wc);
+          if (!ok) break;
+          if (t == 0 || act_b) {
+            tc_fence_after();
+            mma_rows_x_rows<D, BF16>(tmem + (2 * t + buf) * kTileRows, q_base + qs * C::TILE,
+                                     k_base + (2 * kb + t) * C::TILE);
+            umma_commit_warp(&sh.s_full[t][buf]);
+          } else if (lane == 0) {
+            mbar_arrive(&sh.s_full[t][buf]);
+          }
+        }
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kKwKeys, q = q_base + qs * C::TILE, k = k_base + kb * 2 * C::TILE;
-        if (kw_active(a, s, cu, 1)) kw_issue<D, BF16, 256>(d, q, k);
-        else kw_issue<D, BF16, 128>(d, q, k);
-        umma_commit_warp(&sh.s_full[buf]);
         umma_commit_warp(&sh.q_free[qs]);
         if (++qs == C::NQ) {
           qs = 0;
@@ -566,10 +532,9 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           const float whole = rintf(hi);
           row[x] = make_float2(-whole, ex2_approx(-((hi - whole) + lo)));
         }
-        // Unit n - 3 has been released: its slot's last reader, and the barrier
-        // phase before the one that this arrival counts in, are past.
-        if (n > 2 && !mbar_wait_warp(&sh.s_free[(n - 3) & 1], ((n - 3) >> 1) & 1, wc)) break;
-        KwInfo& w = sh.info[n % kKwInfos];
+        const int buf = n & 1, par = ((n >> 1) - 1) & 1;
+        if (n > 1 && !mbar_wait2_warp(&sh.s_free[0][buf], par, &sh.s_free[1][buf], par, wc)) break;
+        KwInfo& w = sh.info[buf];
 #pragma unroll
         for (int x = 0; x < 4; ++x) w.row[x * 32 + lane] = row[x];
         if (lane == 0) {
@@ -588,12 +553,9 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(n == 0 ? &sh.info0 : &sh.s_full[(n - 1) & 1]);
+        if (lane < 2) mbar_arrive(&sh.s_full[lane][buf]);
         if (kw_advance(a, s, cu)) from_start = true;
       }
-      // The last unit has no next one; n units have been announced.
-      if (n > 2 && !mbar_wait_warp(&sh.s_free[(n - 3) & 1], ((n - 3) >> 1) & 1, wc)) n = 0;
-      if (n > 0 && lane == 0) mbar_arrive(&sh.s_full[(n - 1) & 1]);
     }
   } else if (u0 < u1) {
     setmaxnreg_inc<104>();
