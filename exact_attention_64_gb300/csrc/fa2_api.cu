@@ -361,6 +361,13 @@ int host_device_setup(int* num_sms, int** status) {
   return st;
 }
 int host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+int host_take_fault(int kind, unsigned long long* timeout_ns) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (g_fault_kind != kind) return 0;
+  g_fault_kind = 0;
+  *timeout_ns = g_fault_timeout_ns;
+  return 1;
+}
 int host_map_16bit(CUtensorMap* m, const void* ptr, int BH, int N, int d, int dtype) {
   return make_map_16bit(m, ptr, BH, N, d, dtype);
 }
@@ -711,7 +718,7 @@ int fa2_fwd_schedule(int B, int H, int N, int causal, int num_sms, int* num_ctas
 int fa2_last_cuda_error(void) { return g_last_cuda_error; }
 
 int fa2_debug_arm_fault(int kind, int timeout_ms) {
-  if (kind < 0 || kind > 4) return FA2_ERR_INVALID_ARG;
+  if (kind < 0 || (kind > 4 && kind != 6)) return FA2_ERR_INVALID_ARG;
   if (kind != 0 && (timeout_ms < 1 || timeout_ms > 5000)) return FA2_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   g_fault_kind = kind;

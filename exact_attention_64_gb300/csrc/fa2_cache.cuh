@@ -16,7 +16,8 @@
 
 namespace fa2 {
 
-constexpr int kDevPage = 9;  // equals FA2_ERR_PAGE of the public header
+constexpr int kDevPage = 9;     // equals FA2_ERR_PAGE of the public header
+constexpr int kMaxGroup = 128;  // query heads per key head
 
 // Division of 0 <= n < 2^31 by a run-time d >= 1 as one multiplication: with
 // s = ceil(log2 d) and m = floor(2^(31+s) / d) + 1, n / d = (n m) >> (31 + s),
@@ -183,6 +184,7 @@ struct KeyWeightArgs {
   float scale_log2;       // scale * log2(e)
   int* status;
   unsigned long long timeout_ns;
+  int fault;              // 0 normally; failure-path test: the first Q tile of each CTA never loads
 };
 
 }  // namespace fa2

@@ -21,7 +21,6 @@ cudaError_t launch_key_weights(int d, bool bf16, bool causal, const CUtensorMap&
 
 namespace {
 
-constexpr int kMaxGroup = 128;    // query heads per key head
 constexpr int kDecodeCtas = 304;  // most CTAs of a decode: two on each of 152 SMs
 constexpr int kKwCtas = 152;      // most CTAs of the key weights
 constexpr long long kMaxRows = (1LL << 31) - 1;
@@ -116,7 +115,7 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
 
 int check_heads(int Hq, int Hkv) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA2_ERR_INVALID_ARG;
-  if (Hq > 65535 || Hq / Hkv > kMaxGroup) return FA2_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hq / Hkv > fa2::kMaxGroup) return FA2_ERR_UNSUPPORTED;
   return FA2_OK;
 }
 
@@ -339,6 +338,7 @@ int fa2_key_weights(const void* q, const void* k, const float* lse, const int* q
   // themselves per step in the mean, and the scale gives that back.
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (1.0 + d / 16 * 1.25e-8));
   a.timeout_ns = fa2::kDefaultWaitTimeoutNs;
+  a.fault = fa2::host_take_fault(6, &a.timeout_ns);
   const int ctas = sms < kKwCtas ? sms : kKwCtas;
   (void)cudaGetLastError();
   const cudaError_t e = fa2::launch_key_weights(d, dtype == FA2_BF16, causal != 0, tq, tk, a, ctas,

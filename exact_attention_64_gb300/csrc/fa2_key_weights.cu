@@ -455,9 +455,11 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         }
         if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
         if (!ok) break;
-        mbar_arrive_expect_tx(&sh.q_full[qs], C::TILE);
-        load_tile<D>(smem + C::OFF_Q + qs * C::TILE, &tm_q, &sh.q_full[qs], cu.i * kTileRows,
-                     cu.b * a.Hq + cu.h * a.g + cu.gh);
+        if (a.fault == 0 || u > u0) {
+          mbar_arrive_expect_tx(&sh.q_full[qs], C::TILE);
+          load_tile<D>(smem + C::OFF_Q + qs * C::TILE, &tm_q, &sh.q_full[qs], cu.i * kTileRows,
+                       cu.b * a.Hq + cu.h * a.g + cu.gh);
+        }
         ++used;
         if (++qs == C::NQ) {
           qs = 0;
@@ -530,7 +532,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           const float hi = l * kLog2e;
           const float lo = fmaf(l, kLog2e, -hi) + l * kLog2eRest;
           const float whole = rintf(hi);
-          row[x] = make_float2(-whole, ex2_approx(-((hi - whole) + lo)));
+          // L = +inf: no weight (2^-inf), as in e^(s - L).
+          row[x] = make_float2(-whole, isinf(hi) ? 1.f : ex2_approx(-((hi - whole) + lo)));
         }
         const int buf = n & 1, par = ((n >> 1) - 1) & 1;
         if (n > 1 && !mbar_wait2_warp(&sh.s_free[0][buf], par, &sh.s_free[1][buf], par, wc)) break;

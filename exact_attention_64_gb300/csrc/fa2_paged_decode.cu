@@ -43,7 +43,6 @@ constexpr int kDecWarps = 4;
 // the same bytes at both head sizes.
 template <int D>
 constexpr int kUnit = decode_unit(D);
-constexpr int kMaxGroup = 128;  // query heads per key head
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr float kLog2ef = 1.4426950408889634f;
 
@@ -454,11 +453,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         if (gh < a.g) {
           if (whole) {
             const size_t row = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + gh;
-            const float inv = S > 0.f ? 1.f / S : 0.f;
+            const float inv = S == 0.f ? 0.f : 1.f / S;
             uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + e0);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) dst[x] = pack_x2<BF16>(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-            if (e0 == 0) a.lse[row] = S > 0.f ? (M + log2f(S)) * kLn2f : -INFINITY;
+            if (e0 == 0) a.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
           } else {
             float4* dst = reinterpret_cast<float4*>(
                 a.part_o + (static_cast<size_t>(slot) * C::HEADS + nt * 8 + hd) * D + e0);
@@ -615,10 +614,10 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
       __syncthreads();
     }
     if (lane < 8 && (!wide || warp == 0)) {
-      const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
+      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
       *reinterpret_cast<uint2*>(a.o + (row0 + hd) * D + e0) =
           make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
-      if (e0 == 0) a.lse[row0 + hd] = ml.y > 0.f ? (ml.x + log2f(ml.y)) * kLn2f : -INFINITY;
+      if (e0 == 0) a.lse[row0 + hd] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2f;
     }
   }
   __syncthreads();
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
           }
           float v;
           if (whole) v = a.lse[static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + hd] * kLog2ef;
-          else v = ml.y > 0.f ? ml.x + log2f(ml.y) : -INFINITY;
+          else v = ml.y == 0.f ? -INFINITY : ml.x + log2f(ml.y);
           if (lane == 0) s_lse[hd] = v;
         }
         __syncthreads();

@@ -468,6 +468,7 @@ int fa2_last_cuda_error(void);
  *      first dO tile of every K/V column worker;
  *   4  the next fa2_bwd (or fa2_bwd_qk, fa2_bwd_noalloc): the first V tile of
  *      every dQ worker;
+ *   6  the next fa2_key_weights: the first Q tile of every CTA (there is no 5);
  *   0  disarms.
  * Outputs of the faulted call are undefined. Exists to test the failure path
  * without hanging or faulting the GPU. */

@@ -132,6 +132,9 @@ def _check_evict(fa2, c, w, pos, budget, recent, in_place, with_pos):
     (2, 2, 64, 16, [700, 650], 1, 1),
     (1, 2, 64, 64, [5000], 1237, 100),    # past 4096 slots: a cluster
     (2, 1, 64, 128, [9001, 4500], 4400, 0),
+    (1, 2, 64, 64, [5001], 5000, 10),     # one too many, in a cluster
+    (1, 1, 64, 64, [40000], 20000, 100),  # keys in shared memory
+    (1, 1, 64, 64, [33001], 33000, 7),
 ])
 @pytest.mark.parametrize("kind", ["plain", "ties", "equal", "odd", "rising"])
 def test_evict(cuda_device, fa2_lib, B, Hkv, d, ps, lens, budget, recent, kind):

@@ -122,3 +122,22 @@ def test_key_weights_in_a_graph_follows_lengths(cuda_device, fa2_lib):
         want = fa2_lib.key_weights(q, k, lse, causal=True, q_lens=ql)
         torch.cuda.synchronize()
         assert torch.equal(w, want)
+
+
+def test_key_weights_of_rows_without_weight(cuda_device, fa2_lib):
+    """L = +inf gives a query no weight, as e^(s - L) does."""
+    q, k, lse, scale = _inputs(1, 2, 1, 300, 300, 64, BF16, False, 5)
+    lse[0, 0, 10:140] = float("inf")
+    lse[0, 1, 299] = float("inf")
+    _check(fa2_lib, q, k, lse, False, scale)
+
+
+def test_key_weights_timeout_path(cuda_device, fa2_lib):
+    """A Q tile that never arrives: the bounded wait runs out, the status says so,
+    and the next call is correct."""
+    q, k, lse, scale = _inputs(1, 2, 2, 700, 700, 128, BF16, True, 6)
+    assert fa2_lib.load_library().fa2_debug_arm_fault(6, 20) == 0
+    fa2_lib.key_weights(q.cuda(), k.cuda(), lse.cuda(), causal=True)
+    assert fa2_lib.device_status() == 6
+    assert fa2_lib.device_status() == 0
+    _check(fa2_lib, q, k, lse, True, scale)

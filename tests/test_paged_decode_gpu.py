@@ -25,6 +25,8 @@ CASES = [
     (70, 8, 4, 64, 16, None),             # more items than CTAs, several per CTA
     (5, 16, 16, 128, 48, [0, 0, 600, 0, 1]),
     (4, 5, 5, 128, 4096, [100, 4096, 4097, 3]),
+    (200, 2, 1, 128, 8, [0] * 60 + [9] * 60 + [0] * 40 + [33] * 40),  # whole warps of lengths empty
+    (1, 128, 1, 64, 16, [300]),           # the largest group
 ]
 
 
@@ -188,3 +190,28 @@ def test_decode_offsets_past_32_bits(cuda_device, fa2_lib):
     o2, lse2 = fa2_lib.paged_decode(q, ks, vs, ts, ls)
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_lets_nan_and_infinities_through(cuda_device, fa2_lib):
+    """A NaN key makes its heads NaN, L too; a key with a score of -inf weighs
+    nothing; other heads and sequences do not notice."""
+    c = Cache(3, 2, 64, 16, [100, 100, 100], BF16, seed=10)
+    kc, vc, table, lens = c.gpu()
+    q = c.query(4).cuda().abs()
+    want_o, want_l = fa2_lib.paged_decode(q, kc, vc, table, lens)
+    page, off = int(c.table[0, 2]), 5
+    kc[page, 1, off] = float("nan")
+    kc[int(c.table[1, 0]), 0, 3] = -float("inf")
+    w = torch.zeros(3, 2, c.L, device="cuda")
+    o, lse = fa2_lib.paged_decode(q, kc, vc, table, lens, weights=w)
+    torch.cuda.synchronize()
+    assert fa2_lib.device_status() == 0
+    assert o[0, 2:].isnan().all() and lse[0, 2:].isnan().all() and w[0, 1, :100].isnan().all()
+    assert torch.equal(o[0, :2], want_o[0, :2]) and torch.equal(o[2], want_o[2]) and torch.equal(lse[2], want_l[2])
+    assert torch.equal(o[1, 2:], want_o[1, 2:])
+    assert o[1].isfinite().all() and lse[1].isfinite().all() and w[1, 0, 3] == 0
+    see = [np.ones(100, bool) for _ in range(3)]
+    see[1][3] = False
+    ref, lref, _ = oc.paged_decode(bits64(q), bits64(c.k), bits64(c.v), c.table.numpy(), c.lens.numpy(), 64 ** -0.5,
+                                   visible=see)
+    assert (np.abs(bits64(lse)[1, :2] - lref[1, :2]) < 1e-4).all()
