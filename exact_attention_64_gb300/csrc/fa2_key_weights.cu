@@ -10,28 +10,27 @@
 // exponential for it. A unit of 128 queries x 256 keys takes 1024 clocks of
 // tensor core at d = 128 (512 at d = 64) and 1220 of the exponentials: a loop of
 // the same arithmetic alone reaches 26.8 per clock and SM. The kernel takes
-// about 1800: with the products taken out 1710, with the arithmetic taken out
-// 1780, so neither alone holds it up. Each warp also waits for its product, for
-// TMEM (slow to answer while the tensor core accumulates there) and at each 16
-// columns for the tail of its own arithmetic, and four warps per scheduler hide
-// two thirds of that.
+// about 1630 at B = 2, H = 16, N = 8192, not causal: with the products taken out
+// 1340, with the arithmetic taken out 1320. The rest is the wait for a product
+// that cannot begin before its S has been read.
 //
-// Layout: TMEM lane = query, column = key, and a thread keeps the running sums
-// of its 64 columns in registers over all query tiles of an item. So L is one
-// scalar per thread and tile, nothing is read from shared memory between the
-// product and the sums (its bandwidth belongs to the product's operands), and
-// the sum over lanes happens once per item. The transposed form (lane = key)
-// needs no such sum but a broadcast read of L per column: 290 us against 236 at
-// B = 2, H = 16, N = 8192, d = 128, causal.
+// Layout: S^T = K Q^T, TMEM lane = key, column = query, so that a thread's sums
+// are one key's and need no other lane, and a key that the causal mask hides
+// takes out whole columns of a warp. -L log2(e) is read from shared memory, four
+// queries at a time. A product is 128 keys x 256 queries (two query tiles of one
+// head, when there are two): per flop it reads three quarters of the shared
+// memory of one that is 128 wide, which runs at shared memory's limit. TMEM
+// holds one S for each of the item's two tiles, A and B; the eight warps of one
+// tile work while the tensor core forms the other's. Each tile has an issuer of
+// its own: at a diagonal B has less to do, and runs ahead (B = 8, 16/4 heads,
+// N = 2048: 50 us against 56 with one issuer in fixed order; with a lock that
+// keeps the two from issuing at once 85).
 //
-// A work item is 256 keys, tiles A and B, so that a Q tile fetched from L2
-// feeds two products; two groups of four compute warps own 64 columns of each.
-// All of TMEM is two S buffers per tile. Not kept: two groups of 128 columns
-// (254 us, two warps per scheduler); one product 256 wide with one barrier for
-// both tiles (231 us there, but 56 against 51 on B = 8, 16/4 heads, N = 2048,
-// where more tiles are masked); a part of the exponentials as a polynomial on the
-// FMA pipes (248 with one pair of eight, 265 with two); four units in a row
-// without a break at d = 128 (279: spills).
+// At B = 2, H = 16, N = 8192, d = 128 it takes 210 us causal and 371 not causal.
+// The other orientation, lane = query with a thread's 64 sums in registers, takes
+// 236 and 431 there, and 51 at the N = 2048 above. Also not kept: eight compute warps with 64 columns in
+// flight (272 us, two warps per scheduler), S in halves of 128 queries with a
+// barrier each (296), one issuer that polls both tiles (239).
 //
 // Split: the (item, query head, query tile) units of all items, in that order,
 // are cut into one run per SM of equal length. An item inside one run is
@@ -45,8 +44,6 @@ namespace fa2 {
 
 constexpr int kKwKeys = 256;  // keys per item
 constexpr int kKwThreads = 640;  // 4 control warps, 4 groups of 4 compute warps
-constexpr float kLog2eRest = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
-
 
 // Query tiles [i0, nq) of item kb; none: no query sees its keys.
 struct KwShape {
@@ -88,6 +85,7 @@ struct KwCursor {
   int b, h, kb, gh, i;  // sequence, key head, item, query head of the group, query tile
   int qlen, nq;
   long long to_end;     // units left in the item, this one included
+  long long at;         // the unit's place among all
 };
 
 // Cursor of unit u < T, by a whole warp.
@@ -138,12 +136,14 @@ __device__ __forceinline__ KwCursor kw_cursor(const KeyWeightArgs& a, const KwSh
   k.gh = static_cast<int>(r / w);
   k.i = s.i0(lo) + static_cast<int>(r - static_cast<long long>(k.gh) * w);
   k.to_end = static_cast<long long>(w) * s.g - r;
+  k.at = u;
   return k;
 }
 
 // Next unit; true when it begins an item.
 __device__ __forceinline__ bool kw_advance(const KeyWeightArgs& a, const KwShape& s, KwCursor& k) {
   --k.to_end;
+  ++k.at;
   if (++k.i < k.nq) return false;
   k.i = s.i0(k.kb);
   if (++k.gh < s.g) return false;
@@ -168,211 +168,173 @@ __device__ __forceinline__ bool kw_advance(const KeyWeightArgs& a, const KwShape
   return true;
 }
 
-// Whether tile t (128 keys) of the unit has a visible key: B of the first
-// diagonal tile has none, nor has one past the keys.
-__device__ __forceinline__ bool kw_active(const KeyWeightArgs& a, const KwShape& s, const KwCursor& k, int t) {
+// A step: one unit, or two that follow each other in one query head, whose query
+// tiles then form one product 256 wide.
+__device__ __forceinline__ int kw_step(const KwCursor& k, long long left) {
+  return left > 1 && k.i + 1 < k.nq ? 2 : 1;
+}
+// Advances past a step; true when the next unit begins an item.
+__device__ __forceinline__ bool kw_advance_step(const KeyWeightArgs& a, const KwShape& s, KwCursor& k, int cnt) {
+  bool fresh = kw_advance(a, s, k);
+  if (cnt == 2) fresh = kw_advance(a, s, k);
+  return fresh;
+}
+// Whether tile t (128 keys) has a visible key in a step.
+__device__ __forceinline__ bool kw_active(const KeyWeightArgs& a, const KwShape& s, const KwCursor& k, int cnt, int t) {
   const int kt = 2 * k.kb + t;
-  return kt * kTileRows < a.Nk && (!s.causal || k.i >= kt);
+  return kt * kTileRows < a.Nk && (!s.causal || k.i + cnt - 1 >= kt);
 }
 
-// Shared memory: two K buffers of 256 rows (the next item's keys arrive while
-// this one's are in use) and a ring of Q tiles.
+// Shared memory: the item's two K tiles, and a ring of Q steps.
 template <int D>
 struct KwCfg {
   static constexpr int TILE = kTileRows * D * 2;
-  static constexpr int NQ = D == 128 ? 2 : 8;  // Q tiles in flight: 64 KiB, 128 KiB
+  static constexpr int NQ = D == 128 ? 2 : 4;  // steps in flight: 128 KiB
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_Q = 4 * TILE;
-  static constexpr int SMEM = OFF_Q + NQ * TILE + 1024;
+  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int SMEM = OFF_Q + NQ * 2 * TILE + 1024;
 };
 
-// What the compute warps need to know of a unit, written by a warp of its own:
-// it keeps the unit arithmetic out of registers that hold sums. One slot per S
-// buffer.
+// What the compute warps need to know of a step, written ahead by a warp of its
+// own.
+constexpr int kKwInfos = 4;
 struct KwInfo {
-  float2 row[kTileRows];  // (nl, f) of each query, see kw_chunk
-  float* dst;             // where the 256 sums go when the unit ends a run of its item
-  int keys;               // how many of them there are
-  int flags;              // 1, 2: tile A, B active; 4, 8: masked; 16: ends the run
-  int d0;                 // first query minus first key (not causal: past every key)
-  int rows;               // queries of the tile below the sequence's end
+  float4 nl[2 * kTileRows / 4];  // -L log2(e) of each query
+  float* dst;                    // where the 256 sums go when the step ends a run of its item
+  int keys;                      // how many of them there are
+  int flags;                     // 1, 2: tile A, B active; 4, 8: masked; 16: the sums go out; 32: two units;
+                                 // 64: the last step
+  int d0;                        // first query minus first key (not causal: past every key)
+  int rows;                      // queries of the step below the sequence's end
 };
 
 template <int D>
 struct KwShared {
-  uint64_t k_full[2], k_free[2];
+  uint64_t k_full[2], k_free[2];  // per tile
   uint64_t q_full[KwCfg<D>::NQ], q_free[KwCfg<D>::NQ];
-  uint64_t s_full[2][2], s_free[2][2];  // [tile][buffer]
-  uint64_t mma_done;
+  uint64_t i_full[kKwInfos], i_free[kKwInfos];
+  uint64_t s_full[2], s_free[2];  // per tile
+  uint64_t sum_full[2], sum_free[2];
+  uint64_t mma_done[2];
   uint32_t tmem_base;
   int abort_flag;
-  uint64_t sum_full[4], sum_free[4];  // per group
-  float2 sums[4][3][32];  // per group: the sums of 64 keys of its warps 1 .. 3
-  KwInfo info[2];
+  float sum[2][kTileRows];
+  alignas(16) KwInfo info[kKwInfos];
 };
 
-// 16 columns (keys) of one query row: acc += e^(score - L), as
-// 2^(s c + nl) f with nl an integer and f in 2^-0.5 .. 2^0.5. With MASK only
-// keys below lim count.
-template <bool MASK>
-__device__ __forceinline__ void kw_chunk(const uint32_t (&v)[16], float2* acc, float c, float nl, float f,
-                                         int lim) {
-  const float2 c2 = make_float2(c, c), n2 = make_float2(nl, nl), f2 = make_float2(f, f);
+// S^T = K Q^T of one tile and step: M = 128 keys, N = 128 or 256 queries. The
+// step's query rows lie in one slab of 256 rows per 64 columns.
+template <int D, bool BF16, int N>
+__device__ __forceinline__ void kw_issue(uint32_t d_tmem, uint32_t k_smem, uint32_t q_smem) {
+  constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, false, false);
 #pragma unroll
-  for (int x = 0; x < 16; x += 2) {
-    const float2 e = f2_fma(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c2, n2);
-    float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    if constexpr (MASK) {
-      p.x = x < lim ? p.x : 0.f;
-      p.y = x + 1 < lim ? p.y : 0.f;
-    }
-    acc[x / 2] = f2_fma(p, f2, acc[x / 2]);
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t ad = make_sdesc_sw128(k_smem + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024);
+    const uint64_t bd = make_sdesc_sw128(q_smem + (kk / 4) * (2 * kTileRows * 128) + (kk % 4) * 32, 16, 1024);
+    umma_ss_warp(d_tmem, ad, bd, idesc, kk > 0 ? 1u : 0u);
   }
 }
 
-// The compute warps: group cg has columns 64 cg .. 64 cg + 63 (half of tile
-// cg / 2), a thread one query row (TMEM lane), with the sums of its 64 keys in
-// registers.
-template <int D>
-__device__ __forceinline__ void kw_compute(KwShared<D>& sh, uint32_t tmem, float c, long long units, int warp,
-                                           int lane, const WaitCtx& wc) {
-  const int cg = (warp - 4) >> 2, t = cg >> 1, quad = warp & 3, r = quad * 32 + lane;
-  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 2 * t * kTileRows + (cg & 1) * 64;
-  float2 acc[32];
+// 32 queries (columns) of one key: acc += 2^(s c - L log2 e). With MASK only
+// columns whose bit is set count.
+template <bool MASK>
+__device__ __forceinline__ void kw_chunk(const uint32_t (&v)[32], const float4* nl, float2 (&acc)[2], float c,
+                                         uint32_t bits = 0) {
+  const float2 c2 = make_float2(c, c);
 #pragma unroll
-  for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
-  auto release = [&](int buf) {  // the buffer and its unit's facts have been read
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.s_free[t][buf]);
-  };
-  int n = 0, flushes = 0;
-  while (units > 0) {
-    const int buf = n & 1;
-    const uint32_t ts = t_lane + buf * kTileRows;
-    if (!mbar_wait_warp(&sh.s_full[t][buf], (n >> 1) & 1, wc)) return;
-    tc_fence_after();
-    int flags = sh.info[buf].flags;
-    float* dst = sh.info[buf].dst;
-    int keys = sh.info[buf].keys;
-    const float2 row = sh.info[buf].row[r];
-    const int plain = 1 << t, kind = 5 << t;  // active, not masked
-    if ((flags & kind) == plain) {
-      uint32_t va[16], vb[16];
-      tmem_ld_32x32b_x16(ts, va);
-      tmem_wait_ld();
-      reg_fence(va);
-      tmem_ld_32x32b_x16(ts + 16, vb);
-      kw_chunk<false>(va, acc, c, row.x, row.y, 0);
-      tmem_wait_ld();
-      reg_fence(vb);
-      tmem_ld_32x32b_x16(ts + 32, va);
-      kw_chunk<false>(vb, acc + 8, c, row.x, row.y, 0);
-      tmem_wait_ld();
-      reg_fence(va);
-      tmem_ld_32x32b_x16(ts + 48, vb);
-      kw_chunk<false>(va, acc + 16, c, row.x, row.y, 0);
-      tmem_wait_ld();
-      reg_fence(vb);
-      release(buf);
-      ++n;
-      --units;
-      if (D == 64 && !(flags & 16)) {
-        // The same item goes on: its next unit's first columns are asked for
-        // before this one's last are worked on, so that every other wait for a
-        // product and for TMEM is hidden. (Always doing so carries loads across
-        // the loop's back edge, which costs spills: twice the time.) Worth it
-        // where the products are short: 214 against 227 us at d = 64, 239
-        // against 237 at d = 128 (B = 2, H = 16, N = 8192, causal).
-        if (!mbar_wait_warp(&sh.s_full[t][buf ^ 1], (n >> 1) & 1, wc)) return;
-        tc_fence_after();
-        const int f1 = sh.info[buf ^ 1].flags;
-        if ((f1 & kind) == plain) {
-          const float2 row1 = sh.info[buf ^ 1].row[r];
-          const uint32_t t1 = t_lane + (buf ^ 1) * kTileRows;
-          tmem_ld_32x32b_x16(t1, va);
-          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+  for (int x = 0; x < 32; x += 4) {
+    const float4 n = nl[x / 4];
+    const float2 s0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+    const float2 s1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+    const float2 e0 = f2_fma(s0, c2, make_float2(n.x, n.y));
+    const float2 e1 = f2_fma(s1, c2, make_float2(n.z, n.w));
+    float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+    float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+    if constexpr (MASK) {
+      p0.x = bits & (1u << x) ? p0.x : 0.f;
+      p0.y = bits & (1u << (x + 1)) ? p0.y : 0.f;
+      p1.x = bits & (1u << (x + 2)) ? p1.x : 0.f;
+      p1.y = bits & (1u << (x + 3)) ? p1.y : 0.f;
+    }
+    acc[0] = f2_add(acc[0], p0);
+    acc[1] = f2_add(acc[1], p1);
+  }
+}
+
+// The compute warps: group (t, j) = tile t, half j of its columns; a thread =
+// one key (TMEM lane).
+template <int D>
+__device__ __forceinline__ void kw_compute(const KeyWeightArgs& a, KwShared<D>& sh, uint32_t tmem, int warp,
+                                           int lane, const WaitCtx& wc) {
+  const int t = ((warp - 4) >> 2) & 1, j = (warp - 4) >> 3, quad = warp & 3, r = quad * 32 + lane;
+  const uint32_t ts = tmem + (static_cast<uint32_t>(quad * 32) << 16) + t * 2 * kTileRows + j * 32;
+  const float c = a.scale_log2;
+  float2 acc[2];
+  acc[0] = acc[1] = make_float2(0.f, 0.f);
+  int done = 0, sums = 0;  // S of this tile, and its sums, so far
+  for (int n = 0, flags = 0; !(flags & 64); ++n) {
+    const int st = n % kKwInfos;
+    if (!mbar_wait_warp(&sh.i_full[st], (n / kKwInfos) & 1, wc)) return;
+    const KwInfo& w = sh.info[st];
+    flags = w.flags;
+    if (flags & (1 << t)) {
+      if (!mbar_wait_warp(&sh.s_full[t], done & 1, wc)) return;
+      ++done;
+      tc_fence_after();
+      auto release = [&]() {  // S has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_free[t]);
+      };
+      uint32_t v[2][32];
+      if ((flags & (32 | 4 << t)) == 32) {
+        tmem_ld_32x32b_x32(ts, v[0]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
           tmem_wait_ld();
-          reg_fence(va);
-          tmem_ld_32x32b_x16(t1 + 16, vb);
-          kw_chunk<false>(va, acc, c, row1.x, row1.y, 0);
-          tmem_wait_ld();
-          reg_fence(vb);
-          tmem_ld_32x32b_x16(t1 + 32, va);
-          kw_chunk<false>(vb, acc + 8, c, row1.x, row1.y, 0);
-          tmem_wait_ld();
-          reg_fence(va);
-          tmem_ld_32x32b_x16(t1 + 48, vb);
-          kw_chunk<false>(va, acc + 16, c, row1.x, row1.y, 0);
-          tmem_wait_ld();
-          reg_fence(vb);
-          flags = f1;
-          dst = sh.info[buf ^ 1].dst;
-          keys = sh.info[buf ^ 1].keys;
-          release(buf ^ 1);
-          kw_chunk<false>(vb, acc + 24, c, row1.x, row1.y, 0);
-          ++n;
-          --units;
-        } else {
-          kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
+          reg_fence(v[m & 1]);
+          if (m < 3) tmem_ld_32x32b_x32(ts + (m + 1) * 64, v[(m + 1) & 1]);
+          else release();
+          kw_chunk<false>(v[m & 1], w.nl + (2 * m + j) * 8, acc, c);
         }
       } else {
-        kw_chunk<false>(vb, acc + 24, c, row.x, row.y, 0);
-      }
-    } else {
-      if (flags & plain) {
-        // Visible keys of this row, from the group's first one.
-        const int lim = r < sh.info[buf].rows ? sh.info[buf].d0 + r - cg * 64 + 1 : 0;
-#pragma unroll
-        for (int x = 0; x < 64; x += 16) {
-          if (__all_sync(0xffffffffu, lim <= x)) break;  // the warp's rows see none of the rest
-          uint32_t va[16];
-          tmem_ld_32x32b_x16(ts + x, va);
+        // Columns that this key's sum takes: queries from the key on (causal)
+        // and below the sequence's end. A warp's diagonal lies in one chunk.
+        const int first = t * kTileRows + quad * 32 - w.d0, hi = min(w.rows, flags & 32 ? 256 : 128);
+        const int m0 = first <= 0 ? 0 : (first / 32 - j + 1) >> 1, m1 = ((hi + 31) / 32 - j + 1) >> 1;
+        if (m0 >= m1) release();
+#pragma unroll 1
+        for (int m = m0; m < m1; ++m) {
+          const int x = (2 * m + j) * 32;
+          tmem_ld_32x32b_x32(ts + m * 64, v[0]);
           tmem_wait_ld();
-          reg_fence(va);
-          kw_chunk<true>(va, acc + x / 2, c, row.x, row.y, lim - x);
+          reg_fence(v[0]);
+          if (m + 1 == m1) release();
+          const uint32_t bits = (x > first ? ~0u : ~0u << lane) & (x + 32 <= hi ? ~0u : ~(~0u << (hi - x)));
+          if (x > first && x + 32 <= hi) kw_chunk<false>(v[0], w.nl + x / 4, acc, c);
+          else kw_chunk<true>(v[0], w.nl + x / 4, acc, c, bits);
         }
       }
-      release(buf);
-      ++n;
-      --units;
     }
     if (flags & 16) {
-      // Sums over the warp's 32 rows by halving: lane l ends with keys 2 l and
-      // 2 l + 1; the group's first warp adds the four warps' in order.
-#pragma unroll
-      for (int o = 16, m = 16; o > 0; o >>= 1, m >>= 1) {
-#pragma unroll
-        for (int x = 0; x < m; ++x) {
-          const bool up = lane & o;
-          const float2 keep = up ? acc[x + m] : acc[x], give = up ? acc[x] : acc[x + m];
-          acc[x] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, give.x, o),
-                               keep.y + __shfl_xor_sync(0xffffffffu, give.y, o));
-        }
-      }
-      if (quad > 0) {
-        if (flushes > 0 && !mbar_wait_warp(&sh.sum_free[cg], (flushes - 1) & 1, wc)) return;
-        sh.sums[cg][quad - 1][lane] = acc[0];
+      const int key = t * kTileRows + r;
+      const float2 x = f2_add(acc[0], acc[1]);
+      if (j == 1) {
+        if (sums > 0 && !mbar_wait_warp(&sh.sum_free[t], (sums - 1) & 1, wc)) return;
+        sh.sum[t][r] = x.x + x.y;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.sum_full[cg]);
+        if (lane == 0) mbar_arrive(&sh.sum_full[t]);
       } else {
-        if (!mbar_wait_warp(&sh.sum_full[cg], flushes & 1, wc)) return;
-        float2 sum = acc[0];
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          const float2 y = sh.sums[cg][x][lane];
-          sum = make_float2(sum.x + y.x, sum.y + y.y);
-        }
+        if (!mbar_wait_warp(&sh.sum_full[t], sums & 1, wc)) return;
+        if (key < w.keys) w.dst[key] = x.x + x.y + sh.sum[t][r];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.sum_free[cg]);
-        const int key = cg * 64 + 2 * lane;
-        if (key < keys) dst[key] = sum.x;
-        if (key + 1 < keys) dst[key + 1] = sum.y;
+        if (lane == 0) mbar_arrive(&sh.sum_free[t]);
       }
-      ++flushes;
-#pragma unroll
-      for (int x = 0; x < 32; ++x) acc[x] = make_float2(0.f, 0.f);
+      ++sums;
+      acc[0] = acc[1] = make_float2(0.f, 0.f);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.i_free[st]);
   }
 }
 
@@ -386,33 +348,35 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   __shared__ KwShared<D> sh;
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Barriers are set up by one lane of three warps, TMEM by a fourth, while the
-  // others already look for their first unit.
+  // Barriers are set up by one lane of three warps, TMEM by a fourth, while all
+  // of the control warps look for their first unit.
   if (lane == 0) {
     if (warp == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&sh.k_full[t], 1);
+        mbar_init(&sh.k_free[t], 1);
+      }
       for (int i = 0; i < C::NQ; ++i) {
         mbar_init(&sh.q_full[i], 1);
-        mbar_init(&sh.q_free[i], 1);
+        mbar_init(&sh.q_free[i], 2);
       }
       sh.abort_flag = 0;
       fence_mbar_init();
     } else if (warp == 2) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sh.k_full[i], 1);
-        mbar_init(&sh.k_free[i], 1);
-        for (int t = 0; t < 2; ++t) {
-          mbar_init(&sh.s_full[t][i], 2);  // the product and the unit's facts
-          mbar_init(&sh.s_free[t][i], 8);  // one arrival per compute warp of the tile
-        }
+      for (int i = 0; i < kKwInfos; ++i) {
+        mbar_init(&sh.i_full[i], 1);
+        mbar_init(&sh.i_free[i], 16);  // one arrival per compute warp
       }
-      mbar_init(&sh.mma_done, 1);
       fence_mbar_init();
     } else if (warp == 3) {
-      for (int i = 0; i < 4; ++i) {
-        mbar_init(&sh.sum_full[i], 3);
-        mbar_init(&sh.sum_free[i], 1);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&sh.s_full[t], 1);
+        mbar_init(&sh.mma_done[t], 1);
+        mbar_init(&sh.s_free[t], 8);  // one arrival per compute warp of the tile
+        mbar_init(&sh.sum_full[t], 4);
+        mbar_init(&sh.sum_free[t], 4);
       }
       fence_mbar_init();
     }
@@ -435,117 +399,115 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   const WaitCtx wc{a.status, &sh.abort_flag, a.timeout_ns};
 
   if (warp < 4) {
-    // 4 x 32 x 64 + 16 x 32 x 104 = 61,440 = the launch's 640 x 96 registers.
-    setmaxnreg_dec<64>();
     if (warp == 0 && lane == 0 && u0 < u1) {
-      // Producer: the Q tiles of the units, K of each item before its first.
-      int items = 0, qs = 0, qph = 0, used = 0;
+      // Producer: the query tiles of the steps, K of each item before its first.
+      int items = 0, qs = 0, qph = 0, used = 0, loads[2] = {0, 0};
       bool ok = true, fresh = true;
-      for (long long u = u0; u < u1 && ok; ++u) {
-        if (fresh) {
-          const int kb = items & 1;
-          if (items > 1) ok = mbar_wait(&sh.k_free[kb], ((items >> 1) - 1) & 1, wc);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&sh.k_full[kb], 2 * C::TILE);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            load_tile<D>(smem + C::OFF_K + (2 * kb + t) * C::TILE, &tm_k, &sh.k_full[kb],
-                         cu.kb * kKwKeys + t * kTileRows, cu.b * a.Hkv + cu.h);
-          ++items;
-        }
+      while (cu.at < u1 && ok) {
+        const int cnt = kw_step(cu, u1 - cu.at);
         if (used >= C::NQ) ok = mbar_wait(&sh.q_free[qs], qph ^ 1, wc);
         if (!ok) break;
-        if (a.fault == 0 || u > u0) {
-          mbar_arrive_expect_tx(&sh.q_full[qs], C::TILE);
-          load_tile<D>(smem + C::OFF_Q + qs * C::TILE, &tm_q, &sh.q_full[qs], cu.i * kTileRows,
-                       cu.b * a.Hq + cu.h * a.g + cu.gh);
+        if (a.fault == 0 || used > 0) {
+          mbar_arrive_expect_tx(&sh.q_full[qs], cnt * C::TILE);
+          for (int j = 0; j < cnt; ++j)
+#pragma unroll
+            for (int sl = 0; sl < D / 64; ++sl)
+              tma_load_3d(smem + C::OFF_Q + qs * 2 * C::TILE + (2 * sl + j) * (kTileRows * 128), &tm_q, &sh.q_full[qs],
+                          sl * 64, (cu.i + j) * kTileRows, cu.b * a.Hq + cu.h * a.g + cu.gh);
         }
         ++used;
         if (++qs == C::NQ) {
           qs = 0;
           qph ^= 1;
         }
-        fresh = kw_advance(a, s, cu);
+        if (fresh) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (items > 0 && ok) ok = mbar_wait(&sh.k_free[t], (items - 1) & 1, wc);
+            if (!ok) continue;
+            mbar_arrive_expect_tx(&sh.k_full[t], C::TILE);
+            load_tile<D>(smem + C::OFF_K + t * C::TILE, &tm_k, &sh.k_full[t], cu.kb * kKwKeys + t * kTileRows,
+                         cu.b * a.Hkv + cu.h);
+            ++loads[t];
+          }
+          ++items;
+        }
+        fresh = kw_advance_step(a, s, cu, cnt);
       }
       if (!ok) {  // copies in flight land before the CTA ends
-        for (int x = 0; x < 2; ++x) {
-          const int uses = (items + 1 - x) / 2;
-          if (uses > 0) mbar_wait_drain(&sh.k_full[x], (uses - 1) & 1, a.timeout_ns);
-        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (loads[t] > 0) mbar_wait_drain(&sh.k_full[t], (loads[t] - 1) & 1, a.timeout_ns);
         for (int x = 0; x < C::NQ; ++x) {
           const int uses = used / C::NQ + (x < used % C::NQ ? 1 : 0);
           if (uses > 0) mbar_wait_drain(&sh.q_full[x], (uses - 1) & 1, a.timeout_ns);
         }
       }
-    } else if (warp == 1 && u0 < u1) {
-      // Issuer: S of unit n into buffer n % 2.
-      int items = 0, qs = 0, qph = 0, n = 0;
-      bool ok = true, fresh = true;
-      const uint32_t k_base = smem_u32(smem + C::OFF_K), q_base = smem_u32(smem + C::OFF_Q);
-      for (long long u = u0; u < u1; ++u, ++n) {
-        if (fresh) {
-          ok = mbar_wait_warp(&sh.k_full[items & 1], (items >> 1) & 1, wc);
-          if (!ok) break;
-          ++items;
+    } else if ((warp & 1) && u0 < u1) {
+      // Issuers: S^T of tile A by warp 1, of tile B by warp 3. While the groups
+      // of one tile work the tensor core forms the other's.
+      const int t = warp >> 1;
+      int items = 0, qs = 0, qph = 0, done = 0;
+      bool fresh = true;
+      const uint32_t k = smem_u32(smem + C::OFF_K) + t * C::TILE, acc = tmem + t * 2 * kTileRows;
+      while (cu.at < u1) {
+        const int cnt = kw_step(cu, u1 - cu.at);
+        if (!mbar_wait_warp(&sh.q_full[qs], qph, wc)) break;
+        if (fresh && !mbar_wait_warp(&sh.k_full[t], items++ & 1, wc)) break;
+        const uint32_t q = smem_u32(smem + C::OFF_Q) + qs * 2 * C::TILE;
+        if (kw_active(a, s, cu, cnt, t)) {
+          if (done > 0 && !mbar_wait_warp(&sh.s_free[t], (done - 1) & 1, wc)) break;
+          tc_fence_after();
+          if (cnt == 1) kw_issue<D, BF16, 128>(acc, k, q);
+          else if (!kw_active(a, s, cu, 1, t)) kw_issue<D, BF16, 128>(acc + kTileRows, k, q + kTileRows * 128);
+          else kw_issue<D, BF16, 256>(acc, k, q);
+          umma_commit_warp(&sh.s_full[t]);
+          ++done;
         }
-        const int buf = n & 1, kb = (items - 1) & 1;
-        ok = mbar_wait_warp(&sh.q_full[qs], qph, wc);
-        const bool act_b = kw_active(a, s, cu, 1);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (ok && n > 1) ok = mbar_wait_warp(&sh.s_free[t][buf], ((n >> 1) - 1) & 1, wc);
-          if (!ok) break;
-          if (t == 0 || act_b) {
-            tc_fence_after();
-            mma_rows_x_rows<D, BF16>(tmem + (2 * t + buf) * kTileRows, q_base + qs * C::TILE,
-                                     k_base + (2 * kb + t) * C::TILE);
-            umma_commit_warp(&sh.s_full[t][buf]);
-          } else if (lane == 0) {
-            mbar_arrive(&sh.s_full[t][buf]);
-          }
-        }
-        if (!ok) break;
         umma_commit_warp(&sh.q_free[qs]);
+        if (cu.to_end == cnt) umma_commit_warp(&sh.k_free[t]);
         if (++qs == C::NQ) {
           qs = 0;
           qph ^= 1;
         }
-        fresh = kw_advance(a, s, cu);
-        if (fresh) umma_commit_warp(&sh.k_free[kb]);
+        fresh = kw_advance_step(a, s, cu, cnt);
       }
-      umma_commit_warp(&sh.mma_done);
-      mbar_wait_drain(&sh.mma_done, 0, a.timeout_ns);
+      umma_commit_warp(&sh.mma_done[t]);
+      mbar_wait_drain(&sh.mma_done[t], 0, a.timeout_ns);
     } else if (warp == 2 && u0 < u1) {
       int n = 0;
       bool from_start = cu.to_end == static_cast<long long>(cu.nq - s.i0(cu.kb)) * s.g;
-      for (long long u = u0; u < u1; ++u, ++n) {
+      for (; cu.at < u1; ++n) {
+        const int cnt = kw_step(cu, u1 - cu.at);
         const float* lse = a.lse + (static_cast<size_t>(cu.b) * a.Hq + static_cast<size_t>(cu.h) * a.g + cu.gh) * a.N;
         const int q0 = cu.i * kTileRows;
-        float2 row[4];
+        float4 nl[2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int q = q0 + x * 32 + lane;
-          const float l = q < cu.qlen ? __ldg(lse + q) : 0.f;
-          // 2^(s c - L log2 e) with the integer part of L log2 e in the exponent
-          // and the rest as a factor: neither is rounded against the large
-          // exponents of s and L.
-          const float hi = l * kLog2e;
-          const float lo = fmaf(l, kLog2e, -hi) + l * kLog2eRest;
-          const float whole = rintf(hi);
-          // L = +inf: no weight (2^-inf), as in e^(s - L).
-          row[x] = make_float2(-whole, isinf(hi) ? 1.f : ex2_approx(-((hi - whole) + lo)));
+        for (int x = 0; x < 2; ++x) {
+          float l[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int q = q0 + x * kTileRows + lane * 4 + y;
+            l[y] = x < cnt && q < cu.qlen ? __ldg(lse + q) : 0.f;
+          }
+          nl[x] = make_float4(-l[0] * kLog2e, -l[1] * kLog2e, -l[2] * kLog2e, -l[3] * kLog2e);
         }
-        const int buf = n & 1, par = ((n >> 1) - 1) & 1;
-        if (n > 1 && !mbar_wait2_warp(&sh.s_free[0][buf], par, &sh.s_free[1][buf], par, wc)) break;
-        KwInfo& w = sh.info[buf];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) w.row[x * 32 + lane] = row[x];
+        const int st = n % kKwInfos;
+        if (n >= kKwInfos && !mbar_wait_warp(&sh.i_free[st], (n / kKwInfos - 1) & 1, wc)) break;
+        KwInfo& w = sh.info[st];
+        w.nl[lane] = nl[0];
+        w.nl[32 + lane] = nl[1];
         if (lane == 0) {
-          const bool item_end = cu.to_end == 1, flush = item_end || u + 1 == u1;
-          const bool tail = q0 + kTileRows > cu.qlen;
-          w.flags = 1 | (kw_active(a, s, cu, 1) ? 2 : 0) | (tail || (s.causal && cu.i == 2 * cu.kb) ? 4 : 0) |
-                    (tail || (s.causal && cu.i == 2 * cu.kb + 1) ? 8 : 0) | (flush ? 16 : 0);
-          w.d0 = s.causal ? q0 - cu.kb * kKwKeys : 2 * kKwKeys;
+          const bool item_end = cu.to_end == cnt, last = cu.at + cnt == u1;
+          const bool tail = q0 + cnt * kTileRows > cu.qlen;
+          int flags = (item_end || last ? 16 : 0) | (cnt == 2 ? 32 : 0) | (last ? 64 : 0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (kw_active(a, s, cu, cnt, t)) flags |= 1 << t;
+            if (tail || (s.causal && cu.i <= 2 * cu.kb + t)) flags |= 4 << t;
+          }
+          w.flags = flags;
+          w.d0 = s.causal ? q0 - cu.kb * kKwKeys : 2 * kKwKeys;  // a multiple of 32
           w.rows = cu.qlen - q0;
           if (from_start && item_end) {
             w.dst = a.out + (static_cast<size_t>(cu.b) * a.Hkv + cu.h) * a.Nk + cu.kb * kKwKeys;
@@ -556,15 +518,12 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
         __syncwarp();
-        if (lane < 2) mbar_arrive(&sh.s_full[lane][buf]);
-        if (kw_advance(a, s, cu)) from_start = true;
+        if (lane == 0) mbar_arrive(&sh.i_full[st]);
+        if (kw_advance_step(a, s, cu, cnt)) from_start = true;
       }
     }
-  } else if (u0 < u1) {
-    setmaxnreg_inc<104>();
-    kw_compute<D>(sh, tmem, a.scale_log2, u1 - u0, warp, lane, wc);
   } else {
-    setmaxnreg_inc<104>();
+    if (u0 < u1) kw_compute<D>(a, sh, tmem, warp, lane, wc);
   }
   __syncwarp();
   tc_fence_before();
