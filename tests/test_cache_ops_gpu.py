@@ -143,6 +143,24 @@ def test_evict(cuda_device, fa2_lib, B, Hkv, d, ps, lens, budget, recent, kind):
     _check_evict(fa2_lib, c, w, pos, budget, recent, in_place=seed % 2 == 0, with_pos=kind != "ties")
 
 
+@pytest.mark.parametrize("n", [300, 5000, 20000])
+@pytest.mark.parametrize("digit", range(4))
+@pytest.mark.parametrize("extra", [-1, 0, 1])
+def test_evict_at_a_digit_border(cuda_device, fa2_lib, n, digit, extra):
+    """A budget at, or one off, the number of weights above the border of the
+    keys' `digit`-th byte: 120 of them, the others below it."""
+    high, low = ((0x3F000000, 0x3E000000), (0x3F800000, 0x3F7F0000), (0x3F808000, 0x3F807F00),
+                 (0x3F808001, 0x3F808000))[digit]
+    c, w, pos = _evict_case(1, 2, 64, 16, [n], BF16, digit, "plain")
+    free = 8 * (3 - digit)
+    bits = torch.randint(0, 1 << free, w.shape, generator=c.g, dtype=torch.int32)
+    for h in range(2):
+        top = torch.zeros(c.L, dtype=torch.bool)
+        top[torch.randperm(n, generator=c.g)[:120]] = True
+        bits[0, h] += torch.where(top, high, low).to(torch.int32)
+    _check_evict(fa2_lib, c, bits.view(torch.float32), pos, 120 + extra, 0, in_place=False, with_pos=True)
+
+
 def test_evict_in_place_is_evict_out_of_place(cuda_device, fa2_lib):
     c, w, pos = _evict_case(2, 2, 64, 16, [900, 600], BF16, 5, "plain")
     _check_evict(fa2_lib, c, w, pos, 500, 50, in_place=True, with_pos=True)
