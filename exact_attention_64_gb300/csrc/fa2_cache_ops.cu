@@ -12,7 +12,7 @@ namespace fa2 {
 // flight together, took 90, 128 and 207 us and 3.4, 4.4 and 6.5 us.
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -23,6 +23,7 @@ template <int D>
 __global__ void __launch_bounds__(kAppendThreads) fa2_cache_append_kernel(const AppendArgs a) {
   constexpr int CH = D / 8;                 // 16-byte chunks of a row
   constexpr int ROWS = kAppendThreads / CH;  // rows per CTA
+  grid_dependency_wait();
   const CacheView& c = a.c;
   const int ch = threadIdx.x % CH;
   const long long r = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / CH;
@@ -31,16 +32,16 @@ __global__ void __launch_bounds__(kAppendThreads) fa2_cache_append_kernel(const 
   if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < c.B; b += kAppendThreads) {
       const int n = seq_len(c, b);
-      const int want = a.num_new != nullptr ? __ldg(a.num_new + b) : a.T;
+      const int want = a.num_new != nullptr ? ld_global(a.num_new + b) : a.T;
       const int cnt = cut_len(want, a.T);
-      if (n != __ldg(c.lens + b) || cnt != want || n > c.L - cnt) report_page(c.status);
+      if (n != ld_global(c.lens + b) || cnt != want || n > c.L - cnt) report_page(c.status);
       a.lens_out[b] = n > c.L - cnt ? c.L : n + cnt;
     }
   }
   if (r >= a.rows) return;
   const int rr = static_cast<int>(r), bh = div_by(rr, a.fT), i = rr - bh * a.T;
   const int b = div_by(bh, a.fH), h = bh - b * c.Hkv;
-  const int cnt = a.num_new != nullptr ? __ldg(a.num_new + b) : a.T;
+  const int cnt = a.num_new != nullptr ? ld_global(a.num_new + b) : a.T;
   const int slot = seq_len(c, b) + i;
   if (i >= cnt || slot >= c.L) return;  // padding, or no room in the table
   const uint4 kx = ld_once(reinterpret_cast<const uint4*>(a.k + static_cast<size_t>(rr) * D) + ch);
@@ -54,18 +55,15 @@ __global__ void __launch_bounds__(kAppendThreads) fa2_cache_append_kernel(const 
   reinterpret_cast<uint4*>(a.vc + static_cast<size_t>(row) * D)[ch] = vx;
   if (ch != 0) return;
   const size_t at = static_cast<size_t>(bh) * c.L + slot;
-  if (a.weights != nullptr) a.weights[at] = a.new_weights != nullptr ? __ldg(a.new_weights + rr) : 0.f;
-  if (a.positions != nullptr) a.positions[at] = __ldg(a.next_pos + b) + i;
+  if (a.weights != nullptr) a.weights[at] = a.new_weights != nullptr ? ld_global(a.new_weights + rr) : 0.f;
+  if (a.positions != nullptr) a.positions[at] = ld_global(a.next_pos + b) + i;
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
   const int per = kAppendThreads / (a.d / 8);
   const long long grid = (a.rows + per - 1) / per;
-  if (a.d == 64)
-    fa2_cache_append_kernel<64><<<static_cast<unsigned>(grid), kAppendThreads, 0, stream>>>(a);
-  else
-    fa2_cache_append_kernel<128><<<static_cast<unsigned>(grid), kAppendThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(a.d == 64 ? fa2_cache_append_kernel<64> : fa2_cache_append_kernel<128>,
+                          dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0, stream, a);
 }
 
 // ---- Eviction --------------------------------------------------------------
@@ -197,6 +195,7 @@ template <int D, bool REG>
 __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const EvictArgs a, int C) {
   extern __shared__ uint32_t s_keys[];
   __shared__ EvictShared sh;
+  grid_dependency_wait();
   grid_launch_dependents();
   const CacheView& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
   const bool copy_w = a.w_out != a.w_in, copy_p = p_in != nullptr && a.p_out != a.p_in;
   if (rank == 0 && tid == 0) {
     if (h == 0) {
-      if (n != __ldg(c.lens + b)) report_page(c.status);
+      if (n != ld_global(c.lens + b)) report_page(c.status);
       a.lens_out[b] = k;
     }
     if (n <= a.budget) a.counts[item] = 0;
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kEvictThreads) fa2_cache_evict_kernel(const Ev
   const int j0 = min(n, rank * run * kEvictWarps), j1 = min(n, j0 + run * kEvictWarps);
   const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
   const long long first_recent =
-      p_in != nullptr ? static_cast<long long>(__ldg(a.next_pos + b)) - a.recent : 0;
+      p_in != nullptr ? static_cast<long long>(ld_global(a.next_pos + b)) - a.recent : 0;
   auto key_of = [&](int j, float w, int pos) -> uint32_t {
     // Without positions the slots are in the order of their tokens.
     const bool is_recent = p_in != nullptr ? pos >= first_recent : j >= n - a.recent;
@@ -505,13 +504,15 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   cfg.blockDim = dim3(kEvictThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = C;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a, C);
   if (e != cudaSuccess || a.list <= kInlineMoves) return e;
   constexpr int per_cta = kMoveThreads / 32 * kMovesPerWarp;

@@ -59,7 +59,7 @@ struct KwShape {
 
 __device__ __forceinline__ int kw_qlen(const KeyWeightArgs& a, int b) {
   if (a.q_lens == nullptr) return a.N;
-  return min(max(__ldg(a.q_lens + b), 0), a.N);
+  return min(max(ld_global(a.q_lens + b), 0), a.N);
 }
 __device__ __forceinline__ int kw_tiles(int n) { return (n + kTileRows - 1) / kTileRows; }
 
@@ -346,7 +346,6 @@ __global__ void __launch_bounds__(kKwThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   __shared__ KwShared<D> sh;
-  grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Barriers are set up by one lane of three warps, TMEM by a fourth, while all
   // of the control warps look for their first unit.
@@ -382,6 +381,8 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     }
   }
   __syncwarp();
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (warp == 1) {
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int q = q0 + x * kTileRows + lane * 4 + y;
-            l[y] = x < cnt && q < cu.qlen ? __ldg(lse + q) : 0.f;
+            l[y] = x < cnt && q < cu.qlen ? ld_global(lse + q) : 0.f;
           }
           nl[x] = make_float4(-l[0] * kLog2e, -l[1] * kLog2e, -l[2] * kLog2e, -l[3] * kLog2e);
         }
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(kKwKeys) fa2_key_weights_join_kernel(const Key
   const long long G = T < ctas ? T : ctas;
   const long long before = kw_before(a, s, b, lane);
   grid_dependency_wait();
+  grid_launch_dependents();
   const int key = kb * kKwKeys + threadIdx.x;
   float* dst = a.out + static_cast<size_t>(bh) * a.Nk + key;
   const long long n = s.before(kb + 1, nq) - s.before(kb, nq);
@@ -569,8 +571,7 @@ static cudaError_t launch_key_weights_t(const CUtensorMap& tq, const CUtensorMap
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, KwCfg<D>::SMEM, done);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kKwThreads, KwCfg<D>::SMEM, stream>>>(tq, tk, a, s);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3(ctas), dim3(kKwThreads), KwCfg<D>::SMEM, stream, tq, tk, a, s);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_key_weights_join_kernel, dim3(static_cast<unsigned>(a.B * a.Hkv) * a.nkb),
                           dim3(kKwKeys), 0, stream, a, s, ctas);

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
+  grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   const int cta = blockIdx.x;
   if (cta == 0 && warp == 0)
     for (int b = lane; b < c.B; b += 32)
-      if (__ldg(c.lens + b) != seq_len(c, b)) report_page(c.status);
+      if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
   if (cta >= G) return;
   const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
   UnitCursor cc = map.at(u0);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     if (in) {
       const int p = div_by(slot, c.ps);
       off = slot - p * c.ps.d;
-      pg = __ldg(c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
+      pg = ld_global(c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
     }
   };
   auto copy_next = [&](int st) {
@@ -281,8 +282,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
             a.q + (static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + (hd < a.g ? hd : 0)) * D);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qf[nt][kk][0] = hd < a.g ? __ldg(qp + kk * 8 + t) : 0u;
-          qf[nt][kk][1] = hd < a.g ? __ldg(qp + kk * 8 + 4 + t) : 0u;
+          qf[nt][kk][0] = hd < a.g ? ld_global(qp + kk * 8 + t) : 0u;
+          qf[nt][kk][1] = hd < a.g ? ld_global(qp + kk * 8 + 4 + t) : 0u;
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
@@ -726,8 +727,7 @@ static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) 
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kDecWarps * 32, C::SMEM, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3(ctas), dim3(kDecWarps * 32), C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas * a.join_split),
                           dim3(kJoinThreads), 0, stream, a);
