@@ -150,6 +150,7 @@ struct DecodeArgs {
   int Hq, g;              // query heads; query heads per key head
   int HG;                 // head tiles per key head
   int join_split;         // blocks of the join per CTA of the decode
+  int whole;              // a CTA has one whole item, and there is no join
   float scale_log2;       // scale * log2(e)
 };
 

@@ -9,7 +9,10 @@
 // is bytes in flight and an even share of the cache for every SM whatever the
 // lengths; the arithmetic only has to stay out of the way.
 //
-// Split. The cache's slots are cut into units of 64 (sequence, then key head,
+// Short tables (see the rule at the launch): a CTA has one item, the slots of one
+// (sequence, key head), and there is nothing to join and no second launch.
+//
+// Split, for all others. The cache's slots are cut into units of 64 (sequence, then key head,
 // then slot) and CTA c of G takes units [c T / G, (c+1) T / G) of the T units
 // that the lengths in device memory amount to: every CTA reads the same share
 // of the cache, with one long sequence or many uneven ones, and the same launch
@@ -179,6 +182,49 @@ __device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
   return static_cast<int>(div_pos((u + 1) * G - 1, T));
 }
 
+// w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
+// slot are read at a time.
+template <int THREADS, int VEC>
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, int j0, int j1, const float* s_lse) {
+  constexpr int U = 4;  // slots per thread in flight
+  const int g = a.g;
+  for (int j = j0 + threadIdx.x; j < j1; j += U * THREADS) {
+    float w[U], add[U];
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int jj = j + y * THREADS;
+      w[y] = jj < j1 ? a.w_in[base + jj] : 0.f;
+      add[y] = 0.f;
+    }
+    for (int hd = 0; hd < g; hd += VEC) {
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        const int jj = j + y * THREADS;
+        if (jj >= j1) continue;
+        const float* lg = a.logits + (base + jj) * g + hd;
+        float x[VEC];
+        if constexpr (VEC == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(lg);
+        else if constexpr (VEC == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(lg);
+        else x[0] = *lg;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) add[y] += x[e] == -INFINITY ? 0.f : ex2_approx(x[e] - s_lse[hd + e]);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int jj = j + y * THREADS;
+      if (jj < j1) a.w_out[base + jj] = w[y] + add[y];
+    }
+  }
+}
+
+template <int THREADS>
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, int j0, int j1, const float* s_lse) {
+  if (a.g % 4 == 0) add_weights<THREADS, 4>(a, base, j0, j1, s_lse);
+  else if (a.g % 2 == 0) add_weights<THREADS, 2>(a, base, j0, j1, s_lse);
+  else add_weights<THREADS, 1>(a, base, j0, j1, s_lse);
+}
+
 template <int D, int NT>
 struct DecCfg {
   static constexpr int ROW = D * 2;                        // bytes of a row
@@ -198,21 +244,41 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
+  __shared__ float s_lse[C::HEADS];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const UnitMap<D> map(c, HH, lane);
-  const long long T = map.T;
-  const long long G = min(static_cast<long long>(gridDim.x), T);
   const int cta = blockIdx.x;
-  if (cta == 0 && warp == 0)
-    for (int b = lane; b < c.B; b += 32)
-      if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
-  if (cta >= G) return;
-  const long long u0 = unit_begin(cta, G, T), u1 = unit_begin(cta + 1, G, T);
-  UnitCursor cc = map.at(u0);
+  long long u0 = 0, u1 = 0;
+  UnitCursor cc{};
+  if (a.whole) {
+    cc.b = cta / HH;
+    cc.hh = cta - cc.b * HH;
+    cc.n = seq_len(c, cc.b);
+    u1 = cc.ntiles = tiles_of<D>(cc.n);
+    if (cc.hh == 0 && threadIdx.x == 0 && ld_global(c.lens + cc.b) != cc.n) report_page(c.status);
+    if (cc.n == 0) {  // no token: o = 0, L = -inf
+      const int h = cc.hh / a.HG, head0 = (cc.hh - h * a.HG) * C::HEADS;
+      const size_t row = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + head0;
+      const int heads = min(C::HEADS, a.g - head0);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D);
+      for (int x = threadIdx.x; x < heads * D / 2; x += kDecWarps * 32) dst[x] = 0u;
+      if (threadIdx.x < heads) a.lse[row + threadIdx.x] = -INFINITY;
+      return;
+    }
+  } else {
+    const UnitMap<D> map(c, HH, lane);
+    const long long T = map.T, G = min(static_cast<long long>(gridDim.x), T);
+    if (cta == 0 && warp == 0)
+      for (int b = lane; b < c.B; b += 32)
+        if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
+    if (cta >= G) return;
+    u0 = unit_begin(cta, G, T);
+    u1 = unit_begin(cta + 1, G, T);
+    cc = map.at(u0);
+  }
   UnitCursor ic = cc;  // next unit to copy
   const uint64_t pol = read_once_policy();
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
@@ -269,6 +335,22 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   float m[NT][2], l[NT][2];
   int st = 0;
   const int t = lane & 3, r8 = lane >> 2;
+  auto load_q = [&](const UnitCursor& k) {
+    const int h = a.HG == 1 ? k.hh : k.hh / a.HG;
+    const int head0 = (k.hh - h * a.HG) * C::HEADS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int hd = head0 + nt * 8 + r8;
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(
+          a.q + (static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + (hd < a.g ? hd : 0)) * D);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[nt][kk][0] = hd < a.g ? ld_global(qp + kk * 8 + t) : 0u;
+        qf[nt][kk][1] = hd < a.g ? ld_global(qp + kk * 8 + 4 + t) : 0u;
+      }
+    }
+  };
+  load_q(cc);
 #pragma unroll 1
   for (long long u = u0; u < u1; ++u) {
     const bool first = u == u0 || cc.tile == 0;
@@ -277,14 +359,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     if (first) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int hd = head0 + nt * 8 + r8;
-        const uint32_t* qp = reinterpret_cast<const uint32_t*>(
-            a.q + (static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + (hd < a.g ? hd : 0)) * D);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          qf[nt][kk][0] = hd < a.g ? ld_global(qp + kk * 8 + t) : 0u;
-          qf[nt][kk][1] = hd < a.g ? ld_global(qp + kk * 8 + 4 + t) : 0u;
-        }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
 #pragma unroll
@@ -405,7 +479,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     st = st + 1 == C::STAGES ? 0 : st + 1;
 
     if (u + 1 == u1 || cc.tile + 1 == cc.ntiles) {
-      // End of a segment: the four warps' (m, l, O) are merged.
+      // End of a segment: the four warps' (m, l, O) are merged, while the next
+      // one's queries are on their way.
+      UnitCursor next = cc;
+      unit_advance<D>(c, HH, next);
+      if (u + 1 < u1) load_q(next);
       const bool from_start = cc.tile - (u - u0) <= 0;  // the segment begins with its item
       const bool whole = from_start && cc.tile + 1 == cc.ntiles;
       const int slot = 2 * cta + (from_start ? 1 : 0);
@@ -458,7 +536,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
             uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + row * D + e0);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) dst[x] = pack_x2<BF16>(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-            if (e0 == 0) a.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+            if (e0 == 0) {
+              const float lse = S == 0.f ? -INFINITY : M + log2f(S);
+              a.lse[row] = lse * kLn2f;
+              if constexpr (WEIGHTS) s_lse[nt * 8 + hd] = lse;
+            }
           } else {
             float4* dst = reinterpret_cast<float4*>(
                 a.part_o + (static_cast<size_t>(slot) * C::HEADS + nt * 8 + hd) * D + e0);
@@ -472,6 +554,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       }
     }
     unit_advance<D>(c, HH, cc);
+  }
+  if constexpr (WEIGHTS) {
+    if (a.whole) {  // a key head is one item: its weights from the logits that this CTA wrote
+      const int hh = cta % HH, b = cta / HH;
+      add_weights<kDecWarps * 32>(a, (static_cast<size_t>(b) * c.Hkv + hh) * c.L, 0, seq_len(c, b), s_lse);
+    }
   }
 }
 
@@ -520,42 +608,6 @@ __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 2;
 constexpr int kJoinUnits = 8;
-
-// w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
-// slot are read at a time.
-template <int VEC>
-__device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, int j0, int j1, const float* s_lse) {
-  constexpr int U = 4;  // slots per thread in flight
-  const int g = a.g;
-  for (int j = j0 + threadIdx.x; j < j1; j += U * kJoinThreads) {
-    float w[U], add[U];
-#pragma unroll
-    for (int y = 0; y < U; ++y) {
-      const int jj = j + y * kJoinThreads;
-      w[y] = jj < j1 ? a.w_in[base + jj] : 0.f;
-      add[y] = 0.f;
-    }
-    for (int hd = 0; hd < g; hd += VEC) {
-#pragma unroll
-      for (int y = 0; y < U; ++y) {
-        const int jj = j + y * kJoinThreads;
-        if (jj >= j1) continue;
-        const float* lg = a.logits + (base + jj) * g + hd;
-        float x[VEC];
-        if constexpr (VEC == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(lg);
-        else if constexpr (VEC == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(lg);
-        else x[0] = *lg;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) add[y] += x[e] == -INFINITY ? 0.f : ex2_approx(x[e] - s_lse[hd + e]);
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < U; ++y) {
-      const int jj = j + y * kJoinThreads;
-      if (jj < j1) a.w_out[base + jj] = w[y] + add[y];
-    }
-  }
-}
 
 // O and L of the heads of one cut item, by block `sub` of `subs` of CTA `cta`.
 // Pieces of 32 elements of a head are dealt to the blocks of all its parts.
@@ -624,6 +676,66 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
   __syncthreads();
 }
 
+// A piece of 32 elements of one head of an item with few parts, by a warp: four
+// groups of 8 lanes have two parts each, whose (m, l) and O are read together.
+constexpr int kFewParts = 8;
+template <int D, bool BF16, int NT>
+struct FewParts {
+  float2 ml[2];
+  float4 v[2];
+  size_t row;
+  int e0;
+  bool on;
+
+  // Piece `i` of those dealt to CTA `cta`, if the item is cut and has as many.
+  __device__ __forceinline__ void load(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int cta, int i,
+                                       int lane) {
+    constexpr int HEADS = 8 * NT, PC = D / 32;
+    const int P = p.c1 - p.c0 + 1, y = cta - p.c0 + P * i;
+    const int h = k.hh / a.HG, hg = k.hh - h * a.HG;
+    on = P > 1 && y < min(HEADS, a.g - hg * HEADS) * PC;
+    const int hd = y / PC;
+    e0 = (y - hd * PC) * 32 + (lane & 7) * 4;
+    row = static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + hg * HEADS + hd;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = p.c0 + (lane >> 3) + 4 * u;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on && x <= p.c1) {
+        const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
+        ml[u] = a.part_ml[at];
+        v[u] = *reinterpret_cast<const float4*>(a.part_o + at * D + e0);
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(const DecodeArgs& a, int lane) const {
+    if (!on) return;
+    float M = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float f[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) f[u] = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - M);
+    float S = f[0] * ml[0].y + f[1] * ml[1].y;
+    float4 acc = make_float4(f[0] * v[0].x + f[1] * v[1].x, f[0] * v[0].y + f[1] * v[1].y,
+                             f[0] * v[0].z + f[1] * v[1].z, f[0] * v[0].w + f[1] * v[1].w);
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, o);
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+    }
+    if (lane >= 8) return;
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    *reinterpret_cast<uint2*>(a.o + row * D + e0) =
+        make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+    if (e0 == 0) a.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+  }
+};
+
 template <int D, bool BF16, int NT, bool WEIGHTS>
 __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const DecodeArgs a) {
   constexpr int HEADS = 8 * NT, WARPS = kJoinThreads / 32;
@@ -654,19 +766,34 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
       if (sub > 0) cc = map.at(v0);
     }
   }
-  grid_dependency_wait();
-  // Sequences without a token: o = 0, L = -inf.
+  // Sequences without a token: o = 0, L = -inf. (All before the decode has ended
+  // once this kernel runs, and the decode itself leaves their rows alone.)
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     if (seq_len(c, b) > 0) continue;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
     for (int x = threadIdx.x; x < a.Hq * D / 2; x += kJoinThreads) dst[x] = 0u;
     for (int x = threadIdx.x; x < a.Hq; x += kJoinThreads) a.lse[static_cast<size_t>(b) * a.Hq + x] = -INFINITY;
   }
+  grid_dependency_wait();
   if (cta >= G || sub >= subs) return;
   // Only the first and the last item of a CTA can be cut.
   const long long b_first = u0 - first.tile, b_last = u1 - 1 - last.tile;  // their first units
   const ItemParts pf = item_parts(b_first, first.ntiles, G, T);
   const bool cut_first = pf.c0 != pf.c1;
+  if constexpr (!WEIGHTS) {
+    const bool two = b_last > b_first;
+    const ItemParts pl = two ? item_parts(b_last, last.ntiles, G, T) : ItemParts{0, 0};
+    if (pf.c1 - pf.c0 < kFewParts && pl.c1 - pl.c0 < kFewParts) {
+      for (int i = warp;; i += WARPS) {
+        FewParts<D, BF16, NT> x, y;
+        x.load(a, first, pf, cta, i, lane);
+        y.load(a, last, pl, cta, i, lane);
+        if (!x.on && !y.on) return;
+        x.finish(a, lane);
+        y.finish(a, lane);
+      }
+    }
+  }
   if (cut_first)
     join_item<D, BF16, NT>(a, first, pf, cta, sub, subs, warp, lane, WEIGHTS && v0 < b_first + first.ntiles, s_ml[0],
                            s_acc);
@@ -705,9 +832,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
         __syncthreads();
         const size_t base = (static_cast<size_t>(cc.b) * c.Hkv + h) * c.L;
         const int j0 = cc.tile * kUnit<D>, j1 = min((cc.tile + cnt) * kUnit<D>, cc.n);
-        if (a.g % 4 == 0) add_weights<4>(a, base, j0, j1, s_lse);
-        else if (a.g % 2 == 0) add_weights<2>(a, base, j0, j1, s_lse);
-        else add_weights<1>(a, base, j0, j1, s_lse);
+        add_weights<kJoinThreads>(a, base, j0, j1, s_lse);
         __syncthreads();  // s_lse is rewritten by the next item
       }
       cc.tile += cnt - 1;
@@ -727,6 +852,9 @@ static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) 
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, C::SMEM, done);
   if (e != cudaSuccess) return e;
+  if (a.whole)
+    return launch_dependent(kern, dim3(static_cast<unsigned>(a.c.B) * a.c.Hkv * a.HG), dim3(kDecWarps * 32), C::SMEM,
+                            stream, a);
   e = launch_dependent(kern, dim3(ctas), dim3(kDecWarps * 32), C::SMEM, stream, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas * a.join_split),
