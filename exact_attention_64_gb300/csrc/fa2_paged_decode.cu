@@ -756,7 +756,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
   if (cta < G) {
     u0 = unit_begin(cta, G, T);
     u1 = unit_begin(cta + 1, G, T);
-    subs = static_cast<int>(max(1LL, min(static_cast<long long>(split), div_pos(u1 - u0, kJoinUnits))));
+    // The same for every CTA, whose shares may differ by one unit: the pieces of
+    // an item are dealt to the blocks of all its parts.
+    subs = static_cast<int>(max(1LL, min(static_cast<long long>(split), div_pos(div_pos(T, G), kJoinUnits))));
     if (sub < subs) {
       v0 = u0 + div_pos((u1 - u0) * sub, subs);
       v1 = u0 + div_pos((u1 - u0) * (sub + 1), subs);

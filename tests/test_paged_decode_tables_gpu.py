@@ -66,3 +66,12 @@ def test_equal_share_and_whole_items_see_the_same(cuda_device, fa2_lib):
         assert torch.equal(a.isnan(), b.isnan())
         a, b = a.nan_to_num(0.0), b.nan_to_num(0.0)
         assert ((a - b).abs() <= rel * a.abs() + 300 * 8 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("units", [72, 80, 145, 147, 151, 154, 231])
+def test_shares_of_unequal_length(cuda_device, fa2_lib, units):
+    """32 items over the CTAs, shares of 7 or 8, of 15 or 16, ... units each, in a
+    table with room for more."""
+    n = units * 64
+    c = Cache(4, 8, 128, 64, [n, n - 5, n, n - 63], BF16, seed=units, width=units + 60)
+    _check(fa2_lib, c, 16, 1.0, True, BF16)
