@@ -95,7 +95,8 @@ int head_tile(int g) { return g <= 8 ? 8 : 16; }
 int decode_ctas(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
   const int g = Hq / Hkv, unit = fa2::decode_unit(d);
   const long long L = static_cast<long long>(page_size) * max_pages;
-  const long long units = static_cast<long long>(B) * Hkv * ((g + head_tile(g) - 1) / head_tile(g)) * ((L + unit - 1) / unit);
+  const long long items = static_cast<long long>(B) * Hkv * ((g + head_tile(g) - 1) / head_tile(g));
+  const long long units = items * ((L + unit - 1) / unit);
   return units < kDecodeCtas ? static_cast<int>(units) : kDecodeCtas;
 }
 
@@ -110,7 +111,7 @@ int decode_ctas(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
 bool decode_whole(int B, int Hkv, int d, int page_size, int max_pages, int HG, int slots, bool weights) {
   const long long unit = fa2::decode_unit(d), units = (static_cast<long long>(page_size) * max_pages + unit - 1) / unit;
   const long long items = static_cast<long long>(B) * Hkv * HG, waves = (items + slots - 1) / slots;
-  if (items > 0x7fffffffLL || (weights && HG > 1)) return false;
+  if (weights && HG > 1) return false;
   const bool filled = waves == 1 ? 5 * items >= 2 * slots : 5 * items >= 4 * waves * slots;
   return units <= (filled ? 8 : 4);
 }

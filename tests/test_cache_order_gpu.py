@@ -2,6 +2,8 @@
 ended, and must still see all of it: results without a synchronisation, behind
 work of other streams, and in graphs, bit for bit those of one call at a time."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -141,4 +143,32 @@ def test_inputs_of_another_stream_in_a_graph(cuda_device, fa2_lib, op, before):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(after, want))
+    assert fa2_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("op", ["decode", "append", "evict", "key_weights"])
+def test_the_default_stream_waits_for_blocking_streams(cuda_device, fa2_lib, op):
+    """The producer on a stream that the default stream synchronises with, and
+    no event."""
+    s = _Late(fa2_lib)
+    s.reset()
+    s.produce()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in s.call(op)]
+    raw = ctypes.c_void_p()
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(raw))) == 0
+    side = torch.cuda.ExternalStream(raw.value)
+    try:
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        for _ in range(3):
+            s.reset()
+            s.x.add_(1)
+            with torch.cuda.stream(side):
+                s.produce()
+            got = s.call(op)
+            torch.cuda.synchronize()
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(got, want))
+    finally:
+        torch.cuda.synchronize()
+        assert int(torch.cuda.cudart().cudaStreamDestroy(raw.value)) == 0
     assert fa2_lib.device_status() == 0
