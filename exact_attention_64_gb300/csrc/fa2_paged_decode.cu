@@ -579,6 +579,10 @@ __device__ __forceinline__ ItemParts item_parts(long long ub, int ntiles, long l
 // Workspace slot of CTA x's part of an item whose first part is CTA c0's.
 __device__ __forceinline__ int part_slot(int x, int c0) { return 2 * x + (x == c0 ? 1 : 0); }
 
+// 2^(from - to) for a reference that rises to `to`. 1 at -inf, where all that
+// there is are zeros, or NaN that has to stay.
+__device__ __forceinline__ float step_down(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
+
 // (M, S) of one head over an item's parts, by a whole warp.
 __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int hd, ItemParts p, int lane) {
   float M = -INFINITY, S = 0.f;
@@ -586,13 +590,13 @@ __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int 
   for (int x = p.c0 + lane; x <= p.c1; x += 32) {
     const float2 ml = part_ml[static_cast<size_t>(part_slot(x, p.c0)) * heads + hd];
     const float n = fmaxf(M, ml.x);
-    if (n != -INFINITY) S = S * ex2_approx(M - n) + ml.y * ex2_approx(ml.x - n);
+    S = S * step_down(M, n) + ml.y * step_down(ml.x, n);
     M = n;
   }
   float top = M;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  S = top == -INFINITY ? 0.f : S * ex2_approx(M - top);
+  S *= step_down(M, top);
 #pragma unroll
   for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
   return make_float2(top, S);
@@ -609,7 +613,19 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 2;
 constexpr int kJoinUnits = 8;
 
-// O and L of the heads of one cut item, by block `sub` of `subs` of CTA `cta`.
+// Elements e0 .. e0 + 3 of a head's output, and its L.
+template <int D, bool BF16>
+__device__ __forceinline__ void store_piece(const DecodeArgs& a, size_t row, int e0, float M, float S,
+                                            const float4& acc) {
+  const float inv = S == 0.f ? 0.f : 1.f / S;
+  *reinterpret_cast<uint2*>(a.o + row * D + e0) =
+      make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+  if (e0 == 0) a.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+}
+
+// With weights: O and L of the heads of one cut item, by block `sub` of `subs` of
+// CTA `cta`, and (M, S) of its heads. (The forms below without weights, with the
+// heads' (M, S) formed apart: up to 1 us slower.)
 // Pieces of 32 elements of a head are dealt to the blocks of all its parts.
 template <int D, bool BF16, int NT>
 __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int cta, int sub,
@@ -638,7 +654,7 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
       const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
       const float px = a.part_ml[at].x;
       const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + e0);
-      const float f = px == -INFINITY ? 0.f : ex2_approx(px - ml.x);
+      const float f = step_down(px, ml.x);
       acc.x += f * v.x;
       acc.y += f * v.y;
       acc.z += f * v.z;
@@ -667,10 +683,7 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
       __syncthreads();
     }
     if (lane < 8 && (!wide || warp == 0)) {
-      const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-      *reinterpret_cast<uint2*>(a.o + (row0 + hd) * D + e0) =
-          make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
-      if (e0 == 0) a.lse[row0 + hd] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2f;
+      store_piece<D, BF16>(a, row0 + hd, e0, ml.x, ml.y, acc);
     }
   }
   __syncthreads();
@@ -678,6 +691,7 @@ __device__ __forceinline__ void join_item(const DecodeArgs& a, const UnitCursor&
 
 // A piece of 32 elements of one head of an item with few parts, by a warp: four
 // groups of 8 lanes have two parts each, whose (m, l) and O are read together.
+// Block x of the P that hold the parts has the pieces x, x + P, ...
 constexpr int kFewParts = 8;
 template <int D, bool BF16, int NT>
 struct FewParts {
@@ -687,13 +701,10 @@ struct FewParts {
   int e0;
   bool on;
 
-  // Piece `i` of those dealt to CTA `cta`, if the item is cut and has as many.
-  __device__ __forceinline__ void load(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int cta, int i,
-                                       int lane) {
+  __device__ __forceinline__ void load(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int y, int lane) {
     constexpr int HEADS = 8 * NT, PC = D / 32;
-    const int P = p.c1 - p.c0 + 1, y = cta - p.c0 + P * i;
     const int h = k.hh / a.HG, hg = k.hh - h * a.HG;
-    on = P > 1 && y < min(HEADS, a.g - hg * HEADS) * PC;
+    on = p.c1 > p.c0 && p.c1 - p.c0 < kFewParts && y < min(HEADS, a.g - hg * HEADS) * PC;
     const int hd = y / PC;
     e0 = (y - hd * PC) * 32 + (lane & 7) * 4;
     row = static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + hg * HEADS + hd;
@@ -716,7 +727,7 @@ struct FewParts {
     for (int o = 8; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float f[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) f[u] = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - M);
+    for (int u = 0; u < 2; ++u) f[u] = step_down(ml[u].x, M);
     float S = f[0] * ml[0].y + f[1] * ml[1].y;
     float4 acc = make_float4(f[0] * v[0].x + f[1] * v[1].x, f[0] * v[0].y + f[1] * v[1].y,
                              f[0] * v[0].z + f[1] * v[1].z, f[0] * v[0].w + f[1] * v[1].w);
@@ -728,11 +739,62 @@ struct FewParts {
       acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
       acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
     }
-    if (lane >= 8) return;
-    const float inv = S == 0.f ? 0.f : 1.f / S;
-    *reinterpret_cast<uint2*>(a.o + row * D + e0) =
-        make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
-    if (e0 == 0) a.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+    if (lane < 8) store_piece<D, BF16>(a, row, e0, M, S, acc);
+  }
+};
+
+// The same of an item with many parts, by the block: 32 groups of 8 threads.
+template <int D, bool BF16, int NT>
+struct ManyParts {
+  float M, S;
+  float4 acc;
+  size_t row;
+  int e0;
+  bool on;
+
+  __device__ __forceinline__ void add(float m, float l, const float4& v) {
+    const float n = fmaxf(M, m), f = step_down(M, n), g = step_down(m, n);
+    M = n;
+    S = S * f + l * g;
+    acc = make_float4(acc.x * f + v.x * g, acc.y * f + v.y * g, acc.z * f + v.z * g, acc.w * f + v.w * g);
+  }
+  __device__ __forceinline__ void load(const DecodeArgs& a, const UnitCursor& k, ItemParts p, int y) {
+    constexpr int HEADS = 8 * NT, PC = D / 32;
+    const int h = k.hh / a.HG, hg = k.hh - h * a.HG;
+    on = p.c1 - p.c0 >= kFewParts && y < min(HEADS, a.g - hg * HEADS) * PC;
+    const int hd = y / PC;
+    e0 = (y - hd * PC) * 32 + (threadIdx.x & 7) * 4;
+    row = static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + hg * HEADS + hd;
+    M = -INFINITY;
+    S = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!on) return;
+#pragma unroll 4
+    for (int x = p.c0 + (threadIdx.x >> 3); x <= p.c1; x += kJoinThreads / 8) {
+      const size_t at = static_cast<size_t>(part_slot(x, p.c0)) * HEADS + hd;
+      const float2 ml = a.part_ml[at];
+      add(ml.x, ml.y, *reinterpret_cast<const float4*>(a.part_o + at * D + e0));
+    }
+  }
+  __device__ __forceinline__ void finish(const DecodeArgs& a, float4 (*s_acc)[8], float2* s_part) {
+    if (!on) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, S, o);
+      const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                   __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+      add(m, l, v);
+    }
+    if (lane < 8) s_acc[warp][lane] = acc;
+    if (lane == 0) s_part[warp] = make_float2(M, S);
+    __syncthreads();
+    if (warp == 0 && lane < 8) {
+#pragma unroll
+      for (int x = 1; x < kJoinThreads / 32; ++x) add(s_part[x].x, s_part[x].y, s_acc[x][lane]);
+      store_piece<D, BF16>(a, row, e0, M, S, acc);
+    }
+    __syncthreads();
   }
 };
 
@@ -742,6 +804,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
   const int split = a.join_split;
   __shared__ float2 s_ml[2][HEADS];  // of the CTA's first and last item, if cut
   __shared__ float4 s_acc[WARPS][8];
+  __shared__ float2 s_part[WARPS];
   __shared__ float s_lse[kMaxGroup];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
@@ -781,30 +844,34 @@ __global__ void __launch_bounds__(kJoinThreads, 4) fa2_paged_join_kernel(const D
   // Only the first and the last item of a CTA can be cut.
   const long long b_first = u0 - first.tile, b_last = u1 - 1 - last.tile;  // their first units
   const ItemParts pf = item_parts(b_first, first.ntiles, G, T);
-  const bool cut_first = pf.c0 != pf.c1;
+  const ItemParts pl = b_last > b_first ? item_parts(b_last, last.ntiles, G, T) : ItemParts{0, 0};
+  const bool cut_first = pf.c0 != pf.c1, cut_last = pl.c0 != pl.c1;
   if constexpr (!WEIGHTS) {
-    const bool two = b_last > b_first;
-    const ItemParts pl = two ? item_parts(b_last, last.ntiles, G, T) : ItemParts{0, 0};
-    if (pf.c1 - pf.c0 < kFewParts && pl.c1 - pl.c0 < kFewParts) {
+    const int at_f = cta - pf.c0, at_l = cta - pl.c0, P = pf.c1 - pf.c0 + 1, Q = pl.c1 - pl.c0 + 1;
+    if ((cut_first && P <= kFewParts) || (cut_last && Q <= kFewParts)) {
       for (int i = warp;; i += WARPS) {
         FewParts<D, BF16, NT> x, y;
-        x.load(a, first, pf, cta, i, lane);
-        y.load(a, last, pl, cta, i, lane);
-        if (!x.on && !y.on) return;
+        x.load(a, first, pf, at_f + P * i, lane);
+        y.load(a, last, pl, at_l + Q * i, lane);
+        if (!x.on && !y.on) break;
         x.finish(a, lane);
         y.finish(a, lane);
       }
     }
-  }
-  if (cut_first)
-    join_item<D, BF16, NT>(a, first, pf, cta, sub, subs, warp, lane, WEIGHTS && v0 < b_first + first.ntiles, s_ml[0],
-                           s_acc);
-  bool cut_last = false;
-  if (b_last > b_first) {
-    const ItemParts pl = item_parts(b_last, last.ntiles, G, T);
-    cut_last = pl.c0 != pl.c1;
-    if (cut_last)
-      join_item<D, BF16, NT>(a, last, pl, cta, sub, subs, warp, lane, WEIGHTS && v1 > b_last, s_ml[1], s_acc);
+    if (P > kFewParts || Q > kFewParts) {
+      for (int i = 0;; ++i) {
+        ManyParts<D, BF16, NT> x, y;
+        x.load(a, first, pf, at_f + P * i);
+        y.load(a, last, pl, at_l + Q * i);
+        if (!x.on && !y.on) break;
+        x.finish(a, s_acc, s_part);
+        y.finish(a, s_acc, s_part);
+      }
+    }
+  } else {
+    if (cut_first)
+      join_item<D, BF16, NT>(a, first, pf, cta, sub, subs, warp, lane, v0 < b_first + first.ntiles, s_ml[0], s_acc);
+    if (cut_last) join_item<D, BF16, NT>(a, last, pl, cta, sub, subs, warp, lane, v1 > b_last, s_ml[1], s_acc);
   }
   if constexpr (WEIGHTS) {
     for (long long u = v0; u < v1;) {

@@ -75,3 +75,21 @@ def test_shares_of_unequal_length(cuda_device, fa2_lib, units):
     n = units * 64
     c = Cache(4, 8, 128, 64, [n, n - 5, n, n - 63], BF16, seed=units, width=units + 60)
     _check(fa2_lib, c, 16, 1.0, True, BF16)
+
+
+@pytest.mark.parametrize("n,width", [(300, 20), (300, 200), (3000, 200), (40000, 2500)])
+def test_a_head_of_nan_keys_is_nan(cuda_device, fa2_lib, n, width):
+    """Whatever the number of parts that are joined: none, few, many."""
+    c = Cache(2, 2, 64, 16, [n, n], BF16, seed=n, width=width)
+    kc, vc, table, lens = c.gpu()
+    kc[table[0].long(), 1] = float("nan")
+    w = torch.zeros(2, 2, c.L, device="cuda")
+    q = c.query(2).cuda()
+    o, lse = fa2_lib.paged_decode(q, kc, vc, table, lens, weights=w)
+    o2, lse2 = fa2_lib.paged_decode(q, kc, vc, table, lens)
+    torch.cuda.synchronize()
+    assert fa2_lib.device_status() == 0
+    for x, y in ((o, lse), (o2, lse2)):
+        assert x[0, 1].isnan().all() and y[0, 1].isnan()
+        assert x[0, 0].isfinite().all() and x[1].isfinite().all() and y[1].isfinite().all() and y[0, 0].isfinite()
+    assert w[0, 1, :n].isnan().all() and w[0, 0].isfinite().all() and w[1].isfinite().all()
