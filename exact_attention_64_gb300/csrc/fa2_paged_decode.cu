@@ -564,10 +564,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
 }
 
 // ---- Join ------------------------------------------------------------------
-// The same CTAs over the same units. The parts of a cut item are joined by the
-// CTAs that hold them, part x taking heads x, x + P, ... of the tile; then, with
-// weights, every CTA adds its own slots' weights, e^(s - L) summed over the
-// group's heads, from the logits that it wrote.
+// The same CTAs over the same units. The P parts of a cut item are joined by the
+// CTAs that hold them, each taking every P-th piece of 32 elements of a head;
+// then, with weights, every CTA adds its own slots' weights, e^(s - L) summed over
+// the group's heads, from the logits that it wrote.
 
 // Parts [c0, c1] of the item of units [ub, ub + ntiles).
 struct ItemParts {
@@ -603,12 +603,14 @@ __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int 
 }
 
 // What bounds the join: the latency of a few dependent reads, and with weights
-// the logits, which come from L2. So a CTA's range is shared by up to
-// kJoinSplit blocks when there are logits, one per kJoinUnits units, and a
-// thread has several loads in flight. All blocks have to be resident at once:
-// 2 x 304 blocks of 256 threads with 64 registers fill the SMs; with 4 x 304
-// those waiting for the decode to end kept the rest out (118 us against 110 for
-// the decode of 32 sequences, 613 MB, with weights).
+// the logits, which come from L2. Without weights (m, l) and O are read together
+// and a CTA's two cut items at once (8 heads of 512 slots 5.8 us with the decode,
+// 6.5 with (m, l) first and one item after the other; of 2048 slots 7.6 and 10.2).
+// With weights a thread has several loads in flight, and a CTA's range is shared
+// by up to kJoinSplit blocks, one per kJoinUnits units. All blocks have to be
+// resident at once: 2 x 304 blocks of 256 threads with 64 registers fill the SMs;
+// with 4 x 304 those waiting for the decode to end kept the rest out (118 us
+// against 110 for the decode of 32 sequences, 613 MB, with weights).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 2;
 constexpr int kJoinUnits = 8;
