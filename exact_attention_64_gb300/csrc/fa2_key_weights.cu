@@ -435,14 +435,14 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         }
         fresh = kw_advance_step(a, s, cu, cnt);
       }
-      if (!ok) {  // copies in flight land before the CTA ends
+      // Copies in flight land before the CTA ends, whoever has given up. (If nobody
+      // has, they are landing anyway.)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (loads[t] > 0) mbar_wait_drain(&sh.k_full[t], (loads[t] - 1) & 1, a.timeout_ns);
-        for (int x = 0; x < C::NQ; ++x) {
-          const int uses = used / C::NQ + (x < used % C::NQ ? 1 : 0);
-          if (uses > 0) mbar_wait_drain(&sh.q_full[x], (uses - 1) & 1, a.timeout_ns);
-        }
+      for (int t = 0; t < 2; ++t)
+        if (loads[t] > 0) mbar_wait_drain(&sh.k_full[t], (loads[t] - 1) & 1, a.timeout_ns);
+      for (int x = 0; x < C::NQ; ++x) {
+        const int uses = used / C::NQ + (x < used % C::NQ ? 1 : 0);
+        if (uses > 0) mbar_wait_drain(&sh.q_full[x], (uses - 1) & 1, a.timeout_ns);
       }
     } else if ((warp & 1) && u0 < u1) {
       // Issuers: S^T of tile A by warp 1, of tile B by warp 3. While the groups
