@@ -26,13 +26,13 @@
 // ends. 16-byte copies follow any page size, a page per slot included, which a
 // bulk copy of a page's run cannot.
 //
-// Products. S^T = K Q^T and O^T += V^T P^T with m16n8k16 matrix instructions:
-// the 16 slots (or 16 columns of V) are the long side and 8 query heads the
-// short one. At 8 heads a slot costs 512 bytes (d = 128) and 2 x 16/16 of these
-// instructions, far below what they can do at the memory's pace, so tcgen05
-// (M = 128 rows of which g would be used) would gain nothing here. P is split
-// into a 16-bit value and a 16-bit remainder, two products, so that the output
-// carries the one rounding at the end and no rounding of P.
+// Products. S^T = K Q^T with m16n8k16 matrix instructions: the 16 slots are the
+// long side and 8 query heads the short one; O^T += V^T P^T with the same, 16
+// columns of V the long side. At 8 heads a slot costs 512 bytes (d = 128) and 2 x
+// 16/16 to 3 x 16/16 of these instructions, far below what they can do at the
+// memory's pace, so tcgen05 (M = 128 rows of which g would be used) would gain
+// nothing here. P enters its product in pieces (see "P" below), so that the output
+// carries the one rounding at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -93,6 +93,80 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// D (16 x 8, fp32) += A (16 x 8) B (8 x 8), both read to 11 significant bits and
+// with the exponents of fp32.
+__device__ __forceinline__ void mma1688_tf32(float (&d)[4], const float (&a)[4], float b0, float b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+                 "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+// ---- P -------------------------------------------------------------------
+// P of 16 slots and 8 heads, transposed from the accumulator's layout (slots r8
+// and r8 + 8, heads 2t and 2t + 1) into that of a second operand (slots 2t, 2t + 1,
+// 2t + 8 and 2t + 9, head r8), and its product with V.
+constexpr uint32_t kLow16 = 0x5410u, kHigh16 = 0x7632u;  // both low, both high halves
+
+// bf16: a number and the remainder, 16 bits together (2^-17 of p).
+template <bool BF16>
+struct ProbT;
+
+template <>
+struct ProbT<true> {
+  uint32_t b[2][2];
+  __device__ __forceinline__ void set(const float (&p)[4]) {
+    const uint32_t h0 = pack_x2<true>(p[0], p[1]), h1 = pack_x2<true>(p[2], p[3]);
+    const float2 b0 = unpack_x2<true>(h0), b1 = unpack_x2<true>(h1);
+    b[0][0] = transpose8(h0);
+    b[0][1] = transpose8(h1);
+    b[1][0] = transpose8(pack_x2<true>(p[0] - b0.x, p[1] - b0.y));
+    b[1][1] = transpose8(pack_x2<true>(p[2] - b1.x, p[3] - b1.y));
+  }
+  __device__ __forceinline__ void add(float (&o)[4], const uint32_t (&va)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mma16816<true>(o, va, b[i][0], b[i][1]);
+  }
+};
+
+// fp16 has no exponents for small p: in two fp16 numbers a slot 2^-25 below the
+// largest of its warp would be lost, and such slots together can be what o is made
+// of. So V, exact in 11 bits, is multiplied in tf32 by two pieces of p, 11 bits each
+// (cut: 2^-21 of p at most). Two fp16 numbers took 13.5 us where this takes 14.6
+// (B = 32, 8 heads of 500 slots, d = 128), 30.7 and 33.3 (B = 16, 64/4 heads of 4000
+// slots), 27.0 and 28.2 (B = H = 16, 2047 slots, d = 64); large batches are at
+// memory's pace either way.
+__device__ __forceinline__ float high_tf32(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+
+template <>
+struct ProbT<false> {
+  float hi[4], lo[4];
+  __device__ __forceinline__ void set(const float (&p)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = __float_as_uint(p[2 * i]), y = __float_as_uint(p[2 * i + 1]);
+      const uint32_t u = transpose8(__byte_perm(x, y, kLow16)), v = transpose8(__byte_perm(x, y, kHigh16));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t z = __byte_perm(u, v, j == 0 ? kLow16 : kHigh16);
+        hi[2 * i + j] = high_tf32(__uint_as_float(z));
+        lo[2 * i + j] = high_tf32(__uint_as_float(z) - hi[2 * i + j]);
+      }
+    }
+  }
+  // The order of the 8 slots of an instruction is free: its k = t and t + 4 are
+  // slots 2t and 2t + 1, the two halves of a register of V.
+  __device__ __forceinline__ void add(float (&o)[4], const uint32_t (&va)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = unpack_x2<false>(va[2 * i]), y = unpack_x2<false>(va[2 * i + 1]);
+      const float v[4] = {x.x, y.x, x.y, y.y};
+      mma1688_tf32(o, v, hi[2 * i], hi[2 * i + 1]);
+      mma1688_tf32(o, v, lo[2 * i], lo[2 * i + 1]);
+    }
+  }
+};
 
 // ---- Units ---------------------------------------------------------------
 // HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
@@ -389,7 +463,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(s[rb][nt], ka, qf[nt][kk][0], qf[nt][kk][1]);
         }
       }
-      uint32_t ph[C::RB][NT][2], pl[C::RB][NT][2];
+      ProbT<BF16> pt[C::RB][NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[C::RB][4];
@@ -451,12 +525,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           p[3] = ex2_approx(x[rb][3] - z1);
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
-          const uint32_t h0 = pack_x2<BF16>(p[0], p[1]), h1 = pack_x2<BF16>(p[2], p[3]);
-          const float2 b0 = unpack_x2<BF16>(h0), b1 = unpack_x2<BF16>(h1);
-          ph[rb][nt][0] = transpose8(h0);
-          ph[rb][nt][1] = transpose8(h1);
-          pl[rb][nt][0] = transpose8(pack_x2<BF16>(p[0] - b0.x, p[1] - b0.y));
-          pl[rb][nt][1] = transpose8(pack_x2<BF16>(p[2] - b1.x, p[3] - b1.y));
+          pt[rb][nt].set(p);
         }
       }
       const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
@@ -467,10 +536,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           uint32_t va[4];
           ldsm4_t(va, vb + (rb * 16 + vr) * C::ROW + (((2 * dt + vc) ^ (vr & 7)) * 16));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816<BF16>(o[nt][dt], va, ph[rb][nt][0], ph[rb][nt][1]);
-            mma16816<BF16>(o[nt][dt], va, pl[rb][nt][0], pl[rb][nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt) pt[rb][nt].add(o[nt][dt], va);
         }
       }
     }

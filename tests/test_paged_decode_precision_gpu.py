@@ -1,0 +1,107 @@
+"""What the decode's output carries: the one rounding at its end, and no rounding
+of the probabilities that would show through it."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+from tests.cache_cases import BF16, FP16, Cache, bits64
+
+pytestmark = pytest.mark.gpu
+
+
+def _sink(d, ps, n, gap, dtype, sink_at=0):
+    """One slot whose score lies `gap` log2 units above all others and whose V is
+    0; the others have one score, and V of one sign. (q, cache, scale, q.k of the
+    sink): the scores are exact."""
+    c = Cache(1, 1, d, ps, [n], dtype, seed=n, nan=False)
+    flat_k, flat_v = c.k.view(-1, d), c.v.view(-1, d)
+    j = torch.arange(n)
+    rows = c.table[0].long()[j // ps] * ps + j % ps
+    flat_k[rows] = 0
+    flat_k[rows[sink_at], 0] = 1.0
+    flat_v[rows] = (1.0 + torch.rand(n, d, generator=c.g)).to(dtype)
+    flat_v[rows[sink_at]] = 0
+    q = torch.zeros(1, 1, d, dtype=dtype)
+    q[0, 0, 0] = 1.0
+    return c, q, gap * float(np.log(2.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("gap", [20.0, 23.1, 25.2, 26.0, 31.5])
+@pytest.mark.parametrize("d,ps,n,width", [(128, 16, 4096, 256), (64, 64, 4096, 64), (128, 16, 500, 32),
+                                          (64, 16, 30, 2)])
+def test_slots_far_below_the_largest_count(cuda_device, fa2_lib, dtype, gap, d, ps, n, width):
+    """p of every slot but one is 2^-gap of the largest's: they are all that the
+    output is made of."""
+    c, q, scale = _sink(d, ps, n, gap, dtype, sink_at=n // 3)
+    c.v *= 256  # so that the output stays a normal number in fp16
+    kc, vc, table, lens = c.gpu()
+    w = torch.zeros(1, 1, c.L, device="cuda")
+    o, lse = fa2_lib.paged_decode(q.cuda(), kc, vc, table, lens, scale=scale, weights=w)
+    o2, _ = fa2_lib.paged_decode(q.cuda(), kc, vc, table, lens, scale=scale)
+    torch.cuda.synchronize()
+    assert fa2_lib.device_status() == 0
+    scale = float(np.float32(scale))
+    ref, lref, p = oc.paged_decode(bits64(q), bits64(c.k), bits64(c.v), c.table.numpy(), c.lens.numpy(), scale)
+    # The score times scale * log2(e) is a rounding of the factor (2^-24 of it) and
+    # one of the product, each at most gap * 2^-24 log2 units: ln 2 of that in p;
+    # exp2 2^-22. Up to n/4 terms of one sign in a warp, added 8 or 16 at a time by
+    # instructions that may cut the sum (2^-23 each), then 40 further roundings.
+    rel = gap * 2 * 2.0 ** -24 * 0.7 + 2.0 ** -22 + (n / 32 + 40) * 2.0 ** -23
+    half = torch.finfo(dtype).eps / 2
+    tiny = torch.finfo(dtype).smallest_normal * half  # half a step of a subnormal
+    for got in (o, o2):
+        err = np.abs(bits64(got) - ref)
+        assert (err <= np.abs(ref) * (half * 1.01 + rel + 2.0 ** -19) + tiny).all(), np.max(err / np.abs(ref))
+    want = p[0]
+    assert (np.abs(bits64(w[0, :, :n]) - want) <= want * (rel + 2.0 ** -20)).all()
+
+
+def _scale_of(gap):
+    """A float32 near gap * ln 2 whose product with log2(e) is a float32 but for
+    2^-28 of itself, so that the kernel's factor is the exact one."""
+    f = np.float32(gap * np.log(2.0))
+    while True:
+        x = float(f) / np.log(2.0)
+        if abs(float(np.float32(x)) / x - 1) < 2.0 ** -28:
+            return float(f)
+        f = np.nextafter(f, np.float32(100))
+
+
+@pytest.mark.parametrize("dtype", [FP16], ids=["fp16"])
+@pytest.mark.parametrize("gap", [1.96, 3.96, 9.96, 11.95])
+def test_rounded_once(cuda_device, fa2_lib, dtype, gap):
+    """16 slots, one with a score `gap` log2 units above the others and V = 0. Every
+    output that does not lie at a border between two steps is the rounded exact
+    value. (At these gaps two bf16 numbers are 2^-17.2 off p, and two fp16 numbers,
+    at the last two, 2^-15.4 and 2^-13.3.)"""
+    B, H, d = 64, 16, 128
+    c = Cache(B, H, d, 16, [16] * B, dtype, seed=int(gap * 100))
+    c.k[:] = 0
+    c.v[:] = (1.0 + torch.rand(c.v.shape, generator=c.g)).to(dtype)
+    b = torch.arange(B)
+    sink = torch.randint(0, 16, (B,), generator=c.g)
+    page = c.table[:, 0].long()
+    c.k[page[b], :, sink, 0] = 1.0
+    c.v[page[b], :, sink] = 0.0
+    q = torch.zeros(B, H, d, dtype=dtype)
+    q[:, :, 0] = 1.0
+    kc, vc, table, lens = c.gpu()
+    scale = _scale_of(gap)
+    o, _ = fa2_lib.paged_decode(q.cuda(), kc, vc, table, lens, scale=scale)
+    torch.cuda.synchronize()
+    e = np.exp(-scale)
+    ref = bits64(c.v)[page.numpy()].sum(2) * (e / (1.0 + 15.0 * e))
+    # Score and factor are exact; exp2 is good to 2^-22; 15 terms of one sign are
+    # added by up to four instructions that may each cut 2^-23; the sum of p, its
+    # reciprocal and the last product are off by 5, 2 and 1 half steps (2^-24); fp16
+    # keeps p as two numbers of 11 bits: 2^-21.
+    rel = 2.0 ** -28 * gap + 2.0 ** -22 + 4 * 2.0 ** -23 + 8 * 2.0 ** -24 + (2.0 ** -21 if dtype == FP16 else 0)
+    assert rel < 2.0 ** -18.5
+    sure = torch.from_numpy(ref * (1 - rel)).to(dtype) == torch.from_numpy(ref * (1 + rel)).to(dtype)
+    assert sure.float().mean() > 0.99
+    near = torch.from_numpy(ref).to(dtype)
+    wrong = (o.cpu() != near) & sure
+    assert not wrong.any(), int(wrong.sum())
