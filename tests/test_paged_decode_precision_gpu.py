@@ -70,7 +70,7 @@ def _scale_of(gap):
         f = np.nextafter(f, np.float32(100))
 
 
-@pytest.mark.parametrize("dtype", [FP16], ids=["fp16"])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("gap", [1.96, 3.96, 9.96, 11.95])
 def test_rounded_once(cuda_device, fa2_lib, dtype, gap):
     """16 slots, one with a score `gap` log2 units above the others and V = 0. Every
