@@ -114,6 +114,11 @@ constexpr uint32_t kLow16 = 0x5410u, kHigh16 = 0x7632u;  // both low, both high 
 // and are 1 to 4 % faster where memory is not the bound: 17.2 us against 17.6 for
 // B = 8, 32/8 heads of 2000 slots, 30.6 and 31.8 for B = 16, 64/4 heads of 4000; the
 // tf32 form below took 18.0 and 33.7.)
+//
+// A piece after the first is never 0: it would make 0 * inf = NaN of an infinite V.
+// The smallest normal number in its place adds nothing that a 16-bit V shows.
+constexpr float kLeastPiece = 1.17549435e-38f;
+
 __device__ __forceinline__ float high_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_high(float x, float y) {
   return __byte_perm(__float_as_uint(x), __float_as_uint(y), kHigh16);
@@ -132,7 +137,7 @@ struct ProbT<true> {
       b[i][0] = transpose8(pack_high(r[0], r[1]));
       b[i][1] = transpose8(pack_high(r[2], r[3]));
 #pragma unroll
-      for (int y = 0; y < 4; ++y) r[y] -= high_bf16(r[y]);
+      for (int y = 0; y < 4; ++y) r[y] = fmaxf(r[y] - high_bf16(r[y]), kLeastPiece);
     }
   }
   __device__ __forceinline__ void add(float (&o)[4], const uint32_t (&va)[4]) const {
@@ -162,7 +167,7 @@ struct ProbT<false> {
       for (int j = 0; j < 2; ++j) {
         const uint32_t z = __byte_perm(u, v, j == 0 ? kLow16 : kHigh16);
         hi[2 * i + j] = high_tf32(__uint_as_float(z));
-        lo[2 * i + j] = high_tf32(__uint_as_float(z) - hi[2 * i + j]);
+        lo[2 * i + j] = high_tf32(fmaxf(__uint_as_float(z) - hi[2 * i + j], kLeastPiece));
       }
     }
   }

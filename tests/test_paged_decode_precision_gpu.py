@@ -105,3 +105,37 @@ def test_rounded_once(cuda_device, fa2_lib, dtype, gap):
     near = torch.from_numpy(ref).to(dtype)
     wrong = (o.cpu() != near) & sure
     assert not wrong.any(), int(wrong.sum())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("n,width", [(30, 4), (600, 80), (3000, 200)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_values_come_out_infinite(cuda_device, fa2_lib, dtype, n, width, d):
+    """A V entry of +-inf makes its element of o +-inf, as p * inf does; both signs
+    in one column, or NaN, make NaN; all other elements are as without it."""
+    c = Cache(2, 2, d, 16, [n, n - 1], dtype, seed=n, width=width)
+    kc, vc, table, lens = c.gpu()
+    q = c.query(8).cuda()
+    bad = vc.clone()
+
+    def at(b, j):
+        return int(c.table[b, j // 16]), j % 16
+
+    p, s = at(0, n // 2)
+    bad[p, 1, s, 3] = float("inf")
+    bad[p, 1, s, 7] = -float("inf")
+    bad[p, 1, s, d - 1] = -float("inf")
+    p, s = at(0, n - 1)
+    bad[p, 1, s, d - 1] = float("inf")
+    p, s = at(1, 5)
+    bad[p, 0, s, 1] = float("nan")
+    for weights in (None, torch.zeros(2, 2, c.L, device="cuda")):
+        want, lse0 = fa2_lib.paged_decode(q, kc, vc, table, lens, weights=weights)
+        o, lse = fa2_lib.paged_decode(q, kc, bad, table, lens, weights=weights)
+        torch.cuda.synchronize()
+        want[0, 4:, 3], want[0, 4:, 7], want[0, 4:, d - 1] = float("inf"), -float("inf"), float("nan")
+        want[1, :4, 1] = float("nan")
+        assert torch.equal(o.isnan(), want.isnan())
+        assert torch.equal(o.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+        assert torch.equal(lse, lse0)
+    assert fa2_lib.device_status() == 0
