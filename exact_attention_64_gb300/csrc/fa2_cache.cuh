@@ -62,8 +62,9 @@ struct CacheView {
 
 // A length or a page that the cache does not have is never followed: the
 // length is cut to what the table can hold, the page's slots are left out, and
-// the status word says so.
-__device__ __forceinline__ void report_page(int* status) { atomicExch(status, kDevPage); }
+// the status word says so, unless it holds a wait that ran out: bad lengths can be
+// what that left behind.
+__device__ __forceinline__ void report_page(int* status) { atomicCAS(status, kDevOk, kDevPage); }
 
 __device__ __forceinline__ int cut_len(int n, int L) { return min(max(n, 0), L); }
 

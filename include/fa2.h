@@ -399,8 +399,8 @@ size_t fa2_key_weights_workspace_size(void);
 
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: FA2_OK, or FA2_ERR_DEVICE_TIMEOUT if any kernel since the last call
- * gave up on a bounded wait, FA2_ERR_PAGE if a paged-cache kernel met a bad
- * page, length or count, or FA2_ERR_CUDA if the synchronisation failed. */
+ * gave up on a bounded wait, else FA2_ERR_PAGE if a paged-cache kernel met a bad
+ * page, length or count; or FA2_ERR_CUDA if the synchronisation failed. */
 int fa2_get_device_status(void* stream);
 
 /* Static, human-readable name of a status code. */
