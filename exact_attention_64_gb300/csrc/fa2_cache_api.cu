@@ -349,12 +349,9 @@ int fa2_key_weights(const void* q, const void* k, const float* lse, const int* q
   a.N = N;
   a.Nk = Nk;
   a.nkb = (Nk + 255) / 256;
-  // The tensor core cuts the running sum of a product toward zero at each of
-  // its d / 16 steps (a simulation of that predicts the error measured here,
-  // 9e-7 of the weights at N = 8192 with Q ~ N(0, 3^2); rounding to nearest
-  // would give 1e-7). Scores therefore come out smaller by about 1.25e-8 of
-  // themselves per step in the mean, and the scale gives that back.
-  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (1.0 + d / 16 * 1.25e-8));
+  // The forward's factor, rounded as it is there: with the L that the forward makes
+  // of its scores the weights of a query sum to 1.
+  a.scale_log2 = scale * 1.4426950408889634f;
   a.timeout_ns = fa2::kDefaultWaitTimeoutNs;
   a.fault = fa2::host_take_fault(6, &a.timeout_ns);
   const int ctas = sms < kKwCtas ? sms : kKwCtas;
