@@ -42,8 +42,9 @@ __global__ void __launch_bounds__(kAppendThreads) fa2_cache_append_kernel(const 
   const int rr = static_cast<int>(r), bh = div_by(rr, a.fT), i = rr - bh * a.T;
   const int b = div_by(bh, a.fH), h = bh - b * c.Hkv;
   const int cnt = a.num_new != nullptr ? ld_global(a.num_new + b) : a.T;
-  const int slot = seq_len(c, b) + i;
-  if (i >= cnt || slot >= c.L) return;  // padding, or no room in the table
+  const int n = seq_len(c, b);
+  if (i >= cnt || i >= c.L - n) return;  // padding, or no room in the table (n + i may not fit in 31 bits)
+  const int slot = n + i;
   const uint4 kx = ld_once(reinterpret_cast<const uint4*>(a.k + static_cast<size_t>(rr) * D) + ch);
   const uint4 vx = ld_once(reinterpret_cast<const uint4*>(a.v + static_cast<size_t>(rr) * D) + ch);
   const int row = slot_row(c, b, h, slot);
