@@ -135,6 +135,14 @@ inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, s
 // Slots per unit of the decode: 32 KiB of K and V.
 __host__ __device__ constexpr int decode_unit(int d) { return 64 * (128 / d); }
 
+// The eviction's moves: a list of more than kInlineMoves is left to a second launch
+// of this many CTAs.
+constexpr int kInlineMoves = 256;
+constexpr int kMovesPerCta = 64;
+constexpr long long move_ctas(long long items, long long list) {
+  return list > kInlineMoves ? items * ((list + kMovesPerCta - 1) / kMovesPerCta) : 0;
+}
+
 // ---- Arguments ------------------------------------------------------------
 struct DecodeArgs {
   CacheView c;

@@ -130,6 +130,12 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
   return s;
 }
 
+// Longest list of moves of an eviction: slots below the budget, or past it.
+long long evict_list(int page_size, int max_pages, int budget) {
+  const long long past = static_cast<long long>(max_pages) * page_size - budget;
+  return past <= 0 ? 0 : past < budget ? past : budget;
+}
+
 int check_heads(int Hq, int Hkv) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return FA2_ERR_INVALID_ARG;
   if (Hq > 65535 || Hq / Hkv > fa2::kMaxGroup) return FA2_ERR_UNSUPPORTED;
@@ -249,8 +255,8 @@ int fa2_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
 
 size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pages, int budget) {
   if (check_cache(B, Hkv, 64, 1, page_size, max_pages, FA2_BF16) != FA2_OK || budget < 1) return 0;
-  const long long L = static_cast<long long>(max_pages) * page_size;
-  const long long list = budget < L ? (budget < L - budget ? budget : L - budget) : 0;
+  const long long list = evict_list(page_size, max_pages, budget);
+  if (fa2::move_ctas(static_cast<long long>(B) * Hkv, list) > kMaxRows) return 0;
   return 2 * align_up(static_cast<size_t>(B) * Hkv * list * 4, 256) + align_up(static_cast<size_t>(B) * Hkv * 4, 256);
 }
 
@@ -265,6 +271,8 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
   if (budget < 1 || recent < 0 || recent > budget) return FA2_ERR_INVALID_ARG;
   int st = check_cache(B, Hkv, d, num_pages, page_size, max_pages, dtype);
   if (st != FA2_OK) return st;
+  const long long list = evict_list(page_size, max_pages, budget);
+  if (fa2::move_ctas(static_cast<long long>(B) * Hkv, list) > kMaxRows) return FA2_ERR_UNSUPPORTED;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
       !aligned(weights, 4) || !aligned(weights_out, 4) || !aligned(positions, 4) ||
       !aligned(positions_out, 4) || !aligned(next_pos, 4) || !aligned(lens_out, 4))
@@ -293,7 +301,7 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
   a.p_out = positions_out;
   a.next_pos = next_pos;
   a.lens_out = lens_out;
-  a.list = budget < a.c.L ? (budget < a.c.L - budget ? budget : a.c.L - budget) : 0;
+  a.list = static_cast<int>(list);
   const size_t lists = align_up(static_cast<size_t>(B) * Hkv * a.list * 4, 256);
   a.holes = static_cast<int*>(workspace);
   a.movers = reinterpret_cast<int*>(static_cast<char*>(workspace) + lists);

@@ -107,7 +107,6 @@ constexpr int kEvictRegs = 8;      // keys a thread can hold: 4096 slots per CTA
 constexpr int kEvictKeys = 49152;  // keys a CTA's shared memory can hold: 192 KiB
 constexpr int kMoveThreads = 256;
 constexpr int kMovesPerWarp = 8;
-constexpr int kInlineMoves = 256;  // longest list that the selecting cluster works off itself
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -518,9 +517,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a, C);
   if (e != cudaSuccess || a.list <= kInlineMoves) return e;
-  constexpr int per_cta = kMoveThreads / 32 * kMovesPerWarp;
-  const int chunks = (a.list + per_cta - 1) / per_cta;
-  if (items * chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  static_assert(kMoveThreads / 32 * kMovesPerWarp == kMovesPerCta, "move_ctas counts these");
+  const int chunks = static_cast<int>(move_ctas(1, a.list));
   return launch_dependent(a.d == 64 ? fa2_cache_move_kernel<64> : fa2_cache_move_kernel<128>,
                           dim3(static_cast<unsigned>(items * chunks)), dim3(kMoveThreads), 0, stream, a, chunks);
 }

@@ -361,7 +361,8 @@ int fa2_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
  *                 left as they were; each may be its input itself.
  *   positions, positions_out, next_pos : all or none. next_pos[b] is the
  *                 position that the next token will get.
- *   budget      : >= 1.  recent: 0 .. budget.
+ *   budget      : >= 1.  recent: 0 .. budget. With M = min(budget, L - budget):
+ *                 B * Hkv * ceil(M / 64) < 2^31.
  *   lens_out    : device int32 [B], not lens itself.
  *   workspace   : device, >= fa2_cache_evict_workspace_size(...) bytes,
  *                 256-byte aligned, scratch owned by the caller.
