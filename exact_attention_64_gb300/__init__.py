@@ -467,8 +467,11 @@ def _native():
         try:
             from . import _binding
         except ImportError as e:
+            from .build import BINDING_ERROR
+
+            why = BINDING_ERROR.read_text() if BINDING_ERROR.exists() else str(e)
             raise RuntimeError("the native binding is not built; run "
-                               "`python -m exact_attention_64_gb300.build`") from e
+                               f"`python -m exact_attention_64_gb300.build` ({why})") from e
         _native_mod = _binding
     return _native_mod
 

@@ -1,11 +1,13 @@
 """Builds libfa2.so (the sm_103a CUDA library behind include/fa2.h) in-tree.
 
 Every CUDA translation unit under csrc/ is compiled by nvcc for sm_103a in
-parallel, then linked into exact_attention_64_gb300/libfa2.so; csrc/binding.cpp,
-the native Python entry points of the per-token calls, is compiled by g++ beside
-them and linked against it as exact_attention_64_gb300/_binding.so. A rebuild
-only happens when a source or header is newer than the libraries, or when the
-binding was built for another PyTorch or Python.
+parallel, then linked into exact_attention_64_gb300/libfa2.so. That needs nothing
+but CUDA's toolkit. csrc/binding.cpp, the native Python entry points of the
+per-token calls, is compiled by g++ beside them and linked against it as
+exact_attention_64_gb300/_binding.so, where PyTorch is installed; if that fails the
+library is there all the same, a warning says why, and the calls that need the
+binding raise. Each is rebuilt only when one of its sources or headers is newer, the
+binding also when it was built for another PyTorch or Python.
 """
 
 from __future__ import annotations
@@ -14,16 +16,19 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 ROOT = PKG.parent
+HEADER = ROOT / "include" / "fa2.h"
 BUILD = ROOT / "_build"
 LIB = PKG / "libfa2.so"
 BINDING = PKG / "_binding.so"
 BINDING_FOR = BUILD / "binding_for.txt"  # the PyTorch and Python it was built for
+BINDING_ERROR = BUILD / "binding_error.txt"  # why it could not be built
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
@@ -38,24 +43,33 @@ def _sources():
     return sorted(CSRC.glob("*.cu"))
 
 
-def _deps():
-    return (sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) +
-            sorted(CSRC.glob("*.cpp")) + [ROOT / "include" / "fa2.h"])
+def _lib_deps():
+    return sorted(CSRC.glob("*.cu")) + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + [HEADER]
 
 
-def _torch_tag() -> str:
-    import torch
+def _stale(out: Path, deps) -> bool:
+    return not out.exists() or any(p.stat().st_mtime > out.stat().st_mtime for p in deps)
 
+
+def _torch_tag():
+    """What the binding is built for, or None without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     return f"{torch.__version__} {sys.version}"
 
 
+def _binding_stale() -> bool:
+    tag = _torch_tag()
+    if tag is None:
+        return False
+    return (_stale(BINDING, [CSRC / "binding.cpp", HEADER]) or not BINDING_FOR.exists()
+            or BINDING_FOR.read_text() != tag)
+
+
 def needs_build() -> bool:
-    if not LIB.exists() or not BINDING.exists() or not BINDING_FOR.exists():
-        return True
-    if BINDING_FOR.read_text() != _torch_tag():
-        return True
-    t = min(LIB.stat().st_mtime, BINDING.stat().st_mtime)
-    return any(p.stat().st_mtime > t for p in _deps())
+    return _stale(LIB, _lib_deps()) or _binding_stale()
 
 
 def _run(cmd, what, verbose):
@@ -93,11 +107,29 @@ def _link_binding(obj: Path, verbose: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile and link libfa2.so and the native binding; returns the library's
-    path. Raises on failure."""
-    if not force and not needs_build():
+    """Compile and link libfa2.so, and the native binding where PyTorch is
+    installed; returns the library's path. Raises if the library fails, warns if
+    the binding does."""
+    lib = force or _stale(LIB, _lib_deps())
+    binding = _torch_tag() is not None and (force or _binding_stale())
+    if not lib and not binding:
         return LIB
     BUILD.mkdir(exist_ok=True)
+    with ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 1)) as ex:
+        binding_obj = ex.submit(_compile_binding, verbose) if binding else None
+        if lib:
+            _build_lib(ex, verbose)
+        if binding:
+            BINDING_ERROR.unlink(missing_ok=True)
+            try:
+                _link_binding(binding_obj.result(), verbose)
+            except (RuntimeError, OSError) as e:
+                BINDING_ERROR.write_text(str(e))
+                warnings.warn(f"the native binding was not built: {e}", RuntimeWarning, stacklevel=2)
+    return LIB
+
+
+def _build_lib(ex, verbose: bool) -> None:
     nvcc = _nvcc()
 
     def compile_one(src: Path) -> Path:
@@ -106,17 +138,12 @@ def build(force: bool = False, verbose: bool = False) -> Path:
         _run(cmd, f"nvcc failed on {src.name}", verbose)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding, verbose)
-        objs = list(ex.map(compile_one, _sources()))
-        binding_obj = binding.result()
+    objs = list(ex.map(compile_one, _sources()))
     tmp = LIB.with_suffix(".so.tmp")
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", str(tmp), *map(str, objs),
            "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
     _run(cmd, "link failed", verbose)
     os.replace(tmp, LIB)
-    _link_binding(binding_obj, verbose)
-    return LIB
 
 
 if __name__ == "__main__":
