@@ -139,3 +139,32 @@ def test_infinite_values_come_out_infinite(cuda_device, fa2_lib, dtype, n, width
         assert torch.equal(o.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
         assert torch.equal(lse, lse0)
     assert fa2_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("B,Hq,Hkv,d,n,width", [(8, 16, 4, 128, 777, 60), (4, 32, 2, 64, 500, 32),
+                                                (16, 8, 8, 128, 250, 16)])
+def test_error_in_the_mean(cuda_device, fa2_lib, dtype, B, Hq, Hkv, d, n, width):
+    """L and the weights are 32-bit sums of 32-bit terms: their errors' rms, not the
+    largest that could be. Where a weight comes from, scores are about 2 and L is
+    ln n + 1/2. A score is cut at each of d / 16 steps (2^-23 of it) and rounded with
+    its factor (2^-23); L is a sum of n / 32 terms a lane (2^-24 each), a logarithm,
+    and four roundings of L's size (2^-24); a weight has both errors, exp2's 2^-22
+    and three roundings of L's size more."""
+    c = Cache(B, Hkv, d, 16, [n] * B, dtype, seed=n, width=width)
+    q = c.query(Hq)
+    kc, vc, table, lens = c.gpu()
+    w = torch.zeros(B, Hkv, c.L, device="cuda")
+    o, lse = fa2_lib.paged_decode(q.cuda(), kc, vc, table, lens, weights=w)
+    torch.cuda.synchronize()
+    ref, lref, p = oc.paged_decode(bits64(q), bits64(c.k), bits64(c.v), c.table.numpy(), c.lens.numpy(),
+                                   float(np.float32(d ** -0.5)))
+    L, score = float(np.log(n)) + 0.5, 2 * (d / 16 + 1) * 2.0 ** -23
+    tol = score + (n / 32 + 4 * L) * 2.0 ** -24 + 2.0 ** -22
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    assert rms(bits64(lse) - lref) <= tol
+    want = np.stack(p)
+    assert rms(bits64(w)[:, :, :n] - want) <= (tol + score + 3 * L * 2.0 ** -24 + 2.0 ** -22) * rms(want)
+    # o: its rounding's own rms, whatever came before it.
+    near = bits64(torch.from_numpy(ref).to(dtype))
+    assert rms(bits64(o) - ref) <= 1.0005 * rms(near - ref)
