@@ -88,7 +88,12 @@ size_t slot_bytes(int B, int Hkv, int page_size, int max_pages) {
 }
 
 // Query heads that one item of the decode carries: 8 fill the short side of
-// its products; 16 read a group's keys half as often.
+// its products; 16 read a group's keys half as often, and cost registers and
+// products that a group of 8 would leave empty. B = 8, 8000 slots, d = 128, bf16:
+// 16 heads to a key head 22.9 us with tiles of 16 and 32.2 with tiles of 8, 9 heads
+// 29.0 and 35.6, 32 heads 22.5 and 29.7, 128 heads 51 and 71; at d = 64 15.9 and
+// 19.0, 18.8 and 21.3, 14.9 and 17.7, 29.5 and 38.9. With weights the same, but for
+// 128 heads at d = 64 (205 and 197).
 int head_tile(int g) { return g <= 8 ? 8 : 16; }
 
 // Most CTAs that a decode can use: one per unit of a full table.
@@ -104,9 +109,11 @@ int decode_ctas(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
 // It saves the join and the merges at cut ends, and costs where a CTA's one item
 // takes longer than its share would: with few items, with a last wave of CTAs
 // that leaves most of the `slots` CTAs that run at once idle, with uneven
-// lengths. Four units (256 slots at d = 128, 512 at d = 64) take 5.5 us whole
-// and 5.4 split for 8 items, 9.2 and 14.0 for 256; eight units 8.8 and 5.5 for 8
-// items, 11.0 and 13.4 for 128, 14.0 and 18.7 for 256, 22.4 and 20.9 for 320.
+// lengths. Four units (256 slots at d = 128, 512 at d = 64) take 6.1 us whole
+// and 6.1 split for 8 items, 9.2 and 15.1 for 256; eight units 9.6 and 6.1 for 8
+// items, 11.7 and 14.5 for 128, 14.0 and 19.3 for 256, 22.9 and 22.5 for 320 (d =
+// 128). The table's width decides, lengths being known on the device only: the
+// same 256 items of 256 slots in a table of 8192 are split, 14.9 us.
 // With weights a CTA has to have all heads of its key head.
 bool decode_whole(int B, int Hkv, int d, int page_size, int max_pages, int HG, int slots, bool weights) {
   const long long unit = fa2::decode_unit(d), units = (static_cast<long long>(page_size) * max_pages + unit - 1) / unit;

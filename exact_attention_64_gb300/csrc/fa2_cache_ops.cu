@@ -5,9 +5,9 @@ namespace fa2 {
 
 // ---- Append ----------------------------------------------------------------
 // New token i of sequence b and key head h goes to slot lens[b] + i. A copy:
-// bound by HBM for prompts (521 MB in 85 us, 6.15 TB/s, at B = 4, 32 heads of up
+// bound by HBM for prompts (521 MB in 84 us, 6.17 TB/s, at B = 4, 32 heads of up
 // to 8192 tokens, d = 128) and by three dependent reads for single tokens (256
-// heads in 2.8 us). One thread moves 16 bytes of K and of V; consecutive threads
+// heads in 3.0 us). One thread moves 16 bytes of K and of V; consecutive threads
 // walk a row. One row per thread: two, four and eight per thread, their loads in
 // flight together, took 90, 128 and 207 us and 3.4, 4.4 and 6.5 us.
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
@@ -79,20 +79,21 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // Selection: the key becomes a 32-bit integer of the same order, and the
 // budget-th largest is found digit by digit, 8 bits a pass, from histograms,
 // until all keys that share the digits so far stay: after the third pass as a
-// rule (2 heads of 16384 slots 14.5 us back to back, 15.3 with a fourth pass always).
+// rule (2 heads of 16384 slots 13.1 us back to back, 14.5 with a fourth pass always).
 // (The first digit counted in 4 to 16 copies, against collisions: 0.3 us slower.
-// Three passes of 11 bits and fewer collisions: no faster in one CTA, and 17
-// against 12 us in a cluster of 8, whose CTAs read each other's counters.) A
+// Three passes of 11 bits and fewer collisions, before the early launches: no
+// faster in one CTA, and 17 against 12 us in a cluster of 8, whose CTAs read each
+// other's counters.) A
 // (sequence, key head) is the work of one cluster, a warp has a run of its
 // slots, and the keys stay in registers, so that weights and positions are
 // read once; the histograms of a pass are added up through distributed shared
 // memory. Integer counts: the result does not depend on any order. Rows too
 // long for the registers of a cluster keep their keys in its shared memory
-// (keys in shared memory throughout: 19 us for 128 heads of 8192 slots, against
-// 15), and past that make them again from global memory. One slot too
-// many, the steady state of a bounded cache, needs no histogram: the smallest
-// key goes, of equal ones the highest slot (5.8 us for 256 heads of 2049 slots,
-// against 12.3).
+// (keys in shared memory throughout: 56.0 us for 128 heads of 8192 slots cut to
+// 2048, against 51.4; 2 heads of 16384 15.1 and 13.1), and past that make them again
+// from global memory. One slot too many, the steady state of a bounded cache, needs
+// no histogram: the smallest key goes, of equal ones the highest slot (4.4 us for
+// 256 heads of 2049 slots in a table of 2064, against 8.4).
 //
 // Moves: a warp takes 8 at a time, so that 4 KiB per warp are in flight. A few
 // moves per row (a cache that is one token over) are made by the cluster that
@@ -100,7 +101,10 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
 // moves, because the clusters of a wave find theirs at the same time and would
 // leave the memory idle until then. (32 moves per warp, looked up at once and
 // copied four rows at a time with four more on their way: no faster for 128
-// heads of 8192 slots, 14.0 us against 13.0 for 2 of 16384.)
+// heads of 8192 slots, 14.0 us against 13.0 for 2 of 16384.) What "many" is goes by
+// the list's capacity, min(budget, L - budget), and so by the table: the 256 heads
+// of 2049 slots take 11.3 us in a table of 4096 and 17.4 in one of 8192, for a second
+// launch that finds one move each, and for clusters of two.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictRegs = 8;      // keys a thread can hold: 4096 slots per CTA
@@ -482,7 +486,8 @@ cudaError_t launch_cache_evict(const EvictArgs& a0, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.c.B) * a.c.Hkv;
   // CTAs per (sequence, key head): doubled from 1 to 8 while a CTA has more
   // slots than its registers take. More CTAs than that cost more in cluster
-  // barriers than they save: 2 heads of 16384 slots 13.0 us with 4, 13.7 with 8.
+  // barriers than they save: 2 heads of 16384 slots 13.1 us with 4, 14.0 with 8; 128
+  // of 8192 51.4 with 2, 60.9 with 4.
   constexpr int kReg = kEvictThreads * kEvictRegs;
   const auto share = [&](int C) {  // slots of a CTA
     const int run = (((a.c.L + C - 1) / C + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;

@@ -26,7 +26,8 @@
 // N = 2048: 50 us against 56 with one issuer in fixed order; with a lock that
 // keeps the two from issuing at once 85).
 //
-// At B = 2, H = 16, N = 8192, d = 128 it takes 210 us causal and 371 not causal.
+// At B = 2, H = 16, N = 8192, d = 128 it takes 211 to 223 us causal and 371 to 390
+// not causal, by the clock that the power limit leaves; d = 64: 179 and 336.
 // The other orientation, lane = query with a thread's 64 sums in registers, takes
 // 236 and 431 there, and 51 at the N = 2048 above. Also not kept: eight compute warps with 64 columns in
 // flight (272 us, two warps per scheduler), S in halves of 128 queries with a

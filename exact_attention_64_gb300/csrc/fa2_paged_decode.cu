@@ -4,10 +4,11 @@
 //   lens[b] slots of a sequence; with weights also
 //   w_out[j] = w_in[j] + sum over the query heads of a key head of e^(s_j - L).
 //
-// What bounds it: every cached K and V byte is read once for 4 g flop per
-// element (g query heads share a key head), so HBM. What a design has to give
-// is bytes in flight and an even share of the cache for every SM whatever the
-// lengths; the arithmetic only has to stay out of the way.
+// What bounds it: every cached K and V byte is read once for up to 16 query heads
+// of a key head (once more for each further 16) and 4 flop per element and head,
+// so HBM. What a design has to give is bytes in flight and an even share of the
+// cache for every SM whatever the lengths; the arithmetic only has to stay out of
+// the way.
 //
 // Short tables (see the rule at the launch): a CTA has one item, the slots of one
 // (sequence, key head), and there is nothing to join and no second launch.
@@ -49,8 +50,8 @@ constexpr int kUnit = decode_unit(D);
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr float kLog2ef = 1.4426950408889634f;
 
-// `pol`: the cache is read once, so its lines leave L2 first; what the join
-// reads again (logits, partial results) stays.
+// `pol`: the cache is read once (by a group of up to 16 heads), so its lines leave
+// L2 first; what the join reads again (logits, partial results) stays.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));

@@ -302,7 +302,8 @@ int fa2_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, 
  *                      order, and each head has kept other tokens).
  *   d, dtype         : as in fa2_fwd. Query heads: Hq = g * Hkv, g <= 128; query
  *                      head x reads key head x / g. B, Hq, Hkv <= 65535;
- *                      num_pages * Hkv * page_size < 2^31; L <= 2^30.
+ *                      B * Hkv < 2^27; num_pages * Hkv * page_size < 2^31;
+ *                      L <= 2^30.
  *
  * Lengths, counts and pages are read on the device, so a captured graph follows
  * them. A page number outside 0 .. num_pages - 1 is not followed: its slots
@@ -322,7 +323,11 @@ int fa2_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, 
  *   weights_out : may be weights itself.
  *   workspace   : device, >= fa2_paged_decode_workspace_size(...) bytes,
  *                 256-byte aligned, scratch owned by the caller.
- * The result does not depend on timing: repeated calls give the same bits. */
+ * P is not rounded before its product with V (fp16: to 2^-21 of itself), so o
+ * carries the rounding to dtype and errors of fp32's size. An infinite V entry of a
+ * slot that weighs anything gives an infinite o. The cache is read once for each 16
+ * query heads of a key head. The result does not depend on timing: repeated calls
+ * give the same bits. */
 int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, const int* table,
                      const int* lens, const float* weights, float* weights_out, void* o, float* lse,
                      int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
@@ -339,6 +344,7 @@ size_t fa2_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_s
  *   k, v        : device [B][Hkv][T][d] dtype, 16-byte aligned (a prompt as
  *                 fa2_fwd takes it, or T = 1).
  *   num_new     : device int32 [B], 0 .. T (a padded batch), or NULL: T each.
+ *                 B * Hkv * T < 2^31.
  *   weights     : or NULL; the new slots get new_weights[B][Hkv][T] (fp32; for a
  *                 prompt, fa2_key_weights), or 0 if that is NULL.
  *   positions   : or NULL; the new slots get next_pos[b] + i (int32 [B]).
