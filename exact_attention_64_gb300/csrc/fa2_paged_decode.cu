@@ -116,9 +116,10 @@ constexpr uint32_t kLow16 = 0x5410u, kHigh16 = 0x7632u;  // both low, both high 
 // B = 8, 32/8 heads of 2000 slots, 30.6 and 31.8 for B = 16, 64/4 heads of 4000; the
 // tf32 form below took 18.0 and 33.7.)
 //
-// A piece after the first is never 0: it would make 0 * inf = NaN of an infinite V.
-// The smallest normal number in its place adds nothing that a 16-bit V shows.
-constexpr float kLeastPiece = 1.17549435e-38f;
+// A piece after the first is positive where p is: 0 would make 0 * inf = NaN of an
+// infinite V. At least 2^-40 of p, it adds nothing that shows; a slot that weighs
+// nothing adds nothing.
+constexpr float kLeastPiece = 9.094947e-13f;
 
 __device__ __forceinline__ float high_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_high(float x, float y) {
@@ -138,7 +139,7 @@ struct ProbT<true> {
       b[i][0] = transpose8(pack_high(r[0], r[1]));
       b[i][1] = transpose8(pack_high(r[2], r[3]));
 #pragma unroll
-      for (int y = 0; y < 4; ++y) r[y] = fmaxf(r[y] - high_bf16(r[y]), kLeastPiece);
+      for (int y = 0; y < 4; ++y) r[y] = fmaxf(r[y] - high_bf16(r[y]), p[y] * kLeastPiece);
     }
   }
   __device__ __forceinline__ void add(float (&o)[4], const uint32_t (&va)[4]) const {
@@ -168,7 +169,7 @@ struct ProbT<false> {
       for (int j = 0; j < 2; ++j) {
         const uint32_t z = __byte_perm(u, v, j == 0 ? kLow16 : kHigh16);
         hi[2 * i + j] = high_tf32(__uint_as_float(z));
-        lo[2 * i + j] = high_tf32(fmaxf(__uint_as_float(z) - hi[2 * i + j], kLeastPiece));
+        lo[2 * i + j] = high_tf32(fmaxf(__uint_as_float(z) - hi[2 * i + j], __uint_as_float(z) * kLeastPiece));
       }
     }
   }

@@ -168,3 +168,33 @@ def test_error_in_the_mean(cuda_device, fa2_lib, dtype, B, Hq, Hkv, d, n, width)
     # o: its rounding's own rms, whatever came before it.
     near = bits64(torch.from_numpy(ref).to(dtype))
     assert rms(bits64(o) - ref) <= 1.0005 * rms(near - ref)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("n,width", [(30, 4), (600, 80)])
+def test_a_slot_that_weighs_nothing_adds_nothing(cuda_device, fa2_lib, dtype, n, width):
+    """Scores of -inf beside values as large as the type has: o is exactly what the
+    other slots, whose V is 0, make of it; and a slot that weighs little adds no more
+    than that."""
+    d = 64
+    c = Cache(1, 2, d, 16, [n], dtype, seed=n, width=width)
+    j = torch.arange(n)
+    page, off = c.table[0].long()[j // 16], j % 16
+    c.k[page, :, off], c.v[page, :, off] = 0.0, 0.0
+    heavy = torch.arange(0, n, 7)
+    c.k[page[heavy], 0, off[heavy], 0] = -float("inf")
+    c.k[page[heavy], 1, off[heavy], 0] = -100.0
+    c.v[page[heavy], :, off[heavy]] = torch.finfo(dtype).max
+    kc, vc, table, lens = c.gpu()
+    q = torch.zeros(1, 2, d, dtype=dtype)
+    q[:, :, 0] = 1.0
+    o, lse = fa2_lib.paged_decode(q.cuda(), kc, vc, table, lens, scale=0.5)
+    torch.cuda.synchronize()
+    assert fa2_lib.device_status() == 0
+    assert (o[0, 0] == 0).all()
+    light = n - len(heavy)
+    # e^-50 of each heavy one; what is left out of p or added to it is below 2^-20 of it.
+    want = len(heavy) * np.exp(-50.0) * torch.finfo(dtype).max / light
+    tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    assert (np.abs(bits64(o[0, 1]) - want) <= want * (torch.finfo(dtype).eps + 2.0 ** -12) + tiny).all()
+    assert abs(float(lse[0, 0]) - np.log(light)) < 1e-5
