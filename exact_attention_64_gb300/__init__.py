@@ -34,6 +34,10 @@ __all__ = [
     "cache_append",
     "cache_evict",
     "key_weights",
+    "rotary",
+    "rotary_forward",
+    "rotary_backward",
+    "rotary_frequencies",
     "fwd_grid",
     "fwd_block_work",
     "fwd_schedule",
@@ -100,6 +104,9 @@ def load_library() -> ctypes.CDLL:
         "fa2_cache_evict_workspace_size": (sz, [i] * 5),
         "fa2_key_weights": (i, [vp] * 5 + [i] * 7 + [f, i, vp, sz, vp]),
         "fa2_key_weights_workspace_size": (sz, []),
+        "fa2_rotary_fwd": (i, [vp] * 9 + [i] * 8 + [f, f, i, i, vp]),
+        "fa2_rotary_bwd": (i, [vp] * 13 + [i] * 8 + [f, f, i, i, vp, sz, vp]),
+        "fa2_rotary_bwd_workspace_size": (sz, [i] * 6),
         "fa2_get_device_status": (i, [vp]),
         "fa2_status_string": (ctypes.c_char_p, [i]),
         "fa2_fwd_grid": (i, [i, i, i, _c_int_p, _c_int_p]),
@@ -538,3 +545,118 @@ def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_l
     ``cache_evict`` take.
     """
     return (_native_mod or _native()).key_weights(q, k, lse, causal, scale, q_lens, out, workspace)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0, method: str = "linear",
+                       original: int = 8192, low: float = 1.0, high: float = 4.0, device=None):
+    """Radians per position of each pair, float64 ``[rotary_dim / 2]``: what
+    ``rotary`` takes as ``freqs``.
+
+    f_j = base^(-2j / rotary_dim), stretched for contexts ``factor`` times longer
+    than the ``original`` one: "linear" divides every frequency by factor; "base"
+    raises the base so that the slowest is divided by it and the fastest kept;
+    "bands" keeps a pair that makes at least ``high`` turns in the original context,
+    divides one of at most ``low`` turns, and blends the two in between.
+    """
+    if rotary_dim < 2 or rotary_dim % 2 or base <= 0 or factor <= 0:
+        raise ValueError("needs an even rotary_dim >= 2, base > 0 and factor > 0")
+    e = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    if method == "base":
+        if rotary_dim == 2:
+            raise ValueError("method 'base' needs more than one pair")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = torch.tensor(base, dtype=torch.float64) ** -e
+    if method == "linear":
+        f = f / factor
+    elif method == "bands":
+        if not high > low:
+            raise ValueError("needs high > low")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    elif method != "base":
+        raise ValueError("method must be 'linear', 'base' or 'bands'")
+    return f.to(device) if device is not None else f
+
+
+def rotary_forward(q, k, freqs, positions=None, interleaved: bool = False, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, amplitude: float = 1.0, q_out=None, k_out=None):
+    """Queries and keys turned by their positions, with ``q_weight`` and ``k_weight``
+    normed per head first (fa2_rotary_fwd).
+
+    q ``[B, Hq, N, d]``, k ``[B, Hkv, N, d]`` or None: any strides with contiguous
+    rows, such as a projection's ``[B, N, H, d]`` output transposed. freqs float64
+    ``[r / 2]`` (``rotary_frequencies``): the first r elements of a head are turned,
+    as pairs (j, j + r / 2), or (2j, 2j + 1) if interleaved. positions int32 ``[B]``
+    (of each sequence's first token) or ``[B, N]``; None: 0 .. N - 1. Weights ``[d]``
+    of q's type or float32. amplitude multiplies the turned elements. Returns
+    (q_out, k_out), contiguous unless given.
+    """
+    return (_native_mod or _native()).rotary_forward(q, k, freqs, positions, interleaved, q_weight, k_weight, eps,
+                                                     amplitude, q_out, k_out)
+
+
+def rotary_backward(dq, dk, freqs, positions=None, interleaved: bool = False, q=None, k=None, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, amplitude: float = 1.0, q_grad=None, k_grad=None,
+                    workspace=None):
+    """Gradients (q_grad, k_grad, q_weight_grad, k_weight_grad) of ``rotary_forward``
+    given those of its outputs; the last two None without weights, which need q and
+    k. New gradients are laid out like q and k if these are given (without weights
+    they serve for nothing else), else contiguous.
+    """
+    return (_native_mod or _native()).rotary_backward(dq, dk, freqs, positions, interleaved, q, k, q_weight, k_weight,
+                                                      eps, amplitude, q_grad, k_grad, workspace)
+
+
+def _rows16(t):
+    """t with rows that the kernels can read: contiguous, 16-byte steps."""
+    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(n == 1 or s % 8 == 0 for n, s in
+                                                             zip(t.shape[:3], t.stride()[:3]))
+    return t if ok else t.contiguous()
+
+
+class _RotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude):
+        ctx.set_materialize_grads(False)
+        norm = q_weight is not None
+        ctx.save_for_backward(freqs, positions, q_weight, k_weight, *((q, k) if norm else (None, None)))
+        ctx.options = (interleaved, eps, amplitude)
+        # Gradients are laid out like the inputs.
+        ctx.token_major = [t is not None and t.stride(2) > t.stride(1) for t in (q, k)]
+        return rotary_forward(q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        freqs, positions, *rest = ctx.saved_tensors
+        weights, inputs = rest[:2], rest[2:]
+        interleaved, eps, amplitude = ctx.options
+        out, w_out = [None, None], [None, None]
+        todo = [i for i in (0, 1) if grads[i] is not None]
+        if not todo:
+            return (None,) * 9
+        grads = [None if g is None else _rows16(g) for g in grads]
+        like = []
+        for i in (0, 1):
+            t = None
+            if grads[i] is not None:
+                B, H, N, d = grads[i].shape
+                t = (grads[i].new_empty(B, N, H, d).transpose(1, 2) if ctx.token_major[i] else
+                     grads[i].new_empty(B, H, N, d))
+            like.append(t)
+        if len(todo) == 2:
+            out[0], out[1], w_out[0], w_out[1] = rotary_backward(
+                grads[0], grads[1], freqs, positions, interleaved, *inputs, *weights, eps, amplitude, *like)
+        else:
+            i = todo[0]
+            out[i], _, w_out[i], _ = rotary_backward(grads[i], None, freqs, positions, interleaved, inputs[i], None,
+                                                     weights[i], None, eps, amplitude, like[i])
+        return out[0], out[1], None, None, None, w_out[0], w_out[1], None, None
+
+
+def rotary(q, k, freqs, positions=None, interleaved: bool = False, q_weight=None, k_weight=None,
+           eps: float = 1e-6, amplitude: float = 1.0):
+    """Differentiable ``rotary_forward``: gradients of q, k and the weights."""
+    return _RotaryFunction.apply(q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude)

@@ -1,5 +1,5 @@
 // Python entry points of the calls that generation makes once per token
-// (paged_decode, cache_append, cache_evict, key_weights): argument checks,
+// (paged_decode, cache_append, cache_evict, key_weights, rotary_*): argument checks,
 // output and workspace tensors, and the C ABI call, in one step of native code.
 // Such a call takes a few microseconds on the GPU, and marshalling it in Python
 // took about three times as long. Like the rest of the binding it only
@@ -292,9 +292,176 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A [B, H, N, d] tensor of any strides whose rows are contiguous: its address, and
+// its strides of batch, head and token into `st`.
+void* need_rows(const char* name, const Tensor& t, Sizes shape, at::ScalarType type, int dev, long long* st) {
+  const auto s = t.sizes();
+  if (!t.is_cuda() || t.get_device() != dev)
+    value_error(std::string(name) + " must be a CUDA tensor on cuda:" + std::to_string(dev < 0 ? 0 : dev));
+  if (s.size() != 4 || !std::equal(s.begin(), s.end(), shape.begin()) || t.scalar_type() != type) {
+    std::string m = std::string(name) + " must have shape (";
+    for (const int64_t x : shape) m += std::to_string(x) + ", ";
+    m.resize(m.size() - 2);
+    value_error(m + ") and dtype " + c10::toString(type));
+  }
+  if (t.stride(3) != 1) value_error(std::string(name) + " must have contiguous rows");
+  for (int i = 0; i < 3; ++i) st[i] = s[i] > 1 ? t.stride(i) : 0;
+  return t.data_ptr();
+}
+
+struct Rotary {
+  int B, Hq, Hk, N, d, r, pos_mode, interleaved, dtype, wtype, dev;
+  at::ScalarType type, weight;
+  float eps, amplitude;
+  const double* freqs;
+  const int* positions;
+  void *qw, *kw;
+};
+
+float float_of(PyObject* o) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) throw python_error();
+  return static_cast<float>(x);
+}
+
+// The arguments that both directions share; q and k: the tensors to turn.
+Rotary rotary_of(const Tensor& q, PyObject* ko, PyObject* fo, PyObject* po, PyObject* inter, PyObject* qw, PyObject* kw,
+                 PyObject* eps, PyObject* amp) {
+  if (!q.is_cuda()) value_error("q must be a CUDA tensor");
+  if (q.dim() != 4) value_error("expected a [B, H, N, d] tensor");
+  Rotary a{};
+  a.dtype = dtype_code("q", q);
+  a.type = q.scalar_type();
+  a.dev = q.get_device();
+  a.B = as_int("B", q.size(0));
+  a.Hq = as_int("Hq", q.size(1));
+  a.N = as_int("N", q.size(2));
+  a.d = as_int("d", q.size(3));
+  if (ko != Py_None) {
+    const Tensor& k = tensor("k", ko);
+    if (k.dim() != 4) value_error("expected a [B, H, N, d] tensor");
+    a.Hk = as_int("Hkv", k.size(1));
+    if (a.Hk == 0) value_error("k has no heads");
+  }
+  const Tensor& f = tensor("freqs", fo);
+  if (f.dim() != 1) value_error("freqs must be one-dimensional");
+  a.r = as_int("rotary_dim", 2 * f.size(0));
+  a.freqs = need<double>("freqs", f, {f.size(0)}, at::kDouble, a.dev);
+  if (po != Py_None) {
+    const Tensor& p = tensor("positions", po);
+    a.pos_mode = p.dim() == 2 ? 2 : 1;
+    a.positions = a.pos_mode == 2 ? need<int>("positions", p, {a.B, a.N}, at::kInt, a.dev)
+                                  : need<int>("positions", p, {a.B}, at::kInt, a.dev);
+  }
+  a.interleaved = PyObject_IsTrue(inter);
+  if (a.interleaved < 0) throw python_error();
+  if ((qw == Py_None) != (kw == Py_None) && ko != Py_None) value_error("q_weight and k_weight go together");
+  if (ko == Py_None && kw != Py_None) value_error("k_weight needs k");
+  a.weight = a.type;
+  if (qw != Py_None) {
+    const Tensor& w = tensor("q_weight", qw);
+    if (w.scalar_type() == at::kFloat) a.weight = at::kFloat;
+    a.qw = need("q_weight", w, {a.d}, a.weight, a.dev);
+    if (kw != Py_None) a.kw = need("k_weight", tensor("k_weight", kw), {a.d}, a.weight, a.dev);
+  }
+  a.wtype = a.weight == at::kFloat ? FA2_FP32 : a.dtype;
+  a.eps = float_of(eps);
+  a.amplitude = float_of(amp);
+  return a;
+}
+
+// The caller's strided tensor, or a new one laid out like `like` (or contiguous).
+Tensor rows_output(const char* name, PyObject* o, Sizes shape, const Rotary& a, const Tensor* like, long long* st) {
+  const Tensor t = o != Py_None ? tensor(name, o)
+                   : like != nullptr
+                       ? at::empty_like(*like)
+                       : at::empty(at::IntArrayRef(shape.begin(), shape.size()),
+                                   at::TensorOptions().dtype(a.type).device(at::kCUDA, static_cast<c10::DeviceIndex>(a.dev)));
+  need_rows(name, t, shape, a.type, a.dev, st);
+  return t;
+}
+
+PyObject* pack_results(std::initializer_list<const Tensor*> ts) {
+  PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (r == nullptr) throw python_error();
+  Py_ssize_t i = 0;
+  for (const Tensor* t : ts) {
+    PyObject* x = Py_None;
+    if (t->defined()) x = THPVariable_Wrap(*t);
+    else Py_INCREF(x);
+    PyTuple_SET_ITEM(r, i++, x);
+  }
+  return r;
+}
+
+// q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude, q_out, k_out
+PyObject* rotary_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arity(n, 11)) return nullptr;
+  const Tensor& q = tensor("q", a[0]);
+  const Rotary r = rotary_of(q, a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]);
+  long long st[12] = {};
+  const Sizes qs = {r.B, r.Hq, r.N, r.d}, ks = {r.B, r.Hk, r.N, r.d};
+  const void* qp = need_rows("q", q, qs, r.type, r.dev, st);
+  const void* kp = r.Hk > 0 ? need_rows("k", tensor("k", a[1]), ks, r.type, r.dev, st + 3) : nullptr;
+  if (r.Hk == 0 && a[10] != Py_None) value_error("k_out needs k");
+  const Tensor qo = rows_output("q_out", a[9], qs, r, nullptr, st + 6);
+  Tensor ko;
+  if (r.Hk > 0) ko = rows_output("k_out", a[10], ks, r, nullptr, st + 9);
+  void *qop = qo.data_ptr(), *kop = r.Hk > 0 ? ko.data_ptr() : nullptr;
+  run("fa2_rotary_fwd", r.dev, [&](void* stream) {
+    return fa2_rotary_fwd(qp, kp, r.freqs, r.positions, r.qw, r.kw, qop, kop, st, r.B, r.Hq, r.Hk, r.N, r.d, r.r,
+                          r.pos_mode, r.interleaved, r.eps, r.amplitude, r.dtype, r.wtype, stream);
+  });
+  return pack_results({&qo, &ko});
+  END_HANDLE_TH_ERRORS
+}
+
+// dq, dk, freqs, positions, interleaved, q, k, q_weight, k_weight, eps, amplitude, q_grad, k_grad, workspace
+PyObject* rotary_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arity(n, 14)) return nullptr;
+  const Tensor& dq = tensor("dq", a[0]);
+  const Rotary r = rotary_of(dq, a[1], a[2], a[3], a[4], a[7], a[8], a[9], a[10]);
+  const bool norm = r.qw != nullptr, both = r.Hk > 0;
+  if (norm && (a[5] == Py_None || (both && a[6] == Py_None))) value_error("the gradients of a norm need q and k");
+  if (!both && (a[6] != Py_None || a[12] != Py_None)) value_error("k and k_grad need dk");
+  long long st[18] = {};
+  const Sizes qs = {r.B, r.Hq, r.N, r.d}, ks = {r.B, r.Hk, r.N, r.d};
+  const void* dqp = need_rows("dq", dq, qs, r.type, r.dev, st);
+  const void* dkp = both ? need_rows("dk", tensor("dk", a[1]), ks, r.type, r.dev, st + 3) : nullptr;
+  // Without a norm q and k only say how the new gradients are laid out.
+  const Tensor* ql = a[5] != Py_None ? &tensor("q", a[5]) : nullptr;
+  const Tensor* kl = both && a[6] != Py_None ? &tensor("k", a[6]) : nullptr;
+  const void* qp = ql != nullptr ? need_rows("q", *ql, qs, r.type, r.dev, st + 6) : nullptr;
+  const void* kp = kl != nullptr ? need_rows("k", *kl, ks, r.type, r.dev, st + 9) : nullptr;
+  const Tensor qg = rows_output("q_grad", a[11], qs, r, ql, st + 12);
+  Tensor kg, qwg, kwg;
+  if (both) kg = rows_output("k_grad", a[12], ks, r, kl, st + 15);
+  Space ws{};
+  if (norm) {
+    const auto opt = at::TensorOptions().dtype(r.weight).device(at::kCUDA, static_cast<c10::DeviceIndex>(r.dev));
+    qwg = at::empty({r.d}, opt);
+    if (both) kwg = at::empty({r.d}, opt);
+    ws = workspace(a[13], fa2_rotary_bwd_workspace_size(r.B, r.Hq, r.Hk, r.N, r.d, 1), "fa2_rotary_bwd_workspace_size",
+                   r.dev);
+  }
+  void *qgp = qg.data_ptr(), *kgp = both ? kg.data_ptr() : nullptr;
+  void *qwp = norm ? qwg.data_ptr() : nullptr, *kwp = norm && both ? kwg.data_ptr() : nullptr;
+  void* wp = norm ? ws.t.data_ptr() : nullptr;
+  run("fa2_rotary_bwd", r.dev, [&](void* stream) {
+    return fa2_rotary_bwd(dqp, dkp, norm ? qp : nullptr, norm ? kp : nullptr, r.freqs, r.positions, r.qw, r.kw, qgp, kgp,
+                          qwp, kwp, st, r.B, r.Hq, r.Hk, r.N, r.d, r.r, r.pos_mode, r.interleaved, r.eps, r.amplitude,
+                          r.dtype, r.wtype, wp, ws.bytes, stream);
+  });
+  return pack_results({&qg, &kg, &qwg, &kwg});
+  END_HANDLE_TH_ERRORS
+}
+
 #define FA2_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FA2_METHOD(paged_decode), FA2_METHOD(cache_append), FA2_METHOD(cache_evict),
-                           FA2_METHOD(key_weights), {nullptr, nullptr, 0, nullptr}};
+                           FA2_METHOD(key_weights), FA2_METHOD(rotary_forward), FA2_METHOD(rotary_backward),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -60,7 +60,8 @@ typedef enum fa2_status {
                                  count outside the cache (see "Paged key-value cache") */
 } fa2_status;
 
-typedef enum fa2_dtype { FA2_FP16 = 0, FA2_BF16 = 1 } fa2_dtype;
+/* FA2_FP32: the norm weights of fa2_rotary_fwd and fa2_rotary_bwd only. */
+typedef enum fa2_dtype { FA2_FP16 = 0, FA2_BF16 = 1, FA2_FP32 = 2 } fa2_dtype;
 
 /* Forward pass (FlashAttention-2 forward: Q rows outer, K/V tiles inner, online
  * softmax with running max m and sum l, one division by l at the end, only
@@ -403,6 +404,60 @@ int fa2_key_weights(const void* q, const void* k, const float* lse, const int* q
                     void* workspace, size_t workspace_bytes, void* stream);
 
 size_t fa2_key_weights_workspace_size(void);
+
+/* ---- Rotary positions -------------------------------------------------------
+ * Queries and keys turned by their positions, as attention expects them, from a
+ * projection's output in its own layout; with weights, each head's row is normed
+ * first, in the same pass. For a row x of d elements at position p:
+ *   n = (mean(x^2) + eps)^(-1/2),  u_i = x_i n weight_i     (no weights: u = x)
+ *   y_a = amplitude (u_a cos t - u_b sin t),  y_b = amplitude (u_b cos t + u_a sin t),
+ *   t = p freqs[j]
+ * for the pairs j < rotary_dim / 2, with (a, b) = (j, j + rotary_dim / 2), or
+ * (2j, 2j + 1) if interleaved; y_i = u_i for i >= rotary_dim. Sums and angles are
+ * not rounded below 32 bits (an angle is exact to 2^-31 turns at any position), y is
+ * rounded once. The sum of squares of a row has to be finite in fp32.
+ *   q, k          : device [B][Hq][N][d], [B][Hk][N][d] dtype, rows of d contiguous
+ *                   elements, 16-byte aligned, other strides below. k may be NULL
+ *                   (Hk = 0, and nothing that belongs to it).
+ *   freqs         : device fp64 [rotary_dim / 2], radians per position, finite.
+ *   positions     : device int32; position_mode 0: NULL, token i of every sequence is
+ *                   at position i; 1: [B], at positions[b] + i; 2: [B][N]. Positions
+ *                   fit in 31 bits and a sign.
+ *   q_weight, k_weight : device [d] of weight_dtype (dtype or FA2_FP32), 16-byte
+ *                   aligned; both (k_weight with k) or neither.
+ *   q_out, k_out  : like q and k, written. Their rows must not overlap, nor anything
+ *                   that is read; q_out and k_out may be heads side by side in one
+ *                   buffer.
+ *   strides       : host, 12 element strides: batch, head and token of q, k, q_out and
+ *                   k_out; >= 0, multiples of 8 (that of a dimension of size 1 is not
+ *                   used). An input's stride may be 0.
+ *   rotary_dim    : a multiple of 16, 16 .. d.   d: 64 or 128.   eps: >= 0.
+ *   limits        : B, Hq, Hk <= 65535; B * N * (ceil(Hq / 4) + ceil(Hk / 4)) < 2^31. */
+int fa2_rotary_fwd(const void* q, const void* k, const double* freqs, const int* positions, const void* q_weight,
+                   const void* k_weight, void* q_out, void* k_out, const long long* strides, int B, int Hq, int Hk,
+                   int N, int d, int rotary_dim, int position_mode, int interleaved, float eps, float amplitude,
+                   int dtype, int weight_dtype, void* stream);
+
+/* Gradients of fa2_rotary_fwd. With g the gradient of y turned back by -t (and
+ * amplitude), per row
+ *   weight_grad_i = sum over rows of g_i x_i n,
+ *   x_grad_i = n (weight_i g_i - x_i n mean_k(weight_k g_k x_k n));  no weights: x_grad = g.
+ *   dq, dk           : gradients of q_out and k_out.
+ *   q, k             : the forward's inputs; NULL without weights.
+ *   q_grad, k_grad   : written; layout rules of q_out and k_out.
+ *   q_weight_grad, k_weight_grad : device [d] of weight_dtype, written; with weights.
+ *   strides          : host, 18: of dq, dk, q, k, q_grad and k_grad.
+ *   workspace        : device, >= fa2_rotary_bwd_workspace_size(...) bytes, 256-byte
+ *                      aligned, scratch owned by the caller; without weights unused.
+ * Repeated calls give the same bits. */
+int fa2_rotary_bwd(const void* dq, const void* dk, const void* q, const void* k, const double* freqs,
+                   const int* positions, const void* q_weight, const void* k_weight, void* q_grad, void* k_grad,
+                   void* q_weight_grad, void* k_weight_grad, const long long* strides, int B, int Hq, int Hk, int N,
+                   int d, int rotary_dim, int position_mode, int interleaved, float eps, float amplitude, int dtype,
+                   int weight_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fa2_rotary_bwd; norm: with weights. 0 for invalid sizes. */
+size_t fa2_rotary_bwd_workspace_size(int B, int Hq, int Hk, int N, int d, int norm);
 
 /* Synchronises `stream`, then returns and clears the current device's status
  * word: FA2_OK, or FA2_ERR_DEVICE_TIMEOUT if any kernel since the last call
