@@ -33,6 +33,7 @@ __all__ = [
     "paged_decode",
     "cache_append",
     "cache_evict",
+    "cache_resize",
     "key_weights",
     "rotary",
     "rotary_forward",
@@ -102,6 +103,8 @@ def load_library() -> ctypes.CDLL:
         "fa2_cache_append": (i, [vp] * 12 + [i] * 8 + [vp]),
         "fa2_cache_evict": (i, [vp] * 10 + [i] * 9 + [vp, sz, vp]),
         "fa2_cache_evict_workspace_size": (sz, [i] * 5),
+        "fa2_cache_resize": (i, [vp] * 7 + [i] * 4 + [vp, sz, vp]),
+        "fa2_cache_resize_workspace_size": (sz, [i] * 4),
         "fa2_key_weights": (i, [vp] * 5 + [i] * 7 + [f, i, vp, sz, vp]),
         "fa2_key_weights_workspace_size": (sz, []),
         "fa2_rotary_fwd": (i, [vp] * 9 + [i] * 8 + [f, f, i, i, vp]),
@@ -531,6 +534,23 @@ def cache_evict(k_cache, v_cache, table, lens, weights, budget: int, recent: int
     return (_native_mod or _native()).cache_evict(k_cache, v_cache, table, lens, weights, budget, recent,
                                                   positions, next_pos, weights_out, positions_out,
                                                   lens_out, workspace)
+
+
+def cache_resize(table, lens, new_lens, refs, free_pages, num_free, page_size: int, lens_out=None,
+                 workspace=None):
+    """Gives each sequence the pages of its new length, in place: requests that
+    begin (lens 0), grow, were cut by an eviction, or end (new_lens 0).
+
+    table int32 ``[B, max_pages]``; lens, new_lens int32 ``[B]``; refs int32
+    ``[num_pages]``, how many sequences name each page; free_pages int32
+    ``[num_pages]`` and num_free int32 ``[1]``, the list of pages with none. Pages
+    past a new length are given back first; then sequences that grow take pages from
+    the list's end, in their order, while they last. Returns int32 [B]: new_lens, or
+    lens for those that found none. A program that lets several sequences name a
+    page adds to its refs.
+    """
+    return (_native_mod or _native()).cache_resize(table, lens, new_lens, refs, free_pages, num_free, page_size,
+                                                   lens_out, workspace)
 
 
 def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, q_lens=None, out=None,

@@ -262,6 +262,38 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// table, lens, new_lens, refs, free_pages, num_free, page_size, lens_out, workspace
+PyObject* cache_resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arity(n, 9)) return nullptr;
+  const Tensor &t = tensor("table", a[0]), &r = tensor("refs", a[3]);
+  if (!t.is_cuda()) value_error("table must be a CUDA tensor");
+  if (t.dim() != 2) value_error("expected a [B, max_pages] table");
+  if (r.dim() != 1) value_error("expected refs of [num_pages]");
+  const int dev = t.get_device(), B = as_int("B", t.size(0)), width = as_int("max_pages", t.size(1)),
+            pages = as_int("num_pages", r.size(0));
+  const int64_t size = PyLong_AsLongLong(a[6]);
+  if (PyErr_Occurred()) throw python_error();
+  if (size < 1) value_error("page_size must be at least 1");
+  const int ps = as_int("page_size", size);
+  int* tp = need<int>("table", t, {B, width}, at::kInt, dev);
+  const int* lp = need<int>("lens", tensor("lens", a[1]), {B}, at::kInt, dev);
+  const int* np = need<int>("new_lens", tensor("new_lens", a[2]), {B}, at::kInt, dev);
+  int* rp = need<int>("refs", r, {pages}, at::kInt, dev);
+  int* fp = need<int>("free_pages", tensor("free_pages", a[4]), {pages}, at::kInt, dev);
+  int* cp = need<int>("num_free", tensor("num_free", a[5]), {1}, at::kInt, dev);
+  const Tensor out = output("lens_out", a[7], {B}, at::kInt, dev);
+  const Space ws = workspace(a[8], fa2_cache_resize_workspace_size(B, pages, ps, width), "fa2_cache_resize_workspace_size",
+                             dev);
+  int* op = static_cast<int*>(out.data_ptr());
+  void* wp = ws.t.data_ptr();
+  run("fa2_cache_resize", dev, [&](void* stream) {
+    return fa2_cache_resize(tp, lp, np, rp, fp, cp, op, B, pages, ps, width, wp, ws.bytes, stream);
+  });
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // q, k, lse, causal, scale, q_lens, out, workspace
 PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -461,7 +493,7 @@ PyObject* rotary_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FA2_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FA2_METHOD(paged_decode), FA2_METHOD(cache_append), FA2_METHOD(cache_evict),
                            FA2_METHOD(key_weights), FA2_METHOD(rotary_forward), FA2_METHOD(rotary_backward),
-                           {nullptr, nullptr, 0, nullptr}};
+                           FA2_METHOD(cache_resize), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -198,6 +198,23 @@ struct EvictArgs {
   int cached;             // keys of a CTA's slots fit in its shared memory
 };
 
+struct ResizeArgs {
+  int* table;             // [B][max_pages]
+  const int* lens;        // [B]
+  const int* new_lens;    // [B]
+  int* refs;              // [num_pages]
+  int* free_pages;        // [num_pages]
+  int* num_free;          // [1]
+  int* lens_out;          // [B]
+  int* owner;             // workspace [num_pages]: a release of each page given back
+  int* gone;              // workspace [B * max_pages]: the page of each release
+  int B, num_pages, max_pages;
+  int L;                  // max_pages * page_size
+  int group;              // sequences per prefix sum
+  FastDiv ps;
+  int* status;
+};
+
 struct KeyWeightArgs {
   const float* lse;       // [B*Hq][N]
   const int* q_lens;      // [B] or nullptr

@@ -15,6 +15,8 @@ cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArg
                                 cudaStream_t stream);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_resize(const ResizeArgs& a, cudaStream_t stream);
+int resize_group(int B);
 cudaError_t launch_key_weights(int d, bool bf16, bool causal, const CUtensorMap& tq, const CUtensorMap& tk,
                                const KeyWeightArgs& a, int ctas, cudaStream_t stream);
 }  // namespace fa2
@@ -318,6 +320,55 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
   a.d = d;
   (void)cudaGetLastError();
   const cudaError_t e = fa2::launch_cache_evict(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
+}
+
+size_t fa2_cache_resize_workspace_size(int B, int num_pages, int page_size, int max_pages) {
+  if (check_cache(B, 1, 64, 1, page_size, max_pages, FA2_BF16) != FA2_OK || num_pages < 1) return 0;
+  if (static_cast<long long>(B) * max_pages > kMaxRows) return 0;
+  return align_up(static_cast<size_t>(num_pages) * 4, 256) + align_up(static_cast<size_t>(B) * max_pages * 4, 256);
+}
+
+int fa2_cache_resize(int* table, const int* lens, const int* new_lens, int* refs, int* free_pages, int* num_free,
+                     int* lens_out, int B, int num_pages, int page_size, int max_pages, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!table || !lens || !new_lens || !refs || !free_pages || !num_free || !lens_out) return FA2_ERR_INVALID_ARG;
+  if (num_pages < 1) return FA2_ERR_INVALID_ARG;
+  int st = check_cache(B, 1, 64, 1, page_size, max_pages, FA2_BF16);
+  if (st != FA2_OK) return st;
+  if (static_cast<long long>(B) * max_pages > kMaxRows) return FA2_ERR_UNSUPPORTED;
+  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(new_lens, 4) || !aligned(refs, 4) ||
+      !aligned(free_pages, 4) || !aligned(num_free, 4) || !aligned(lens_out, 4))
+    return FA2_ERR_ALIGNMENT;
+  const size_t need = fa2_cache_resize_workspace_size(B, num_pages, page_size, max_pages);
+  if (workspace == nullptr || workspace_bytes < need) return FA2_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FA2_ERR_ALIGNMENT;
+  const size_t lb = static_cast<size_t>(B) * 4, pb = static_cast<size_t>(num_pages) * 4;
+  const Buf ins[] = {{lens, lb}, {new_lens, lb}};
+  const Buf outs[] = {{table, static_cast<size_t>(B) * max_pages * 4}, {refs, pb}, {free_pages, pb}, {num_free, 4},
+                      {lens_out, lb}, {workspace, need}};
+  if (any_overlap(outs, ins)) return FA2_ERR_OVERLAP;
+  int sms = 0;
+  fa2::ResizeArgs a{};
+  st = fa2::host_device_setup(&sms, &a.status);
+  if (st != FA2_OK) return st;
+  a.table = table;
+  a.lens = lens;
+  a.new_lens = new_lens;
+  a.refs = refs;
+  a.free_pages = free_pages;
+  a.num_free = num_free;
+  a.lens_out = lens_out;
+  a.owner = static_cast<int*>(workspace);
+  a.gone = reinterpret_cast<int*>(static_cast<char*>(workspace) + align_up(pb, 256));
+  a.B = B;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.L = max_pages * page_size;
+  a.group = fa2::resize_group(B);
+  a.ps = fa2::fast_div(page_size);
+  (void)cudaGetLastError();
+  const cudaError_t e = fa2::launch_cache_resize(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
 }
 

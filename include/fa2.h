@@ -385,6 +385,38 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
  * most min(budget, L - budget) moves and their count. 0 for invalid sizes. */
 size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pages, int budget);
 
+/* Page tables brought from one set of lengths to another, in place: new requests
+ * (lens[b] = 0), growth, eviction and the end of a sequence (new_lens[b] = 0) alike.
+ * A sequence has the pages table[b][i], i < ceil(length / page_size).
+ *   Pages past the new length are given back: refs[page] falls by one, and a page
+ *   whose count reaches 0 goes to the free list. Then each sequence that grows takes
+ *   the pages it lacks from the end of the list, sequences in order; taken pages get
+ *   the count 1. The first sequence for which the list does not suffice, and all that
+ *   grow by pages after it, get none and keep their length. The pages that are freed
+ *   go to the list in reverse order of (sequence, page index) - of several releases of
+ *   one page the last counts - so that undoing a resize restores the list.
+ *   table       : device int32 [B][max_pages]; entries past a length are left as they
+ *                 were.
+ *   lens, new_lens : device int32 [B], 0 .. L (cut to it, FA2_ERR_PAGE).
+ *   refs        : device int32 [num_pages]: how many sequences name each page; 0: it is
+ *                 in the free list. A program that shares a page adds to its count.
+ *   free_pages  : device int32 [num_pages], num_free: device int32 [1]: the free list
+ *                 is free_pages[0 .. num_free - 1].
+ *   lens_out    : device int32 [B]: new_lens[b], or lens[b] where the pages did not
+ *                 suffice. Not lens or new_lens.
+ *   workspace   : device, >= fa2_cache_resize_workspace_size(...) bytes, 256-byte
+ *                 aligned, scratch owned by the caller.
+ * B * max_pages < 2^31. A page number that the cache does not have, or a page given
+ * back more often than it was named, is not freed and sets FA2_ERR_PAGE; the pool's
+ * contents are then undefined (but stay within it). Repeated calls give the same
+ * bits. */
+int fa2_cache_resize(int* table, const int* lens, const int* new_lens, int* refs, int* free_pages, int* num_free,
+                     int* lens_out, int B, int num_pages, int page_size, int max_pages, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Workspace of fa2_cache_resize; 0 for invalid sizes. */
+size_t fa2_cache_resize_workspace_size(int B, int num_pages, int page_size, int max_pages);
+
 /* Accumulated attention weight of a prompt's keys, after fa2_fwd / fa2_fwd_qk:
  *   out[b][h][j] = sum over the g = Hq / Hkv query heads x of key head h and the
  *   queries i < q_lens[b] that see key j of e^(scale q_i . k_j - lse_i).
