@@ -31,6 +31,7 @@ __all__ = [
     "device_status",
     "attention",
     "paged_decode",
+    "prefix_decode",
     "cache_append",
     "cache_evict",
     "cache_resize",
@@ -100,6 +101,8 @@ def load_library() -> ctypes.CDLL:
                                      sz, vp, vp]),
         "fa2_paged_decode": (i, [vp] * 9 + [i] * 7 + [f, i, vp, sz, vp]),
         "fa2_paged_decode_workspace_size": (sz, [i] * 7),
+        "fa2_prefix_decode": (i, [vp] * 9 + [i] * 8 + [f, i, vp, sz, vp]),
+        "fa2_prefix_decode_workspace_size": (sz, [i] * 6),
         "fa2_cache_append": (i, [vp] * 12 + [i] * 8 + [vp]),
         "fa2_cache_evict": (i, [vp] * 10 + [i] * 9 + [vp, sz, vp]),
         "fa2_cache_evict_workspace_size": (sz, [i] * 5),
@@ -501,6 +504,21 @@ def paged_decode(q, k_cache, v_cache, table, lens, scale: float | None = None, w
     """
     return (_native_mod or _native()).paged_decode(q, k_cache, v_cache, table, lens, scale, weights,
                                                    weights_out, out, lse, workspace)
+
+
+def prefix_decode(q, k_cache, v_cache, table, lens, prefix, prefix_len, scale: float | None = None, out=None,
+                  lse=None, workspace=None):
+    """``paged_decode`` for sequences that begin with the same slots, such as a common
+    prompt: those are attended to once for the whole batch.
+
+    prefix int32 ``[prefix_pages]``: the pages of the shared slots; prefix_len int32
+    ``[1]``: how many slots. Sequences of at least prefix_len slots have the prefix in
+    their first slots (their tables name the same pages; where it ends inside a page
+    that page may be a copy); shorter ones are read by their own table alone. Other
+    arguments and results as in ``paged_decode``; weights are not gathered.
+    """
+    return (_native_mod or _native()).prefix_decode(q, k_cache, v_cache, table, lens, prefix, prefix_len, scale, out,
+                                                    lse, workspace)
 
 
 def cache_append(k, v, k_cache, v_cache, table, lens, num_new=None, weights=None,

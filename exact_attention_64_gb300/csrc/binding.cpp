@@ -201,6 +201,40 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// q, k_cache, v_cache, table, lens, prefix, prefix_len, scale, out, lse, workspace
+PyObject* prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arity(n, 11)) return nullptr;
+  const Cache c = cache_of(a[1], a[2], a[3], a[4]);
+  const Tensor &q = tensor("q", a[0]), &p = tensor("prefix", a[5]);
+  if (q.dim() != 3) value_error("expected a [B, Hq, d] query");
+  if (p.dim() != 1) value_error("expected a [prefix_pages] prefix");
+  const int64_t Hq = q.size(1);
+  const void* qp = need("q", q, {c.B, Hq, c.d}, c.type, c.dev);
+  const int hq = as_int("Hq", Hq), pages = as_int("prefix_pages", p.size(0));
+  const int* pp = need<int>("prefix", p, {pages}, at::kInt, c.dev);
+  const int* pl = need<int>("prefix_len", tensor("prefix_len", a[6]), {1}, at::kInt, c.dev);
+  const float scale = scale_of(a[7], c.d);
+  const Tensor o = output("out", a[8], {c.B, Hq, c.d}, c.type, c.dev);
+  const Tensor lse = output("lse", a[9], {c.B, Hq}, at::kFloat, c.dev);
+  const Space ws = workspace(a[10], fa2_prefix_decode_workspace_size(c.B, hq, c.Hkv, c.d, c.ps, c.width),
+                             "fa2_prefix_decode_workspace_size", c.dev);
+  void* op = o.data_ptr();
+  float* lp = static_cast<float*>(lse.data_ptr());
+  void* wp = ws.t.data_ptr();
+  run("fa2_prefix_decode", c.dev, [&](void* stream) {
+    return fa2_prefix_decode(qp, c.k, c.v, c.table, c.lens, pp, pl, op, lp, c.B, hq, c.Hkv, c.d, c.pages, c.ps, c.width,
+                             pages, scale, c.dtype, wp, ws.bytes, stream);
+  });
+  PyObject* r0 = THPVariable_Wrap(o);
+  PyObject* r1 = THPVariable_Wrap(lse);
+  PyObject* r = PyTuple_Pack(2, r0, r1);
+  Py_XDECREF(r0);
+  Py_XDECREF(r1);
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
 // k, v, k_cache, v_cache, table, lens, num_new, weights, new_weights, positions, next_pos, lens_out
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -493,7 +527,7 @@ PyObject* rotary_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FA2_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FA2_METHOD(paged_decode), FA2_METHOD(cache_append), FA2_METHOD(cache_evict),
                            FA2_METHOD(key_weights), FA2_METHOD(rotary_forward), FA2_METHOD(rotary_backward),
-                           FA2_METHOD(cache_resize), {nullptr, nullptr, 0, nullptr}};
+                           FA2_METHOD(cache_resize), FA2_METHOD(prefix_decode), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -371,6 +371,9 @@ int host_take_fault(int kind, unsigned long long* timeout_ns) {
 int host_map_16bit(CUtensorMap* m, const void* ptr, int BH, int N, int d, int dtype) {
   return make_map_16bit(m, ptr, BH, N, d, dtype);
 }
+int host_map_rows(CUtensorMap* m, const void* ptr, int rows, int d, int dtype, int box_rows) {
+  return make_map_16bit(m, ptr, 1, rows, d, dtype, box_rows);
+}
 }  // namespace fa2
 
 extern "C" {
@@ -718,7 +721,7 @@ int fa2_fwd_schedule(int B, int H, int N, int causal, int num_sms, int* num_ctas
 int fa2_last_cuda_error(void) { return g_last_cuda_error; }
 
 int fa2_debug_arm_fault(int kind, int timeout_ms) {
-  if (kind < 0 || (kind > 4 && kind != 6)) return FA2_ERR_INVALID_ARG;
+  if (kind < 0 || (kind > 4 && kind != 6 && kind != 7)) return FA2_ERR_INVALID_ARG;
   if (kind != 0 && (timeout_ms < 1 || timeout_ms > 5000)) return FA2_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lock(g_mu);
   g_fault_kind = kind;

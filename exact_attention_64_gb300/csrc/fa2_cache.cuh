@@ -161,6 +161,39 @@ struct DecodeArgs {
   int join_split;         // blocks of the join per CTA of the decode
   int whole;              // a CTA has one whole item, and there is no join
   float scale_log2;       // scale * log2(e)
+  const int* prefix;      // shared prefix: its pages [prefix_pages]
+  const int* prefix_len;  // [1]
+  int prefix_cap;         // slots that the prefix can have at most
+  long long* starts;      // workspace [B + 1]: units of the sequences before each
+  int box;                // slots of one copy: a power of two, at most 16, that divides the page size
+};
+
+// The part of an item and a CTA: from one part to the next either number grows, or both.
+__host__ __device__ constexpr int shared_part(int item, int cta) { return item + cta; }
+
+// A shared prefix: its slots, and those of them in whole copies, which are attended to
+// once for all sequences of at least `len` slots.
+struct PrefixLen {
+  int len, cut;
+};
+__device__ __forceinline__ PrefixLen prefix_slots(const DecodeArgs& a) {
+  const int n = cut_len(ld_global(a.prefix_len), a.prefix_cap);
+  return PrefixLen{n, n & ~(a.box - 1)};
+}
+
+// Attention to a prefix that sequences share.
+struct PrefixArgs {
+  DecodeArgs d;           // the slots behind the prefix: its view of the cache and its parts
+  int head_tile;          // query heads of an item behind the prefix
+  int tail_ctas;          // CTAs that work on them
+  int items;              // Hkv * ceil(rows / 256)
+  int rows;               // B * g query rows of a key head: row R is head R % g of sequence R / g
+  FastDiv fg;
+  int ctas;               // of the prefix
+  float* part_o;          // workspace [items + ctas][256][d]: unnormalised O of a segment
+  float2* part_ml;        // workspace [items + ctas][256]: its (m, l)
+  unsigned long long timeout_ns;
+  int fault;              // 0 normally; failure-path test: the first V tile of each CTA never loads
 };
 
 struct AppendArgs {

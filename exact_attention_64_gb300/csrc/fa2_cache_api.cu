@@ -1,6 +1,7 @@
 // C ABI of the paged key-value cache and of the key weights: argument
 // validation, workspace layout and launches. Declarations and argument
 // contracts live in include/fa2.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cuda.h>
@@ -15,6 +16,8 @@ cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArg
                                 cudaStream_t stream);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_decode(int d, bool bf16, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
+                                 cudaStream_t stream);
 cudaError_t launch_cache_resize(const ResizeArgs& a, cudaStream_t stream);
 int resize_group(int B);
 cudaError_t launch_key_weights(int d, bool bf16, bool causal, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -24,6 +27,7 @@ cudaError_t launch_key_weights(int d, bool bf16, bool causal, const CUtensorMap&
 namespace {
 
 constexpr int kDecodeCtas = 304;  // most CTAs of a decode: two on each of 152 SMs
+constexpr int kPrefixCtas = 152;  // most CTAs of a shared prefix
 constexpr int kKwCtas = 152;      // most CTAs of the key weights
 constexpr long long kMaxRows = (1LL << 31) - 1;
 constexpr long long kMaxSlots = 1LL << 30;  // slots that a table row can name
@@ -139,6 +143,30 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
   return s;
 }
 
+// Items of a shared prefix: up to 256 of the B * g query rows of a key head.
+long long prefix_items(int B, int Hq, int Hkv) {
+  return static_cast<long long>(Hkv) * ((static_cast<long long>(B) * (Hq / Hkv) + 255) / 256);
+}
+
+// Workspace of a decode with a shared prefix: the parts of both kernels, and where
+// each sequence's units begin.
+struct PrefixSpace {
+  size_t po, pml, so, sml, starts, total;
+};
+PrefixSpace prefix_space(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
+  PrefixSpace s{};
+  const int ht = head_tile(Hq / Hkv);
+  const size_t rows = static_cast<size_t>(prefix_items(B, Hq, Hkv) + kPrefixCtas) * 256;
+  const size_t own = (static_cast<size_t>(B) * Hkv * ((Hq / Hkv + ht - 1) / ht) +
+                      decode_ctas(B, Hq, Hkv, d, page_size, max_pages)) * ht;
+  s.pml = s.po + align_up(rows * d * 4, 256);
+  s.so = s.pml + align_up(rows * 8, 256);
+  s.sml = s.so + align_up(own * d * 4, 256);
+  s.starts = s.sml + align_up(own * 8, 256);
+  s.total = s.starts + align_up(static_cast<size_t>(B + 1) * 8, 256);
+  return s;
+}
+
 // Longest list of moves of an eviction: slots below the budget, or past it.
 long long evict_list(int page_size, int max_pages, int budget) {
   const long long past = static_cast<long long>(max_pages) * page_size - budget;
@@ -213,6 +241,79 @@ int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, co
   (void)cudaGetLastError();  // a non-sticky error of another caller is not ours
   const cudaError_t e =
       fa2::launch_paged_decode(d, dtype == FA2_BF16, ht, a, ctas, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
+}
+
+size_t fa2_prefix_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
+  if (check_heads(Hq, Hkv) != FA2_OK) return 0;
+  if (check_cache(B, Hkv, d, 1, page_size, max_pages, FA2_BF16) != FA2_OK) return 0;
+  return prefix_space(B, Hq, Hkv, d, page_size, max_pages).total;
+}
+
+int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int* table, const int* lens,
+                      const int* prefix, const int* prefix_len, void* o, float* lse, int B, int Hq, int Hkv, int d,
+                      int num_pages, int page_size, int max_pages, int prefix_pages, float scale, int dtype,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !table || !lens || !prefix || !prefix_len || !o || !lse) return FA2_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f) || prefix_pages < 1) return FA2_ERR_INVALID_ARG;
+  int st = check_heads(Hq, Hkv);
+  if (st != FA2_OK) return st;
+  st = check_cache(B, Hkv, d, num_pages, page_size, max_pages, dtype);
+  if (st != FA2_OK) return st;
+  if (static_cast<long long>(prefix_pages) * page_size > kMaxSlots) return FA2_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(table, 4) ||
+      !aligned(lens, 4) || !aligned(prefix, 4) || !aligned(prefix_len, 4) || !aligned(lse, 4))
+    return FA2_ERR_ALIGNMENT;
+  const PrefixSpace s = prefix_space(B, Hq, Hkv, d, page_size, max_pages);
+  if (workspace == nullptr || workspace_bytes < s.total) return FA2_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FA2_ERR_ALIGNMENT;
+  const size_t qb = static_cast<size_t>(B) * Hq * d * 2, cb = cache_bytes(Hkv, d, num_pages, page_size);
+  const Buf ins[] = {{q, qb}, {k_cache, cb}, {v_cache, cb}, {table, static_cast<size_t>(B) * max_pages * 4},
+                     {lens, static_cast<size_t>(B) * 4}, {prefix, static_cast<size_t>(prefix_pages) * 4}, {prefix_len, 4}};
+  const Buf outs[] = {{o, qb}, {lse, static_cast<size_t>(B) * Hq * 4}, {workspace, s.total}};
+  if (any_overlap(outs, ins)) return FA2_ERR_OVERLAP;
+  int sms = 0;
+  fa2::PrefixArgs a{};
+  fa2::DecodeArgs& c = a.d;
+  c.c = make_view(table, lens, B, Hkv, num_pages, page_size, max_pages);
+  st = fa2::host_device_setup(&sms, &c.c.status);
+  if (st != FA2_OK) return st;
+  c.box = 1;
+  while (c.box < 16 && page_size % (2 * c.box) == 0) c.box *= 2;
+  CUtensorMap tk, tv;
+  const int rows = num_pages * Hkv * page_size;
+  if (fa2::host_map_rows(&tk, k_cache, rows, d, dtype, c.box) || fa2::host_map_rows(&tv, v_cache, rows, d, dtype, c.box))
+    return FA2_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  c.q = static_cast<const uint16_t*>(q);
+  c.k = static_cast<const uint16_t*>(k_cache);
+  c.v = static_cast<const uint16_t*>(v_cache);
+  c.o = static_cast<uint16_t*>(o);
+  c.lse = lse;
+  c.part_o = reinterpret_cast<float*>(ws + s.so);
+  c.part_ml = reinterpret_cast<float2*>(ws + s.sml);
+  c.starts = reinterpret_cast<long long*>(ws + s.starts);
+  c.Hq = Hq;
+  c.g = Hq / Hkv;
+  a.head_tile = head_tile(c.g);
+  c.HG = (c.g + a.head_tile - 1) / a.head_tile;
+  c.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  c.prefix = prefix;
+  c.prefix_len = prefix_len;
+  c.prefix_cap = prefix_pages * page_size;
+  const int most = decode_ctas(B, Hq, Hkv, d, page_size, max_pages);
+  a.tail_ctas = 2 * sms < most ? 2 * sms : most;
+  a.rows = B * c.g;
+  a.fg = fa2::fast_div(c.g);
+  a.items = static_cast<int>(prefix_items(B, Hq, Hkv));
+  const long long units = a.items * ((static_cast<long long>(c.prefix_cap) + 127) / 128);
+  a.ctas = static_cast<int>(std::min<long long>(units, std::min(sms, kPrefixCtas)));
+  a.part_o = reinterpret_cast<float*>(ws + s.po);
+  a.part_ml = reinterpret_cast<float2*>(ws + s.pml);
+  a.timeout_ns = fa2::kDefaultWaitTimeoutNs;
+  a.fault = fa2::host_take_fault(7, &a.timeout_ns);
+  (void)cudaGetLastError();
+  const cudaError_t e = fa2::launch_prefix_decode(d, dtype == FA2_BF16, tk, tv, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
 }
 

@@ -1,0 +1,135 @@
+// How a decode cuts the slots of all sequences into units, and its CTAs' shares of
+// them (see fa2_paged_decode.cu).
+#pragma once
+#include "fa2_cache.cuh"
+
+namespace fa2 {
+
+// Slots per unit: 32 KiB of K and V. A warp has 16 (d = 128) or 32 (d = 64) of
+// them, so that its fixed cost per unit (maximum, ring, cursor) is spread over
+// the same bytes at both head sizes.
+template <int D>
+constexpr int kUnit = decode_unit(D);
+constexpr float kLn2f = 0.6931471805599453f;
+constexpr float kLog2ef = 1.4426950408889634f;
+
+// ---- Units ---------------------------------------------------------------
+// HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
+// SHARED: a sequence that reaches the prefix has the slots behind it only.
+template <int D>
+__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
+
+// Quotient of 0 <= a and b > 0; 32 bits when they do, which is nearly always.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+struct UnitCursor {
+  int b, hh, tile;  // sequence, item of the sequence, unit of the item
+  int n, ntiles;    // slots of the sequence, units of the item
+  int start;        // SHARED: slots of the prefix before them
+};
+
+// Slots of the prefix that a sequence of n slots leaves to it.
+__device__ __forceinline__ int prefix_of(int n, const PrefixLen& p) { return n >= p.len ? p.cut : 0; }
+
+// The units of all sequences, by a whole warp: T, and where a unit lies. Up to
+// 32 sequences are read once and their running sums stay with the lanes.
+template <int D, bool SHARED = false>
+struct UnitMap {
+  const CacheView& c;
+  int HH, lane;
+  PrefixLen P;
+  int n;
+  long long incl, T;
+
+  __device__ UnitMap(const CacheView& view, int hh, int l, PrefixLen prefix = {}) : c(view), HH(hh), lane(l), P(prefix) {
+    n = length(lane);
+    incl = scan(n);
+    T = __shfl_sync(0xffffffffu, incl, 31);
+    for (int b0 = 32; b0 < c.B; b0 += 32) T += __shfl_sync(0xffffffffu, scan(length(b0 + lane)), 31);
+  }
+  __device__ int length(int b) const {
+    if (b >= c.B) return 0;
+    const int x = seq_len(c, b);
+    return SHARED ? x - prefix_of(x, P) : x;
+  }
+  // out[b]: units of the sequences before b; out[B] = T.
+  __device__ void write_starts(long long* out) const {
+    long long base = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+      const int len = b0 == 0 ? n : length(b0 + lane);
+      const long long sum = scan(len);
+      if (b0 + lane < c.B) out[b0 + lane] = base + sum - static_cast<long long>(tiles_of<D>(len)) * HH;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) out[c.B] = T;
+  }
+  __device__ long long scan(int slots) const {
+    long long t = static_cast<long long>(tiles_of<D>(slots)) * HH;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    return t;
+  }
+  // Cursor of unit u < T.
+  __device__ UnitCursor at(long long u) const {
+    long long base = 0, sum = incl;
+    int len = n;
+    for (int b0 = 0;; b0 += 32) {
+      const unsigned hit = __ballot_sync(0xffffffffu, u < base + sum);
+      if (hit != 0u) {
+        const int src = __ffs(hit) - 1;
+        UnitCursor k;
+        k.b = b0 + src;
+        k.n = __shfl_sync(0xffffffffu, len, src);
+        k.ntiles = tiles_of<D>(k.n);
+        k.start = SHARED ? prefix_of(seq_len(c, k.b), P) : 0;
+        const long long r = u - (base + __shfl_sync(0xffffffffu, sum, src) - static_cast<long long>(k.ntiles) * HH);
+        k.hh = static_cast<int>(div_pos(r, k.ntiles));
+        k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
+        return k;
+      }
+      if (b0 + 32 >= c.B) return UnitCursor{};
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      len = length(b0 + 32 + lane);
+      sum = scan(len);
+    }
+  }
+};
+
+template <int D, bool SHARED = false>
+__device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k, PrefixLen P = {}) {
+  if (++k.tile < k.ntiles) return;
+  k.tile = 0;
+  if (++k.hh < HH) return;
+  k.hh = 0;
+  do {
+    if (++k.b >= c.B) {
+      k.n = k.ntiles = 0;
+      return;
+    }
+    k.n = seq_len(c, k.b);
+    if constexpr (SHARED) {
+      k.start = prefix_of(k.n, P);
+      k.n -= k.start;
+    }
+  } while (k.n == 0);
+  k.ntiles = tiles_of<D>(k.n);
+}
+
+// Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer
+// units than CTAs, T CTAs take one each.
+__device__ __forceinline__ long long unit_begin(long long x, long long G, long long T) { return div_pos(x * T, G); }
+__device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
+  return static_cast<int>(div_pos((u + 1) * G - 1, T));
+}
+
+// 2^(from - to) for a reference that rises to `to`. 1 at -inf, where all that
+// there is are zeros, or NaN that has to stay.
+__device__ __forceinline__ float step_down(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
+
+}  // namespace fa2

@@ -16,6 +16,9 @@ int host_cuda_fail(cudaError_t e);
 // 128-byte swizzled, zero fill past row N.
 int host_map_16bit(CUtensorMap* m, const void* ptr, int BH, int N, int d, int dtype);
 
+// The same over `rows` rows, in boxes of box_rows rows.
+int host_map_rows(CUtensorMap* m, const void* ptr, int rows, int d, int dtype, int box_rows);
+
 // 1 if the fault of this kind is armed, which disarms it and sets the wait
 // bound that came with it; else 0.
 int host_take_fault(int kind, unsigned long long* timeout_ns);

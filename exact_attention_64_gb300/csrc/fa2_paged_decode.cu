@@ -37,18 +37,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "fa2_cache.cuh"
+#include "fa2_decode_units.cuh"
 
 namespace fa2 {
 
 constexpr int kDecWarps = 4;
-// Slots per unit: 32 KiB of K and V. A warp has 16 (d = 128) or 32 (d = 64) of
-// them, so that its fixed cost per unit (maximum, ring, cursor) is spread over
-// the same bytes at both head sizes.
-template <int D>
-constexpr int kUnit = decode_unit(D);
-constexpr float kLn2f = 0.6931471805599453f;
-constexpr float kLog2ef = 1.4426950408889634f;
 
 // `pol`: the cache is read once (by a group of up to 16 heads), so its lines leave
 // L2 first; what the join reads again (logits, partial results) stays.
@@ -186,94 +179,6 @@ struct ProbT<false> {
   }
 };
 
-// ---- Units ---------------------------------------------------------------
-// HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
-template <int D>
-__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
-
-// Quotient of 0 <= a and b > 0; 32 bits when they do, which is nearly always.
-__device__ __forceinline__ long long div_pos(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-struct UnitCursor {
-  int b, hh, tile;  // sequence, item of the sequence, unit of the item
-  int n, ntiles;    // slots of the sequence, units of the item
-};
-
-// The units of all sequences, by a whole warp: T, and where a unit lies. Up to
-// 32 sequences are read once and their running sums stay with the lanes.
-template <int D>
-struct UnitMap {
-  const CacheView& c;
-  int HH, lane, n;
-  long long incl, T;
-
-  __device__ UnitMap(const CacheView& view, int hh, int l) : c(view), HH(hh), lane(l) {
-    n = length(lane);
-    incl = scan(n);
-    T = __shfl_sync(0xffffffffu, incl, 31);
-    for (int b0 = 32; b0 < c.B; b0 += 32) T += __shfl_sync(0xffffffffu, scan(length(b0 + lane)), 31);
-  }
-  __device__ int length(int b) const { return b < c.B ? seq_len(c, b) : 0; }
-  __device__ long long scan(int slots) const {
-    long long t = static_cast<long long>(tiles_of<D>(slots)) * HH;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    return t;
-  }
-  // Cursor of unit u < T.
-  __device__ UnitCursor at(long long u) const {
-    long long base = 0, sum = incl;
-    int len = n;
-    for (int b0 = 0;; b0 += 32) {
-      const unsigned hit = __ballot_sync(0xffffffffu, u < base + sum);
-      if (hit != 0u) {
-        const int src = __ffs(hit) - 1;
-        UnitCursor k;
-        k.b = b0 + src;
-        k.n = __shfl_sync(0xffffffffu, len, src);
-        k.ntiles = tiles_of<D>(k.n);
-        const long long r = u - (base + __shfl_sync(0xffffffffu, sum, src) - static_cast<long long>(k.ntiles) * HH);
-        k.hh = static_cast<int>(div_pos(r, k.ntiles));
-        k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
-        return k;
-      }
-      if (b0 + 32 >= c.B) return UnitCursor{};
-      base += __shfl_sync(0xffffffffu, sum, 31);
-      len = length(b0 + 32 + lane);
-      sum = scan(len);
-    }
-  }
-};
-
-template <int D>
-__device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k) {
-  if (++k.tile < k.ntiles) return;
-  k.tile = 0;
-  if (++k.hh < HH) return;
-  k.hh = 0;
-  do {
-    if (++k.b >= c.B) {
-      k.n = k.ntiles = 0;
-      return;
-    }
-    k.n = seq_len(c, k.b);
-  } while (k.n == 0);
-  k.ntiles = tiles_of<D>(k.n);
-}
-
-// Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer
-// units than CTAs, T CTAs take one each.
-__device__ __forceinline__ long long unit_begin(long long x, long long G, long long T) { return div_pos(x * T, G); }
-__device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
-  return static_cast<int>(div_pos((u + 1) * G - 1, T));
-}
-
 // w_out += e^(s - L) over the group's heads for slots [j0, j1). VEC logits of a
 // slot are read at a time.
 template <int THREADS, int VEC>
@@ -330,22 +235,27 @@ struct DecCfg {
   static constexpr int HEADS = 8 * NT;                     // query heads of a tile
 };
 
-template <int D, bool BF16, int NT, bool WEIGHTS>
+// SHARED: the slots behind a prefix that another kernel of the call attends to at the
+// same time (fa2_prefix_decode.cu), which has waited for what came before the call and
+// lets this one begin early; this one ends after it. Every segment is left as a part.
+template <int D, bool BF16, int NT, bool WEIGHTS, bool SHARED = false>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
   using C = DecCfg<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
   __shared__ float s_lse[C::HEADS];
-  grid_dependency_wait();
+  if constexpr (!SHARED) grid_dependency_wait();
   grid_launch_dependents();
+  PrefixLen P{};
+  if constexpr (SHARED) P = prefix_slots(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
   const int cta = blockIdx.x;
   long long u0 = 0, u1 = 0;
   UnitCursor cc{};
-  if (a.whole) {
+  if (!SHARED && a.whole) {
     cc.b = cta / HH;
     cc.hh = cta - cc.b * HH;
     cc.n = seq_len(c, cc.b);
@@ -361,12 +271,18 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       return;
     }
   } else {
-    const UnitMap<D> map(c, HH, lane);
+    const UnitMap<D, SHARED> map(c, HH, lane, P);
     const long long T = map.T, G = min(static_cast<long long>(gridDim.x), T);
     if (cta == 0 && warp == 0)
       for (int b = lane; b < c.B; b += 32)
         if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
-    if (cta >= G) return;
+    if constexpr (SHARED) {
+      if (cta == 0 && warp == 1) map.write_starts(a.starts);  // for the join
+    }
+    if (cta >= G) {
+      if constexpr (SHARED) grid_dependency_wait();
+      return;
+    }
     u0 = unit_begin(cta, G, T);
     u1 = unit_begin(cta + 1, G, T);
     cc = map.at(u0);
@@ -386,8 +302,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     in = left > 0 && slot < ic.n;
     hk = a.HG == 1 ? ic.hh : ic.hh / a.HG;
     if (in) {
-      const int p = div_by(slot, c.ps);
-      off = slot - p * c.ps.d;
+      const int at = SHARED ? slot + ic.start : slot, p = div_by(at, c.ps);
+      off = at - p * c.ps.d;
       pg = ld_global(c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
     }
   };
@@ -412,7 +328,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0, pol);
         }
       }
-      unit_advance<D>(c, HH, ic);
+      unit_advance<D, SHARED>(c, HH, ic, P);
       --left;
       look_up();
     }
@@ -566,11 +482,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       // End of a segment: the four warps' (m, l, O) are merged, while the next
       // one's queries are on their way.
       UnitCursor next = cc;
-      unit_advance<D>(c, HH, next);
+      unit_advance<D, SHARED>(c, HH, next, P);
       if (u + 1 < u1) load_q(next);
       const bool from_start = cc.tile - (u - u0) <= 0;  // the segment begins with its item
-      const bool whole = from_start && cc.tile + 1 == cc.ntiles;
-      const int slot = 2 * cta + (from_start ? 1 : 0);
+      const bool whole = !SHARED && from_start && cc.tile + 1 == cc.ntiles;
+      const int slot = SHARED ? shared_part(cc.b * HH + cc.hh, cta) : 2 * cta + (from_start ? 1 : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -637,8 +553,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         __syncthreads();
       }
     }
-    unit_advance<D>(c, HH, cc);
+    unit_advance<D, SHARED>(c, HH, cc, P);
   }
+  if constexpr (SHARED) grid_dependency_wait();
   if constexpr (WEIGHTS) {
     if (a.whole) {  // a key head is one item: its weights from the logits that this CTA wrote
       const int hh = cta % HH, b = cta / HH;
@@ -662,10 +579,6 @@ __device__ __forceinline__ ItemParts item_parts(long long ub, int ntiles, long l
 }
 // Workspace slot of CTA x's part of an item whose first part is CTA c0's.
 __device__ __forceinline__ int part_slot(int x, int c0) { return 2 * x + (x == c0 ? 1 : 0); }
-
-// 2^(from - to) for a reference that rises to `to`. 1 at -inf, where all that
-// there is are zeros, or NaN that has to stay.
-__device__ __forceinline__ float step_down(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }
 
 // (M, S) of one head over an item's parts, by a whole warp.
 __device__ __forceinline__ float2 join_ml(const float2* part_ml, int heads, int hd, ItemParts p, int lane) {
@@ -1014,6 +927,26 @@ static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_paged_join_kernel<D, BF16, NT, WEIGHTS>, dim3(ctas * a.join_split),
                           dim3(kJoinThreads), 0, stream, a);
+}
+
+template <int D, bool BF16, int NT>
+static cudaError_t launch_suffix_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
+  using C = DecCfg<D, NT>;
+  auto kern = fa2_paged_decode_kernel<D, BF16, NT, false, true>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(kern, C::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(ctas), dim3(kDecWarps * 32), C::SMEM, stream, a);
+}
+
+// The slots behind a shared prefix, as parts.
+cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas, cudaStream_t stream) {
+  const bool one = head_tile == 8;
+  if (d == 64)
+    return bf16 ? (one ? launch_suffix_t<64, true, 1>(a, ctas, stream) : launch_suffix_t<64, true, 2>(a, ctas, stream))
+                : (one ? launch_suffix_t<64, false, 1>(a, ctas, stream) : launch_suffix_t<64, false, 2>(a, ctas, stream));
+  return bf16 ? (one ? launch_suffix_t<128, true, 1>(a, ctas, stream) : launch_suffix_t<128, true, 2>(a, ctas, stream))
+              : (one ? launch_suffix_t<128, false, 1>(a, ctas, stream) : launch_suffix_t<128, false, 2>(a, ctas, stream));
 }
 
 cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas,

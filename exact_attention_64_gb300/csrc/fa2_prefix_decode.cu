@@ -1,0 +1,622 @@
+// Attention of one new token per sequence over a paged cache, for sequences that
+// begin with the same slots.
+//
+//   s_j = scale q . k_j, o = sum_j e^(s_j - L) v_j, L = ln sum_j e^(s_j)
+//
+// over the P shared slots and a sequence's own behind them. The sum splits: with (m, l,
+// O) = (reference, sum of 2^(s - m), sum of 2^(s - m) v) of any set of slots, those of a
+// union are l = sum 2^(m_i - m) l_i and so on. So the prefix is attended to once, by the
+// queries of all sequences together; each sequence's own slots as in fa2_paged_decode;
+// and a last launch joins the parts.
+//
+// What bounds it: for R = B g query rows of a key head the prefix costs 4 R flop per
+// cached element of 2 bytes, so up to about 128 rows it is bound by HBM, and past that by
+// the products and their exponentials. fa2_paged_decode would read the prefix B times.
+//
+// Prefix: the forward's shape with paged keys. Query rows are the TMEM lanes, 128 to a
+// tile; an item is up to two tiles (256 rows) of one key head and all tiles of 128
+// slots, and CTA c of G has the units [c T / G, (c + 1) T / G) of the T = items x slot
+// tiles, so that every SM has the same share whatever the sizes. A segment (an item's
+// part in a CTA) leaves (m, l, O) in the workspace.
+//   warps 0, 3   copies of K and of V: one TMA box of up to 16 slots x 64 columns per
+//                lane and page piece, into 128-slot tiles with the 128-byte swizzle.
+//   warp 1       the products: S = Q K^T, then O += P V with P read from TMEM.
+//   warps 4-11   two groups of 128 threads, a thread per row, each with an S and an O in
+//                TMEM: one per row tile, or, when the item has one tile only, both on it
+//                with every other slot tile each, joined at the segment's end.
+// P enters its product as two 16-bit numbers, rounded and remainder: bf16 to 2^-18 of
+// p, which is what the scores' fp32 rounding leaves; fp16, which has no exponents for
+// small p, with the largest at up to 2^15 and 2^-24 as the last place, 2^-36 of a row's
+// reference or less. The third bf16 piece that would make P exact has no room in TMEM
+// (S and O of two tiles fill it), and would be half a product more.
+#include "fa2_common.cuh"
+#include "fa2_decode_units.cuh"
+
+namespace fa2 {
+
+template <int D>
+struct PfxCfg {
+  static constexpr int SLAB = kTileRows * 128;            // 128 rows x 64 columns
+  static constexpr int TILE = kTileRows * D * 2;
+  static constexpr int NS = D == 128 ? 2 : 4;             // ring depth of K and of V
+  static constexpr int OFF_K = 2 * TILE;                  // after the two Q tiles
+  static constexpr int OFF_V = OFF_K + NS * TILE;
+  static constexpr int OFF_STAGE = OFF_V + NS * TILE;     // 4 KiB per row warp
+  static constexpr int SMEM = OFF_STAGE + 8 * 4096 + 1024;
+  static_assert(SMEM + 2048 <= 232448, "with the static part at most what a CTA can have");
+  static constexpr int THREADS = 384;
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t TM_S(int t) { return t * 128u; }  // P: its two pieces, 64 columns each
+  __host__ __device__ static constexpr uint32_t TM_O(int t) { return 256u + t * D; }
+};
+
+template <int D>
+struct PfxShared {
+  uint64_t q_full;
+  uint64_t k_full[PfxCfg<D>::NS], k_empty[PfxCfg<D>::NS];
+  uint64_t v_full[PfxCfg<D>::NS], v_empty[PfxCfg<D>::NS];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t ml_full;
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  float m[2][kTileRows], l1[kTileRows];  // both streams' references, the second's sums
+};
+
+// A CTA's units, cut into segments of one item.
+struct PfxWork {
+  int P, tiles;          // slots in whole boxes, tiles of 128 of them
+  long long u0, u1, G, T;
+};
+struct PfxSeg {
+  int item, h, row0, rows;  // key head, first query row, rows (up to 256)
+  int tile0, cnt;           // slot tiles
+  bool two;
+};
+
+__device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta) {
+  PfxWork w;
+  w.P = prefix_slots(a.d).cut;
+  w.tiles = (w.P + kTileRows - 1) / kTileRows;
+  w.T = static_cast<long long>(a.items) * w.tiles;
+  w.G = min(static_cast<long long>(a.ctas), w.T);
+  w.u0 = w.u1 = 0;
+  if (cta < w.G) {
+    w.u0 = unit_begin(cta, w.G, w.T);
+    w.u1 = unit_begin(cta + 1, w.G, w.T);
+  }
+  return w;
+}
+__device__ __forceinline__ PfxSeg pfx_seg(const PrefixArgs& a, const PfxWork& w, long long u) {
+  PfxSeg s;
+  const int blocks = a.items / a.d.c.Hkv;
+  s.item = static_cast<int>(div_pos(u, w.tiles));
+  s.tile0 = static_cast<int>(u - static_cast<long long>(s.item) * w.tiles);
+  s.cnt = static_cast<int>(min(static_cast<long long>(w.tiles - s.tile0), w.u1 - u));
+  s.h = s.item / blocks;
+  s.row0 = (s.item - s.h * blocks) * 2 * kTileRows;
+  s.rows = min(2 * kTileRows, a.rows - s.row0);
+  s.two = s.rows > kTileRows;
+  return s;
+}
+
+// Cache row of box i of a slot tile, or -1: past the prefix, or a page that the cache
+// does not have.
+__device__ __forceinline__ int pfx_row(const PrefixArgs& a, int P, int h, int tile, int i) {
+  const CacheView& c = a.d.c;
+  const int slot = tile * kTileRows + i * a.d.box;
+  if (slot >= P) return -1;
+  const int p = div_by(slot, c.ps);
+  return page_row(c, ld_global(a.d.prefix + p), h, slot - p * c.ps.d);
+}
+
+// ---- Copies: a warp for K and one for V -------------------------------------
+template <int D>
+__device__ bool pfx_producer(const PrefixArgs& a, const PfxWork& w, const CUtensorMap& map, uint64_t* full,
+                             uint64_t* empty, uint8_t* ring, int lane, bool report, bool fault, const WaitCtx& wc) {
+  using C = PfxCfg<D>;
+  const int boxes = kTileRows / a.d.box, bytes = a.d.box * 128;
+  const int nowhere = a.d.c.num_pages * a.d.c.Hkv * a.d.c.ps.d;  // past the cache: reads as zeros
+  int g = 0;
+  bool ok = true;
+  for (long long u = w.u0; u < w.u1 && ok;) {
+    const PfxSeg s = pfx_seg(a, w, u);
+    for (int j = 0; j < s.cnt; ++j, ++g) {
+      const int st = g % C::NS, tile = s.tile0 + j;
+      int row = lane < boxes ? pfx_row(a, w.P, s.h, tile, lane) : -1;
+      ok = mbar_wait_warp(&empty[st], ((g / C::NS) & 1) ^ 1, wc);
+      if (!ok) break;
+      if (fault && g == 0) continue;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], C::TILE);
+      __syncwarp();
+      for (int i = lane; i < boxes; i += 32) {
+        if (i >= 32) row = pfx_row(a, w.P, s.h, tile, i);
+        if (report && row < 0 && tile * kTileRows + i * a.d.box < w.P) report_page(a.d.c.status);
+        const int at = row < 0 ? nowhere : row;
+        uint8_t* dst = ring + st * C::TILE + i * bytes;
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::SLAB, &map, &full[st], x * 64, at, 0);
+      }
+      __syncwarp();
+    }
+    u += s.cnt;
+  }
+  // Whoever gave up, this warp's copies land before the CTA ends.
+  if (lane == 0)
+    for (int x = max(0, g - C::NS); x < g; ++x)
+      if (!(fault && x == 0)) mbar_wait_drain(&full[x % C::NS], (x / C::NS) & 1, a.timeout_ns);
+  return ok;
+}
+
+// ---- Products -----------------------------------------------------------------
+// Task i of a segment: row tile i & 1 with slot tile i / 2 (two row tiles), or the one
+// row tile with slot tile i for stream i & 1. S(i) and S(i + 1) are in flight; S(i + 2)
+// follows O += P(i) V, which reads the P that it overwrites.
+template <int D, bool BF16>
+__device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem,
+                           const WaitCtx& wc) {
+  using C = PfxCfg<D>;
+  constexpr uint32_t id_s = make_idesc_f16(kTileRows, kTileRows, BF16, false, false);
+  constexpr uint32_t id_o = make_idesc_f16(kTileRows, D, BF16, false, true);
+  const uint32_t q = smem_u32(smem), k = q + C::OFF_K, v = q + C::OFF_V;
+  int g0 = 0, segs = 0, tasks[2] = {0, 0};
+  bool ok = true;
+  for (long long u = w.u0; u < w.u1 && ok; ++segs) {
+    const PfxSeg s = pfx_seg(a, w, u);
+    const int n = s.two ? 2 * s.cnt : s.cnt, sh2 = s.two ? 1 : 0;
+    auto issue_s = [&](int i) {
+      const int g = g0 + (i >> sh2), st = g % C::NS, t = i & 1;
+      if (!s.two || t == 0) {
+        if (!mbar_wait_warp(&sh.k_full[st], (g / C::NS) & 1, wc)) return false;
+        tc_fence_after();
+      }
+      const uint32_t qt = q + (s.two ? t : 0) * C::TILE, kt = k + st * C::TILE;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * C::SLAB + (kk % 4) * 32;
+        umma_ss_warp(tmem + C::TM_S(t), make_sdesc_sw128(qt + off, 16, 1024), make_sdesc_sw128(kt + off, 16, 1024), id_s,
+                     kk > 0 ? 1u : 0u);
+      }
+      umma_commit_warp(&sh.s_full[t]);
+      if (!s.two || t == 1) umma_commit_warp(&sh.k_empty[st]);
+      return true;
+    };
+    ok = mbar_wait_warp(&sh.q_full, segs & 1, wc);
+    if (!ok) break;
+    tc_fence_after();
+    ok = issue_s(0) && (n < 2 || issue_s(1));
+    for (int i = 0; i < n && ok; ++i) {
+      const int g = g0 + (i >> sh2), st = g % C::NS, t = i & 1;
+      ok = mbar_wait2_warp(&sh.v_full[st], (g / C::NS) & 1, &sh.p_full[t], tasks[t] & 1, wc);
+      if (!ok) break;
+      ++tasks[t];
+      tc_fence_after();
+      const uint32_t vt = v + st * C::TILE;
+#pragma unroll
+      for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+        for (int kk = 0; kk < kTileRows / 16; ++kk)
+          umma_ts_warp(tmem + C::TM_O(t), tmem + C::TM_S(t) + piece * 64 + kk * 8,
+                       make_sdesc_sw128(vt + kk * 2048, C::SLAB, 1024), id_o,
+                       (i >= 2 || piece > 0 || kk > 0) ? 1u : 0u);
+      umma_commit_warp(&sh.o_full[t]);
+      if (!s.two || t == 1) umma_commit_warp(&sh.v_empty[st]);
+      if (i + 2 < n) ok = issue_s(i + 2);
+    }
+    g0 += s.cnt;
+    u += s.cnt;
+  }
+  // Every product that was issued completes before TMEM is released.
+  umma_commit_warp(&sh.mma_done);
+  mbar_wait_drain(&sh.mma_done, 0, a.timeout_ns);
+  return ok;
+}
+
+// ---- Rows -----------------------------------------------------------------------
+template <bool BF16>
+constexpr float kPfxBias = BF16 ? 0.f : 12.f;     // log2 of the largest p after a reference is set
+template <bool BF16>
+constexpr float kPfxRescale = BF16 ? 8.f : 3.f;   // how far a row's maximum may pass its reference (log2 units)
+
+// Which columns of a slot tile count: a bit per box.
+struct PfxMask {
+  uint32_t w[4];
+  bool all;
+};
+__device__ __forceinline__ PfxMask pfx_mask(const PrefixArgs& a, int P, int h, int tile, int lane) {
+  const int boxes = kTileRows / a.d.box;
+  PfxMask m;
+  m.all = true;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    m.w[x] = 0u;
+    if (32 * x >= boxes) break;
+    const bool in = lane + 32 * x < boxes;
+    m.w[x] = __ballot_sync(0xffffffffu, in && pfx_row(a, P, h, tile, lane + 32 * x) >= 0);
+    m.all = m.all && m.w[x] == __ballot_sync(0xffffffffu, in);
+  }
+  return m;
+}
+
+// One slot tile of a thread's row: P from S, the row's sum, and O's rescale when the
+// reference moves (only when the maximum passes it by kPfxRescale: exact, O and l share
+// it).
+template <int D, bool BF16>
+__device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, uint32_t t_o, const PfxMask& mask,
+                                         int box, float sl2, bool first, int done, float& m_ref, float& l, int lane,
+                                         const WaitCtx& wc) {
+  if (!mbar_wait_warp(&sh.s_full[t], done & 1, wc)) return false;
+  __syncwarp();
+  tc_fence_after();
+  uint32_t s[128];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+  tmem_wait_ld();
+  reg_fence(s);
+  if (!mask.all) {
+    const int lb = __ffs(box) - 1;
+#pragma unroll
+    for (int c = 0; c < 128; ++c) {
+      const int i = c >> lb;
+      const uint32_t word = i < 64 ? (i < 32 ? mask.w[0] : mask.w[1]) : (i < 96 ? mask.w[2] : mask.w[3]);
+      if (!((word >> (i & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+    }
+  }
+  float mx8[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[8 + x]));
+#pragma unroll
+  for (int c = 16; c < 128; c += 16)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
+  const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+  const float m_new = fmaxf(m_ref, mx);
+  const bool rescale = (m_new - m_ref) * sl2 > kPfxRescale<BF16>;  // also from -inf
+  float alpha = 1.f;
+  if (rescale) {
+    alpha = ex2_approx((m_ref - m_new) * sl2);
+    m_ref = m_new;
+  }
+  const float neg = m_ref == -INFINITY ? 0.f : kPfxBias<BF16> - m_ref * sl2;
+  float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 sl = make_float2(sl2, sl2), ng = make_float2(neg, neg);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t hi[32], lo[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const int e = 64 * half + 2 * c;
+      const float2 x = f2_fma(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl, ng);
+      const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      rs[c & 3] = f2_add(rs[c & 3], p);
+      hi[c] = pack_x2<BF16>(p.x, p.y);
+      const float2 r = f2_sub(p, unpack_x2<BF16>(hi[c]));
+      lo[c] = pack_x2<BF16>(r.x, r.y);
+    }
+    tmem_st_32x32b_x32(t_s + 32 * half, hi);
+    tmem_st_32x32b_x32(t_s + 64 + 32 * half, lo);
+  }
+  l = l * alpha + (((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y)));
+  tmem_wait_st();
+  if (!first && __any_sync(0xffffffffu, rescale)) {
+    if (!mbar_wait_warp(&sh.o_full[t], (done - 1) & 1, wc)) return false;
+    __syncwarp();
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      tmem_ld_32x32b_x32(t_o + c, o);
+      tmem_wait_ld();
+      reg_fence(o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+      tmem_st_32x32b_x32(t_o + c, o);
+    }
+    tmem_wait_st();
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.p_full[t]);
+  return true;
+}
+
+// Query rows of a warp (32 of them, from row0 on) into a Q tile.
+template <int D>
+__device__ __forceinline__ void pfx_load_q(const PrefixArgs& a, int h, int row0, int in_tile, uint8_t* tile, int lane) {
+  constexpr int CH = D / 8, PER = 32 / CH;
+  const DecodeArgs& d = a.d;
+  const int ch = lane % CH;
+#pragma unroll
+  for (int x = 0; x < 32 / PER; x += 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int R = row0 + (x + y) * PER + lane / CH;
+      v[y] = make_uint4(0u, 0u, 0u, 0u);
+      if (R < a.rows) {
+        const int b = div_by(R, a.fg), gx = R - b * d.g;
+        v[y] = ld_global(reinterpret_cast<const uint4*>(
+                             d.q + (static_cast<size_t>(b) * d.Hq + static_cast<size_t>(h) * d.g + gx) * D) + ch);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int r = in_tile + (x + y) * PER + lane / CH;
+      *reinterpret_cast<uint4*>(tile + (ch / 8) * PfxCfg<D>::SLAB + r * 128 + (((ch % 8) ^ (r & 7)) * 16)) = v[y];
+    }
+  }
+}
+
+// Columns [c0, c1) of a warp's 32 rows, x f0 + y f1, to rows of a part. y only with
+// JOIN, and then only if it has been written (any).
+template <int D, bool JOIN>
+__device__ __forceinline__ void pfx_store(uint32_t tx, uint32_t ty, float f0, float f1, bool any, int c0, int c1,
+                                          float* dst, int rows, int lane, float4* slice) {
+  const int sub = lane >> 3, seg = lane & 7;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    uint32_t x[32], y[32];
+    tmem_ld_32x32b_x32(tx + c, x);
+    if (JOIN && any) tmem_ld_32x32b_x32(ty + c, y);
+    tmem_wait_ld();
+    reg_fence(x);
+    if (JOIN && any) {
+      reg_fence(y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      slice[lane * 8 + (i ^ (lane & 7))] = make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                                       __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + sub;
+      const float4 v = slice[r * 8 + (seg ^ (r & 7))];
+      if (r < rows) reinterpret_cast<float4*>(dst + static_cast<size_t>(r) * D + c)[seg] = v;
+    }
+    __syncwarp();
+  }
+}
+
+template <int D, bool BF16>
+__device__ bool pfx_rows(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem, int cta,
+                         int warp, int lane, const WaitCtx& wc) {
+  using C = PfxCfg<D>;
+  const int t = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+  const uint32_t t_s = lanes + C::TM_S(t), t_o = lanes + C::TM_O(t);
+  float4* slice = reinterpret_cast<float4*>(smem + C::OFF_STAGE + (warp - 4) * 4096);
+  const float sl2 = a.d.scale_log2;
+  int done[2] = {0, 0};  // tasks of both streams so far
+  int joined = 0;        // segments of one row tile
+  for (long long u = w.u0; u < w.u1;) {
+    const PfxSeg s = pfx_seg(a, w, u);
+    // Queries: tile t, or the one tile by the first group. All products that read the
+    // tile's last contents have completed (o_full below).
+    if (t == 0 || s.two) {
+      pfx_load_q<D>(a, s.h, s.row0 + t * kTileRows + quad * 32, quad * 32, smem + t * C::TILE, lane);
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full);
+    const int n0 = s.two ? s.cnt : (s.cnt + 1) / 2, n1 = s.two ? s.cnt : s.cnt / 2, n = t ? n1 : n0;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const PfxMask mask = pfx_mask(a, w.P, s.h, s.tile0 + (s.two ? i : 2 * i + t), lane);
+      if (!pfx_step<D, BF16>(sh, t, t_s, t_o, mask, a.d.box, sl2, i == 0, done[t] + i, m_ref, l, lane, wc)) return false;
+    }
+    done[0] += n0;
+    done[1] += n1;
+    if ((t == 0 || !s.two) && !mbar_wait_warp(&sh.o_full[0], (done[0] - 1) & 1, wc)) return false;
+    if ((t == 1 || !s.two) && n1 > 0 && !mbar_wait_warp(&sh.o_full[1], (done[1] - 1) & 1, wc)) return false;
+    __syncwarp();
+    tc_fence_after();
+    const float M = m_ref == -INFINITY ? -INFINITY : m_ref * sl2 - kPfxBias<BF16>;
+    const size_t part = static_cast<size_t>(shared_part(s.item, cta)) * 2 * kTileRows;
+    if (s.two) {
+      const int rows = min(32, s.rows - t * kTileRows - quad * 32);
+      pfx_store<D, false>(t_o, 0u, 1.f, 0.f, false, 0, D, a.part_o + (part + t * kTileRows + quad * 32) * D, rows, lane,
+                          slice);
+      if (lane < rows) a.part_ml[part + t * kTileRows + r] = make_float2(M, l);
+    } else {
+      // Both streams' sums of the same rows, half of the columns each. (The next
+      // segment's queries are complete, and sh.m free, when every warp is past this.)
+      sh.m[t][r] = M;
+      if (t == 1) sh.l1[r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.ml_full);
+      if (!mbar_wait_warp(&sh.ml_full, joined & 1, wc)) return false;
+      ++joined;
+      const float m0 = sh.m[0][r], m1 = sh.m[1][r];
+      const float top = fmaxf(m0, m1), f0 = step_down(m0, top), f1 = step_down(m1, top);
+      const int rows = min(32, s.rows - quad * 32);
+      pfx_store<D, true>(lanes + C::TM_O(0), lanes + C::TM_O(1), n1 > 0 ? f0 : 1.f, f1, n1 > 0, t * (D / 2),
+                         (t + 1) * (D / 2), a.part_o + (part + quad * 32) * D, rows, lane, slice);
+      if (t == 0 && lane < rows)
+        a.part_ml[part + r] = n1 > 0 ? make_float2(top, l * f0 + sh.l1[r] * f1) : make_float2(M, l);
+    }
+    tc_fence_before();
+    u += s.cnt;
+  }
+  return true;
+}
+
+static_assert(sizeof(PfxShared<128>) <= 2048 && sizeof(PfxShared<64>) <= 2048, "counted by PfxCfg");
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(PfxCfg<D>::THREADS, 1)
+    fa2_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PrefixArgs a) {
+  using C = PfxCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  __shared__ PfxShared<D> sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.q_full, 8);
+    mbar_init(&sh.ml_full, 8);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_full[t], 4);
+      mbar_init(&sh.o_full[t], 1);
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  grid_dependency_wait();
+  grid_launch_dependents();  // the kernel of the own slots relies on the wait above
+  const int cta = blockIdx.x;
+  const PfxWork w = pfx_work(a, cta);
+  if (cta == 0 && threadIdx.x == 0 && ld_global(a.d.prefix_len) != prefix_slots(a.d).len) report_page(a.d.c.status);
+  const WaitCtx wc{a.d.c.status, &sh.abort_flag, a.timeout_ns};
+  if (warp < 4) {
+    setmaxnreg_dec<88>();  // 4 x 32 x 88 + 8 x 32 x 208 = 64,512 = the launch's 384 x 168
+    if (warp == 0)
+      pfx_producer<D>(a, w, tm_k, sh.k_full, sh.k_empty, smem + C::OFF_K, lane, true, false, wc);
+    else if (warp == 3)
+      pfx_producer<D>(a, w, tm_v, sh.v_full, sh.v_empty, smem + C::OFF_V, lane, false, a.fault != 0, wc);
+    else if (warp == 1)
+      pfx_issuer<D, BF16>(a, w, sh, smem, tmem, wc);
+  } else {
+    setmaxnreg_inc<208>();
+    pfx_rows<D, BF16>(a, w, sh, smem, tmem, cta, warp, lane, wc);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---- Join -----------------------------------------------------------------------
+// A block has the query heads of one sequence and key head; a head's parts, of the
+// prefix and of its own slots, are dealt to as many of its 8 warps as there are per
+// head. A warp takes 1 (d = 128) or 2 parts at a time, (m, l) and O read together.
+constexpr int kPjThreads = 256, kPjWarps = kPjThreads / 32;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const PrefixArgs a) {
+  constexpr int LPR = D / 4, PPW = 32 / LPR;
+  __shared__ float s_m[kPjWarps], s_l[kPjWarps];
+  __shared__ float4 s_acc[kPjWarps][LPR];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const DecodeArgs& d = a.d;
+  const CacheView& c = d.c;
+  const int b = blockIdx.x / c.Hkv, h = blockIdx.x - b * c.Hkv;
+  int per_head = kPjWarps;  // warps of a head
+  while (per_head > 1 && kPjWarps / per_head < d.g) per_head >>= 1;
+  const int heads = kPjWarps / per_head, sub = warp % per_head;
+  grid_dependency_wait();
+  const PrefixLen P = prefix_slots(d);
+  const int len = seq_len(c, b), first = prefix_of(len, P), own = len - first;
+  const int HH = c.Hkv * d.HG, own_tiles = tiles_of<D>(own);
+  const long long T = d.starts[c.B], G = min(static_cast<long long>(a.tail_ctas), T), start = d.starts[b];
+  const long long pt = (P.cut + kTileRows - 1) / kTileRows, PT = pt * a.items, PG = min(static_cast<long long>(a.ctas), PT);
+  for (int x0 = 0; x0 < d.g; x0 += heads) {
+    const int gx = x0 + warp / per_head;
+    const bool on = gx < d.g;
+    float M = -INFINITY, S = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float m, float l, const float4& v) {
+      const float n = fmaxf(M, m), f = step_down(M, n), e = step_down(m, n);
+      M = n;
+      S = S * f + l * e;
+      acc = make_float4(acc.x * f + v.x * e, acc.y * f + v.y * e, acc.z * f + v.z * e, acc.w * f + v.w * e);
+    };
+    if (on) {
+      // Parts of the prefix, then own ones.
+      int np = 0, ns = 0, pi = 0, pc = 0, oi = 0, oc = 0, prow = 0;
+      if (first > 0) {
+        const int R = b * d.g + gx;
+        pi = h * (a.items / c.Hkv) + R / (2 * kTileRows);
+        prow = R % (2 * kTileRows);
+        pc = unit_cta(pi * pt, PG, PT);
+        np = unit_cta(pi * pt + pt - 1, PG, PT) - pc + 1;
+      }
+      if (own > 0) {
+        const int hh = h * d.HG + gx / a.head_tile;
+        oi = b * HH + hh;
+        const long long ub = start + static_cast<long long>(hh) * own_tiles;
+        oc = unit_cta(ub, G, T);
+        ns = unit_cta(ub + own_tiles - 1, G, T) - oc + 1;
+      }
+      const int e = (lane % LPR) * 4;
+#pragma unroll 4
+      for (int i = sub * PPW + lane / LPR; i < np + ns; i += per_head * PPW) {
+        const bool pre = i < np;
+        const size_t at = pre ? static_cast<size_t>(shared_part(pi, pc + i)) * (2 * kTileRows) + prow
+                              : static_cast<size_t>(shared_part(oi, oc + i - np)) * a.head_tile + gx % a.head_tile;
+        const float2 ml = (pre ? a.part_ml : d.part_ml)[at];
+        add(ml.x, ml.y, *reinterpret_cast<const float4*>((pre ? a.part_o : d.part_o) + at * D + e));
+      }
+    }
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, S, o);
+      const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                   __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+      add(m, l, v);
+    }
+    if (per_head > 1) {
+      if (lane < LPR) s_acc[warp][lane] = acc;
+      if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = S;
+      }
+      __syncthreads();
+      if (sub == 0 && lane < LPR)
+        for (int y = 1; y < per_head; ++y) add(s_m[warp + y], s_l[warp + y], s_acc[warp + y][lane]);
+      __syncthreads();
+    }
+    if (on && sub == 0 && lane < LPR) {
+      const size_t row = static_cast<size_t>(b) * d.Hq + static_cast<size_t>(h) * d.g + gx;
+      const float inv = S == 0.f ? 0.f : 1.f / S;
+      *reinterpret_cast<uint2*>(d.o + row * D + lane * 4) =
+          make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+      if (lane == 0) d.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+    }
+  }
+}
+
+cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas, cudaStream_t stream);
+
+template <int D, bool BF16>
+static cudaError_t launch_prefix_t(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a, cudaStream_t stream) {
+  auto kern = fa2_prefix_kernel<D, BF16>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, PfxCfg<D>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(a.ctas), dim3(PfxCfg<D>::THREADS), PfxCfg<D>::SMEM, stream, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  e = launch_decode_suffix(D, BF16, a.head_tile, a.d, a.tail_ctas, stream);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa2_prefix_join_kernel<D, BF16>, dim3(static_cast<unsigned>(a.d.c.B) * a.d.c.Hkv),
+                          dim3(kPjThreads), 0, stream, a);
+}
+
+cudaError_t launch_prefix_decode(int d, bool bf16, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,
+                                 cudaStream_t stream) {
+  if (d == 64) return bf16 ? launch_prefix_t<64, true>(tk, tv, a, stream) : launch_prefix_t<64, false>(tk, tv, a, stream);
+  return bf16 ? launch_prefix_t<128, true>(tk, tv, a, stream) : launch_prefix_t<128, false>(tk, tv, a, stream);
+}
+
+}  // namespace fa2

@@ -339,6 +339,33 @@ int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, co
 size_t fa2_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages,
                                        int weights);
 
+/* fa2_paged_decode (without weights) for sequences that begin with the same slots,
+ * which are read and multiplied once for all of them. Sequence b has the prefix if
+ * lens[b] >= prefix_len; its first prefix_len slots must then hold what the prefix's
+ * slots hold (as a rule they are the same pages; the last one, where the prefix ends
+ * inside a page, may be a copy). A shorter sequence is read by its own table alone.
+ *   prefix      : device int32 [prefix_pages]: the prefix's pages, in order.
+ *   prefix_len  : device int32 [1]: its slots, 0 .. prefix_pages * page_size (cut to
+ *                 it, FA2_ERR_PAGE).
+ *   prefix_pages: >= 1; prefix_pages * page_size <= 2^30.
+ *   workspace   : device, >= fa2_prefix_decode_workspace_size(...) bytes, 256-byte
+ *                 aligned, scratch owned by the caller.
+ *   other arguments as in fa2_paged_decode.
+ * Prefix slots past the last multiple of 16 (or of the largest power of two that
+ * divides page_size, if that is less) are read for each sequence by its own table. In
+ * the prefix P enters its product with a relative error of 2^-18 (bf16), or 2^-22 and
+ * 2^-36 of the row's largest (fp16), and an entry of V that is not finite makes o not
+ * finite. The result does not depend on timing: repeated calls give the same bits. */
+int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int* table, const int* lens,
+                      const int* prefix, const int* prefix_len, void* o, float* lse, int B, int Hq, int Hkv, int d,
+                      int num_pages, int page_size, int max_pages, int prefix_pages, float scale, int dtype,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of fa2_prefix_decode: the parts of the prefix, 256 fp32 rows of d for each
+ * 256 query rows of a key head and each CTA, and of the own slots. 0 for invalid
+ * sizes. */
+size_t fa2_prefix_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages);
+
 /* Appends new tokens: token i < num_new[b] of sequence b goes to slot
  * lens[b] + i; lens_out[b] = lens[b] + num_new[b]. Tokens past L are dropped
  * (FA2_ERR_PAGE).
@@ -563,6 +590,7 @@ int fa2_last_cuda_error(void);
  *   4  the next fa2_bwd (or fa2_bwd_qk, fa2_bwd_noalloc): the first V tile of
  *      every dQ worker;
  *   6  the next fa2_key_weights: the first Q tile of every CTA (there is no 5);
+ *   7  the next fa2_prefix_decode: the first V tile of every CTA of the prefix;
  *   0  disarms.
  * Outputs of the faulted call are undefined. Exists to test the failure path
  * without hanging or faulting the GPU. */
