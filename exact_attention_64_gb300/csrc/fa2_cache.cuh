@@ -164,7 +164,11 @@ struct DecodeArgs {
   const int* prefix;      // shared prefix: its pages [prefix_pages]
   const int* prefix_len;  // [1]
   int prefix_cap;         // slots that the prefix can have at most
-  long long* starts;      // workspace [B + 1]: units of the sequences before each
+  long long* starts;      // workspace [B + 1]: units before those of each sequence
+  int rows;               // query rows of a key head, B * g: row R is head R % g of sequence R / g
+  FastDiv fg;
+  int row_tiles;          // tiles of query rows whose prefix this kernel attends to itself, per key head, or 0
+  FastDiv ft;             // row_tiles
   int box;                // slots of one copy: a power of two, at most 16, that divides the page size
 };
 
@@ -186,9 +190,8 @@ struct PrefixArgs {
   DecodeArgs d;           // the slots behind the prefix: its view of the cache and its parts
   int head_tile;          // query heads of an item behind the prefix
   int tail_ctas;          // CTAs that work on them
-  int items;              // Hkv * ceil(rows / 256)
-  int rows;               // B * g query rows of a key head: row R is head R % g of sequence R / g
-  FastDiv fg;
+  int items;              // Hkv * ceil(rows / 256), or 0: d.row_tiles
+  FastDiv fblocks;        // items per key head
   int ctas;               // of the prefix
   float* part_o;          // workspace [items + ctas][256][d]: unnormalised O of a segment
   float2* part_ml;        // workspace [items + ctas][256]: its (m, l)

@@ -143,6 +143,21 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
   return s;
 }
 
+// Whether the prefix is attended to by the kernel of the own slots, in items of 8 or 16
+// of the rows = B g query rows of a key head. That saves a launch and the other kernel's
+// start, about 6 us, but reads and multiplies the prefix once for each 16 rows. (32/8
+// heads, d = 128, inside and outside: 2000 slots, 64 rows 20.9 and 21.3 us, 96 rows 26.1
+// and 22.4; 512 slots, 128 rows 16.4 and 19.8, 256 rows 25.0 and 24.2; 8192 slots, 32
+// rows 23.1 and 23.2, 48 rows 34.2 and 23.8. Two heads of 16384 slots, d = 64, 64 rows 17.6
+// and 17.8, 128 rows 27.2 and 20.9.)
+bool prefix_inside(int B, int Hq, int Hkv, int d, long long prefix_cap) {
+  const long long rows = static_cast<long long>(B) * (Hq / Hkv), tiles = (rows + 15) / 16;
+  return tiles == 1 || tiles * Hkv * prefix_cap <= 65536LL * 128 / d;
+}
+int prefix_head_tile(int B, int Hq, int Hkv, bool inside) {
+  return inside && static_cast<long long>(B) * (Hq / Hkv) > 8 ? 16 : head_tile(Hq / Hkv);
+}
+
 // Items of a shared prefix: up to 256 of the B * g query rows of a key head.
 long long prefix_items(int B, int Hq, int Hkv) {
   return static_cast<long long>(Hkv) * ((static_cast<long long>(B) * (Hq / Hkv) + 255) / 256);
@@ -153,12 +168,18 @@ long long prefix_items(int B, int Hq, int Hkv) {
 struct PrefixSpace {
   size_t po, pml, so, sml, starts, total;
 };
-PrefixSpace prefix_space(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
+PrefixSpace prefix_space(int B, int Hq, int Hkv, int d) {
   PrefixSpace s{};
-  const int ht = head_tile(Hq / Hkv);
-  const size_t rows = static_cast<size_t>(prefix_items(B, Hq, Hkv) + kPrefixCtas) * 256;
-  const size_t own = (static_cast<size_t>(B) * Hkv * ((Hq / Hkv + ht - 1) / ht) +
-                      decode_ctas(B, Hq, Hkv, d, page_size, max_pages)) * ht;
+  const int g = Hq / Hkv;
+  // Whichever kernel attends to the prefix.
+  const size_t rows = B * g <= 16 ? 0 : static_cast<size_t>(prefix_items(B, Hq, Hkv) + kPrefixCtas) * 256;
+  size_t own = 0;
+  for (const bool inside : {false, true}) {
+    const size_t ht = prefix_head_tile(B, Hq, Hkv, inside);
+    const size_t items = static_cast<size_t>(B) * Hkv * ((g + ht - 1) / ht) +
+                         (inside ? Hkv * ((static_cast<size_t>(B) * g + ht - 1) / ht) : 0);
+    own = std::max(own, (items + kDecodeCtas) * ht);
+  }
   s.pml = s.po + align_up(rows * d * 4, 256);
   s.so = s.pml + align_up(rows * 8, 256);
   s.sml = s.so + align_up(own * d * 4, 256);
@@ -247,7 +268,7 @@ int fa2_paged_decode(const void* q, const void* k_cache, const void* v_cache, co
 size_t fa2_prefix_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size, int max_pages) {
   if (check_heads(Hq, Hkv) != FA2_OK) return 0;
   if (check_cache(B, Hkv, d, 1, page_size, max_pages, FA2_BF16) != FA2_OK) return 0;
-  return prefix_space(B, Hq, Hkv, d, page_size, max_pages).total;
+  return prefix_space(B, Hq, Hkv, d).total;
 }
 
 int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int* table, const int* lens,
@@ -264,7 +285,7 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(table, 4) ||
       !aligned(lens, 4) || !aligned(prefix, 4) || !aligned(prefix_len, 4) || !aligned(lse, 4))
     return FA2_ERR_ALIGNMENT;
-  const PrefixSpace s = prefix_space(B, Hq, Hkv, d, page_size, max_pages);
+  const PrefixSpace s = prefix_space(B, Hq, Hkv, d);
   if (workspace == nullptr || workspace_bytes < s.total) return FA2_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return FA2_ERR_ALIGNMENT;
   const size_t qb = static_cast<size_t>(B) * Hq * d * 2, cb = cache_bytes(Hkv, d, num_pages, page_size);
@@ -295,23 +316,33 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   c.starts = reinterpret_cast<long long*>(ws + s.starts);
   c.Hq = Hq;
   c.g = Hq / Hkv;
-  a.head_tile = head_tile(c.g);
+  c.prefix_cap = prefix_pages * page_size;
+  const bool inside = prefix_inside(B, Hq, Hkv, d, c.prefix_cap);
+  a.head_tile = prefix_head_tile(B, Hq, Hkv, inside);
   c.HG = (c.g + a.head_tile - 1) / a.head_tile;
   c.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   c.prefix = prefix;
   c.prefix_len = prefix_len;
-  c.prefix_cap = prefix_pages * page_size;
-  const int most = decode_ctas(B, Hq, Hkv, d, page_size, max_pages);
-  a.tail_ctas = 2 * sms < most ? 2 * sms : most;
-  a.rows = B * c.g;
-  a.fg = fa2::fast_div(c.g);
-  a.items = static_cast<int>(prefix_items(B, Hq, Hkv));
-  const long long units = a.items * ((static_cast<long long>(c.prefix_cap) + 127) / 128);
-  a.ctas = static_cast<int>(std::min<long long>(units, std::min(sms, kPrefixCtas)));
+  c.rows = B * c.g;
+  c.fg = fa2::fast_div(c.g);
+  // At most one CTA per unit of full tables.
+  const int unit = fa2::decode_unit(d);
+  long long units = static_cast<long long>(B) * Hkv * c.HG * ((static_cast<long long>(c.c.L) + unit - 1) / unit);
+  if (inside) {
+    c.row_tiles = (c.rows + a.head_tile - 1) / a.head_tile;
+    c.ft = fa2::fast_div(c.row_tiles);
+    units += static_cast<long long>(Hkv) * c.row_tiles * ((static_cast<long long>(c.prefix_cap) + unit - 1) / unit);
+  } else {
+    a.items = static_cast<int>(prefix_items(B, Hq, Hkv));
+    a.fblocks = fa2::fast_div(a.items / Hkv);
+    a.ctas = static_cast<int>(std::min<long long>(a.items * ((static_cast<long long>(c.prefix_cap) + 127) / 128),
+                                                  std::min(sms, kPrefixCtas)));
+  }
+  a.tail_ctas = static_cast<int>(std::min<long long>(units, std::min(2 * sms, kDecodeCtas)));
   a.part_o = reinterpret_cast<float*>(ws + s.po);
   a.part_ml = reinterpret_cast<float2*>(ws + s.pml);
   a.timeout_ns = fa2::kDefaultWaitTimeoutNs;
-  a.fault = fa2::host_take_fault(7, &a.timeout_ns);
+  if (!inside) a.fault = fa2::host_take_fault(7, &a.timeout_ns);
   (void)cudaGetLastError();
   const cudaError_t e = fa2::launch_prefix_decode(d, dtype == FA2_BF16, tk, tv, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);

@@ -15,7 +15,8 @@ constexpr float kLog2ef = 1.4426950408889634f;
 
 // ---- Units ---------------------------------------------------------------
 // HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
-// SHARED: a sequence that reaches the prefix has the slots behind it only.
+// SHARED: a sequence that reaches the prefix has the slots behind it only; before all
+// sequences may come items of the prefix itself (b = -1, hh their number).
 template <int D>
 __device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
 
@@ -55,16 +56,15 @@ struct UnitMap {
     const int x = seq_len(c, b);
     return SHARED ? x - prefix_of(x, P) : x;
   }
-  // out[b]: units of the sequences before b; out[B] = T.
-  __device__ void write_starts(long long* out) const {
-    long long base = 0;
+  // out[b]: units before those of sequence b, `base` before all; out[B] = base + T.
+  __device__ void write_starts(long long* out, long long base) const {
+    if (lane == 0) out[c.B] = base + T;
     for (int b0 = 0; b0 < c.B; b0 += 32) {
       const int len = b0 == 0 ? n : length(b0 + lane);
       const long long sum = scan(len);
       if (b0 + lane < c.B) out[b0 + lane] = base + sum - static_cast<long long>(tiles_of<D>(len)) * HH;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) out[c.B] = T;
   }
   __device__ long long scan(int slots) const {
     long long t = static_cast<long long>(tiles_of<D>(slots)) * HH;
@@ -102,10 +102,10 @@ struct UnitMap {
 };
 
 template <int D, bool SHARED = false>
-__device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k, PrefixLen P = {}) {
+__device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k, PrefixLen P = {}, int prefix_items = 0) {
   if (++k.tile < k.ntiles) return;
   k.tile = 0;
-  if (++k.hh < HH) return;
+  if (++k.hh < (SHARED && k.b < 0 ? prefix_items : HH)) return;
   k.hh = 0;
   do {
     if (++k.b >= c.B) {

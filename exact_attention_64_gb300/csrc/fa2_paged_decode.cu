@@ -235,9 +235,11 @@ struct DecCfg {
   static constexpr int HEADS = 8 * NT;                     // query heads of a tile
 };
 
-// SHARED: the slots behind a prefix that another kernel of the call attends to at the
-// same time (fa2_prefix_decode.cu), which has waited for what came before the call and
-// lets this one begin early; this one ends after it. Every segment is left as a part.
+// SHARED: the slots behind a prefix (fa2_prefix_decode.cu). Every segment is left as a
+// part. The prefix is either this kernel's, in items of their own that come first (8 NT
+// query rows of a key head, whatever sequences they are of), or that of another kernel
+// of the call, which has waited for what came before the call and lets this one begin
+// early; this one ends after it.
 template <int D, bool BF16, int NT, bool WEIGHTS, bool SHARED = false>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
   using C = DecCfg<D, NT>;
@@ -245,10 +247,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
   __shared__ float s_lse[C::HEADS];
-  if constexpr (!SHARED) grid_dependency_wait();
+  if (!SHARED || a.row_tiles > 0) grid_dependency_wait();
   grid_launch_dependents();
   PrefixLen P{};
-  if constexpr (SHARED) P = prefix_slots(a);
+  int PI = 0;  // items of the prefix
+  if constexpr (SHARED) {
+    P = prefix_slots(a);
+    if (P.cut > 0) PI = a.row_tiles * a.c.Hkv;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
@@ -272,12 +278,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     }
   } else {
     const UnitMap<D, SHARED> map(c, HH, lane, P);
-    const long long T = map.T, G = min(static_cast<long long>(gridDim.x), T);
+    const long long PU = SHARED ? static_cast<long long>(PI) * tiles_of<D>(P.cut) : 0;
+    const long long T = PU + map.T, G = min(static_cast<long long>(gridDim.x), T);
     if (cta == 0 && warp == 0)
       for (int b = lane; b < c.B; b += 32)
         if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
     if constexpr (SHARED) {
-      if (cta == 0 && warp == 1) map.write_starts(a.starts);  // for the join
+      if (cta == 0 && warp == 1) map.write_starts(a.starts, PU);  // for the join
+      if (cta == 0 && threadIdx.x == 0 && a.row_tiles > 0 && ld_global(a.prefix_len) != P.len) report_page(c.status);
     }
     if (cta >= G) {
       if constexpr (SHARED) grid_dependency_wait();
@@ -285,8 +293,25 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     }
     u0 = unit_begin(cta, G, T);
     u1 = unit_begin(cta + 1, G, T);
-    cc = map.at(u0);
+    if (SHARED && u0 < PU) {
+      cc.b = -1;
+      cc.n = P.cut;
+      cc.ntiles = tiles_of<D>(P.cut);
+      cc.hh = static_cast<int>(div_pos(u0, cc.ntiles));
+      cc.tile = static_cast<int>(u0 - static_cast<long long>(cc.hh) * cc.ntiles);
+      cc.start = 0;
+    } else {
+      cc = map.at(u0 - PU);
+    }
   }
+  // Key head of an item, and its first row: a head of the group, or a query row.
+  auto key_head = [&](const UnitCursor& k) {
+    if (SHARED && k.b < 0) return div_by(k.hh, a.ft);
+    return a.HG == 1 ? k.hh : k.hh / a.HG;
+  };
+  auto first_row = [&](const UnitCursor& k, int h) {
+    return (k.hh - h * (SHARED && k.b < 0 ? a.row_tiles : a.HG)) * C::HEADS;
+  };
   UnitCursor ic = cc;  // next unit to copy
   const uint64_t pol = read_once_policy();
   const uint32_t ring = smem_u32(smem) + warp * (C::STAGES * C::STAGE);
@@ -300,11 +325,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   auto look_up = [&]() {
     const int slot = ic.tile * kUnit<D> + warp * C::ROWS + (lane & (C::ROWS - 1));
     in = left > 0 && slot < ic.n;
-    hk = a.HG == 1 ? ic.hh : ic.hh / a.HG;
+    hk = key_head(ic);
     if (in) {
       const int at = SHARED ? slot + ic.start : slot, p = div_by(at, c.ps);
       off = at - p * c.ps.d;
-      pg = ld_global(c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
+      pg = ld_global(SHARED && ic.b < 0 ? a.prefix + p : c.table + static_cast<size_t>(ic.b) * c.max_pages + p);
     }
   };
   auto copy_next = [&](int st) {
@@ -328,7 +353,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0, pol);
         }
       }
-      unit_advance<D, SHARED>(c, HH, ic, P);
+      unit_advance<D, SHARED>(c, HH, ic, P, PI);
       --left;
       look_up();
     }
@@ -344,17 +369,22 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   int st = 0;
   const int t = lane & 3, r8 = lane >> 2;
   auto load_q = [&](const UnitCursor& k) {
-    const int h = a.HG == 1 ? k.hh : k.hh / a.HG;
-    const int head0 = (k.hh - h * a.HG) * C::HEADS;
+    const int h = key_head(k), head0 = first_row(k, h);
+    const int rows = SHARED && k.b < 0 ? a.rows : a.g;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int hd = head0 + nt * 8 + r8;
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(
-          a.q + (static_cast<size_t>(k.b) * a.Hq + static_cast<size_t>(h) * a.g + (hd < a.g ? hd : 0)) * D);
+      int b = k.b, x = hd < rows ? hd : 0;
+      if (SHARED && b < 0) {
+        b = div_by(x, a.fg);
+        x -= b * a.g;
+      }
+      const uint32_t* qp =
+          reinterpret_cast<const uint32_t*>(a.q + (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * a.g + x) * D);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        qf[nt][kk][0] = hd < a.g ? ld_global(qp + kk * 8 + t) : 0u;
-        qf[nt][kk][1] = hd < a.g ? ld_global(qp + kk * 8 + 4 + t) : 0u;
+        qf[nt][kk][0] = hd < rows ? ld_global(qp + kk * 8 + t) : 0u;
+        qf[nt][kk][1] = hd < rows ? ld_global(qp + kk * 8 + 4 + t) : 0u;
       }
     }
   };
@@ -362,8 +392,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
 #pragma unroll 1
   for (long long u = u0; u < u1; ++u) {
     const bool first = u == u0 || cc.tile == 0;
-    const int h = a.HG == 1 ? cc.hh : cc.hh / a.HG;
-    const int head0 = (cc.hh - h * a.HG) * C::HEADS;  // first head of the tile inside its group
+    const int h = key_head(cc);
+    const int head0 = first_row(cc, h);  // first head of the tile inside its group
     if (first) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -482,11 +512,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       // End of a segment: the four warps' (m, l, O) are merged, while the next
       // one's queries are on their way.
       UnitCursor next = cc;
-      unit_advance<D, SHARED>(c, HH, next, P);
+      unit_advance<D, SHARED>(c, HH, next, P, PI);
       if (u + 1 < u1) load_q(next);
       const bool from_start = cc.tile - (u - u0) <= 0;  // the segment begins with its item
       const bool whole = !SHARED && from_start && cc.tile + 1 == cc.ntiles;
-      const int slot = SHARED ? shared_part(cc.b * HH + cc.hh, cta) : 2 * cta + (from_start ? 1 : 0);
+      const int slot = SHARED ? shared_part((cc.b < 0 ? 0 : PI + cc.b * HH) + cc.hh, cta) : 2 * cta + (from_start ? 1 : 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -529,7 +559,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           }
         }
         const int gh = head0 + nt * 8 + hd;
-        if (gh < a.g) {
+        if (gh < (SHARED && cc.b < 0 ? a.rows : a.g)) {
           if (whole) {
             const size_t row = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(h) * a.g + gh;
             const float inv = S == 0.f ? 0.f : 1.f / S;
@@ -553,7 +583,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         __syncthreads();
       }
     }
-    unit_advance<D, SHARED>(c, HH, cc, P);
+    unit_advance<D, SHARED>(c, HH, cc, P, PI);
   }
   if constexpr (SHARED) grid_dependency_wait();
   if constexpr (WEIGHTS) {

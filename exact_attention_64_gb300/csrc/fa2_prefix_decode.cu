@@ -46,7 +46,8 @@ struct PfxCfg {
   static_assert(SMEM + 2048 <= 232448, "with the static part at most what a CTA can have");
   static constexpr int THREADS = 384;
   static constexpr uint32_t TMEM_COLS = 512;
-  __host__ __device__ static constexpr uint32_t TM_S(int t) { return t * 128u; }  // P: its two pieces, 64 columns each
+  // P overwrites S, 32 slots in 32 columns: 16 of the first pieces, 16 of the second.
+  __host__ __device__ static constexpr uint32_t TM_S(int t) { return t * 128u; }
   __host__ __device__ static constexpr uint32_t TM_O(int t) { return 256u + t * D; }
 };
 
@@ -89,13 +90,12 @@ __device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta) {
 }
 __device__ __forceinline__ PfxSeg pfx_seg(const PrefixArgs& a, const PfxWork& w, long long u) {
   PfxSeg s;
-  const int blocks = a.items / a.d.c.Hkv;
   s.item = static_cast<int>(div_pos(u, w.tiles));
   s.tile0 = static_cast<int>(u - static_cast<long long>(s.item) * w.tiles);
   s.cnt = static_cast<int>(min(static_cast<long long>(w.tiles - s.tile0), w.u1 - u));
-  s.h = s.item / blocks;
-  s.row0 = (s.item - s.h * blocks) * 2 * kTileRows;
-  s.rows = min(2 * kTileRows, a.rows - s.row0);
+  s.h = div_by(s.item, a.fblocks);
+  s.row0 = (s.item - s.h * a.fblocks.d) * 2 * kTileRows;
+  s.rows = min(2 * kTileRows, a.d.rows - s.row0);
   s.two = s.rows > kTileRows;
   return s;
 }
@@ -151,7 +151,11 @@ __device__ bool pfx_producer(const PrefixArgs& a, const PfxWork& w, const CUtens
 // ---- Products -----------------------------------------------------------------
 // Task i of a segment: row tile i & 1 with slot tile i / 2 (two row tiles), or the one
 // row tile with slot tile i for stream i & 1. S(i) and S(i + 1) are in flight; S(i + 2)
-// follows O += P(i) V, which reads the P that it overwrites.
+// follows O += P(i) V, which reads the P that it overwrites. A task's 24 products take
+// about 1850 clocks (B = 256, 32/8 heads, d = 128), the next one's begin 400 later. Not
+// kept: a warp for each stream, whose products interleave (65 clocks each instead of 77
+// to 90) but whose rows are then all at work at once, 6200 clocks a slot tile of both
+// streams instead of 4600; O in two halves of d in turn, 4900.
 template <int D, bool BF16>
 __device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem,
                            const WaitCtx& wc) {
@@ -196,9 +200,8 @@ __device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& 
       for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
         for (int kk = 0; kk < kTileRows / 16; ++kk)
-          umma_ts_warp(tmem + C::TM_O(t), tmem + C::TM_S(t) + piece * 64 + kk * 8,
-                       make_sdesc_sw128(vt + kk * 2048, C::SLAB, 1024), id_o,
-                       (i >= 2 || piece > 0 || kk > 0) ? 1u : 0u);
+          umma_ts_warp(tmem + C::TM_O(t), tmem + C::TM_S(t) + (kk / 2) * 32 + piece * 16 + (kk % 2) * 8,
+                       make_sdesc_sw128(vt + kk * 2048, C::SLAB, 1024), id_o, (i >= 2 || piece > 0 || kk > 0) ? 1u : 0u);
       umma_commit_warp(&sh.o_full[t]);
       if (!s.two || t == 1) umma_commit_warp(&sh.v_empty[st]);
       if (i + 2 < n) ok = issue_s(i + 2);
@@ -238,6 +241,14 @@ __device__ __forceinline__ PfxMask pfx_mask(const PrefixArgs& a, int P, int h, i
   return m;
 }
 
+// The first piece of two values of p. bf16: cut, one permutation; the remainder then has
+// up to 2^-7 of p, and its rounding leaves 2^-15.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pfx_high(float2 p) {
+  if constexpr (BF16) return __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
+  else return pack_f16x2(p.x, p.y);
+}
+
 // One slot tile of a thread's row: P from S, the row's sum, and O's rescale when the
 // reference moves (only when the maximum passes it by kPfxRescale: exact, O and l share
 // it).
@@ -248,28 +259,38 @@ __device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, 
   if (!mbar_wait_warp(&sh.s_full[t], done & 1, wc)) return false;
   __syncwarp();
   tc_fence_after();
-  uint32_t s[128];
+  // Columns [64 half, 64 half + 64) of S, masked.
+  uint32_t s[64];
+  auto load = [&](int half) {
+    tmem_ld_32x32b_x32(t_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+    tmem_ld_32x32b_x32(t_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+    tmem_wait_ld();
+    reg_fence(s);
+    if (!mask.all) {
+      const int lb = __ffs(box) - 1;
+      const uint32_t w0 = half ? mask.w[2] : mask.w[0], w1 = half ? mask.w[3] : mask.w[1];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
-  tmem_wait_ld();
-  reg_fence(s);
-  if (!mask.all) {
-    const int lb = __ffs(box) - 1;
-#pragma unroll
-    for (int c = 0; c < 128; ++c) {
-      const int i = c >> lb;
-      const uint32_t word = i < 64 ? (i < 32 ? mask.w[0] : mask.w[1]) : (i < 96 ? mask.w[2] : mask.w[3]);
-      if (!((word >> (i & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+      for (int c = 0; c < 64; ++c) {
+        // Box (64 half + c) / box; below 32 boxes a half's are bits of the first word.
+        const int i = (64 * half + c) >> lb;
+        const uint32_t word = box >= 4 ? mask.w[0] : box == 2 ? (half ? mask.w[1] : mask.w[0]) : (c < 32 ? w0 : w1);
+        if (!((word >> (i & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+      }
     }
+  };
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    load(half);
+    float m8[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) m8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[8 + x]));
+#pragma unroll
+    for (int c = 16; c < 64; c += 16)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) m8[x] = fmax3(m8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
+    mx = fmax3(mx, fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
   }
-  float mx8[8];
-#pragma unroll
-  for (int x = 0; x < 8; ++x) mx8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[8 + x]));
-#pragma unroll
-  for (int c = 16; c < 128; c += 16)
-#pragma unroll
-    for (int x = 0; x < 8; ++x) mx8[x] = fmax3(mx8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
-  const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
   const float m_new = fmaxf(m_ref, mx);
   const bool rescale = (m_new - m_ref) * sl2 > kPfxRescale<BF16>;  // also from -inf
   float alpha = 1.f;
@@ -278,25 +299,28 @@ __device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, 
     m_ref = m_new;
   }
   const float neg = m_ref == -INFINITY ? 0.f : kPfxBias<BF16> - m_ref * sl2;
-  float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 sl = make_float2(sl2, sl2), ng = make_float2(neg, neg);
-#pragma unroll
+#pragma unroll 1
   for (int half = 0; half < 2; ++half) {
-    uint32_t hi[32], lo[32];
+    load(half);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const int e = 64 * half + 2 * c;
-      const float2 x = f2_fma(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl, ng);
-      const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      rs[c & 3] = f2_add(rs[c & 3], p);
-      hi[c] = pack_x2<BF16>(p.x, p.y);
-      const float2 r = f2_sub(p, unpack_x2<BF16>(hi[c]));
-      lo[c] = pack_x2<BF16>(r.x, r.y);
+    for (int q = 0; q < 2; ++q) {
+      uint32_t pp[32];  // 32 slots: 16 columns of the rounded values, 16 of the remainders
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int e = 32 * q + 2 * c;
+        const float2 x = f2_fma(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl, ng);
+        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        rs[c & 1] = f2_add(rs[c & 1], p);
+        pp[c] = pfx_high<BF16>(p);
+        const float2 r = f2_sub(p, unpack_x2<BF16>(pp[c]));
+        pp[16 + c] = pack_x2<BF16>(r.x, r.y);
+      }
+      tmem_st_32x32b_x32(t_s + 64 * half + 32 * q, pp);
     }
-    tmem_st_32x32b_x32(t_s + 32 * half, hi);
-    tmem_st_32x32b_x32(t_s + 64 + 32 * half, lo);
   }
-  l = l * alpha + (((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y)));
+  l = l * alpha + ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y));
   tmem_wait_st();
   if (!first && __any_sync(0xffffffffu, rescale)) {
     if (!mbar_wait_warp(&sh.o_full[t], (done - 1) & 1, wc)) return false;
@@ -320,28 +344,28 @@ __device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, 
   return true;
 }
 
-// Query rows of a warp (32 of them, from row0 on) into a Q tile.
+// Rows [r0, r0 + n) of a tile of query rows, by a warp, 8 loads in flight.
 template <int D>
-__device__ __forceinline__ void pfx_load_q(const PrefixArgs& a, int h, int row0, int in_tile, uint8_t* tile, int lane) {
+__device__ __forceinline__ void pfx_load_q(const PrefixArgs& a, int h, int row0, int r0, int n, uint8_t* tile, int lane) {
   constexpr int CH = D / 8, PER = 32 / CH;
   const DecodeArgs& d = a.d;
-  const int ch = lane % CH;
+  const int ch = lane % CH, sub = lane / CH;
+#pragma unroll 1
+  for (int x = 0; x < n; x += 8 * PER) {
+    uint4 v[8];
 #pragma unroll
-  for (int x = 0; x < 32 / PER; x += 4) {
-    uint4 v[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int R = row0 + (x + y) * PER + lane / CH;
+    for (int y = 0; y < 8; ++y) {
+      const int R = row0 + r0 + x + y * PER + sub;
       v[y] = make_uint4(0u, 0u, 0u, 0u);
-      if (R < a.rows) {
-        const int b = div_by(R, a.fg), gx = R - b * d.g;
+      if (R < d.rows) {
+        const int b = div_by(R, d.fg), gx = R - b * d.g;
         v[y] = ld_global(reinterpret_cast<const uint4*>(
                              d.q + (static_cast<size_t>(b) * d.Hq + static_cast<size_t>(h) * d.g + gx) * D) + ch);
       }
     }
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int r = in_tile + (x + y) * PER + lane / CH;
+    for (int y = 0; y < 8; ++y) {
+      const int r = r0 + x + y * PER + sub;
       *reinterpret_cast<uint4*>(tile + (ch / 8) * PfxCfg<D>::SLAB + r * 128 + (((ch % 8) ^ (r & 7)) * 16)) = v[y];
     }
   }
@@ -394,12 +418,11 @@ __device__ bool pfx_rows(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh
   int joined = 0;        // segments of one row tile
   for (long long u = w.u0; u < w.u1;) {
     const PfxSeg s = pfx_seg(a, w, u);
-    // Queries: tile t, or the one tile by the first group. All products that read the
-    // tile's last contents have completed (o_full below).
-    if (t == 0 || s.two) {
-      pfx_load_q<D>(a, s.h, s.row0 + t * kTileRows + quad * 32, quad * 32, smem + t * C::TILE, lane);
-      fence_proxy_async_smem();
-    }
+    // Queries: tile t, or half a warp's rows of the one tile each. All products that
+    // read the tile's last contents have completed (o_full below).
+    if (s.two) pfx_load_q<D>(a, s.h, s.row0 + t * kTileRows, quad * 32, 32, smem + t * C::TILE, lane);
+    else pfx_load_q<D>(a, s.h, s.row0, quad * 32 + t * 16, 16, smem, lane);
+    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_full);
     const int n0 = s.two ? s.cnt : (s.cnt + 1) / 2, n1 = s.two ? s.cnt : s.cnt / 2, n = t ? n1 : n0;
@@ -508,92 +531,101 @@ __global__ void __launch_bounds__(PfxCfg<D>::THREADS, 1)
 }
 
 // ---- Join -----------------------------------------------------------------------
-// A block has the query heads of one sequence and key head; a head's parts, of the
-// prefix and of its own slots, are dealt to as many of its 8 warps as there are per
-// head. A warp takes 1 (d = 128) or 2 parts at a time, (m, l) and O read together.
+// A query row's parts, of the prefix and of its own slots, by `per_row` warps (a power of
+// two, so that each has about four to read at once). A warp takes 1 (d = 128) or 2 parts
+// at a time, (m, l) and O read together.
 constexpr int kPjThreads = 256, kPjWarps = kPjThreads / 32;
+constexpr int kPjResident = 152 * 32;  // warps of the join that run at once
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const PrefixArgs a) {
-  constexpr int LPR = D / 4, PPW = 32 / LPR;
-  __shared__ float s_m[kPjWarps], s_l[kPjWarps];
+__global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const PrefixArgs a, int per_row) {
+  constexpr int LPR = D / 4, PPW = 32 / LPR, U = 4;
+  __shared__ float2 s_ml[kPjWarps];
   __shared__ float4 s_acc[kPjWarps][LPR];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (per_row - 1);
   const DecodeArgs& d = a.d;
   const CacheView& c = d.c;
-  const int b = blockIdx.x / c.Hkv, h = blockIdx.x - b * c.Hkv;
-  int per_head = kPjWarps;  // warps of a head
-  while (per_head > 1 && kPjWarps / per_head < d.g) per_head >>= 1;
-  const int heads = kPjWarps / per_head, sub = warp % per_head;
+  const long long row = (static_cast<long long>(blockIdx.x) * kPjWarps + warp) / per_row;
+  const bool on = row < static_cast<long long>(c.B) * d.Hq;
+  const int b = on ? static_cast<int>(row / d.Hq) : 0, x = on ? static_cast<int>(row - static_cast<long long>(b) * d.Hq) : 0;
+  const int h = div_by(x, d.fg), gx = x - h * d.g;
   grid_dependency_wait();
   const PrefixLen P = prefix_slots(d);
   const int len = seq_len(c, b), first = prefix_of(len, P), own = len - first;
-  const int HH = c.Hkv * d.HG, own_tiles = tiles_of<D>(own);
-  const long long T = d.starts[c.B], G = min(static_cast<long long>(a.tail_ctas), T), start = d.starts[b];
-  const long long pt = (P.cut + kTileRows - 1) / kTileRows, PT = pt * a.items, PG = min(static_cast<long long>(a.ctas), PT);
-  for (int x0 = 0; x0 < d.g; x0 += heads) {
-    const int gx = x0 + warp / per_head;
-    const bool on = gx < d.g;
-    float M = -INFINITY, S = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float m, float l, const float4& v) {
-      const float n = fmaxf(M, m), f = step_down(M, n), e = step_down(m, n);
-      M = n;
-      S = S * f + l * e;
-      acc = make_float4(acc.x * f + v.x * e, acc.y * f + v.y * e, acc.z * f + v.z * e, acc.w * f + v.w * e);
-    };
-    if (on) {
-      // Parts of the prefix, then own ones.
-      int np = 0, ns = 0, pi = 0, pc = 0, oi = 0, oc = 0, prow = 0;
-      if (first > 0) {
-        const int R = b * d.g + gx;
-        pi = h * (a.items / c.Hkv) + R / (2 * kTileRows);
-        prow = R % (2 * kTileRows);
-        pc = unit_cta(pi * pt, PG, PT);
-        np = unit_cta(pi * pt + pt - 1, PG, PT) - pc + 1;
-      }
-      if (own > 0) {
-        const int hh = h * d.HG + gx / a.head_tile;
-        oi = b * HH + hh;
-        const long long ub = start + static_cast<long long>(hh) * own_tiles;
-        oc = unit_cta(ub, G, T);
-        ns = unit_cta(ub + own_tiles - 1, G, T) - oc + 1;
-      }
-      const int e = (lane % LPR) * 4;
-#pragma unroll 4
-      for (int i = sub * PPW + lane / LPR; i < np + ns; i += per_head * PPW) {
+  const long long T = ld_global(d.starts + c.B), start = ld_global(d.starts + b);
+  // Parts of the prefix, then own ones.
+  int np = 0, ns = 0, p_step = 0;
+  size_t p0 = 0, o0 = 0;  // their first rows in the workspace
+  const long long G = min(static_cast<long long>(a.tail_ctas), T);
+  const bool inside = d.row_tiles > 0;  // the prefix was attended to by the kernel of the own slots
+  const int PI = inside && P.cut > 0 ? d.row_tiles * c.Hkv : 0;
+  if (first > 0) {
+    const int R = b * d.g + gx;
+    p_step = inside ? a.head_tile : 2 * kTileRows;
+    const long long tiles = inside ? tiles_of<D>(P.cut) : (P.cut + kTileRows - 1) / kTileRows;
+    const long long PT = inside ? T : tiles * a.items, PG = inside ? G : min(static_cast<long long>(a.ctas), PT);
+    const int item = h * (inside ? d.row_tiles : a.fblocks.d) + R / p_step;
+    const int c0 = unit_cta(item * tiles, PG, PT);
+    np = unit_cta(item * tiles + tiles - 1, PG, PT) - c0 + 1;
+    p0 = static_cast<size_t>(shared_part(item, c0)) * p_step + R % p_step;
+  }
+  if (own > 0) {
+    const int HH = c.Hkv * d.HG, tiles = tiles_of<D>(own), hh = h * d.HG + gx / a.head_tile;
+    const long long u = start + static_cast<long long>(hh) * tiles;
+    const int c0 = unit_cta(u, G, T);
+    ns = unit_cta(u + tiles - 1, G, T) - c0 + 1;
+    o0 = static_cast<size_t>(shared_part(PI + b * HH + hh, c0)) * a.head_tile + gx % a.head_tile;
+  }
+  const float2* p_ml = inside ? d.part_ml : a.part_ml;
+  const float* p_o = inside ? d.part_o : a.part_o;
+  if (!on) np = ns = 0;
+  float M = -INFINITY, S = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m, float l, const float4& v) {
+    const float n = fmaxf(M, m), f = step_down(M, n), e = step_down(m, n);
+    M = n;
+    S = S * f + l * e;
+    acc = make_float4(acc.x * f + v.x * e, acc.y * f + v.y * e, acc.z * f + v.z * e, acc.w * f + v.w * e);
+  };
+  const int e = (lane % LPR) * 4, stride = per_row * PPW;
+#pragma unroll 1
+  for (int i0 = sub * PPW + lane / LPR; i0 < np + ns; i0 += U * stride) {
+    float2 ml[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * stride;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < np + ns) {
         const bool pre = i < np;
-        const size_t at = pre ? static_cast<size_t>(shared_part(pi, pc + i)) * (2 * kTileRows) + prow
-                              : static_cast<size_t>(shared_part(oi, oc + i - np)) * a.head_tile + gx % a.head_tile;
-        const float2 ml = (pre ? a.part_ml : d.part_ml)[at];
-        add(ml.x, ml.y, *reinterpret_cast<const float4*>((pre ? a.part_o : d.part_o) + at * D + e));
+        const size_t at = pre ? p0 + static_cast<size_t>(i) * p_step : o0 + static_cast<size_t>(i - np) * a.head_tile;
+        ml[u] = ld_global((pre ? p_ml : d.part_ml) + at);
+        v[u] = ld_global(reinterpret_cast<const float4*>((pre ? p_o : d.part_o) + at * D + e));
       }
     }
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) {
-      const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, S, o);
-      const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
-                                   __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
-      add(m, l, v);
-    }
-    if (per_head > 1) {
-      if (lane < LPR) s_acc[warp][lane] = acc;
-      if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = S;
-      }
-      __syncthreads();
-      if (sub == 0 && lane < LPR)
-        for (int y = 1; y < per_head; ++y) add(s_m[warp + y], s_l[warp + y], s_acc[warp + y][lane]);
-      __syncthreads();
-    }
-    if (on && sub == 0 && lane < LPR) {
-      const size_t row = static_cast<size_t>(b) * d.Hq + static_cast<size_t>(h) * d.g + gx;
-      const float inv = S == 0.f ? 0.f : 1.f / S;
-      *reinterpret_cast<uint2*>(d.o + row * D + lane * 4) =
-          make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
-      if (lane == 0) d.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
-    }
+    for (int u = 0; u < U; ++u) add(ml[u].x, ml[u].y, v[u]);
+  }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+    const float m = __shfl_xor_sync(0xffffffffu, M, o), l = __shfl_xor_sync(0xffffffffu, S, o);
+    const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                 __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+    add(m, l, v);
+  }
+  if (per_row > 1) {
+    if (lane < LPR) s_acc[warp][lane] = acc;
+    if (lane == 0) s_ml[warp] = make_float2(M, S);
+    __syncthreads();
+    if (sub == 0 && lane < LPR)
+      for (int y = 1; y < per_row; ++y) add(s_ml[warp + y].x, s_ml[warp + y].y, s_acc[warp + y][lane]);
+  }
+  if (on && sub == 0 && lane < LPR) {
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    *reinterpret_cast<uint2*>(d.o + row * D + lane * 4) =
+        make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
+    if (lane == 0) d.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
   }
 }
 
@@ -601,16 +633,27 @@ cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeAr
 
 template <int D, bool BF16>
 static cudaError_t launch_prefix_t(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a, cudaStream_t stream) {
-  auto kern = fa2_prefix_kernel<D, BF16>;
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(kern, PfxCfg<D>::SMEM, done);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(a.ctas), dim3(PfxCfg<D>::THREADS), PfxCfg<D>::SMEM, stream, tk, tv, a);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (a.items > 0) {
+    auto kern = fa2_prefix_kernel<D, BF16>;
+    static std::atomic<unsigned long long> done{0};
+    e = allow_smem(kern, PfxCfg<D>::SMEM, done);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kern, dim3(a.ctas), dim3(PfxCfg<D>::THREADS), PfxCfg<D>::SMEM, stream, tk, tv, a);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_decode_suffix(D, BF16, a.head_tile, a.d, a.tail_ctas, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa2_prefix_join_kernel<D, BF16>, dim3(static_cast<unsigned>(a.d.c.B) * a.d.c.Hkv),
-                          dim3(kPjThreads), 0, stream, a);
+  // Warps per row: four parts each at a time, about (the CTAs that share an item, and own
+  // ones), but no more warps than run at once.
+  const int items = a.items > 0 ? a.items : a.d.row_tiles * a.d.c.Hkv, ctas = a.items > 0 ? a.ctas : a.tail_ctas;
+  const int parts = (ctas + items - 1) / items + 3;
+  const long long rows = static_cast<long long>(a.d.c.B) * a.d.Hq;
+  int per_row = 1;
+  while (per_row < kPjWarps && per_row * 4 * (128 / D) < parts && rows * per_row * 2 <= kPjResident) per_row *= 2;
+  return launch_dependent(fa2_prefix_join_kernel<D, BF16>,
+                          dim3(static_cast<unsigned>((rows * per_row + kPjWarps - 1) / kPjWarps)), dim3(kPjThreads), 0,
+                          stream, a, per_row);
 }
 
 cudaError_t launch_prefix_decode(int d, bool bf16, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a,

@@ -31,9 +31,14 @@ class Shared(Cache):
         self.prefix = first[:max(1, -(-P // ps))].clone()
         self.prefix_len = torch.tensor([P], dtype=torch.int32)
 
-    def args(self, q):
+    def args(self, q, room=False):
+        """room: a list of the prefix's pages with room for 140000 slots; from its length
+        the library decides which kernel attends to the prefix (more than 16 query rows)."""
         kc, vc, table, lens = self.gpu()
-        return [q.cuda(), kc, vc, table, lens, self.prefix.cuda(), self.prefix_len.cuda()]
+        prefix = self.prefix
+        if room:
+            prefix = torch.cat([prefix, torch.full((140000 // self.ps + 1,), -5, dtype=torch.int32)])
+        return [q.cuda(), kc, vc, table, lens, prefix.cuda(), self.prefix_len.cuda()]
 
 
 def _check(c, q, o, lse, scale, visible=None):
@@ -86,13 +91,14 @@ def test_matches_the_oracle(cuda_device, fa2_lib, case, dtype):
     B, Hq, Hkv, d, ps, P, _ = case
     c = Shared(B, Hkv, d, ps, P, _lens(case), dtype, seed=Hq + ps)
     q = c.query(Hq, 1.5)
-    a = c.args(q)
-    o, lse = fa2_lib.prefix_decode(*a)
-    torch.cuda.synchronize()
-    assert fa2_lib.device_status() == 0
-    _check(c, q, o, lse, d ** -0.5)
-    o2, lse2 = fa2_lib.prefix_decode(*a)
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for room in (False, True):
+        a = c.args(q, room)
+        o, lse = fa2_lib.prefix_decode(*a)
+        torch.cuda.synchronize()
+        assert fa2_lib.device_status() == 0
+        _check(c, q, o, lse, d ** -0.5)
+        o2, lse2 = fa2_lib.prefix_decode(*a)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
@@ -100,8 +106,9 @@ def test_matches_the_oracle(cuda_device, fa2_lib, case, dtype):
 def test_sharp_and_flat_rows(cuda_device, fa2_lib, std, scale, dtype):
     c = Shared(20, 2, 128, 16, 900, [900 + 7 * i for i in range(20)], dtype, seed=4)
     q = c.query(8, std)
-    o, lse = fa2_lib.prefix_decode(*c.args(q), scale=scale)
-    _check(c, q, o, lse, scale or 128 ** -0.5)
+    for room in (False, True):
+        o, lse = fa2_lib.prefix_decode(*c.args(q, room), scale=scale)
+        _check(c, q, o, lse, scale or 128 ** -0.5)
 
 
 def test_a_table_with_room_and_a_prefix_list_with_room(cuda_device, fa2_lib):
@@ -117,10 +124,10 @@ def test_a_table_with_room_and_a_prefix_list_with_room(cuda_device, fa2_lib):
 
 def test_outputs_are_the_rounded_exact_values(cuda_device, fa2_lib):
     """Rounded once: nearly every output is the exact value's nearest."""
-    for dtype, most in ((BF16, 0.004), (FP16, 0.02)):
+    for dtype, most, room in ((BF16, 0.004, False), (FP16, 0.02, False), (BF16, 0.004, True), (FP16, 0.02, True)):
         c = Shared(32, 2, 128, 16, 2000, [2000 + 3 * i for i in range(32)], dtype, seed=2)
         q = c.query(8, 2.0)
-        o, _ = fa2_lib.prefix_decode(*c.args(q))
+        o, _ = fa2_lib.prefix_decode(*c.args(q, room))
         ref, _, _ = oc.paged_decode(bits64(q), bits64(c.k), bits64(c.v), c.table.numpy(), c.lens.numpy(), 128 ** -0.5)
         want = torch.from_numpy(ref).to(dtype)
         assert float((o.cpu() != want).float().mean()) <= most
@@ -131,15 +138,15 @@ def test_outputs_are_the_rounded_exact_values(cuda_device, fa2_lib):
 def test_slots_far_below_the_largest_count(cuda_device, fa2_lib):
     """One slot of the largest score has V = 0; what is left of o are the others, 2^-18
     below it (fp16: pieces down to 2^-36 of the row's largest)."""
-    for dtype in (BF16, FP16):
-        c = Shared(3, 1, 64, 16, 4096, [4096, 4096, 4100], dtype, seed=6)
+    for dtype, B in ((BF16, 3), (FP16, 3), (BF16, 40), (FP16, 40)):
+        c = Shared(B, 1, 64, 16, 4096, [4096] * (B - 1) + [4100], dtype, seed=6)
         c.k.zero_()
         page, off = int(c.table[-1, 37]), 5
         c.k[page, 0, off, 0] = 1.0
         c.v[page, 0, off] = 0.0
-        q = torch.zeros(3, 1, 64, dtype=dtype)
+        q = torch.zeros(B, 1, 64, dtype=dtype)
         q[..., 0] = 18.0
-        o, lse = fa2_lib.prefix_decode(*c.args(q), scale=float(np.log(2.0)))
+        o, lse = fa2_lib.prefix_decode(*c.args(q, B > 16), scale=float(np.log(2.0)))
         _check(c, q, o, lse, float(np.float32(np.log(2.0))))
         ref, _, _ = oc.paged_decode(bits64(q), bits64(c.k), bits64(c.v), c.table.numpy(), c.lens.numpy(),
                                     float(np.float32(np.log(2.0))))
@@ -147,18 +154,20 @@ def test_slots_far_below_the_largest_count(cuda_device, fa2_lib):
 
 
 def test_bad_pages_of_the_prefix_are_masked(cuda_device, fa2_lib):
-    for ps, bad in ((16, (1, 3)), (5, (0, 20, 21)), (64, (2,))):
-        c = Shared(4, 2, 64, ps, 250, [250, 300, 13, 260], BF16, seed=8)
+    for ps, bad, B in ((16, (1, 3), 4), (5, (0, 20, 21), 4), (64, (2,), 4), (16, (1, 3), 40), (5, (0, 20, 21), 40),
+                       (64, (2,), 40), (2, (60, 61, 63, 64, 100), 40), (4, (15, 31, 32), 40)):
+        c = Shared(B, 2, 64, ps, 250, [250, 300, 13, 260] * (B // 4), BF16, seed=8)
         q = c.query(4)
-        a = c.args(q)
-        prefix = c.prefix.clone()
+        a = c.args(q, B > 16)
+        prefix = a[5].cpu()
         for i, p in enumerate(bad):
             prefix[p] = -1 if i % 2 else c.k.shape[0]
         a[5] = prefix.cuda()
         o, lse = fa2_lib.prefix_decode(*a)
         torch.cuda.synchronize()
         assert fa2_lib.device_status() == 9
-        cut = 250 // (16 if ps % 16 == 0 else 1) * (16 if ps % 16 == 0 else 1)
+        box = 16 if ps % 16 == 0 else ps if ps in (2, 4) else 1
+        cut = 250 // box * box
         hide = [np.array([not (n >= 250 and j < cut and j // ps in bad) for j in range(n)], bool) for n in c.lens.tolist()]
         _check(c, q, o, lse, 0.125, visible=hide)
 
@@ -189,10 +198,10 @@ def test_lengths_out_of_range(cuda_device, fa2_lib):
 
 def test_a_wait_that_runs_out(cuda_device, fa2_lib):
     """V tiles of the prefix that never arrive: a status, and the next call is right."""
-    for rows, P in ((4, 700), (300, 700)):
+    for rows, P in ((40, 700), (300, 700)):
         c = Shared(rows, 1, 128, 16, P, [P + 3] * rows, BF16, seed=3)
         q = c.query(1)
-        a = c.args(q)
+        a = c.args(q, True)
         assert fa2_lib.load_library().fa2_debug_arm_fault(7, 30) == 0
         fa2_lib.prefix_decode(*a)
         assert fa2_lib.device_status() == 6
@@ -204,21 +213,23 @@ def test_a_wait_that_runs_out(cuda_device, fa2_lib):
 def test_infinite_values(cuda_device, fa2_lib):
     """An infinite V gives outputs that are not finite in its own column, and nothing
     elsewhere; in slots that a sequence does not have it gives nothing."""
-    c = Shared(3, 1, 64, 16, 64, [70, 20, 80], BF16, seed=5)
-    c.v[c.table[-1, 1], 0, 3, 7] = float("inf")
-    q = c.query(2)
-    o, _ = fa2_lib.prefix_decode(*c.args(q))
-    bad = ~torch.isfinite(o.cpu())
-    want = torch.zeros_like(bad)
-    want[0, :, 7] = want[2, :, 7] = True
-    assert torch.equal(bad, want)
+    for rep in (1, 12):
+        c = Shared(3 * rep, 1, 64, 16, 64, [70, 20, 80] * rep, BF16, seed=5)
+        c.v[c.table[-1, 1], 0, 3, 7] = float("inf")
+        q = c.query(2)
+        o, _ = fa2_lib.prefix_decode(*c.args(q, rep > 1))
+        bad = ~torch.isfinite(o.cpu())
+        want = torch.zeros_like(bad)
+        want[0::3, :, 7] = want[2::3, :, 7] = True
+        assert torch.equal(bad, want)
 
 
-def test_graph_follows_lengths_prefix_and_tables(cuda_device, fa2_lib):
-    B, ps = 6, 16
-    c = Shared(B, 2, 128, ps, 400, [420 + 11 * i for i in range(B)], BF16, seed=12, width=40)
+@pytest.mark.parametrize("B", [6, 12])
+def test_graph_follows_lengths_prefix_and_tables(cuda_device, fa2_lib, B):
+    ps = 16
+    c = Shared(B, 2, 128, ps, 400, [420 + 11 * i for i in range(B)], BF16, seed=12, width=45)
     q = c.query(8)
-    a = c.args(q)
+    a = c.args(q, B > 6)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -246,7 +257,7 @@ def test_streams_and_calls_in_a_row(cuda_device, fa2_lib):
     one by one; and on other streams."""
     cs = [Shared(B, 2, 64, 16, P, [P + n for n in range(B)], FP16, seed=B) for B, P in ((2, 3000), (70, 200), (9, 16))]
     qs = [c.query(4) for c in cs]
-    args = [c.args(q) for c, q in zip(cs, qs)]
+    args = [c.args(q, c.B == 70) for c, q in zip(cs, qs)]
     want = []
     for a in args:
         want.append(fa2_lib.prefix_decode(*a))
@@ -276,9 +287,9 @@ def test_streams_and_calls_in_a_row(cuda_device, fa2_lib):
 
 def test_nothing_around_the_outputs_is_written(cuda_device, fa2_lib):
     lib = fa2_lib.load_library()
-    for B, Hq, Hkv, d, P in ((3, 4, 2, 128, 300), (90, 6, 2, 64, 129)):
+    for B, Hq, Hkv, d, P in ((3, 4, 2, 128, 300), (20, 4, 2, 64, 1000), (90, 6, 2, 64, 129)):
         c = Shared(B, Hkv, d, 16, P, [P + 5 * (b % 9) for b in range(B)], BF16, seed=1)
-        a = c.args(c.query(Hq))
+        a = c.args(c.query(Hq), B == 90)
         n = lib.fa2_prefix_decode_workspace_size(B, Hq, Hkv, d, 16, c.table.shape[1])
         guard = 4096
         ws = torch.full((n + 2 * guard,), 0xA5, dtype=torch.uint8, device="cuda")
