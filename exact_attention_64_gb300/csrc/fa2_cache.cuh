@@ -189,7 +189,8 @@ __device__ __forceinline__ PrefixLen prefix_slots(const DecodeArgs& a) {
 struct PrefixArgs {
   DecodeArgs d;           // the slots behind the prefix: its view of the cache and its parts
   int head_tile;          // query heads of an item behind the prefix
-  int tail_ctas;          // CTAs that work on them
+  int tail_ctas;          // CTAs that work on them, as workers or each with four
+  int tail_warps;         // 1: workers are warps
   int items;              // Hkv * ceil(rows / 256), or 0: d.row_tiles
   FastDiv fblocks;        // items per key head
   int ctas;               // of the prefix

@@ -27,6 +27,7 @@ cudaError_t launch_key_weights(int d, bool bf16, bool causal, const CUtensorMap&
 namespace {
 
 constexpr int kDecodeCtas = 304;  // most CTAs of a decode: two on each of 152 SMs
+constexpr int kDecodeWarps = 4;   // workers of a CTA, behind a shared prefix
 constexpr int kPrefixCtas = 152;  // most CTAs of a shared prefix
 constexpr int kKwCtas = 152;      // most CTAs of the key weights
 constexpr long long kMaxRows = (1LL << 31) - 1;
@@ -146,14 +147,19 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
 // Whether the prefix is attended to by the kernel of the own slots, in items of 8 or 16
 // of the rows = B g query rows of a key head. That saves a launch and the other kernel's
 // start, about 6 us, but reads and multiplies the prefix once for each 16 rows. (32/8
-// heads, d = 128, inside and outside: 2000 slots, 64 rows 20.9 and 21.3 us, 96 rows 26.1
-// and 22.4; 512 slots, 128 rows 16.4 and 19.8, 256 rows 25.0 and 24.2; 8192 slots, 32
-// rows 23.1 and 23.2, 48 rows 34.2 and 23.8. Two heads of 16384 slots, d = 64, 64 rows 17.6
-// and 17.8, 128 rows 27.2 and 20.9.)
+// heads, d = 128, inside and outside: 2000 slots, 64 rows 17.3 and 20.8 us, 96 rows 21.5
+// and 22.2, 128 rows 25.2 and 23.8; 512 slots, 256 rows 20.0 and 21.5; 8192 slots, 32 rows
+// 22.5 and 21.3, 48 rows 27.9 and 22.5. Two heads of 16384 slots, d = 64, 48 rows 15.4 and
+// 16.3, 64 rows 17.6 and 16.8, 128 rows 26.1 and 20.0.)
 bool prefix_inside(int B, int Hq, int Hkv, int d, long long prefix_cap) {
   const long long rows = static_cast<long long>(B) * (Hq / Hkv), tiles = (rows + 15) / 16;
-  return tiles == 1 || tiles * Hkv * prefix_cap <= 65536LL * 128 / d;
+  return tiles == 1 || tiles * Hkv * prefix_cap <= 98304LL * 128 / d;
 }
+// Whether the workers of the own slots (and of a prefix inside) are warps: from 96 items
+// on. By CTAs and by warps: 40 items (32/8 heads, 2000 slots and 300 own, d = 128) 12.0 and
+// 15.9 us, 80 items 15.0 and 15.3, 120 items 18.7 and 16.6; 68 items (2 heads, 16384 slots,
+// d = 64) 13.5 and 15.2; 320 items (32 heads, 4096 slots) 32.7 and 25.0.
+bool prefix_by_warps(long long items) { return items >= 96; }
 int prefix_head_tile(int B, int Hq, int Hkv, bool inside) {
   return inside && static_cast<long long>(B) * (Hq / Hkv) > 8 ? 16 : head_tile(Hq / Hkv);
 }
@@ -178,7 +184,7 @@ PrefixSpace prefix_space(int B, int Hq, int Hkv, int d) {
     const size_t ht = prefix_head_tile(B, Hq, Hkv, inside);
     const size_t items = static_cast<size_t>(B) * Hkv * ((g + ht - 1) / ht) +
                          (inside ? Hkv * ((static_cast<size_t>(B) * g + ht - 1) / ht) : 0);
-    own = std::max(own, (items + kDecodeCtas) * ht);
+    own = std::max(own, (items + kDecodeCtas * kDecodeWarps) * ht);
   }
   s.pml = s.po + align_up(rows * d * 4, 256);
   s.so = s.pml + align_up(rows * 8, 256);
@@ -325,19 +331,21 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   c.prefix_len = prefix_len;
   c.rows = B * c.g;
   c.fg = fa2::fast_div(c.g);
-  // At most one CTA per unit of full tables.
-  const int unit = fa2::decode_unit(d);
-  long long units = static_cast<long long>(B) * Hkv * c.HG * ((static_cast<long long>(c.c.L) + unit - 1) / unit);
+  long long items = static_cast<long long>(B) * Hkv * c.HG;
   if (inside) {
     c.row_tiles = (c.rows + a.head_tile - 1) / a.head_tile;
     c.ft = fa2::fast_div(c.row_tiles);
-    units += static_cast<long long>(Hkv) * c.row_tiles * ((static_cast<long long>(c.prefix_cap) + unit - 1) / unit);
+    items += static_cast<long long>(Hkv) * c.row_tiles;
   } else {
     a.items = static_cast<int>(prefix_items(B, Hq, Hkv));
     a.fblocks = fa2::fast_div(a.items / Hkv);
     a.ctas = static_cast<int>(std::min<long long>(a.items * ((static_cast<long long>(c.prefix_cap) + 127) / 128),
                                                   std::min(sms, kPrefixCtas)));
   }
+  a.tail_warps = prefix_by_warps(items);
+  // At most one CTA per unit of full tables.
+  const long long longest = std::max(static_cast<long long>(c.c.L), inside ? static_cast<long long>(c.prefix_cap) : 0LL);
+  const long long units = items * ((longest + fa2::decode_unit(d) - 1) / fa2::decode_unit(d));
   a.tail_ctas = static_cast<int>(std::min<long long>(units, std::min(2 * sms, kDecodeCtas)));
   a.part_o = reinterpret_cast<float*>(ws + s.po);
   a.part_ml = reinterpret_cast<float2*>(ws + s.pml);

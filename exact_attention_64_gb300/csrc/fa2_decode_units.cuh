@@ -10,6 +10,7 @@ namespace fa2 {
 // the same bytes at both head sizes.
 template <int D>
 constexpr int kUnit = decode_unit(D);
+constexpr int kDecWarps = 4;  // of a CTA of the decode
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr float kLog2ef = 1.4426950408889634f;
 
@@ -17,8 +18,13 @@ constexpr float kLog2ef = 1.4426950408889634f;
 // HH = Hkv * HG items per sequence: item hh is head tile hh % HG of key head hh / HG.
 // SHARED: a sequence that reaches the prefix has the slots behind it only; before all
 // sequences may come items of the prefix itself (b = -1, hh their number).
-template <int D>
-__device__ __forceinline__ int tiles_of(int n) { return (n + kUnit<D> - 1) / kUnit<D>; }
+// Its workers are CTAs, or warps with units of a warp's share of the others'.
+enum : int { kNotShared = 0, kSharedCta = 1, kSharedWarp = 2 };
+template <int D, int SHARED = kNotShared>
+__device__ __forceinline__ int tiles_of(int n) {
+  constexpr int U = SHARED == kSharedWarp ? kUnit<D> / kDecWarps : kUnit<D>;
+  return (n + U - 1) / U;
+}
 
 // Quotient of 0 <= a and b > 0; 32 bits when they do, which is nearly always.
 __device__ __forceinline__ long long div_pos(long long a, long long b) {
@@ -37,7 +43,7 @@ __device__ __forceinline__ int prefix_of(int n, const PrefixLen& p) { return n >
 
 // The units of all sequences, by a whole warp: T, and where a unit lies. Up to
 // 32 sequences are read once and their running sums stay with the lanes.
-template <int D, bool SHARED = false>
+template <int D, int SHARED = kNotShared>
 struct UnitMap {
   const CacheView& c;
   int HH, lane;
@@ -54,7 +60,7 @@ struct UnitMap {
   __device__ int length(int b) const {
     if (b >= c.B) return 0;
     const int x = seq_len(c, b);
-    return SHARED ? x - prefix_of(x, P) : x;
+    return SHARED != kNotShared ? x - prefix_of(x, P) : x;
   }
   // out[b]: units before those of sequence b, `base` before all; out[B] = base + T.
   __device__ void write_starts(long long* out, long long base) const {
@@ -62,12 +68,12 @@ struct UnitMap {
     for (int b0 = 0; b0 < c.B; b0 += 32) {
       const int len = b0 == 0 ? n : length(b0 + lane);
       const long long sum = scan(len);
-      if (b0 + lane < c.B) out[b0 + lane] = base + sum - static_cast<long long>(tiles_of<D>(len)) * HH;
+      if (b0 + lane < c.B) out[b0 + lane] = base + sum - static_cast<long long>(tiles_of<D, SHARED>(len)) * HH;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
   __device__ long long scan(int slots) const {
-    long long t = static_cast<long long>(tiles_of<D>(slots)) * HH;
+    long long t = static_cast<long long>(tiles_of<D, SHARED>(slots)) * HH;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, t, o);
@@ -86,8 +92,8 @@ struct UnitMap {
         UnitCursor k;
         k.b = b0 + src;
         k.n = __shfl_sync(0xffffffffu, len, src);
-        k.ntiles = tiles_of<D>(k.n);
-        k.start = SHARED ? prefix_of(seq_len(c, k.b), P) : 0;
+        k.ntiles = tiles_of<D, SHARED>(k.n);
+        k.start = SHARED != kNotShared ? prefix_of(seq_len(c, k.b), P) : 0;
         const long long r = u - (base + __shfl_sync(0xffffffffu, sum, src) - static_cast<long long>(k.ntiles) * HH);
         k.hh = static_cast<int>(div_pos(r, k.ntiles));
         k.tile = static_cast<int>(r - static_cast<long long>(k.hh) * k.ntiles);
@@ -101,11 +107,11 @@ struct UnitMap {
   }
 };
 
-template <int D, bool SHARED = false>
+template <int D, int SHARED = kNotShared>
 __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCursor& k, PrefixLen P = {}, int prefix_items = 0) {
   if (++k.tile < k.ntiles) return;
   k.tile = 0;
-  if (++k.hh < (SHARED && k.b < 0 ? prefix_items : HH)) return;
+  if (++k.hh < (SHARED != kNotShared && k.b < 0 ? prefix_items : HH)) return;
   k.hh = 0;
   do {
     if (++k.b >= c.B) {
@@ -113,12 +119,12 @@ __device__ __forceinline__ void unit_advance(const CacheView& c, int HH, UnitCur
       return;
     }
     k.n = seq_len(c, k.b);
-    if constexpr (SHARED) {
+    if constexpr (SHARED != kNotShared) {
       k.start = prefix_of(k.n, P);
       k.n -= k.start;
     }
   } while (k.n == 0);
-  k.ntiles = tiles_of<D>(k.n);
+  k.ntiles = tiles_of<D, SHARED>(k.n);
 }
 
 // Units [u0, u1) of CTA x of G over T units, and the CTA of unit u. With fewer

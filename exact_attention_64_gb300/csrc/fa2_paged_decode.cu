@@ -41,7 +41,6 @@
 
 namespace fa2 {
 
-constexpr int kDecWarps = 4;
 
 // `pol`: the cache is read once (by a group of up to 16 heads), so its lines leave
 // L2 first; what the join reads again (logits, partial results) stays.
@@ -235,14 +234,18 @@ struct DecCfg {
   static constexpr int HEADS = 8 * NT;                     // query heads of a tile
 };
 
-// SHARED: the slots behind a prefix (fa2_prefix_decode.cu). Every segment is left as a
-// part. The prefix is either this kernel's, in items of their own that come first (8 NT
+// SHARED: the slots behind a prefix (fa2_prefix_decode.cu); every segment is left as a
+// part. Where items are many (kSharedWarp) each warp is a worker of its own, with units of
+// 16 (d = 128) or 32 slots: a CTA that joins its warps at the end of a segment spends 3 us
+// there (256 sequences of 115 slots, 8 heads: 38 us, and 31 by warps); where they are few
+// that is four times the parts to join (rule at the launch). The prefix is either this kernel's, in items of their own that come first (8 NT
 // query rows of a key head, whatever sequences they are of), or that of another kernel
 // of the call, which has waited for what came before the call and lets this one begin
 // early; this one ends after it.
-template <int D, bool BF16, int NT, bool WEIGHTS, bool SHARED = false>
+template <int D, bool BF16, int NT, bool WEIGHTS, int MODE = kNotShared>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
   using C = DecCfg<D, NT>;
+  constexpr bool SHARED = MODE != kNotShared, WARPS = MODE == kSharedWarp;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kDecWarps][8];
   __shared__ uint32_t s_mask[kDecWarps][C::STAGES];
@@ -258,7 +261,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheView& c = a.c;
   const int HH = c.Hkv * a.HG;
-  const int cta = blockIdx.x;
+  const int cta = WARPS ? blockIdx.x * kDecWarps + warp : blockIdx.x;  // worker
+  constexpr int UNIT = WARPS ? C::ROWS : kUnit<D>;
   long long u0 = 0, u1 = 0;
   UnitCursor cc{};
   if (!SHARED && a.whole) {
@@ -277,15 +281,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       return;
     }
   } else {
-    const UnitMap<D, SHARED> map(c, HH, lane, P);
-    const long long PU = SHARED ? static_cast<long long>(PI) * tiles_of<D>(P.cut) : 0;
-    const long long T = PU + map.T, G = min(static_cast<long long>(gridDim.x), T);
-    if (cta == 0 && warp == 0)
+    const UnitMap<D, MODE> map(c, HH, lane, P);
+    const long long PU = SHARED ? static_cast<long long>(PI) * tiles_of<D, MODE>(P.cut) : 0;
+    const long long T = PU + map.T, G = min(static_cast<long long>(gridDim.x) * (WARPS ? kDecWarps : 1), T);
+    if (blockIdx.x == 0 && warp == 0)
       for (int b = lane; b < c.B; b += 32)
         if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
     if constexpr (SHARED) {
-      if (cta == 0 && warp == 1) map.write_starts(a.starts, PU);  // for the join
-      if (cta == 0 && threadIdx.x == 0 && a.row_tiles > 0 && ld_global(a.prefix_len) != P.len) report_page(c.status);
+      if (blockIdx.x == 0 && warp == 1) map.write_starts(a.starts, PU);  // for the join
+      if (blockIdx.x == 0 && threadIdx.x == 0 && a.row_tiles > 0 && ld_global(a.prefix_len) != P.len) report_page(c.status);
     }
     if (cta >= G) {
       if constexpr (SHARED) grid_dependency_wait();
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     if (SHARED && u0 < PU) {
       cc.b = -1;
       cc.n = P.cut;
-      cc.ntiles = tiles_of<D>(P.cut);
+      cc.ntiles = tiles_of<D, MODE>(P.cut);
       cc.hh = static_cast<int>(div_pos(u0, cc.ntiles));
       cc.tile = static_cast<int>(u0 - static_cast<long long>(cc.hh) * cc.ntiles);
       cc.start = 0;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
   int pg = 0, off = 0, hk = 0;
   bool in = false;
   auto look_up = [&]() {
-    const int slot = ic.tile * kUnit<D> + warp * C::ROWS + (lane & (C::ROWS - 1));
+    const int slot = ic.tile * UNIT + (WARPS ? 0 : warp * C::ROWS) + (lane & (C::ROWS - 1));
     in = left > 0 && slot < ic.n;
     hk = key_head(ic);
     if (in) {
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
           cp_async16(dst + C::ROWS * C::ROW, a.v + e, rr >= 0, pol);
         }
       }
-      unit_advance<D, SHARED>(c, HH, ic, P, PI);
+      unit_advance<D, MODE>(c, HH, ic, P, PI);
       --left;
       look_up();
     }
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     }
     cp_async_wait<C::STAGES - 1>();
     __syncwarp();
-    const int slot0 = cc.tile * kUnit<D> + warp * C::ROWS;
+    const int slot0 = cc.tile * UNIT + (WARPS ? 0 : warp * C::ROWS);
     if (slot0 < cc.n) {
       const uint32_t mask = s_mask[warp][st];
       const uint32_t kb = ring + st * C::STAGE, vb = kb + C::ROWS * C::ROW;
@@ -509,10 +513,36 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     st = st + 1 == C::STAGES ? 0 : st + 1;
 
     if (u + 1 == u1 || cc.tile + 1 == cc.ntiles) {
+      if constexpr (WARPS) {
+        // End of a segment: (m, l, O) of its rows, O as 32-byte runs of one row.
+        const size_t row0 = static_cast<size_t>(shared_part((cc.b < 0 ? 0 : PI + cc.b * HH) + cc.hh, cta)) * C::HEADS;
+        const int rows = cc.b < 0 ? a.rows : a.g;
+        UnitCursor next = cc;
+        unit_advance<D, MODE>(c, HH, next, P, PI);
+        if (u + 1 < u1) load_q(next);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float x = l[nt][y];
+#pragma unroll
+            for (int of = 4; of < 32; of <<= 1) x += __shfl_xor_sync(0xffffffffu, x, of);
+            const int hd = nt * 8 + 2 * t + y;
+            if (head0 + hd >= rows) continue;
+            if (r8 == 0) a.part_ml[row0 + hd] = make_float2(m[nt][y], x);
+            float* dst = a.part_o + (row0 + hd) * D + r8;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              dst[dt * 16] = o[nt][dt][y];
+              dst[dt * 16 + 8] = o[nt][dt][2 + y];
+            }
+          }
+        }
+      } else {
       // End of a segment: the four warps' (m, l, O) are merged, while the next
       // one's queries are on their way.
       UnitCursor next = cc;
-      unit_advance<D, SHARED>(c, HH, next, P, PI);
+      unit_advance<D, MODE>(c, HH, next, P, PI);
       if (u + 1 < u1) load_q(next);
       const bool from_start = cc.tile - (u - u0) <= 0;  // the segment begins with its item
       const bool whole = !SHARED && from_start && cc.tile + 1 == cc.ntiles;
@@ -582,8 +612,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
         }
         __syncthreads();
       }
+      }
     }
-    unit_advance<D, SHARED>(c, HH, cc, P, PI);
+    unit_advance<D, MODE>(c, HH, cc, P, PI);
   }
   if constexpr (SHARED) grid_dependency_wait();
   if constexpr (WEIGHTS) {
@@ -960,23 +991,31 @@ static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) 
 }
 
 template <int D, bool BF16, int NT>
-static cudaError_t launch_suffix_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
+static cudaError_t launch_suffix_t(const DecodeArgs& a, bool warps, int ctas, cudaStream_t stream) {
   using C = DecCfg<D, NT>;
-  auto kern = fa2_paged_decode_kernel<D, BF16, NT, false, true>;
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(kern, C::SMEM, done);
+  auto kern = warps ? fa2_paged_decode_kernel<D, BF16, NT, false, kSharedWarp>
+                    : fa2_paged_decode_kernel<D, BF16, NT, false, kSharedCta>;
+  static std::atomic<unsigned long long> done[2];
+  const cudaError_t e = allow_smem(kern, C::SMEM, done[warps]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(ctas), dim3(kDecWarps * 32), C::SMEM, stream, a);
 }
 
-// The slots behind a shared prefix, as parts.
-cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas, cudaStream_t stream) {
-  const bool one = head_tile == 8;
-  if (d == 64)
-    return bf16 ? (one ? launch_suffix_t<64, true, 1>(a, ctas, stream) : launch_suffix_t<64, true, 2>(a, ctas, stream))
-                : (one ? launch_suffix_t<64, false, 1>(a, ctas, stream) : launch_suffix_t<64, false, 2>(a, ctas, stream));
-  return bf16 ? (one ? launch_suffix_t<128, true, 1>(a, ctas, stream) : launch_suffix_t<128, true, 2>(a, ctas, stream))
-              : (one ? launch_suffix_t<128, false, 1>(a, ctas, stream) : launch_suffix_t<128, false, 2>(a, ctas, stream));
+// The slots behind a shared prefix, as parts, by warps or by CTAs.
+cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, bool warps, int ctas,
+                                 cudaStream_t stream) {
+#define FA2_SUFFIX_CASE(DD, BB, NN) \
+  if (d == DD && bf16 == BB && head_tile == 8 * NN) return launch_suffix_t<DD, BB, NN>(a, warps, ctas, stream);
+  FA2_SUFFIX_CASE(64, true, 1)
+  FA2_SUFFIX_CASE(64, true, 2)
+  FA2_SUFFIX_CASE(64, false, 1)
+  FA2_SUFFIX_CASE(64, false, 2)
+  FA2_SUFFIX_CASE(128, true, 1)
+  FA2_SUFFIX_CASE(128, true, 2)
+  FA2_SUFFIX_CASE(128, false, 1)
+  FA2_SUFFIX_CASE(128, false, 2)
+#undef FA2_SUFFIX_CASE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_paged_decode(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas,

@@ -75,12 +75,20 @@ struct PfxSeg {
   bool two;
 };
 
+// CTAs of T units: as few as finish at the same time, so that the own slots' kernel finds
+// room beside them, and fewer parts are to be joined.
+__device__ __forceinline__ long long pfx_ctas(const PrefixArgs& a, long long T) {
+  if (T <= a.ctas) return T;
+  const long long longest = div_pos(T + a.ctas - 1, a.ctas);
+  return div_pos(T + longest - 1, longest);
+}
+
 __device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta) {
   PfxWork w;
   w.P = prefix_slots(a.d).cut;
   w.tiles = (w.P + kTileRows - 1) / kTileRows;
   w.T = static_cast<long long>(a.items) * w.tiles;
-  w.G = min(static_cast<long long>(a.ctas), w.T);
+  w.G = pfx_ctas(a, w.T);
   w.u0 = w.u1 = 0;
   if (cta < w.G) {
     w.u0 = unit_begin(cta, w.G, w.T);
@@ -241,6 +249,25 @@ __device__ __forceinline__ PfxMask pfx_mask(const PrefixArgs& a, int P, int h, i
   return m;
 }
 
+// -inf into the columns of S that do not count.
+__device__ __noinline__ void pfx_hide(uint32_t t_s, const PfxMask& mask, int box) {
+  const int lb = __ffs(box) - 1;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(t_s + 32 * x, s);
+    tmem_wait_ld();
+    reg_fence(s);
+    // Column c's box is c / box; 32 columns' boxes are bits of one word.
+    const uint32_t word = box >= 4 ? mask.w[0] : box == 2 ? mask.w[x / 2] : mask.w[x];
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((word >> (((32 * x + c) >> lb) & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
+    tmem_st_32x32b_x32(t_s + 32 * x, s);
+  }
+  tmem_wait_st();
+}
+
 // The first piece of two values of p. bf16: cut, one permutation; the remainder then has
 // up to 2^-7 of p, and its rounding leaves 2^-15.
 template <bool BF16>
@@ -259,37 +286,24 @@ __device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, 
   if (!mbar_wait_warp(&sh.s_full[t], done & 1, wc)) return false;
   __syncwarp();
   tc_fence_after();
-  // Columns [64 half, 64 half + 64) of S, masked.
-  uint32_t s[64];
-  auto load = [&](int half) {
-    tmem_ld_32x32b_x32(t_s + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-    tmem_ld_32x32b_x32(t_s + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-    tmem_wait_ld();
-    reg_fence(s);
-    if (!mask.all) {
-      const int lb = __ffs(box) - 1;
-      const uint32_t w0 = half ? mask.w[2] : mask.w[0], w1 = half ? mask.w[3] : mask.w[1];
-#pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        // Box (64 half + c) / box; below 32 boxes a half's are bits of the first word.
-        const int i = (64 * half + c) >> lb;
-        const uint32_t word = box >= 4 ? mask.w[0] : box == 2 ? (half ? mask.w[1] : mask.w[0]) : (c < 32 ? w0 : w1);
-        if (!((word >> (i & 31)) & 1u)) s[c] = __float_as_uint(-INFINITY);
-      }
-    }
-  };
+  if (!mask.all) pfx_hide(t_s, mask, box);
+  // Short loops over 32 columns: S is read twice, which costs less than keeping it, and
+  // the kernel's first steps wait for few instructions to arrive.
   float mx = -INFINITY;
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    load(half);
+  for (int x = 0; x < 4; ++x) {
+    uint32_t s[32];
+    tmem_ld_32x32b_x32(t_s + 32 * x, s);
+    tmem_wait_ld();
+    reg_fence(s);
     float m8[8];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) m8[x] = fmaxf(__uint_as_float(s[x]), __uint_as_float(s[8 + x]));
+    for (int c = 0; c < 8; ++c) m8[c] = fmax3(__uint_as_float(s[c]), __uint_as_float(s[8 + c]), __uint_as_float(s[16 + c]));
 #pragma unroll
-    for (int c = 16; c < 64; c += 16)
+    for (int c = 0; c < 8; c += 2) m8[c] = fmax3(m8[c], __uint_as_float(s[24 + c]), m8[c + 1]);
+    mx = fmax3(mx, fmax3(m8[0], m8[2], m8[4]), m8[6]);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) m8[x] = fmax3(m8[x], __uint_as_float(s[c + x]), __uint_as_float(s[c + 8 + x]));
-    mx = fmax3(mx, fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+    for (int c = 1; c < 8; c += 2) mx = fmaxf(mx, __uint_as_float(s[24 + c]));
   }
   const float m_new = fmaxf(m_ref, mx);
   const bool rescale = (m_new - m_ref) * sl2 > kPfxRescale<BF16>;  // also from -inf
@@ -302,23 +316,21 @@ __device__ __forceinline__ bool pfx_step(PfxShared<D>& sh, int t, uint32_t t_s, 
   float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 sl = make_float2(sl2, sl2), ng = make_float2(neg, neg);
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    load(half);
+  for (int x = 0; x < 4; ++x) {
+    uint32_t s[32], pp[32];  // 32 slots: 16 columns of first pieces, 16 of second ones
+    tmem_ld_32x32b_x32(t_s + 32 * x, s);
+    tmem_wait_ld();
+    reg_fence(s);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t pp[32];  // 32 slots: 16 columns of the rounded values, 16 of the remainders
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const int e = 32 * q + 2 * c;
-        const float2 x = f2_fma(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl, ng);
-        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        rs[c & 1] = f2_add(rs[c & 1], p);
-        pp[c] = pfx_high<BF16>(p);
-        const float2 r = f2_sub(p, unpack_x2<BF16>(pp[c]));
-        pp[16 + c] = pack_x2<BF16>(r.x, r.y);
-      }
-      tmem_st_32x32b_x32(t_s + 64 * half + 32 * q, pp);
+    for (int c = 0; c < 16; ++c) {
+      const float2 y = f2_fma(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl, ng);
+      const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+      rs[c & 1] = f2_add(rs[c & 1], p);
+      pp[c] = pfx_high<BF16>(p);
+      const float2 r = f2_sub(p, unpack_x2<BF16>(pp[c]));
+      pp[16 + c] = pack_x2<BF16>(r.x, r.y);
     }
+    tmem_st_32x32b_x32(t_s + 32 * x, pp);
   }
   l = l * alpha + ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y));
   tmem_wait_st();
@@ -556,21 +568,22 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
   // Parts of the prefix, then own ones.
   int np = 0, ns = 0, p_step = 0;
   size_t p0 = 0, o0 = 0;  // their first rows in the workspace
-  const long long G = min(static_cast<long long>(a.tail_ctas), T);
+  const long long G = min(static_cast<long long>(a.tail_ctas) * (a.tail_warps ? kDecWarps : 1), T);  // workers
+  auto own_tiles = [&](int n) { return a.tail_warps ? tiles_of<D, kSharedWarp>(n) : tiles_of<D>(n); };
   const bool inside = d.row_tiles > 0;  // the prefix was attended to by the kernel of the own slots
   const int PI = inside && P.cut > 0 ? d.row_tiles * c.Hkv : 0;
   if (first > 0) {
     const int R = b * d.g + gx;
     p_step = inside ? a.head_tile : 2 * kTileRows;
-    const long long tiles = inside ? tiles_of<D>(P.cut) : (P.cut + kTileRows - 1) / kTileRows;
-    const long long PT = inside ? T : tiles * a.items, PG = inside ? G : min(static_cast<long long>(a.ctas), PT);
+    const long long tiles = inside ? own_tiles(P.cut) : (P.cut + kTileRows - 1) / kTileRows;
+    const long long PT = inside ? T : tiles * a.items, PG = inside ? G : pfx_ctas(a, PT);
     const int item = h * (inside ? d.row_tiles : a.fblocks.d) + R / p_step;
     const int c0 = unit_cta(item * tiles, PG, PT);
     np = unit_cta(item * tiles + tiles - 1, PG, PT) - c0 + 1;
     p0 = static_cast<size_t>(shared_part(item, c0)) * p_step + R % p_step;
   }
   if (own > 0) {
-    const int HH = c.Hkv * d.HG, tiles = tiles_of<D>(own), hh = h * d.HG + gx / a.head_tile;
+    const int HH = c.Hkv * d.HG, tiles = own_tiles(own), hh = h * d.HG + gx / a.head_tile;
     const long long u = start + static_cast<long long>(hh) * tiles;
     const int c0 = unit_cta(u, G, T);
     ns = unit_cta(u + tiles - 1, G, T) - c0 + 1;
@@ -629,7 +642,8 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
   }
 }
 
-cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, bool warps, int ctas,
+                                 cudaStream_t stream);
 
 template <int D, bool BF16>
 static cudaError_t launch_prefix_t(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixArgs& a, cudaStream_t stream) {
@@ -642,11 +656,11 @@ static cudaError_t launch_prefix_t(const CUtensorMap& tk, const CUtensorMap& tv,
     e = launch_dependent(kern, dim3(a.ctas), dim3(PfxCfg<D>::THREADS), PfxCfg<D>::SMEM, stream, tk, tv, a);
     if (e != cudaSuccess) return e;
   }
-  e = launch_decode_suffix(D, BF16, a.head_tile, a.d, a.tail_ctas, stream);
+  e = launch_decode_suffix(D, BF16, a.head_tile, a.d, a.tail_warps != 0, a.tail_ctas, stream);
   if (e != cudaSuccess) return e;
   // Warps per row: four parts each at a time, about (the CTAs that share an item, and own
   // ones), but no more warps than run at once.
-  const int items = a.items > 0 ? a.items : a.d.row_tiles * a.d.c.Hkv, ctas = a.items > 0 ? a.ctas : a.tail_ctas;
+  const int items = a.items > 0 ? a.items : a.d.row_tiles * a.d.c.Hkv, ctas = a.items > 0 ? a.ctas : a.tail_ctas * (a.tail_warps ? kDecWarps : 1);
   const int parts = (ctas + items - 1) / items + 3;
   const long long rows = static_cast<long long>(a.d.c.B) * a.d.Hq;
   int per_row = 1;
