@@ -6,21 +6,24 @@
 // grow take pages from the list's end, in their order, while they last.
 //
 // What bounds it: latency. A step of a served batch changes a few pages, and is the
-// read of the lengths, a scan, and two dependent reads per page. One CTA does that;
-// when many pages change, the eight CTAs of a cluster share them.
+// read of the lengths, a scan, and two dependent reads per page. One CTA does that. When
+// many pages change it is the scattered accesses to counts and owners, five for each
+// page given back, one sector each at about one a clock and SM: the CTAs of a cluster,
+// 16 where the GPU allows it, share them.
 //
 // The result does not depend on timing. Releases and takes are numbered by (sequence,
 // page of the sequence) through prefix sums of their counts; counts fall by atomic
 // integer adds; of several releases that name a page the last in that order stands
 // for it (a maximum), and the list receives the pages in reverse order, the first
 // release at its end, so that a resize that is undone leaves the list as it was.
+#include <atomic>
+
 #include "fa2_cache.cuh"
 
 namespace fa2 {
 
 constexpr int kRszThreads = 1024;
 constexpr int kRszWarps = kRszThreads / 32;
-constexpr int kRszCluster = 8;
 constexpr int kRszGroups = 4096;    // prefix sums kept in shared memory
 constexpr int kRszAlone = 4096;     // releases and takes that one CTA makes by itself
 
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(kRszThreads, 1) fa2_cache_resize_kernel(const 
   grid_dependency_wait();
   grid_launch_dependents();
 
+  const int listed = ld_global(a.num_free), nf = cut_len(listed, a.num_pages);
   // Prefix sums of the counts, by every CTA for itself.
   const int groups = (a.B + a.group - 1) / a.group, per = (groups + kRszThreads - 1) / kRszThreads;
   int2 mine = make_int2(0, 0);
@@ -142,8 +146,7 @@ __global__ void __launch_bounds__(kRszThreads, 1) fa2_cache_resize_kernel(const 
     if (rank > 0) return;
     C = 1;
   }
-  const int nf = cut_len(ld_global(a.num_free), a.num_pages);
-  if (rank == 0 && tid == 0 && nf != ld_global(a.num_free)) report_page(a.status);
+  if (rank == 0 && tid == 0 && nf != listed) report_page(a.status);
 
   int freed = 0;
   if (R > 0) {
@@ -151,36 +154,82 @@ __global__ void __launch_bounds__(kRszThreads, 1) fa2_cache_resize_kernel(const 
     const int warps = C * kRszWarps, run = ((R + warps - 1) / warps + 31) / 32 * 32;
     const long long w0 = static_cast<long long>(rank * kRszWarps + warp) * run;
     const int i0 = static_cast<int>(min(w0, static_cast<long long>(R))), i1 = min(R - i0, run) + i0;
-    for (int i = i0 + lane; i < i1; i += 32) {
-      RszPages pg;
-      int off;
-      const int b = rsz_find<false>(a, sh, groups, i, &pg, &off);
-      int page = ld_global(a.table + static_cast<size_t>(b) * a.max_pages + pg.new_p + off);
-      if (static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages)) {
-        atomicSub(a.refs + page, 1);
-        a.owner[page] = i;  // any one of its releases
-      } else {
-        report_page(a.status);
-        page = -1;
+    constexpr int U = 4;  // releases of a lane whose reads are in flight together
+    int first[U];         // pages of this lane's first U releases, -1: none
+#pragma unroll
+    for (int u = 0; u < U; ++u) first[u] = -1;
+    for (int ib = i0 + lane; ib < i1; ib += 32 * U) {
+      int page[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = ib + 32 * u;
+        page[u] = -1;
+        if (i >= i1) continue;
+        RszPages pg;
+        int off;
+        const int b = rsz_find<false>(a, sh, groups, i, &pg, &off);
+        page[u] = ld_global(a.table + static_cast<size_t>(b) * a.max_pages + pg.new_p + off);
       }
-      a.gone[i] = page;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = ib + 32 * u;
+        if (i >= i1) continue;
+        if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(a.num_pages)) {
+          atomicSub(a.refs + page[u], 1);
+          a.owner[page[u]] = i;  // any one of its releases
+        } else {
+          report_page(a.status);
+          page[u] = -1;
+        }
+        a.gone[i] = page[u];
+        if (ib == i0 + lane) first[u] = page[u];
+      }
     }
-    rsz_sync(C);
-    // The last release of a page that nobody names any more stands for it.
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const int page = a.gone[i];
-      if (page < 0) continue;
-      const int refs = __ldcg(a.refs + page);
-      if (refs < 0) report_page(a.status);  // given back more often than it was named
-      if (refs == 0 && __ldcg(a.owner + page) < i) atomicMax(a.owner + page, i);
-    }
-    rsz_sync(C);
-    auto frees = [&](int i) {
-      const int page = i < i1 ? a.gone[i] : -1;
-      return page >= 0 && __ldcg(a.refs + page) == 0 && __ldcg(a.owner + page) == i;
+    auto page_of = [&](int i, int k) {
+      int p = -1;
+      if (k >= U) return a.gone[i];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k == u) p = first[u];
+      return p;
     };
+    rsz_sync(C);
+    // The last release of a page that nobody names any more stands for it. Where the
+    // owner is another one, a maximum decides; one CTA knows when there is none.
+    uint32_t mine = 0u;  // of this lane's first 32 releases, those that free a page
+    bool clash = false;
+    for (int ib = i0 + lane, kb = 0; ib < i1; ib += 32 * U, kb += U) {
+      int page[U], refs[U], owner[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) page[u] = ib + 32 * u < i1 ? (kb == 0 ? first[u] : a.gone[ib + 32 * u]) : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        refs[u] = page[u] >= 0 ? __ldcg(a.refs + page[u]) : 1;
+        owner[u] = page[u] >= 0 ? __ldcg(a.owner + page[u]) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = ib + 32 * u;
+        if (refs[u] < 0) report_page(a.status);  // given back more often than it was named
+        if (refs[u] != 0) continue;
+        if (kb < 32) mine |= 1u << (kb + u);
+        if (owner[u] != i) clash = true;
+        if (owner[u] < i) atomicMax(a.owner + page[u], i);
+      }
+    }
+    auto owns = [&](int i, int k) { return __ldcg(a.owner + page_of(i, k)) == i; };
+    auto frees = [&](int i, int k) {
+      if (i >= i1) return false;
+      if (k < 32) return (mine >> k & 1u) != 0u;
+      return a.gone[i] >= 0 && __ldcg(a.refs + a.gone[i]) == 0 && owns(i, k);
+    };
+    if (C > 1 || __syncthreads_or(clash)) {
+      rsz_sync(C);
+      for (int i = i0 + lane, k = 0; i < i1 && k < 32; i += 32, ++k)
+        if ((mine >> k & 1u) && !owns(i, k)) mine &= ~(1u << k);
+    }
     int cnt = 0;
-    for (int i = i0; i < i1; i += 32) cnt += __popc(__ballot_sync(0xffffffffu, frees(i + lane)));
+    for (int i = i0, k = 0; i < i1; i += 32, ++k) cnt += __popc(__ballot_sync(0xffffffffu, frees(i + lane, k)));
     if (lane == 0) sh.count[warp] = cnt;
     __syncthreads();
     int at = 0, sum = 0;
@@ -188,19 +237,21 @@ __global__ void __launch_bounds__(kRszThreads, 1) fa2_cache_resize_kernel(const 
       if (w < warp) at += sh.count[w];
       sum += sh.count[w];
     }
-    if (tid == 0) sh.freed = static_cast<uint32_t>(sum);
-    rsz_sync(C);
+    if (C > 1) {
+      if (tid == 0) sh.freed = static_cast<uint32_t>(sum);
+      rsz_sync(C);
+    }
     for (int r = 0; r < C; ++r) {
       const int x = C > 1 ? static_cast<int>(rsz_remote(&sh.freed, r)) : sum;
       if (r < rank) at += x;
       freed += x;
     }
-    for (int i = i0; i < i1; i += 32) {
-      const bool f = frees(i + lane);
+    for (int i = i0, k = 0; i < i1; i += 32, ++k) {
+      const bool f = frees(i + lane, k);
       const unsigned m = __ballot_sync(0xffffffffu, f);
       const long long pos = static_cast<long long>(nf) + freed - 1 - at - __popc(m & ((1u << lane) - 1u));
       if (f) {
-        if (pos < a.num_pages) a.free_pages[pos] = a.gone[i + lane];
+        if (pos < a.num_pages) a.free_pages[pos] = page_of(i + lane, k);
         else report_page(a.status);
       }
       at += __popc(m);
@@ -250,22 +301,47 @@ __global__ void __launch_bounds__(kRszThreads, 1) fa2_cache_resize_kernel(const 
   if (rank == 0 && tid == 0) *a.num_free = have - taken;
 }
 
+// CTAs of a cluster on the current device: 16 if it can run such a cluster, else 8, which
+// every GPU can.
+static cudaError_t rsz_cluster(cudaLaunchConfig_t& cfg, int* out) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>& k = known[dev & 63];
+  if (k.load(std::memory_order_acquire) == 0) {
+    int n = 8, clusters = 0;
+    if (cudaFuncSetAttribute(fa2_cache_resize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+      cfg.gridDim = dim3(16);
+      cfg.attrs[1].val.clusterDim.x = 16;
+      if (cudaOccupancyMaxActiveClusters(&clusters, fa2_cache_resize_kernel, &cfg) == cudaSuccess && clusters > 0) n = 16;
+    }
+    (void)cudaGetLastError();
+    k.store(n, std::memory_order_release);
+  }
+  *out = k.load(std::memory_order_acquire);
+  return cudaSuccess;
+}
+
 cudaError_t launch_cache_resize(const ResizeArgs& a, cudaStream_t stream) {
-  // A table that cannot change more pages than one CTA handles has no need of eight.
-  int C = static_cast<long long>(a.B) * a.max_pages <= kRszAlone ? 1 : kRszCluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(kRszThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = C;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+  // A table that cannot change more pages than one CTA handles needs no more.
+  int C = 1;
+  if (static_cast<long long>(a.B) * a.max_pages > kRszAlone) {
+    const cudaError_t e = rsz_cluster(cfg, &C);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(C);
+  at[1].val.clusterDim.x = C;
   return cudaLaunchKernelEx(&cfg, fa2_cache_resize_kernel, a, C);
 }
 
