@@ -12,7 +12,10 @@
 // What bounds it: every element is read and written once, so HBM. A lane has 16
 // elements of a row, two runs of 8 that hold both ends of its 8 pairs, so that no
 // element changes lanes; 8 (d = 128) or 4 (d = 64) lanes have a row, and keep its
-// token's sines for a run of heads, several of which are in flight at once.
+// token's sines for a run of heads, four of which are in flight at once. 1.07 GB (B = 4, 32
+// and 32 heads, N = 8192, d = 128) take 157 us, 6.84 TB/s, and with a norm 167; one token
+// of 40 heads 3.5. (Two heads in flight and three CTAs per SM 159 and 174; scalar instead
+// of paired fp32 instructions 162 and 184.)
 // Inputs and outputs may have any strides: a projection's token-major rows become
 // the head-major ones of attention without a pass of their own.
 //
@@ -24,7 +27,6 @@
 namespace fa2 {
 
 constexpr int kRotUnroll = 4;     // heads in flight per lane
-constexpr int kRotBwdUnroll = 2;
 
 template <int D>
 struct RotCfg {
@@ -32,53 +34,56 @@ struct RotCfg {
   static constexpr int GROUPS = kRotThreads / LANES;      // rows in work per CTA
 };
 
-// A lane's 16 elements of a row, and where they lie in it.
+// A lane's 16 elements of a row: two runs of 8, one from each half of the turned part
+// (or of the rest), so that neighbouring lanes' runs fill whole sectors. A run holds
+// the first or the second elements of 8 pairs, or 4 pairs if they are interleaved.
 struct RotLane {
-  int e0, e1;   // first elements of its two runs
-  int pair;     // its first pair
-  bool turned;  // its elements are pairs to turn
+  int e0, e1;  // first elements of its two runs
+  int p0, p1;  // pairs of its turns 0 .. 3 and 4 .. 7
+  bool turned;
 };
-__device__ __forceinline__ RotLane rot_lane(int l, int r, int interleaved) {
+__device__ __forceinline__ RotLane rot_lane(int l, int d, int r, int interleaved) {
   RotLane x;
   x.turned = 16 * l < r;
-  x.pair = 8 * l;
-  const bool halves = x.turned && !interleaved;
-  x.e0 = halves ? 8 * l : 16 * l;
-  x.e1 = halves ? r / 2 + 8 * l : 16 * l + 8;
+  x.e0 = x.turned ? 8 * l : r + 8 * (l - r / 16);
+  x.e1 = x.e0 + (x.turned ? r : d - r) / 2;
+  x.p0 = interleaved ? 4 * l : 8 * l;
+  x.p1 = interleaved ? r / 4 + 4 * l : 8 * l + 4;
   return x;
 }
 
+// A lane's 16 elements as 8 neighbouring pairs: fp32 pairs take one instruction where
+// two numbers take two.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack16(const uint4 (&v)[2], float2 (&x)[8]) {
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_x2<BF16>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+  for (int i = 0; i < 8; ++i) x[i] = unpack_x2<BF16>(w[i]);
 }
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_x2<BF16>(x[0], x[1]), pack_x2<BF16>(x[2], x[3]), pack_x2<BF16>(x[4], x[5]),
-                    pack_x2<BF16>(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2* x) {
+  return make_uint4(pack_x2<BF16>(x[0].x, x[0].y), pack_x2<BF16>(x[1].x, x[1].y), pack_x2<BF16>(x[2].x, x[2].y),
+                    pack_x2<BF16>(x[3].x, x[3].y));
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Weights of a lane's elements.
 template <bool BF16>
-__device__ __forceinline__ void load_weight(const void* w, int fp32, const RotLane& ln, float (&out)[16]) {
+__device__ __forceinline__ void load_weight(const void* w, int fp32, const RotLane& ln, float2 (&out)[8]) {
+  if (fp32) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int e = h ? ln.e1 : ln.e0;
-    if (fp32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + e);
+    for (int h = 0; h < 2; ++h) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + (h ? ln.e1 : ln.e0));
       const float4 a = ld_global(p), b = ld_global(p + 1);
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) out[8 * h + i] = v[i];
-    } else {
-      unpack8<BF16>(ld_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + e)), out + 8 * h);
+      out[4 * h] = make_float2(a.x, a.y);
+      out[4 * h + 1] = make_float2(a.z, a.w);
+      out[4 * h + 2] = make_float2(b.x, b.y);
+      out[4 * h + 3] = make_float2(b.z, b.w);
     }
+  } else {
+    const uint4* p = static_cast<const uint4*>(w);
+    const uint4 v[2] = {ld_global(p + ln.e0 / 8), ld_global(p + ln.e1 / 8)};
+    unpack16<BF16>(v, out);
   }
 }
 
@@ -93,35 +98,43 @@ __device__ __forceinline__ void rot_turns(const RotaryArgs& a, unsigned long lon
 
 // A cos t and A sin t of a lane's pairs at a position.
 struct RotTurn {
-  float c[8], s[8];
+  float2 c[4], s[4];
   __device__ __forceinline__ void set(const unsigned long long* s_turn, const RotLane& ln, int pos, float amp,
                                       float sign) {
+    float cv[8], sv[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const unsigned long long f = ln.turned ? s_turn[ln.pair + i] : 0ull;
+      const unsigned long long f = ln.turned ? s_turn[i < 4 ? ln.p0 + i : ln.p1 + i - 4] : 0ull;
       // High word of position * f modulo 2^64: the angle in 2^-32 turns.
       const uint32_t lo = static_cast<uint32_t>(f), hi = static_cast<uint32_t>(f >> 32), p = static_cast<uint32_t>(pos);
       const uint32_t w = __umulhi(p, lo) + p * hi - (pos < 0 ? lo : 0u);
       float sn, cs;
       sincospif(static_cast<float>(static_cast<int>(w)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
-      c[i] = cs * amp;
-      s[i] = sn * amp * sign;
+      cv[i] = cs * amp;
+      sv[i] = sn * amp * sign;
     }
-  }
-  __device__ __forceinline__ void turn(float (&x)[16], int interleaved) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float& a = interleaved ? x[2 * i] : x[i];
-      float& b = interleaved ? x[2 * i + 1] : x[8 + i];
-      const float u = a * c[i] - b * s[i], v = b * c[i] + a * s[i];
-      a = u;
-      b = v;
+    for (int i = 0; i < 4; ++i) {
+      c[i] = make_float2(cv[2 * i], cv[2 * i + 1]);
+      s[i] = make_float2(sv[2 * i], sv[2 * i + 1]);
     }
   }
-  __device__ __forceinline__ void apply(float (&x)[16], const RotLane& ln, int interleaved) const {
+  __device__ __forceinline__ void apply(float2 (&x)[8], const RotLane& ln, int interleaved) const {
     if (!ln.turned) return;
-    if (interleaved) turn(x, 1);
-    else turn(x, 0);
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float cv = i & 1 ? c[i / 2].y : c[i / 2].x, sv = i & 1 ? s[i / 2].y : s[i / 2].x;
+        x[i] = make_float2(x[i].x * cv - x[i].y * sv, x[i].y * cv + x[i].x * sv);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = x[i], b = x[4 + i];
+        x[i] = f2_sub(f2_mul(a, c[i]), f2_mul(b, s[i]));
+        x[4 + i] = f2_fma(b, c[i], f2_mul(a, s[i]));
+      }
+    }
   }
 };
 
@@ -139,6 +152,16 @@ __device__ __forceinline__ int rot_position(const RotaryArgs& a, int t, int b, i
   return ld_global(a.positions + t);
 }
 
+// Sum of the squares of a row, by its lanes.
+template <int D>
+__device__ __forceinline__ float row_squares(const float2 (&x)[8]) {
+  float2 ss = f2_mul(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) ss = f2_fma(x[i], x[i], ss);
+  return row_sum<D>(ss.x + ss.y);
+}
+
+// Row of head h of a token.
 __device__ __forceinline__ uint4* row_at(const RowView& v, int b, int h, int n) {
   return reinterpret_cast<uint4*>(v.p + b * v.sb + h * v.sh + n * v.sn);
 }
@@ -148,13 +171,13 @@ __device__ __forceinline__ uint4* row_at(const RowView& v, int b, int h, int n) 
 // one head are neighbours. Every lane makes the same number of steps, because the
 // norm's sums cross lanes.
 template <int D, bool BF16, bool NORM>
-__global__ void __launch_bounds__(kRotThreads) fa2_rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_kernel(const RotaryArgs a) {
   using C = RotCfg<D>;
   constexpr int U = kRotUnroll;
   __shared__ unsigned long long s_turn[D / 2];
   grid_dependency_wait();
   rot_turns(a, s_turn);
-  const RotLane ln = rot_lane(threadIdx.x % C::LANES, a.r, a.interleaved);
+  const RotLane ln = rot_lane(threadIdx.x % C::LANES, D, a.r, a.interleaved);
   const long long item = static_cast<long long>(blockIdx.x) * C::GROUPS + threadIdx.x / C::LANES;
   const bool on = item < a.tokens * a.chunks;
   const int it = on ? static_cast<int>(item) : 0;
@@ -163,42 +186,39 @@ __global__ void __launch_bounds__(kRotThreads) fa2_rotary_kernel(const RotaryArg
   const RotarySide& s = is_q ? a.q : a.k;
   const int h0 = (is_q ? ck : ck - a.chunks_q) * a.chunk, h1 = on ? s.H : 0;
   const int pos = rot_position(a, t, b, n);
-  float w[16];
+  float2 w[8];
   if constexpr (NORM) load_weight<BF16>(s.weight, a.weight_fp32, ln, w);
   __syncthreads();
   RotTurn tn;
   tn.set(s_turn, ln, pos, a.amplitude, a.sign);
+  const uint4* src = row_at(s.x, b, h0, n);
+  uint4* dst = row_at(s.y, b, h0, n);
+  const long long x_step = s.x.sh / 8, y_step = s.y.sh / 8;
 #pragma unroll 1
-  for (int i = 0; i < a.chunk; i += U) {
+  for (int i = 0; i < a.chunk; i += U, src += U * x_step, dst += U * y_step) {
     uint4 v[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
       if (h0 + i + u < h1) {
-        const uint4* p = row_at(s.x, b, h0 + i + u, n);
-        v[u][0] = ld_global(p + ln.e0 / 8);
-        v[u][1] = ld_global(p + ln.e1 / 8);
+        v[u][0] = ld_global(src + u * x_step + ln.e0 / 8);
+        v[u][1] = ld_global(src + u * x_step + ln.e1 / 8);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float x[16];
-      unpack8<BF16>(v[u][0], x);
-      unpack8<BF16>(v[u][1], x + 8);
+      float2 x[8];
+      unpack16<BF16>(v[u], x);
       if constexpr (NORM) {
-        float ss = 0.f;
+        const float2 inv = both(rsqrtf(row_squares<D>(x) * (1.f / D) + a.eps));
 #pragma unroll
-        for (int j = 0; j < 16; ++j) ss += x[j] * x[j];
-        const float inv = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = x[j] * inv * w[j];
+        for (int j = 0; j < 8; ++j) x[j] = f2_mul(f2_mul(x[j], inv), w[j]);
       }
       tn.apply(x, ln, a.interleaved);
       if (h0 + i + u < h1) {
-        uint4* p = row_at(s.y, b, h0 + i + u, n);
         const bool same = !NORM && !ln.turned;  // passed through, a NaN's bits too
-        p[ln.e0 / 8] = same ? v[u][0] : pack8<BF16>(x);
-        p[ln.e1 / 8] = same ? v[u][1] : pack8<BF16>(x + 8);
+        dst[u * y_step + ln.e0 / 8] = same ? v[u][0] : pack8<BF16>(x);
+        dst[u * y_step + ln.e1 / 8] = same ? v[u][1] : pack8<BF16>(x + 4);
       }
     }
   }
@@ -207,87 +227,117 @@ __global__ void __launch_bounds__(kRotThreads) fa2_rotary_kernel(const RotaryArg
 // Backward with a norm. A CTA's items are all queries or all keys of the same run of
 // heads (blockIdx.y), so that a lane's 16 sums of the weights' gradients stay in
 // registers; at its end the CTA adds up its rows' sums in a fixed order and leaves
-// them in the workspace. (Integer order of adds everywhere: the bits repeat.)
+// them in the workspace, so that the bits repeat. 252 MB (B = 8, 16/4 heads, N = 2048,
+// d = 128) take 51 us with the sum of the CTAs' parts, 4.9 TB/s: 127 registers leave 16
+// warps per SM to hide what the next head's reads do not. (Two heads at a time, read
+// together, without reading ahead: 58; three CTAs per SM spill, 86.)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(const RotaryArgs a) {
   using C = RotCfg<D>;
-  constexpr int U = kRotBwdUnroll, WARPS = kRotThreads / 32;
+  constexpr int WARPS = kRotThreads / 32;
   __shared__ unsigned long long s_turn[D / 2];
-  __shared__ float s_dw[WARPS][D];
+  __shared__ __align__(8) float s_dw[WARPS][D];
   grid_dependency_wait();
   grid_launch_dependents();
   rot_turns(a, s_turn);
   __syncthreads();
-  const RotLane ln = rot_lane(threadIdx.x % C::LANES, a.r, a.interleaved);
+  const RotLane ln = rot_lane(threadIdx.x % C::LANES, D, a.r, a.interleaved);
   const int ck = blockIdx.y;
   const bool is_q = ck < a.chunks_q;
   const RotarySide& s = is_q ? a.q : a.k;
   const int h0 = (is_q ? ck : ck - a.chunks_q) * a.chunk;
   const int steps = min(a.chunk, s.H - h0);
-  float w[16], dw[16];
+  float2 w[8], dw[8];
   load_weight<BF16>(s.weight, a.weight_fp32, ln, w);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) dw[j] = 0.f;
-  for (long long t0 = static_cast<long long>(blockIdx.x) * C::GROUPS; t0 < a.tokens;
-       t0 += static_cast<long long>(gridDim.x) * C::GROUPS) {
-    const long long tt = t0 + threadIdx.x / C::LANES;
+  for (int j = 0; j < 8; ++j) dw[j] = make_float2(0.f, 0.f);
+  const long long x_step = s.src.sh / 8, g_step = s.x.sh / 8, y_step = s.y.sh / 8;
+  const long long stride = static_cast<long long>(gridDim.x) * C::GROUPS;
+  // The rows of one head are read while those of the one before are worked on, from one
+  // token to the next, too.
+  long long tt = static_cast<long long>(blockIdx.x) * C::GROUPS + threadIdx.x / C::LANES;
+  long long block = static_cast<long long>(blockIdx.x) * C::GROUPS;  // the CTA's first token
+  const uint4 *xs = nullptr, *gs = nullptr;
+  uint4* dst = nullptr;
+  RotTurn tn;
+  uint4 v[2], g[2];
+  auto token = [&](int* b, int* n) {
+    const int t = tt < a.tokens ? static_cast<int>(tt) : 0;
+    *b = div_by(t, a.fN);
+    *n = t - *b * a.N;
+    return t;
+  };
+  auto read = [&]() {
+    v[0] = v[1] = g[0] = g[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (tt < a.tokens) {
+      v[0] = ld_global(xs + ln.e0 / 8);
+      v[1] = ld_global(xs + ln.e1 / 8);
+      g[0] = ld_global(gs + ln.e0 / 8);
+      g[1] = ld_global(gs + ln.e1 / 8);
+    }
+  };
+  auto seek = [&]() {  // to the first head of token tt
+    int b, n;
+    (void)token(&b, &n);
+    xs = row_at(s.src, b, h0, n);
+    gs = row_at(s.x, b, h0, n);
+  };
+  if (block < a.tokens) {
+    seek();
+    read();
+  }
+  while (block < a.tokens) {
     const bool on = tt < a.tokens;
-    const int t = on ? static_cast<int>(tt) : 0, b = div_by(t, a.fN), n = t - b * a.N;
-    RotTurn tn;
+    int b, n;
+    const int t = token(&b, &n);
+    dst = row_at(s.y, b, h0, n);
     tn.set(s_turn, ln, rot_position(a, t, b, n), a.amplitude, -1.f);
 #pragma unroll 1
-    for (int i = 0; i < steps; i += U) {
-      uint4 v[U][2], g[U][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v[u][0] = v[u][1] = g[u][0] = g[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && i + u < steps) {
-          const uint4* p = row_at(s.src, b, h0 + i + u, n);
-          v[u][0] = ld_global(p + ln.e0 / 8);
-          v[u][1] = ld_global(p + ln.e1 / 8);
-          p = row_at(s.x, b, h0 + i + u, n);
-          g[u][0] = ld_global(p + ln.e0 / 8);
-          g[u][1] = ld_global(p + ln.e1 / 8);
+    for (int i = 0; i < steps; ++i, dst += y_step) {
+      float2 x[8], y[8];
+      unpack16<BF16>(v, x);
+      unpack16<BF16>(g, y);
+      if (i + 1 < steps) {
+        xs += x_step;
+        gs += g_step;
+        read();
+      } else {
+        tt += stride;
+        block += stride;
+        if (block < a.tokens) {
+          seek();
+          read();
         }
       }
+      tn.apply(y, ln, a.interleaved);
+      const float inv = rsqrtf(row_squares<D>(x) * (1.f / D) + a.eps);
+      // z = g n: dw += z x, dx = z w - x n^2 mean(z w x).
+      float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i + u >= steps) break;
-        float x[16], y[16];
-        unpack8<BF16>(v[u][0], x);
-        unpack8<BF16>(v[u][1], x + 8);
-        unpack8<BF16>(g[u][0], y);
-        unpack8<BF16>(g[u][1], y + 8);
-        tn.apply(y, ln, a.interleaved);
-        float ss = 0.f;
+      for (int j = 0; j < 8; ++j) {
+        y[j] = f2_mul(y[j], both(inv));
+        if (on) dw[j] = f2_fma(y[j], x[j], dw[j]);
+        y[j] = f2_mul(y[j], w[j]);
+        dot = f2_fma(y[j], x[j], dot);
+      }
+      const float c = row_sum<D>(dot.x + dot.y) * (-1.f / D) * inv * inv;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) ss += x[j] * x[j];
-        const float inv = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          x[j] *= inv;
-          if (on) dw[j] += y[j] * x[j];
-          y[j] *= w[j];
-          dot += y[j] * x[j];
-        }
-        dot = row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = (y[j] - x[j] * dot) * inv;
-        if (on) {
-          uint4* p = row_at(s.y, b, h0 + i + u, n);
-          p[ln.e0 / 8] = pack8<BF16>(y);
-          p[ln.e1 / 8] = pack8<BF16>(y + 8);
-        }
+      for (int j = 0; j < 8; ++j) y[j] = f2_fma(x[j], both(c), y[j]);
+      if (on) {
+        dst[ln.e0 / 8] = pack8<BF16>(y);
+        dst[ln.e1 / 8] = pack8<BF16>(y + 4);
       }
     }
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
 #pragma unroll
-    for (int o = C::LANES; o < 32; o <<= 1) dw[j] += __shfl_xor_sync(0xffffffffu, dw[j], o);
-    if (lane < C::LANES) s_dw[warp][(j < 8 ? ln.e0 : ln.e1 - 8) + j] = dw[j];
+    for (int o = C::LANES; o < 32; o <<= 1) {
+      dw[j].x += __shfl_xor_sync(0xffffffffu, dw[j].x, o);
+      dw[j].y += __shfl_xor_sync(0xffffffffu, dw[j].y, o);
+    }
+    if (lane < C::LANES) *reinterpret_cast<float2*>(&s_dw[warp][(j < 4 ? ln.e0 : ln.e1 - 8) + 2 * j]) = dw[j];
   }
   __syncthreads();
   if (threadIdx.x < D) {

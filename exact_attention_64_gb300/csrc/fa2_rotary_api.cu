@@ -143,7 +143,7 @@ int chunks_of(int H, int chunk) { return (H + chunk - 1) / chunk; }
 int turn_chunk(long long tokens, int H, int d) {
   const int groups = fa2::kRotThreads / (d / 16);
   for (int c = 16; c > 4; c /= 2)
-    if (tokens * chunks_of(H, c) >= 1216LL * groups) return c;
+    if (tokens * chunks_of(H, c) >= 608LL * groups) return c;
   return 4;
 }
 
