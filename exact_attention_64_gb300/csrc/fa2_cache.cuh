@@ -101,15 +101,18 @@ __device__ __forceinline__ void grid_dependency_wait() {
 }
 
 // Raises a kernel's shared-memory limit on the current device, once per device
-// (`done`: a mask of devices, one per kernel).
+// (`done`: a mask of devices, one per kernel). beside: all of an SM's memory becomes
+// shared memory, so that another kernel's CTA may come beside this one's.
 template <class K>
-inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done, bool beside = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && beside)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

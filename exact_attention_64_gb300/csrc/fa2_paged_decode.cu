@@ -221,16 +221,17 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, size_t base, in
   else add_weights<THREADS, 1>(a, base, j0, j1, s_lse);
 }
 
-template <int D, int NT>
+template <int D, int NT, int MODE = kNotShared>
 struct DecCfg {
   static constexpr int ROW = D * 2;                        // bytes of a row
   static constexpr int RB = 128 / D;                       // blocks of 16 slots per warp and unit
   static constexpr int ROWS = 16 * RB;                     // slots per warp and unit
   static constexpr int STAGE = 2 * ROWS * ROW;             // a warp's K and V of one unit: 8 KiB
-  static constexpr int STAGES = 3;
-  static constexpr int RING = kDecWarps * STAGES * STAGE;  // 96 KiB per CTA
+  // By warps, behind a prefix: two, so that a CTA fits beside one of the prefix's.
+  static constexpr int STAGES = MODE == kSharedWarp ? 2 : 3;
+  static constexpr int RING = kDecWarps * STAGES * STAGE;  // 96 KiB per CTA (by warps: 64)
   static constexpr int HS = D + 4;                         // merge: floats per head (4: no bank conflicts)
-  static constexpr int SMEM = RING + kDecWarps * 8 * HS * 4;
+  static constexpr int SMEM = RING + (MODE == kSharedWarp ? 0 : kDecWarps * 8 * HS * 4);
   static constexpr int HEADS = 8 * NT;                     // query heads of a tile
 };
 
@@ -244,7 +245,7 @@ struct DecCfg {
 // early; this one ends after it.
 template <int D, bool BF16, int NT, bool WEIGHTS, int MODE = kNotShared>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(const DecodeArgs a) {
-  using C = DecCfg<D, NT>;
+  using C = DecCfg<D, NT, MODE>;
   constexpr bool SHARED = MODE != kNotShared, WARPS = MODE == kSharedWarp;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kDecWarps][8];
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
       if (blockIdx.x == 0 && threadIdx.x == 0 && a.row_tiles > 0 && ld_global(a.prefix_len) != P.len) report_page(c.status);
     }
     if (cta >= G) {
-      if constexpr (SHARED) grid_dependency_wait();
+      if (SHARED && blockIdx.x == 0) grid_dependency_wait();
       return;
     }
     u0 = unit_begin(cta, G, T);
@@ -616,7 +617,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     }
     unit_advance<D, MODE>(c, HH, cc, P, PI);
   }
-  if constexpr (SHARED) grid_dependency_wait();
+  // The kernel ends after the prefix's. One block waits for that: others make room.
+  if (SHARED && blockIdx.x == 0) grid_dependency_wait();
   if constexpr (WEIGHTS) {
     if (a.whole) {  // a key head is one item: its weights from the logits that this CTA wrote
       const int hh = cta % HH, b = cta / HH;
@@ -990,13 +992,12 @@ static cudaError_t launch_decode_t(DecodeArgs a, int ctas, cudaStream_t stream) 
                           dim3(kJoinThreads), 0, stream, a);
 }
 
-template <int D, bool BF16, int NT>
-static cudaError_t launch_suffix_t(const DecodeArgs& a, bool warps, int ctas, cudaStream_t stream) {
-  using C = DecCfg<D, NT>;
-  auto kern = warps ? fa2_paged_decode_kernel<D, BF16, NT, false, kSharedWarp>
-                    : fa2_paged_decode_kernel<D, BF16, NT, false, kSharedCta>;
-  static std::atomic<unsigned long long> done[2];
-  const cudaError_t e = allow_smem(kern, C::SMEM, done[warps]);
+template <int D, bool BF16, int NT, int MODE>
+static cudaError_t launch_suffix_t(const DecodeArgs& a, int ctas, cudaStream_t stream) {
+  using C = DecCfg<D, NT, MODE>;
+  auto kern = fa2_paged_decode_kernel<D, BF16, NT, false, MODE>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(kern, C::SMEM, done, MODE == kSharedWarp);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(ctas), dim3(kDecWarps * 32), C::SMEM, stream, a);
 }
@@ -1005,7 +1006,9 @@ static cudaError_t launch_suffix_t(const DecodeArgs& a, bool warps, int ctas, cu
 cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, bool warps, int ctas,
                                  cudaStream_t stream) {
 #define FA2_SUFFIX_CASE(DD, BB, NN) \
-  if (d == DD && bf16 == BB && head_tile == 8 * NN) return launch_suffix_t<DD, BB, NN>(a, warps, ctas, stream);
+  if (d == DD && bf16 == BB && head_tile == 8 * NN)                          \
+    return warps ? launch_suffix_t<DD, BB, NN, kSharedWarp>(a, ctas, stream) \
+                 : launch_suffix_t<DD, BB, NN, kSharedCta>(a, ctas, stream);
   FA2_SUFFIX_CASE(64, true, 1)
   FA2_SUFFIX_CASE(64, true, 2)
   FA2_SUFFIX_CASE(64, false, 1)

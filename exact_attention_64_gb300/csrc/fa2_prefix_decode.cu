@@ -18,7 +18,7 @@
 // slots, and CTA c of G has the units [c T / G, (c + 1) T / G) of the T = items x slot
 // tiles, so that every SM has the same share whatever the sizes. A segment (an item's
 // part in a CTA) leaves (m, l, O) in the workspace.
-//   warps 0, 3   copies of K and of V: one TMA box of up to 16 slots x 64 columns per
+//   warp 0       copies of K and of V: one TMA box of up to 16 slots x 64 columns per
 //                lane and page piece, into 128-slot tiles with the 128-byte swizzle.
 //   warp 1       the products: S = Q K^T, then O += P V with P read from TMEM.
 //   warps 4-11   two groups of 128 threads, a thread per row, each with an S and an O in
@@ -34,17 +34,29 @@
 
 namespace fa2 {
 
+// Shared memory and registers leave room for a CTA of the own slots' kernel beside each
+// of these: its loads and the prefix's products run at the same time.
 template <int D>
 struct PfxCfg {
-  static constexpr int SLAB = kTileRows * 128;            // 128 rows x 64 columns
+  static constexpr int SLAB = kTileRows * 128;  // 128 rows x 64 columns
   static constexpr int TILE = kTileRows * D * 2;
-  static constexpr int NS = D == 128 ? 2 : 4;             // ring depth of K and of V
-  static constexpr int OFF_K = 2 * TILE;                  // after the two Q tiles
-  static constexpr int OFF_V = OFF_K + NS * TILE;
-  static constexpr int OFF_STAGE = OFF_V + NS * TILE;     // 4 KiB per row warp
-  static constexpr int SMEM = OFF_STAGE + 8 * 4096 + 1024;
-  static_assert(SMEM + 2048 <= 232448, "with the static part at most what a CTA can have");
+  static constexpr int NS = D == 128 ? 3 : 6;   // ring of K and V tiles in turn
+  static constexpr int OFF_RING = 2 * TILE;     // after the two Q tiles
+  // In a Q tile, once its products have completed: 4 KiB for each of its warps' rows on
+  // their way out. With one row tile also both streams' references and the second's sums:
+  // at d = 128 behind those in the second tile, which has no queries then; at d = 64 they
+  // fill the tile.
+  static constexpr int STAGE = 4096;
+  static constexpr int ML_BYTES = 3 * kTileRows * 4;
+  static constexpr int OFF_ML = D == 128 ? TILE + 4 * STAGE : OFF_RING + NS * TILE;
+  static constexpr int SMEM = OFF_RING + NS * TILE + (D == 128 ? 0 : ML_BYTES) + 1024;
+  static_assert(4 * STAGE <= TILE && (D != 128 || OFF_ML + ML_BYTES <= 2 * TILE), "inside the tiles");
   static constexpr int THREADS = 384;
+  // Registers a thread at the launch, and of the control and the row warps from then on.
+  // A split of more than the launch has would wait for ever: the launch checks what the
+  // compiler gave.
+  static constexpr int REGS = 104, REGS_CONTROL = 72, REGS_ROWS = 120;
+  static_assert(4 * 32 * REGS_CONTROL + 8 * 32 * REGS_ROWS <= THREADS * REGS, "the split comes out of the launch's");
   static constexpr uint32_t TMEM_COLS = 512;
   // P overwrites S, 32 slots in 32 columns: 16 of the first pieces, 16 of the second.
   __host__ __device__ static constexpr uint32_t TM_S(int t) { return t * 128u; }
@@ -53,25 +65,25 @@ struct PfxCfg {
 
 template <int D>
 struct PfxShared {
-  uint64_t q_full;
-  uint64_t k_full[PfxCfg<D>::NS], k_empty[PfxCfg<D>::NS];
-  uint64_t v_full[PfxCfg<D>::NS], v_empty[PfxCfg<D>::NS];
+  uint64_t q_full, stored;
+  uint64_t full[PfxCfg<D>::NS], empty[PfxCfg<D>::NS];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t ml_full;
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  float m[2][kTileRows], l1[kTileRows];  // both streams' references, the second's sums
 };
 
-// A CTA's units, cut into segments of one item.
+// A CTA's units, from tile0 of an item on.
 struct PfxWork {
-  int P, tiles;          // slots in whole boxes, tiles of 128 of them
-  long long u0, u1, G, T;
+  int P, tiles;    // slots in whole boxes, tiles of 128 of them
+  int item, tile0;
+  long long left;
 };
+// A segment: the units of one item.
 struct PfxSeg {
-  int item, h, row0, rows;  // key head, first query row, rows (up to 256)
-  int tile0, cnt;           // slot tiles
+  int h, row0, rows;  // key head, first query row, rows (up to 256)
+  int tile0, cnt;     // slot tiles
   bool two;
 };
 
@@ -87,25 +99,31 @@ __device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta) {
   PfxWork w;
   w.P = prefix_slots(a.d).cut;
   w.tiles = (w.P + kTileRows - 1) / kTileRows;
-  w.T = static_cast<long long>(a.items) * w.tiles;
-  w.G = pfx_ctas(a, w.T);
-  w.u0 = w.u1 = 0;
-  if (cta < w.G) {
-    w.u0 = unit_begin(cta, w.G, w.T);
-    w.u1 = unit_begin(cta + 1, w.G, w.T);
+  const long long T = static_cast<long long>(a.items) * w.tiles, G = pfx_ctas(a, T);
+  w.left = 0;
+  w.item = w.tile0 = 0;
+  if (cta < G) {
+    const long long u0 = unit_begin(cta, G, T);
+    w.left = unit_begin(cta + 1, G, T) - u0;
+    w.item = static_cast<int>(div_pos(u0, w.tiles));
+    w.tile0 = static_cast<int>(u0 - static_cast<long long>(w.item) * w.tiles);
   }
   return w;
 }
-__device__ __forceinline__ PfxSeg pfx_seg(const PrefixArgs& a, const PfxWork& w, long long u) {
+__device__ __forceinline__ PfxSeg pfx_seg(const PrefixArgs& a, const PfxWork& w) {
   PfxSeg s;
-  s.item = static_cast<int>(div_pos(u, w.tiles));
-  s.tile0 = static_cast<int>(u - static_cast<long long>(s.item) * w.tiles);
-  s.cnt = static_cast<int>(min(static_cast<long long>(w.tiles - s.tile0), w.u1 - u));
-  s.h = div_by(s.item, a.fblocks);
-  s.row0 = (s.item - s.h * a.fblocks.d) * 2 * kTileRows;
+  s.tile0 = w.tile0;
+  s.cnt = static_cast<int>(min(static_cast<long long>(w.tiles - w.tile0), w.left));
+  s.h = div_by(w.item, a.fblocks);
+  s.row0 = (w.item - s.h * a.fblocks.d) * 2 * kTileRows;
   s.rows = min(2 * kTileRows, a.d.rows - s.row0);
   s.two = s.rows > kTileRows;
   return s;
+}
+__device__ __forceinline__ void pfx_next(PfxWork& w, int cnt) {
+  w.left -= cnt;
+  w.tile0 = 0;
+  ++w.item;
 }
 
 // Cache row of box i of a slot tile, or -1: past the prefix, or a page that the cache
@@ -118,41 +136,49 @@ __device__ __forceinline__ int pfx_row(const PrefixArgs& a, int P, int h, int ti
   return page_row(c, ld_global(a.d.prefix + p), h, slot - p * c.ps.d);
 }
 
-// ---- Copies: a warp for K and one for V -------------------------------------
+// ---- Copies: one warp ---------------------------------------------------------
+// Tile number 2 g (K) and 2 g + 1 (V) of a CTA go through one ring. One warp fills all of
+// it: it has then waited for every phase of a slot's barrier in turn, which a wait by
+// parity needs. (Two warps, for K and for V, would each see every other phase only, and
+// take a slot that has not been read for one that was read twice.)
 template <int D>
-__device__ bool pfx_producer(const PrefixArgs& a, const PfxWork& w, const CUtensorMap& map, uint64_t* full,
-                             uint64_t* empty, uint8_t* ring, int lane, bool report, bool fault, const WaitCtx& wc) {
+__device__ bool pfx_producer(const PrefixArgs& a, PfxWork w, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             PfxShared<D>& sh, uint8_t* ring, int lane, const WaitCtx& wc) {
   using C = PfxCfg<D>;
   const int boxes = kTileRows / a.d.box, bytes = a.d.box * 128;
   const int nowhere = a.d.c.num_pages * a.d.c.Hkv * a.d.c.ps.d;  // past the cache: reads as zeros
-  int g = 0;
+  int x = 0;
   bool ok = true;
-  for (long long u = w.u0; u < w.u1 && ok;) {
-    const PfxSeg s = pfx_seg(a, w, u);
-    for (int j = 0; j < s.cnt; ++j, ++g) {
-      const int st = g % C::NS, tile = s.tile0 + j;
+  while (w.left > 0 && ok) {
+    const PfxSeg s = pfx_seg(a, w);
+    for (int j = 0; j < s.cnt && ok; ++j) {
+      const int tile = s.tile0 + j;
       int row = lane < boxes ? pfx_row(a, w.P, s.h, tile, lane) : -1;
-      ok = mbar_wait_warp(&empty[st], ((g / C::NS) & 1) ^ 1, wc);
-      if (!ok) break;
-      if (fault && g == 0) continue;
-      if (lane == 0) mbar_arrive_expect_tx(&full[st], C::TILE);
-      __syncwarp();
-      for (int i = lane; i < boxes; i += 32) {
-        if (i >= 32) row = pfx_row(a, w.P, s.h, tile, i);
-        if (report && row < 0 && tile * kTileRows + i * a.d.box < w.P) report_page(a.d.c.status);
-        const int at = row < 0 ? nowhere : row;
-        uint8_t* dst = ring + st * C::TILE + i * bytes;
+      for (int kv = 0; kv < 2; ++kv, ++x) {
+        const int st = x % C::NS;
+        ok = mbar_wait_warp(&sh.empty[st], ((x / C::NS) & 1) ^ 1, wc);
+        if (!ok) break;
+        if (a.fault != 0 && x == 1) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], C::TILE);
+        __syncwarp();
+        const CUtensorMap* map = kv ? &tm_v : &tm_k;
+        for (int i = lane; i < boxes; i += 32) {
+          const int rr = i < 32 ? row : pfx_row(a, w.P, s.h, tile, i);
+          if (kv == 0 && rr < 0 && tile * kTileRows + i * a.d.box < w.P) report_page(a.d.c.status);
+          const int at = rr < 0 ? nowhere : rr;
+          uint8_t* dst = ring + st * C::TILE + i * bytes;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + x * C::SLAB, &map, &full[st], x * 64, at, 0);
+          for (int y = 0; y < D / 64; ++y) tma_load_3d(dst + y * C::SLAB, map, &sh.full[st], y * 64, at, 0);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    u += s.cnt;
+    pfx_next(w, s.cnt);
   }
   // Whoever gave up, this warp's copies land before the CTA ends.
   if (lane == 0)
-    for (int x = max(0, g - C::NS); x < g; ++x)
-      if (!(fault && x == 0)) mbar_wait_drain(&full[x % C::NS], (x / C::NS) & 1, a.timeout_ns);
+    for (int y = max(0, x - C::NS); y < x; ++y)
+      if (!(a.fault != 0 && y == 1)) mbar_wait_drain(&sh.full[y % C::NS], (y / C::NS) & 1, a.timeout_ns);
   return ok;
 }
 
@@ -165,24 +191,24 @@ __device__ bool pfx_producer(const PrefixArgs& a, const PfxWork& w, const CUtens
 // to 90) but whose rows are then all at work at once, 6200 clocks a slot tile of both
 // streams instead of 4600; O in two halves of d in turn, 4900.
 template <int D, bool BF16>
-__device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem,
+__device__ bool pfx_issuer(const PrefixArgs& a, PfxWork w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem,
                            const WaitCtx& wc) {
   using C = PfxCfg<D>;
   constexpr uint32_t id_s = make_idesc_f16(kTileRows, kTileRows, BF16, false, false);
   constexpr uint32_t id_o = make_idesc_f16(kTileRows, D, BF16, false, true);
-  const uint32_t q = smem_u32(smem), k = q + C::OFF_K, v = q + C::OFF_V;
+  const uint32_t q = smem_u32(smem), ring = q + C::OFF_RING;
   int g0 = 0, segs = 0, tasks[2] = {0, 0};
   bool ok = true;
-  for (long long u = w.u0; u < w.u1 && ok; ++segs) {
-    const PfxSeg s = pfx_seg(a, w, u);
+  for (; w.left > 0 && ok; ++segs) {
+    const PfxSeg s = pfx_seg(a, w);
     const int n = s.two ? 2 * s.cnt : s.cnt, sh2 = s.two ? 1 : 0;
     auto issue_s = [&](int i) {
-      const int g = g0 + (i >> sh2), st = g % C::NS, t = i & 1;
+      const int x = 2 * (g0 + (i >> sh2)), st = x % C::NS, t = i & 1;
       if (!s.two || t == 0) {
-        if (!mbar_wait_warp(&sh.k_full[st], (g / C::NS) & 1, wc)) return false;
+        if (!mbar_wait_warp(&sh.full[st], (x / C::NS) & 1, wc)) return false;
         tc_fence_after();
       }
-      const uint32_t qt = q + (s.two ? t : 0) * C::TILE, kt = k + st * C::TILE;
+      const uint32_t qt = q + (s.two ? t : 0) * C::TILE, kt = ring + st * C::TILE;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * C::SLAB + (kk % 4) * 32;
@@ -190,7 +216,7 @@ __device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& 
                      kk > 0 ? 1u : 0u);
       }
       umma_commit_warp(&sh.s_full[t]);
-      if (!s.two || t == 1) umma_commit_warp(&sh.k_empty[st]);
+      if (!s.two || t == 1) umma_commit_warp(&sh.empty[st]);
       return true;
     };
     ok = mbar_wait_warp(&sh.q_full, segs & 1, wc);
@@ -198,12 +224,12 @@ __device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& 
     tc_fence_after();
     ok = issue_s(0) && (n < 2 || issue_s(1));
     for (int i = 0; i < n && ok; ++i) {
-      const int g = g0 + (i >> sh2), st = g % C::NS, t = i & 1;
-      ok = mbar_wait2_warp(&sh.v_full[st], (g / C::NS) & 1, &sh.p_full[t], tasks[t] & 1, wc);
+      const int x = 2 * (g0 + (i >> sh2)) + 1, st = x % C::NS, t = i & 1;
+      ok = mbar_wait2_warp(&sh.full[st], (x / C::NS) & 1, &sh.p_full[t], tasks[t] & 1, wc);
       if (!ok) break;
       ++tasks[t];
       tc_fence_after();
-      const uint32_t vt = v + st * C::TILE;
+      const uint32_t vt = ring + st * C::TILE;
 #pragma unroll
       for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
@@ -211,11 +237,11 @@ __device__ bool pfx_issuer(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& 
           umma_ts_warp(tmem + C::TM_O(t), tmem + C::TM_S(t) + (kk / 2) * 32 + piece * 16 + (kk % 2) * 8,
                        make_sdesc_sw128(vt + kk * 2048, C::SLAB, 1024), id_o, (i >= 2 || piece > 0 || kk > 0) ? 1u : 0u);
       umma_commit_warp(&sh.o_full[t]);
-      if (!s.two || t == 1) umma_commit_warp(&sh.v_empty[st]);
+      if (!s.two || t == 1) umma_commit_warp(&sh.empty[st]);
       if (i + 2 < n) ok = issue_s(i + 2);
     }
     g0 += s.cnt;
-    u += s.cnt;
+    pfx_next(w, s.cnt);
   }
   // Every product that was issued completes before TMEM is released.
   umma_commit_warp(&sh.mma_done);
@@ -367,9 +393,9 @@ __device__ __forceinline__ void pfx_load_q(const PrefixArgs& a, int h, int row0,
     uint4 v[8];
 #pragma unroll
     for (int y = 0; y < 8; ++y) {
-      const int R = row0 + r0 + x + y * PER + sub;
+      const int in = x + y * PER + sub, R = row0 + r0 + in;
       v[y] = make_uint4(0u, 0u, 0u, 0u);
-      if (R < d.rows) {
+      if (in < n && R < d.rows) {
         const int b = div_by(R, d.fg), gx = R - b * d.g;
         v[y] = ld_global(reinterpret_cast<const uint4*>(
                              d.q + (static_cast<size_t>(b) * d.Hq + static_cast<size_t>(h) * d.g + gx) * D) + ch);
@@ -377,7 +403,8 @@ __device__ __forceinline__ void pfx_load_q(const PrefixArgs& a, int h, int row0,
     }
 #pragma unroll
     for (int y = 0; y < 8; ++y) {
-      const int r = r0 + x + y * PER + sub;
+      const int in = x + y * PER + sub, r = r0 + in;
+      if (in >= n) continue;
       *reinterpret_cast<uint4*>(tile + (ch / 8) * PfxCfg<D>::SLAB + r * 128 + (((ch % 8) ^ (r & 7)) * 16)) = v[y];
     }
   }
@@ -418,71 +445,77 @@ __device__ __forceinline__ void pfx_store(uint32_t tx, uint32_t ty, float f0, fl
 }
 
 template <int D, bool BF16>
-__device__ bool pfx_rows(const PrefixArgs& a, const PfxWork& w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem, int cta,
+__device__ bool pfx_rows(const PrefixArgs& a, PfxWork w, PfxShared<D>& sh, uint8_t* smem, uint32_t tmem, int cta,
                          int warp, int lane, const WaitCtx& wc) {
   using C = PfxCfg<D>;
   const int t = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   const uint32_t t_s = lanes + C::TM_S(t), t_o = lanes + C::TM_O(t);
-  float4* slice = reinterpret_cast<float4*>(smem + C::OFF_STAGE + (warp - 4) * 4096);
+  float4* slice = reinterpret_cast<float4*>(smem + t * C::TILE + quad * C::STAGE);
+  float* sh_m = reinterpret_cast<float*>(smem + C::OFF_ML);  // [2][128], then the second stream's sums [128]
   const float sl2 = a.d.scale_log2;
-  int done[2] = {0, 0};  // tasks of both streams so far
+  int done = 0;          // tasks of this stream so far
   int joined = 0;        // segments of one row tile
-  for (long long u = w.u0; u < w.u1;) {
-    const PfxSeg s = pfx_seg(a, w, u);
-    // Queries: tile t, or half a warp's rows of the one tile each. All products that
-    // read the tile's last contents have completed (o_full below).
+  for (int seg = 0; w.left > 0; ++seg) {
+    const PfxSeg s = pfx_seg(a, w);
+    if (seg > 0 && !mbar_wait_warp(&sh.stored, (seg - 1) & 1, wc)) return false;  // nobody uses the tiles any more
+    // Queries: tile t, or half a warp's rows of the one tile each.
     if (s.two) pfx_load_q<D>(a, s.h, s.row0 + t * kTileRows, quad * 32, 32, smem + t * C::TILE, lane);
     else pfx_load_q<D>(a, s.h, s.row0, quad * 32 + t * 16, 16, smem, lane);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_full);
-    const int n0 = s.two ? s.cnt : (s.cnt + 1) / 2, n1 = s.two ? s.cnt : s.cnt / 2, n = t ? n1 : n0;
+    const int n1 = s.two ? s.cnt : s.cnt / 2, n = t ? n1 : s.cnt - (s.two ? 0 : n1);  // tasks of the second, of this stream
     float m_ref = -INFINITY, l = 0.f;
     for (int i = 0; i < n; ++i) {
       const PfxMask mask = pfx_mask(a, w.P, s.h, s.tile0 + (s.two ? i : 2 * i + t), lane);
-      if (!pfx_step<D, BF16>(sh, t, t_s, t_o, mask, a.d.box, sl2, i == 0, done[t] + i, m_ref, l, lane, wc)) return false;
+      if (!pfx_step<D, BF16>(sh, t, t_s, t_o, mask, a.d.box, sl2, i == 0, done + i, m_ref, l, lane, wc)) return false;
     }
-    done[0] += n0;
-    done[1] += n1;
-    if ((t == 0 || !s.two) && !mbar_wait_warp(&sh.o_full[0], (done[0] - 1) & 1, wc)) return false;
-    if ((t == 1 || !s.two) && n1 > 0 && !mbar_wait_warp(&sh.o_full[1], (done[1] - 1) & 1, wc)) return false;
+    done += n;
+    if (n > 0 && !mbar_wait_warp(&sh.o_full[t], (done - 1) & 1, wc)) return false;
     __syncwarp();
     tc_fence_after();
     const float M = m_ref == -INFINITY ? -INFINITY : m_ref * sl2 - kPfxBias<BF16>;
-    const size_t part = static_cast<size_t>(shared_part(s.item, cta)) * 2 * kTileRows;
+    const size_t part = static_cast<size_t>(shared_part(w.item, cta)) * 2 * kTileRows;
     if (s.two) {
       const int rows = min(32, s.rows - t * kTileRows - quad * 32);
       pfx_store<D, false>(t_o, 0u, 1.f, 0.f, false, 0, D, a.part_o + (part + t * kTileRows + quad * 32) * D, rows, lane,
                           slice);
       if (lane < rows) a.part_ml[part + t * kTileRows + r] = make_float2(M, l);
     } else {
-      // Both streams' sums of the same rows, half of the columns each. (The next
-      // segment's queries are complete, and sh.m free, when every warp is past this.)
-      sh.m[t][r] = M;
-      if (t == 1) sh.l1[r] = l;
+      // Both streams' sums of the same rows, half of the columns each, when both are
+      // complete.
+      tc_fence_before();
+      sh_m[t * kTileRows + r] = M;
+      if (t == 1) sh_m[2 * kTileRows + r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.ml_full);
       if (!mbar_wait_warp(&sh.ml_full, joined & 1, wc)) return false;
       ++joined;
-      const float m0 = sh.m[0][r], m1 = sh.m[1][r];
+      __syncwarp();
+      tc_fence_after();
+      const float m0 = sh_m[r], m1 = sh_m[kTileRows + r];
       const float top = fmaxf(m0, m1), f0 = step_down(m0, top), f1 = step_down(m1, top);
       const int rows = min(32, s.rows - quad * 32);
       pfx_store<D, true>(lanes + C::TM_O(0), lanes + C::TM_O(1), n1 > 0 ? f0 : 1.f, f1, n1 > 0, t * (D / 2),
                          (t + 1) * (D / 2), a.part_o + (part + quad * 32) * D, rows, lane, slice);
       if (t == 0 && lane < rows)
-        a.part_ml[part + r] = n1 > 0 ? make_float2(top, l * f0 + sh.l1[r] * f1) : make_float2(M, l);
+        a.part_ml[part + r] = n1 > 0 ? make_float2(top, l * f0 + sh_m[2 * kTileRows + r] * f1) : make_float2(M, l);
     }
     tc_fence_before();
-    u += s.cnt;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.stored);
+    pfx_next(w, s.cnt);
   }
   return true;
 }
 
-static_assert(sizeof(PfxShared<128>) <= 2048 && sizeof(PfxShared<64>) <= 2048, "counted by PfxCfg");
+// With a CTA of the own slots' kernel, 64 KiB of ring, and what the system takes of each
+// CTA, at most the 228 KiB of an SM.
+static_assert(PfxCfg<128>::SMEM + sizeof(PfxShared<128>) + 65536 + 512 + 2048 <= 233472, "room for both");
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(PfxCfg<D>::THREADS, 1)
+__global__ void __maxnreg__(PfxCfg<D>::REGS)
     fa2_prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const PrefixArgs a) {
   using C = PfxCfg<D>;
@@ -493,11 +526,10 @@ __global__ void __launch_bounds__(PfxCfg<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, 8);
     mbar_init(&sh.ml_full, 8);
+    mbar_init(&sh.stored, 8);
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
@@ -523,15 +555,13 @@ __global__ void __launch_bounds__(PfxCfg<D>::THREADS, 1)
   if (cta == 0 && threadIdx.x == 0 && ld_global(a.d.prefix_len) != prefix_slots(a.d).len) report_page(a.d.c.status);
   const WaitCtx wc{a.d.c.status, &sh.abort_flag, a.timeout_ns};
   if (warp < 4) {
-    setmaxnreg_dec<88>();  // 4 x 32 x 88 + 8 x 32 x 208 = 64,512 = the launch's 384 x 168
+    setmaxnreg_dec<C::REGS_CONTROL>();
     if (warp == 0)
-      pfx_producer<D>(a, w, tm_k, sh.k_full, sh.k_empty, smem + C::OFF_K, lane, true, false, wc);
-    else if (warp == 3)
-      pfx_producer<D>(a, w, tm_v, sh.v_full, sh.v_empty, smem + C::OFF_V, lane, false, a.fault != 0, wc);
+      pfx_producer<D>(a, w, tm_k, tm_v, sh, smem + C::OFF_RING, lane, wc);
     else if (warp == 1)
       pfx_issuer<D, BF16>(a, w, sh, smem, tmem, wc);
   } else {
-    setmaxnreg_inc<208>();
+    setmaxnreg_inc<C::REGS_ROWS>();
     pfx_rows<D, BF16>(a, w, sh, smem, tmem, cta, warp, lane, wc);
   }
   tc_fence_before();
@@ -651,7 +681,15 @@ static cudaError_t launch_prefix_t(const CUtensorMap& tk, const CUtensorMap& tv,
   if (a.items > 0) {
     auto kern = fa2_prefix_kernel<D, BF16>;
     static std::atomic<unsigned long long> done{0};
-    e = allow_smem(kern, PfxCfg<D>::SMEM, done);
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+      cudaFuncAttributes at;
+      e = cudaFuncGetAttributes(&at, kern);
+      if (e != cudaSuccess) return e;
+      regs.store(at.numRegs, std::memory_order_release);
+    }
+    if (regs.load(std::memory_order_acquire) < PfxCfg<D>::REGS) return cudaErrorInvalidKernelImage;
+    e = allow_smem(kern, PfxCfg<D>::SMEM, done, true);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kern, dim3(a.ctas), dim3(PfxCfg<D>::THREADS), PfxCfg<D>::SMEM, stream, tk, tv, a);
     if (e != cudaSuccess) return e;

@@ -75,6 +75,14 @@ CASES = [
     (3, 2, 2, 64, 64, 20011, [0, 1, 77]),    # a long prefix over few heads
 ]
 
+# Enough units that a CTA of the prefix has several slot tiles, and pieces of two items
+MANY = [
+    (5, 160, 40, 128, 16, 1300, None),       # 20 rows: one tile, both row groups on it
+    (8, 128, 32, 64, 16, 1500, None),        # 32 rows
+    (34, 96, 24, 128, 16, 1500, None),       # 136 rows: two tiles
+    (65, 64, 16, 64, 32, 1700, None),        # 260 rows: items of two tiles and of one
+]
+
 
 def _lens(case):
     B, P, own = case[0], case[5], case[6]
@@ -99,6 +107,22 @@ def test_matches_the_oracle(cuda_device, fa2_lib, case, dtype):
         _check(c, q, o, lse, d ** -0.5)
         o2, lse2 = fa2_lib.prefix_decode(*a)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "_".join(map(str, c[:6])))
+def test_several_tiles_per_cta(cuda_device, fa2_lib, case):
+    B, Hq, Hkv, d, ps, P, _ = case
+    dtype = BF16 if d == 128 else FP16
+    c = Shared(B, Hkv, d, ps, P, _lens(case), dtype, seed=Hq + ps)
+    q = c.query(Hq, 1.5)
+    a = c.args(q, True)
+    first = fa2_lib.prefix_decode(*a)
+    torch.cuda.synchronize()
+    assert fa2_lib.device_status() == 0
+    _check(c, q, *first, d ** -0.5)
+    for _ in range(20):
+        o, lse = fa2_lib.prefix_decode(*a)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
