@@ -307,9 +307,12 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   if (st != FA2_OK) return st;
   c.box = 1;
   while (c.box < 16 && page_size % (2 * c.box) == 0) c.box *= 2;
-  CUtensorMap tk, tv;
+  c.prefix_cap = prefix_pages * page_size;
+  const bool inside = prefix_inside(B, Hq, Hkv, d, c.prefix_cap);
+  CUtensorMap tk{}, tv{};
   const int rows = num_pages * Hkv * page_size;
-  if (fa2::host_map_rows(&tk, k_cache, rows, d, dtype, c.box) || fa2::host_map_rows(&tv, v_cache, rows, d, dtype, c.box))
+  if (!inside && (fa2::host_map_rows(&tk, k_cache, rows, d, dtype, c.box) ||
+                  fa2::host_map_rows(&tv, v_cache, rows, d, dtype, c.box)))
     return FA2_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
   c.q = static_cast<const uint16_t*>(q);
@@ -322,8 +325,6 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   c.starts = reinterpret_cast<long long*>(ws + s.starts);
   c.Hq = Hq;
   c.g = Hq / Hkv;
-  c.prefix_cap = prefix_pages * page_size;
-  const bool inside = prefix_inside(B, Hq, Hkv, d, c.prefix_cap);
   a.head_tile = prefix_head_tile(B, Hq, Hkv, inside);
   c.HG = (c.g + a.head_tile - 1) / a.head_tile;
   c.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);

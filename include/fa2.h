@@ -353,7 +353,7 @@ size_t fa2_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_s
  *   other arguments as in fa2_paged_decode.
  * Prefix slots past the last multiple of 16 (or of the largest power of two that
  * divides page_size, if that is less) are read for each sequence by its own table. In
- * the prefix P enters its product with a relative error of 2^-18 (bf16), or 2^-22 and
+ * the prefix P enters its product with a relative error of 2^-16 (bf16), or 2^-22 and
  * 2^-36 of the row's largest (fp16), and an entry of V that is not finite makes o not
  * finite. The result does not depend on timing: repeated calls give the same bits. */
 int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int* table, const int* lens,

@@ -219,6 +219,20 @@ def test_autograd(cuda_device, fa2_lib, norm):
     assert torch.equal(k.grad, want[1]) and (wk is None or torch.equal(wk.grad, want[3]))
 
 
+def test_autograd_of_one_tensor(cuda_device, fa2_lib):
+    q0, _, g = _inputs(2, 3, 1, 20, 64, FP16, seed=6)
+    f = fa2_lib.rotary_frequencies(64).cuda()
+    for w0 in (None, torch.rand(64, generator=g).cuda()):
+        q = q0.detach().clone().requires_grad_()
+        w = None if w0 is None else w0.clone().requires_grad_()
+        y, none = fa2_lib.rotary(q, None, f, interleaved=True, q_weight=w)
+        assert none is None
+        dy = torch.randn(y.shape, generator=g).to(FP16).cuda()
+        y.backward(dy)
+        want = fa2_lib.rotary_backward(dy, None, f, interleaved=True, q=q0 if w is not None else None, q_weight=w0)
+        assert torch.equal(q.grad, want[0]) and (w is None or torch.equal(w.grad, want[2]))
+
+
 def test_gradient_against_differences(cuda_device, fa2_lib):
     """Differences of the forward itself along the gradient's signs, in its own 16 bits:
     both sides of a step h are rounded by a half step of y, over 2 h. x is on a grid
