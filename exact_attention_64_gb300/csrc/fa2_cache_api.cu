@@ -146,19 +146,20 @@ DecodeSpace decode_space(int B, int Hq, int Hkv, int d, int page_size, int max_p
 
 // Whether the prefix is attended to by the kernel of the own slots, in items of 8 or 16
 // of the rows = B g query rows of a key head. That saves a launch and the other kernel's
-// start, about 6 us, but reads and multiplies the prefix once for each 16 rows. (32/8
-// heads, d = 128, inside and outside: 2000 slots, 64 rows 17.3 and 20.8 us, 96 rows 21.5
-// and 22.2, 128 rows 25.2 and 23.8; 512 slots, 256 rows 20.0 and 21.5; 8192 slots, 32 rows
-// 22.5 and 21.3, 48 rows 27.9 and 22.5. Two heads of 16384 slots, d = 64, 48 rows 15.4 and
-// 16.3, 64 rows 17.6 and 16.8, 128 rows 26.1 and 20.0.)
+// start, but reads and multiplies the prefix once for each 16 rows; one such tile is read
+// once anyway. (32/8 heads, d = 128, inside and outside: 2000 slots, 48 rows 17.0 and 19.7
+// us, 64 rows 17.6 and 19.7, 96 rows 22.0 and 21.3; 512 slots, 128 rows 15.3 and 16.3, 192
+// rows 18.7 and 17.4; 8192 slots, 32 rows 23.6 and 24.0, 48 rows 28.2 and 22.7. Two heads
+// of 16384 slots, d = 64, 32 rows 13.7 and 14.0, 128 rows 26.0 and 17.9.) The list's room
+// decides, the prefix's length being known on the device only.
 bool prefix_inside(int B, int Hq, int Hkv, int d, long long prefix_cap) {
   const long long rows = static_cast<long long>(B) * (Hq / Hkv), tiles = (rows + 15) / 16;
-  return tiles == 1 || tiles * Hkv * prefix_cap <= 98304LL * 128 / d;
+  return tiles == 1 || (tiles <= 8 && tiles * Hkv * prefix_cap <= 65536LL * 128 / d);
 }
 // Whether the workers of the own slots (and of a prefix inside) are warps: from 96 items
-// on. By CTAs and by warps: 40 items (32/8 heads, 2000 slots and 300 own, d = 128) 12.0 and
-// 15.9 us, 80 items 15.0 and 15.3, 120 items 18.7 and 16.6; 68 items (2 heads, 16384 slots,
-// d = 64) 13.5 and 15.2; 320 items (32 heads, 4096 slots) 32.7 and 25.0.
+// on. By CTAs and by warps: 40 items (32/8 heads, 2000 slots and 300 own, d = 128) 12.4 and
+// 16.4 us, 80 items 15.5 and 15.8, 120 items 19.1 and 17.1; 68 items (2 heads, 16384 slots,
+// d = 64) 13.7 and 14.9; 384 items (32 heads, 4096 slots) 33.1 and 25.1.
 bool prefix_by_warps(long long items) { return items >= 96; }
 int prefix_head_tile(int B, int Hq, int Hkv, bool inside) {
   return inside && static_cast<long long>(B) * (Hq / Hkv) > 8 ? 16 : head_tile(Hq / Hkv);

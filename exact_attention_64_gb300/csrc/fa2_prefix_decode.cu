@@ -33,7 +33,7 @@
 // fill it), and would be half a product more.
 //
 // Per CTA and slot tile of two row tiles about 4300 clocks at d = 128, of which the 48
-// products are 3072 at the tensor core's best. B = 256, 32/8 heads, 16384 slots and up to
+// products are about 3070 at the tensor core's best. B = 256, 32/8 heads, 16384 slots and up to
 // 200 own ones: 104 us, of which the prefix's kernel takes about 80.
 #include "fa2_common.cuh"
 #include "fa2_decode_units.cuh"

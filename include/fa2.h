@@ -591,7 +591,7 @@ int fa2_last_cuda_error(void);
  *      every dQ worker;
  *   6  the next fa2_key_weights: the first Q tile of every CTA (there is no 5);
  *   7  the next fa2_prefix_decode whose prefix has a kernel of its own (any of more
- *      than 16 * 65536 query rows times slots, say): the first V tile of its CTAs;
+ *      than 128 query rows to a key head): the first V tile of each of its CTAs;
  *   0  disarms.
  * Outputs of the faulted call are undefined. Exists to test the failure path
  * without hanging or faulting the GPU. */
