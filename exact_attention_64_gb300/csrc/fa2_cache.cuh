@@ -167,7 +167,7 @@ struct DecodeArgs {
   const int* prefix;      // shared prefix: its pages [prefix_pages]
   const int* prefix_len;  // [1]
   int prefix_cap;         // slots that the prefix can have at most
-  long long* starts;      // workspace [B + 1]: units before those of each sequence
+  long long* starts;      // workspace [B + 2]: units before those of each sequence, then the prefix's CTAs
   int rows;               // query rows of a key head, B * g: row R is head R % g of sequence R / g
   FastDiv fg;
   int row_tiles;          // tiles of query rows whose prefix this kernel attends to itself, per key head, or 0

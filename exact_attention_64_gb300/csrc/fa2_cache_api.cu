@@ -191,7 +191,7 @@ PrefixSpace prefix_space(int B, int Hq, int Hkv, int d) {
   s.so = s.pml + align_up(rows * 8, 256);
   s.sml = s.so + align_up(own * d * 4, 256);
   s.starts = s.sml + align_up(own * 8, 256);
-  s.total = s.starts + align_up(static_cast<size_t>(B + 1) * 8, 256);
+  s.total = s.starts + align_up(static_cast<size_t>(B + 2) * 8, 256);
   return s;
 }
 

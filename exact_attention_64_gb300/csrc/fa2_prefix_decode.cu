@@ -101,11 +101,12 @@ __device__ __forceinline__ long long pfx_ctas(const PrefixArgs& a, long long T) 
   return div_pos(T + longest - 1, longest);
 }
 
-__device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta) {
+__device__ __forceinline__ PfxWork pfx_work(const PrefixArgs& a, int cta, long long* ctas) {
   PfxWork w;
   w.P = prefix_slots(a.d).cut;
   w.tiles = (w.P + kTileRows - 1) / kTileRows;
   const long long T = static_cast<long long>(a.items) * w.tiles, G = pfx_ctas(a, T);
+  *ctas = G;
   w.left = 0;
   w.item = w.tile0 = 0;
   if (cta < G) {
@@ -549,7 +550,9 @@ __global__ void __maxnreg__(PfxCfg<D>::REGS)
   grid_dependency_wait();
   grid_launch_dependents();  // the kernel of the own slots relies on the wait above
   const int cta = blockIdx.x;
-  const PfxWork w = pfx_work(a, cta);
+  long long G;
+  const PfxWork w = pfx_work(a, cta, &G);
+  if (cta == 0 && threadIdx.x == 0) a.d.starts[a.d.c.B + 1] = G;  // for the join
   if (cta == 0 && threadIdx.x == 0 && ld_global(a.d.prefix_len) != prefix_slots(a.d).len) report_page(a.d.c.status);
   const WaitCtx wc{a.d.c.status, &sh.abort_flag, a.timeout_ns};
   if (warp < 4) {
@@ -585,38 +588,44 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (per_row - 1);
   const DecodeArgs& d = a.d;
   const CacheView& c = d.c;
-  const long long row = (static_cast<long long>(blockIdx.x) * kPjWarps + warp) / per_row;
+  const long long first_row = static_cast<long long>(blockIdx.x) * (kPjWarps / per_row);
+  const long long row = first_row + warp / per_row;
   const bool on = row < static_cast<long long>(c.B) * d.Hq;
-  const int b = on ? static_cast<int>(row / d.Hq) : 0, x = on ? static_cast<int>(row - static_cast<long long>(b) * d.Hq) : 0;
+  const int b = on ? static_cast<int>(div_pos(row, d.Hq)) : 0, x = on ? static_cast<int>(row - static_cast<long long>(b) * d.Hq) : 0;
   const int h = div_by(x, d.fg), gx = x - h * d.g;
+  const bool inside = d.row_tiles > 0;  // the prefix was attended to by the kernel of the own slots
   grid_dependency_wait();
   const PrefixLen P = prefix_slots(d);
-  const int len = seq_len(c, b), first = prefix_of(len, P), own = len - first;
+  const int len = seq_len(c, b);
   const long long T = ld_global(d.starts + c.B), start = ld_global(d.starts + b);
-  // Parts of the prefix, then own ones.
-  int np = 0, ns = 0, p_step = 0;
-  size_t p0 = 0, o0 = 0;  // their first rows in the workspace
-  const long long G = min(static_cast<long long>(a.tail_ctas) * (a.tail_warps ? kDecWarps : 1), T);  // workers
+  const long long PG = inside ? 0 : ld_global(d.starts + c.B + 1);
+  // Parts of the prefix, then own ones: from the first to the last CTA (worker) of an
+  // item. Lanes 0 and 1 find those of the prefix, 2 and 3 those of the own slots.
+  const int first = prefix_of(len, P), own = len - first;
   auto own_tiles = [&](int n) { return a.tail_warps ? tiles_of<D, kSharedWarp>(n) : tiles_of<D>(n); };
-  const bool inside = d.row_tiles > 0;  // the prefix was attended to by the kernel of the own slots
-  const int PI = inside && P.cut > 0 ? d.row_tiles * c.Hkv : 0;
-  if (first > 0) {
-    const int R = b * d.g + gx;
-    p_step = inside ? a.head_tile : 2 * kTileRows;
-    const long long tiles = inside ? own_tiles(P.cut) : (P.cut + kTileRows - 1) / kTileRows;
-    const long long PT = inside ? T : tiles * a.items, PG = inside ? G : pfx_ctas(a, PT);
-    const int item = h * (inside ? d.row_tiles : a.fblocks.d) + R / p_step;
-    const int c0 = unit_cta(item * tiles, PG, PT);
-    np = unit_cta(item * tiles + tiles - 1, PG, PT) - c0 + 1;
-    p0 = static_cast<size_t>(shared_part(item, c0)) * p_step + R % p_step;
+  const long long G = min(static_cast<long long>(a.tail_ctas) * (a.tail_warps ? kDecWarps : 1), T);  // workers
+  const int R = b * d.g + gx, p_step = inside ? a.head_tile : 2 * kTileRows;
+  const int p_tile = inside ? (a.head_tile == 8 ? R >> 3 : R >> 4) : R / (2 * kTileRows);
+  const int p_item = h * (inside ? d.row_tiles : a.fblocks.d) + p_tile;
+  const int tiles_p = inside ? own_tiles(P.cut) : (P.cut + kTileRows - 1) / kTileRows, tiles_o = own_tiles(own);
+  const int o_tile = a.head_tile == 8 ? gx >> 3 : gx >> 4, hh = h * d.HG + o_tile;
+  const int o_item = (inside && P.cut > 0 ? d.row_tiles * c.Hkv : 0) + b * c.Hkv * d.HG + hh;
+  int cta = 0;
+  {
+    const bool pre = lane < 2;
+    const int tiles = pre ? tiles_p : tiles_o;
+    const long long u0 = pre ? static_cast<long long>(p_item) * tiles : start + static_cast<long long>(hh) * tiles;
+    if (lane < 4 && (pre ? first : own) > 0)
+      cta = unit_cta(u0 + (lane & 1 ? tiles - 1 : 0), pre && !inside ? PG : G,
+                     pre && !inside ? static_cast<long long>(a.items) * tiles : T);
   }
-  if (own > 0) {
-    const int HH = c.Hkv * d.HG, tiles = own_tiles(own), hh = h * d.HG + gx / a.head_tile;
-    const long long u = start + static_cast<long long>(hh) * tiles;
-    const int c0 = unit_cta(u, G, T);
-    ns = unit_cta(u + tiles - 1, G, T) - c0 + 1;
-    o0 = static_cast<size_t>(shared_part(PI + b * HH + hh, c0)) * a.head_tile + gx % a.head_tile;
-  }
+  const int pc = __shfl_sync(0xffffffffu, cta, 0), oc = __shfl_sync(0xffffffffu, cta, 2);
+  int np = __shfl_sync(0xffffffffu, cta, 1) - pc + 1, ns = __shfl_sync(0xffffffffu, cta, 3) - oc + 1;
+  if (first == 0) np = 0;
+  if (own == 0) ns = 0;
+  // Their first rows in the workspace.
+  const size_t p0 = static_cast<size_t>(shared_part(p_item, pc)) * p_step + (R - p_tile * p_step);
+  const size_t o0 = static_cast<size_t>(shared_part(o_item, oc)) * a.head_tile + (gx - o_tile * a.head_tile);
   const float2* p_ml = inside ? d.part_ml : a.part_ml;
   const float* p_o = inside ? d.part_o : a.part_o;
   if (!on) np = ns = 0;
