@@ -315,3 +315,34 @@ def test_streams_and_graphs(cuda_device, fa2_lib):
             want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_captured_training_step(cuda_device, fa2_lib):
+    """Forward and backward through autograd, captured; gradients by autograd.grad."""
+    q, k, g = _inputs(2, 4, 4, 50, 64, BF16, seed=11)
+    f = fa2_lib.rotary_frequencies(64).cuda()
+    q, k = q.detach().clone().requires_grad_(), k.detach().clone().requires_grad_()
+    w = [torch.rand(64, generator=g).cuda().requires_grad_() for _ in range(2)]
+    v, do = torch.randn(2, 4, 50, 64).to(BF16).cuda(), torch.randn(2, 4, 50, 64).to(BF16).cuda()
+
+    def step():
+        qr, kr = fa2_lib.rotary(q, k, f, q_weight=w[0], k_weight=w[1])
+        return torch.autograd.grad(fa2_lib.attention(qr, kr, v, causal=True), (q, k, *w), do)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(2):
+        with torch.no_grad():
+            q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)))
+            w[1].copy_(torch.rand(64, generator=torch.Generator().manual_seed(seed + 5)))
+        graph.replay()
+        got = [t.clone() for t in out]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
