@@ -224,17 +224,30 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_kernel(const Rotary
   }
 }
 
-// Backward with a norm. A CTA's items are all queries or all keys of the same run of
-// heads (blockIdx.y), so that a lane's 16 sums of the weights' gradients stay in
-// registers; at its end the CTA adds up its rows' sums in a fixed order and leaves
-// them in the workspace, so that the bits repeat. 252 MB (B = 8, 16/4 heads, N = 2048,
-// d = 128) take 51 us with the sum of the CTAs' parts, 4.9 TB/s: 127 registers leave 16
-// warps per SM to hide what the next head's reads do not. (Two heads at a time, read
-// together, without reading ahead: 58; three CTAs per SM spill, 86.)
+// 16 bytes to a lane's own place, or zeros there.
+__device__ __forceinline__ void rot_copy16(uint32_t to, const uint4* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
+constexpr int kRotAhead = 3;                    // heads of a lane in its ring
+constexpr int kRotSlot = 4 * kRotThreads * 16;  // bytes of a head of every lane: two runs of x, two of g
+
+// Backward with a norm. A CTA's rows are all of queries or all of keys, so that a lane's
+// 16 sums of the weights' gradients stay in registers; at its end the CTA adds up its
+// rows' sums in a fixed order and leaves them in the workspace, so that the bits repeat.
+// 127 registers leave 16 warps per SM, and a head that they read ahead in registers is 32
+// KiB in flight, which took 50 us for 252 MB (B = 8, 16/4 heads, N = 2048, d = 128). So
+// rows are copied to shared memory, two heads ahead of the one in work, where they need no
+// registers: 44 us with the sum of the CTAs' parts, 5.7 TB/s (three heads ahead the same),
+// and 239 for 1.61 GB (B = 4, 32 + 32 heads, N = 8192), the copy rate. Units of a head of
+// 32 (d = 128) or 64 tokens are dealt evenly, two CTAs for each SM; where units are many, six
+// sevenths of them, and the last seventh in as many small CTAs, which go where a CTA
+// ends first (1.61 GB: 264 without).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(const RotaryArgs a, const RotarySplit sp) {
   using C = RotCfg<D>;
   constexpr int WARPS = kRotThreads / 32;
+  extern __shared__ __align__(16) uint4 s_ring[];
   __shared__ unsigned long long s_turn[D / 2];
   __shared__ __align__(8) float s_dw[WARPS][D];
   grid_dependency_wait();
@@ -242,72 +255,84 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
   rot_turns(a, s_turn);
   __syncthreads();
   const RotLane ln = rot_lane(threadIdx.x % C::LANES, D, a.r, a.interleaved);
-  const int ck = blockIdx.y;
-  const bool is_q = ck < a.chunks_q;
+  // The CTA's units: heads of blocks of GROUPS tokens, in this order.
+  const bool big = static_cast<int>(blockIdx.x) < sp.big_q + sp.big_k;
+  const int x = big ? blockIdx.x : blockIdx.x - sp.big_q - sp.big_k, qs = big ? sp.big_q : sp.small_q;
+  const bool is_q = x < qs;
   const RotarySide& s = is_q ? a.q : a.k;
-  const int h0 = (is_q ? ck : ck - a.chunks_q) * a.chunk;
-  const int steps = min(a.chunk, s.H - h0);
+  const int bigs = is_q ? sp.big_q : sp.big_k, smalls = is_q ? sp.small_q : sp.small_k;
+  const int cta = (is_q ? x : x - qs) + (big ? 0 : bigs);
+  auto before = [&](int c) { return min(c, bigs) * (kRotBig - 1) + c; };
+  const long long units = (a.tokens + C::GROUPS - 1) / C::GROUPS * s.H, u0 = units * before(cta) / before(bigs + smalls);
+  int left = static_cast<int>(units * before(cta + 1) / before(bigs + smalls) - u0);
+  const int block0 = static_cast<int>(u0 / s.H);
+  int h = static_cast<int>(u0 - static_cast<long long>(block0) * s.H);
   float2 w[8], dw[8];
   load_weight<BF16>(s.weight, a.weight_fp32, ln, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) dw[j] = make_float2(0.f, 0.f);
   const long long x_step = s.src.sh / 8, g_step = s.x.sh / 8, y_step = s.y.sh / 8;
-  const long long stride = static_cast<long long>(gridDim.x) * C::GROUPS;
-  // The rows of one head are read while those of the one before are worked on, from one
-  // token to the next, too.
-  long long tt = static_cast<long long>(blockIdx.x) * C::GROUPS + threadIdx.x / C::LANES;
-  long long block = static_cast<long long>(blockIdx.x) * C::GROUPS;  // the CTA's first token
+  // Each lane copies its pieces of the next rows, from one token to the next, into its own
+  // places of shared memory; it alone reads them.
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+  long long tt = static_cast<long long>(block0) * C::GROUPS + threadIdx.x / C::LANES, ct = tt;
+  int ch = h, copies = left, put = 0, take = 0;  // token ct, head ch are copied next
   const uint4 *xs = nullptr, *gs = nullptr;
-  uint4* dst = nullptr;
-  RotTurn tn;
-  uint4 v[2], g[2];
-  auto token = [&](int* b, int* n) {
-    const int t = tt < a.tokens ? static_cast<int>(tt) : 0;
+  auto token = [&](long long x, int* b, int* n) {
+    const int t = x < a.tokens ? static_cast<int>(x) : 0;
     *b = div_by(t, a.fN);
     *n = t - *b * a.N;
     return t;
   };
-  auto read = [&]() {
-    v[0] = v[1] = g[0] = g[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (tt < a.tokens) {
-      v[0] = ld_global(xs + ln.e0 / 8);
-      v[1] = ld_global(xs + ln.e1 / 8);
-      g[0] = ld_global(gs + ln.e0 / 8);
-      g[1] = ld_global(gs + ln.e1 / 8);
-    }
-  };
-  auto seek = [&]() {  // to the first head of token tt
+  auto seek = [&]() {
     int b, n;
-    (void)token(&b, &n);
-    xs = row_at(s.src, b, h0, n);
-    gs = row_at(s.x, b, h0, n);
+    (void)token(ct, &b, &n);
+    xs = row_at(s.src, b, ch, n);
+    gs = row_at(s.x, b, ch, n);
   };
-  if (block < a.tokens) {
-    seek();
-    read();
-  }
-  while (block < a.tokens) {
+  auto copy = [&]() {
+    if (copies > 0) {
+      const bool in = ct < a.tokens;
+      const uint32_t to = ring + put * kRotSlot;
+      rot_copy16(to, xs + ln.e0 / 8, in);
+      rot_copy16(to + kRotThreads * 16, xs + ln.e1 / 8, in);
+      rot_copy16(to + 2 * kRotThreads * 16, gs + ln.e0 / 8, in);
+      rot_copy16(to + 3 * kRotThreads * 16, gs + ln.e1 / 8, in);
+      put = put + 1 == kRotAhead ? 0 : put + 1;
+      xs += x_step;
+      gs += g_step;
+      --copies;
+      if (++ch == s.H) {
+        ch = 0;
+        ct += C::GROUPS;
+        seek();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  seek();
+#pragma unroll 1
+  for (int i = 0; i < kRotAhead - 1; ++i) copy();
+  RotTurn tn;
+  for (; left > 0; tt += C::GROUPS, h = 0) {
     const bool on = tt < a.tokens;
     int b, n;
-    const int t = token(&b, &n);
-    dst = row_at(s.y, b, h0, n);
+    const int t = token(tt, &b, &n);
+    uint4* dst = row_at(s.y, b, h, n);
     tn.set(s_turn, ln, rot_position(a, t, b, n), a.amplitude, -1.f);
+    const int heads = min(left, s.H - h);
+    left -= heads;
 #pragma unroll 1
-    for (int i = 0; i < steps; ++i, dst += y_step) {
+    for (int i = 0; i < heads; ++i, dst += y_step) {
+      copy();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRotAhead - 1) : "memory");
+      const uint4* at = s_ring + take * (kRotSlot / 16) + threadIdx.x;
+      take = take + 1 == kRotAhead ? 0 : take + 1;
       float2 x[8], y[8];
-      unpack16<BF16>(v, x);
-      unpack16<BF16>(g, y);
-      if (i + 1 < steps) {
-        xs += x_step;
-        gs += g_step;
-        read();
-      } else {
-        tt += stride;
-        block += stride;
-        if (block < a.tokens) {
-          seek();
-          read();
-        }
+      {
+        const uint4 v[2] = {at[0], at[kRotThreads]}, g[2] = {at[2 * kRotThreads], at[3 * kRotThreads]};
+        unpack16<BF16>(v, x);
+        unpack16<BF16>(g, y);
       }
       tn.apply(y, ln, a.interleaved);
       const float inv = rsqrtf(row_squares<D>(x) * (1.f / D) + a.eps);
@@ -329,6 +354,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -344,23 +370,29 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
     float x = 0.f;
 #pragma unroll
     for (int y = 0; y < WARPS; ++y) x += s_dw[y][threadIdx.x];
-    a.part[(static_cast<size_t>(ck) * gridDim.x + blockIdx.x) * D + threadIdx.x] = x;
+    a.part[static_cast<size_t>((is_q ? 0 : sp.big_q + sp.small_q) + cta) * D + threadIdx.x] = x;
   }
 }
 
-// The sums of `rows` CTAs, 32 elements of one weight per block (blockIdx.y: queries,
+// The sums of the CTAs' parts, 32 elements of one weight per block (blockIdx.y: queries,
 // keys), in a fixed order.
 constexpr int kRotSumRows = 32;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kRotSumRows) fa2_rotary_weight_kernel(const RotaryArgs a, int per_chunk) {
+__global__ void __launch_bounds__(32 * kRotSumRows) fa2_rotary_weight_kernel(const RotaryArgs a, int ctas_q, int ctas) {
   __shared__ float s_sum[kRotSumRows][33];
   const RotarySide& s = blockIdx.y == 0 ? a.q : a.k;
   const int lane = threadIdx.x % 32, row = threadIdx.x / 32, e = blockIdx.x * 32 + lane;
-  const int first = blockIdx.y == 0 ? 0 : a.chunks_q, last = blockIdx.y == 0 ? a.chunks_q : a.chunks;
+  const int first = blockIdx.y == 0 ? 0 : ctas_q, last = blockIdx.y == 0 ? ctas_q : ctas;
   grid_dependency_wait();
   float x = 0.f;
-#pragma unroll 4
-  for (int i = first * per_chunk + row; i < last * per_chunk; i += kRotSumRows) x += a.part[static_cast<size_t>(i) * D + e];
+  constexpr int U = 8;  // parts that are read at once
+  for (int i = first + row; i < last; i += U * kRotSumRows) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = i + u * kRotSumRows < last ? a.part[static_cast<size_t>(i + u * kRotSumRows) * D + e] : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) x += v[u];
+  }
   s_sum[row][lane] = x;
   __syncthreads();
   if (row != 0 || s.H == 0) return;
@@ -380,12 +412,16 @@ static cudaError_t launch_rotary_t(const RotaryArgs& a, bool norm, cudaStream_t 
 }
 
 template <int D, bool BF16>
-static cudaError_t launch_rotary_bwd_t(const RotaryArgs& a, int per_chunk, cudaStream_t stream) {
-  const cudaError_t e = launch_dependent(fa2_rotary_norm_bwd_kernel<D, BF16>, dim3(per_chunk, a.chunks),
-                                         dim3(kRotThreads), 0, stream, a);
+static cudaError_t launch_rotary_bwd_t(const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream) {
+  const int ctas_q = sp.big_q + sp.small_q, ctas = ctas_q + sp.big_k + sp.small_k;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(fa2_rotary_norm_bwd_kernel<D, BF16>, kRotAhead * kRotSlot, done, true);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(fa2_rotary_norm_bwd_kernel<D, BF16>, dim3(ctas), dim3(kRotThreads),
+                       kRotAhead * kRotSlot, stream, a, sp);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa2_rotary_weight_kernel<D, BF16>, dim3(D / 32, a.k.H > 0 ? 2 : 1),
-                          dim3(32 * kRotSumRows), 0, stream, a, per_chunk);
+                          dim3(32 * kRotSumRows), 0, stream, a, ctas_q, ctas);
 }
 
 cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, cudaStream_t stream) {
@@ -393,11 +429,9 @@ cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, cuda
   return bf16 ? launch_rotary_t<128, true>(a, norm, stream) : launch_rotary_t<128, false>(a, norm, stream);
 }
 
-// Backward with a norm, on a grid of per_chunk CTAs for each run of heads.
-cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, int per_chunk, cudaStream_t stream) {
-  if (d == 64)
-    return bf16 ? launch_rotary_bwd_t<64, true>(a, per_chunk, stream) : launch_rotary_bwd_t<64, false>(a, per_chunk, stream);
-  return bf16 ? launch_rotary_bwd_t<128, true>(a, per_chunk, stream) : launch_rotary_bwd_t<128, false>(a, per_chunk, stream);
+cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream) {
+  if (d == 64) return bf16 ? launch_rotary_bwd_t<64, true>(a, sp, stream) : launch_rotary_bwd_t<64, false>(a, sp, stream);
+  return bf16 ? launch_rotary_bwd_t<128, true>(a, sp, stream) : launch_rotary_bwd_t<128, false>(a, sp, stream);
 }
 
 }  // namespace fa2

@@ -23,6 +23,13 @@ struct RotarySide {
   int H;               // heads; 0: the tensor is absent
 };
 
+// CTAs of the backward with a norm, of queries and of keys. A big one has kRotBig times
+// the work of a small one.
+constexpr int kRotBig = 6;
+struct RotarySplit {
+  int big_q, big_k, small_q, small_k;
+};
+
 struct RotaryArgs {
   RotarySide q, k;
   const double* freqs;   // [r / 2], radians per position

@@ -11,13 +11,14 @@
 
 namespace fa2 {
 cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, cudaStream_t stream);
-cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, int per_chunk, cudaStream_t stream);
+cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream);
 }  // namespace fa2
 
 namespace {
 
 constexpr long long kMaxItems = (1LL << 31) - 1;
-constexpr int kBwdCtas = 608;  // CTAs of the backward with a norm at most, if that leaves one per run of heads
+constexpr int kBwdCtas = 304;  // CTAs of the backward with a norm at most: two on each of 152 SMs
+constexpr long long kBwdSmall = 304 * 24;  // units from which as many small CTAs follow
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -170,21 +171,22 @@ void set_chunks(fa2::RotaryArgs& a, int chunk) {
   a.chunks = a.chunks_q + chunks_of(a.k.H, chunk);
 }
 
-// The grid of the backward with a norm: heads per run, CTAs per run.
-struct BwdGrid {
-  int chunk, per_chunk, ctas;
-};
-BwdGrid bwd_grid(long long tokens, int Hq, int Hk, int d) {
-  BwdGrid g{};
+// The CTAs of the backward with a norm: a tensor's share is as its heads, and each has at
+// least a head of a block of tokens.
+fa2::RotarySplit bwd_split(long long tokens, int Hq, int Hk, int d) {
   const int groups = fa2::kRotThreads / (d / 16);
   const long long blocks = (tokens + groups - 1) / groups;
-  for (g.chunk = 8; g.chunk < 65536; g.chunk *= 2)
-    if (chunks_of(Hq, g.chunk) + chunks_of(Hk, g.chunk) <= kBwdCtas) break;
-  const int chunks = chunks_of(Hq, g.chunk) + chunks_of(Hk, g.chunk);
-  g.per_chunk = static_cast<int>(std::max(1LL, std::min<long long>(blocks, kBwdCtas / chunks)));
-  g.ctas = g.per_chunk * chunks;
-  return g;
+  const int share = std::clamp((kBwdCtas * Hq + (Hq + Hk) / 2) / (Hq + Hk), 1, Hk > 0 ? kBwdCtas - 1 : kBwdCtas);
+  fa2::RotarySplit s{};
+  s.big_q = static_cast<int>(std::min<long long>(share, blocks * Hq));
+  s.big_k = static_cast<int>(std::min<long long>(kBwdCtas - share, blocks * Hk));
+  if (blocks * (Hq + Hk) >= kBwdSmall) {
+    s.small_q = s.big_q;
+    s.small_k = s.big_k;
+  }
+  return s;
 }
+int ctas_of(const fa2::RotarySplit& s) { return s.big_q + s.big_k + s.small_q + s.small_k; }
 
 bool bwd_sizes_ok(int B, int Hq, int Hk, int N, int d) {
   return B >= 1 && N >= 1 && Hq >= 1 && Hk >= 0 && B <= 65535 && Hq <= 65535 && Hk <= 65535 && (d == 64 || d == 128);
@@ -246,7 +248,7 @@ int fa2_rotary_fwd(const void* q, const void* k, const double* freqs, const int*
 size_t fa2_rotary_bwd_workspace_size(int B, int Hq, int Hk, int N, int d, int norm) {
   if (!bwd_sizes_ok(B, Hq, Hk, N, d)) return 0;
   if (!norm) return 256;
-  return static_cast<size_t>(bwd_grid(static_cast<long long>(B) * N, Hq, Hk, d).ctas) * d * 4;
+  return static_cast<size_t>(ctas_of(bwd_split(static_cast<long long>(B) * N, Hq, Hk, d))) * d * 4;
 }
 
 int fa2_rotary_bwd(const void* dq, const void* dk, const void* q, const void* k, const double* freqs,
@@ -329,10 +331,8 @@ int fa2_rotary_bwd(const void* dq, const void* dk, const void* q, const void* k,
   (void)cudaGetLastError();
   cudaError_t e;
   if (norm) {
-    const BwdGrid g = bwd_grid(a.tokens, Hq, Hk, d);
     a.part = static_cast<float*>(workspace);
-    set_chunks(a, g.chunk);
-    e = fa2::launch_rotary_norm_bwd(d, dtype == FA2_BF16, a, g.per_chunk, static_cast<cudaStream_t>(stream));
+    e = fa2::launch_rotary_norm_bwd(d, dtype == FA2_BF16, a, bwd_split(a.tokens, Hq, Hk, d), static_cast<cudaStream_t>(stream));
   } else {
     set_chunks(a, turn_chunk(a.tokens, Hq + Hk, d));
     e = fa2::launch_rotary(d, dtype == FA2_BF16, false, a, static_cast<cudaStream_t>(stream));

@@ -137,6 +137,15 @@ def test_backward(cuda_device, fa2_lib, case):
         assert (np.abs(bits64(wg) - dw) <= tol + _half(w.dtype) * np.abs(dw) * 1.01).all()
 
 
+@pytest.mark.parametrize("case", [
+    (3, 61, 7, 2301, 64, 32, BF16, False, F32, "first", True),
+    (1, 8, 1, 1793, 128, 128, FP16, True, "same", "each", False),
+    (2, 130, 1, 45, 64, 64, BF16, True, F32, "none", False),
+], ids=["large-and-small-ctas", "cuts-inside-tokens", "one-head-of-a-block-each"])
+def test_backward_with_norm_dealt_to_many_ctas(cuda_device, fa2_lib, case):
+    test_backward(cuda_device, fa2_lib, case)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_nothing_else_is_touched(cuda_device, fa2_lib, inter):
     """Passed-through elements keep their bits, and inputs that are not finite reach
