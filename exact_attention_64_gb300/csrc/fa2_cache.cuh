@@ -167,9 +167,11 @@ struct DecodeArgs {
   const int* prefix;      // shared prefix: its pages [prefix_pages]
   const int* prefix_len;  // [1]
   int prefix_cap;         // slots that the prefix can have at most
-  long long* starts;      // workspace [B + 2]: units before those of each sequence, then the prefix's CTAs
+  long long* starts;      // workspace [B + 3]: units before those of each sequence, the prefix's CTAs, uneven_shares
   int rows;               // query rows of a key head, B * g: row R is head R % g of sequence R / g
   FastDiv fg;
+  int early;              // SHARED: CTAs that begin beside the prefix's kernel; 0: all alike
+  int prefix_items;       // with `early`: items of that kernel
   int row_tiles;          // tiles of query rows whose prefix this kernel attends to itself, per key head, or 0
   FastDiv ft;             // row_tiles
   int box;                // slots of one copy: a power of two, at most 16, that divides the page size

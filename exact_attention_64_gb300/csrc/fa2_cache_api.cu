@@ -191,7 +191,7 @@ PrefixSpace prefix_space(int B, int Hq, int Hkv, int d) {
   s.so = s.pml + align_up(rows * 8, 256);
   s.sml = s.so + align_up(own * d * 4, 256);
   s.starts = s.sml + align_up(own * 8, 256);
-  s.total = s.starts + align_up(static_cast<size_t>(B + 2) * 8, 256);
+  s.total = s.starts + align_up(static_cast<size_t>(B + 3) * 8, 256);
   return s;
 }
 
@@ -349,6 +349,10 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   const long long longest = std::max(static_cast<long long>(c.c.L), inside ? static_cast<long long>(c.prefix_cap) : 0LL);
   const long long units = items * ((longest + fa2::decode_unit(d) - 1) / fa2::decode_unit(d));
   a.tail_ctas = static_cast<int>(std::min<long long>(units, std::min(2 * sms, kDecodeCtas)));
+  if (!inside && a.tail_ctas == 2 * sms) {
+    c.early = sms;
+    c.prefix_items = a.items;
+  }
   a.part_o = reinterpret_cast<float*>(ws + s.po);
   a.part_ml = reinterpret_cast<float2*>(ws + s.pml);
   a.timeout_ns = fa2::kDefaultWaitTimeoutNs;

@@ -134,6 +134,45 @@ __device__ __forceinline__ int unit_cta(long long u, long long G, long long T) {
   return static_cast<int>(div_pos((u + 1) * G - 1, T));
 }
 
+// The same where the first `early` workers begin beside the prefix's kernel and the others
+// when it ends: kShares + k parts for kShares - k of a later one. k = 0: all alike.
+constexpr int kShares = 8, kMaxUneven = 4;
+struct UnitDeal {
+  long long T;  // units
+  int S, early, more, less;  // parts of them
+  __device__ __forceinline__ UnitDeal(int G, int first, long long units, int k) : T(units) {
+    early = k == 0 ? 0 : first;
+    more = k == 0 ? 1 : kShares + k;
+    less = k == 0 ? 1 : kShares - k;
+    S = more * early + less * (G - early);
+  }
+  __device__ __forceinline__ long long begin(int x) const {
+    return unit_begin(less * x + (more - less) * min(x, early), S, T);
+  }
+  __device__ __forceinline__ int worker(long long u) const {
+    const int s = unit_cta(u, S, T), e = more * early;
+    const bool late = s >= e;
+    // s / more: below 2^14, so that half of 1 / more is far above the error.
+    const float q = __fdividef(static_cast<float>(late ? s - e : s) + 0.5f, static_cast<float>(late ? less : more));
+    return early == 0 ? s : (late ? early : 0) + static_cast<int>(q);
+  }
+};
+
+// k of a call whose prefix has a kernel of its own: five times the time that the early
+// workers have alone (about 4 us of its start and end, and 4.8, or 3.4 at d = 64, per slot
+// tile of two row tiles) by the time that all units take, as far as every worker then has a
+// unit. 64 sequences behind 8192 slots, 32/8 heads, d = 128, up to 1024 own slots: 47.6 us
+// and 50.6 with equal shares; up to 4000: 110.6 and 111.7 (117.7 with the first case's k);
+// up to 300, all of which are read beside the prefix: 34.7 and 34.0.
+template <int D>
+__device__ __forceinline__ int uneven_shares(const DecodeArgs& a, int cut, int G, int first, long long T, bool warps) {
+  if (a.early == 0 || G < 2 * first || cut == 0) return 0;
+  const float tiles = static_cast<float>(a.prefix_items) * static_cast<float>((cut + 127) / 128);
+  const float alone = 4000.f + __fdividef(tiles * (D == 128 ? 4800.f : 3400.f), static_cast<float>(a.early));  // ns
+  const int k = static_cast<int>(fminf(__fdividef(5.f * alone, static_cast<float>(T) * (warps ? 2.f : 7.f)) + 0.5f, kMaxUneven));
+  return (kShares - k) * T >= (kShares + k) * first + (kShares - k) * (G - first) ? k : 0;
+}
+
 // 2^(from - to) for a reference that rises to `to`. 1 at -inf, where all that
 // there is are zeros, or NaN that has to stay.
 __device__ __forceinline__ float step_down(float from, float to) { return from == to ? 1.f : ex2_approx(from - to); }

@@ -599,11 +599,13 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
   const int len = seq_len(c, b);
   const long long T = ld_global(d.starts + c.B), start = ld_global(d.starts + b);
   const long long PG = inside ? 0 : ld_global(d.starts + c.B + 1);
+  const int uneven = inside ? 0 : static_cast<int>(ld_global(d.starts + c.B + 2));
   // Parts of the prefix, then own ones: from the first to the last CTA (worker) of an
   // item. Lanes 0 and 1 find those of the prefix, 2 and 3 those of the own slots.
   const int first = prefix_of(len, P), own = len - first;
   auto own_tiles = [&](int n) { return a.tail_warps ? tiles_of<D, kSharedWarp>(n) : tiles_of<D>(n); };
-  const long long G = min(static_cast<long long>(a.tail_ctas) * (a.tail_warps ? kDecWarps : 1), T);  // workers
+  const int W = a.tail_warps ? kDecWarps : 1;  // workers of a CTA
+  const UnitDeal deal(static_cast<int>(min(static_cast<long long>(a.tail_ctas) * W, T)), d.early * W, T, uneven);
   const int R = b * d.g + gx, p_step = inside ? a.head_tile : 2 * kTileRows;
   const int p_tile = inside ? (a.head_tile == 8 ? R >> 3 : R >> 4) : R / (2 * kTileRows);
   const int p_item = h * (inside ? d.row_tiles : a.fblocks.d) + p_tile;
@@ -615,9 +617,10 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
     const bool pre = lane < 2;
     const int tiles = pre ? tiles_p : tiles_o;
     const long long u0 = pre ? static_cast<long long>(p_item) * tiles : start + static_cast<long long>(hh) * tiles;
-    if (lane < 4 && (pre ? first : own) > 0)
-      cta = unit_cta(u0 + (lane & 1 ? tiles - 1 : 0), pre && !inside ? PG : G,
-                     pre && !inside ? static_cast<long long>(a.items) * tiles : T);
+    if (lane < 4 && (pre ? first : own) > 0) {
+      const long long u = u0 + (lane & 1 ? tiles - 1 : 0);
+      cta = pre && !inside ? unit_cta(u, PG, static_cast<long long>(a.items) * tiles) : deal.worker(u);
+    }
   }
   const int pc = __shfl_sync(0xffffffffu, cta, 0), oc = __shfl_sync(0xffffffffu, cta, 2);
   int np = __shfl_sync(0xffffffffu, cta, 1) - pc + 1, ns = __shfl_sync(0xffffffffu, cta, 3) - oc + 1;

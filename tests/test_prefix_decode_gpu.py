@@ -125,6 +125,20 @@ def test_several_tiles_per_cta(cuda_device, fa2_lib, case):
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
+UNEVEN = [  # enough slots behind the prefix that its kernel's time decides the CTAs' shares
+    (40, 64, 16, 64, 16, 1024, [200 + i for i in range(40)]),       # 12 parts to 4
+    (40, 64, 16, 64, 16, 1024, [430 - i for i in range(40)]),       # 10 to 6
+    (40, 64, 16, 64, 16, 1000, [900 - 3 * i for i in range(40)]),   # 9 to 7
+    (2, 576, 8, 64, 16, 1024, [1300, 1290]),                        # by CTAs
+    (36, 96, 12, 128, 32, 1500, [i % 5 * 90 for i in range(36)]),   # some with nothing of their own
+]
+
+
+@pytest.mark.parametrize("case", UNEVEN, ids=lambda c: "_".join(map(str, c[:6])) + f"_{c[6][0]}")
+def test_uneven_shares(cuda_device, fa2_lib, case):
+    test_several_tiles_per_cta(cuda_device, fa2_lib, case)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("std,scale", [(12.0, None), (0.0, None), (1.0, 1e-6), (3.0, 2.0)])
 def test_sharp_and_flat_rows(cuda_device, fa2_lib, std, scale, dtype):
