@@ -224,13 +224,127 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_kernel(const Rotary
   }
 }
 
+constexpr int kRotAhead = 3;                    // heads of a lane in its ring
+constexpr int kRotSlot = 4 * kRotThreads * 16;  // bytes of a head of every lane: two runs of x, two of g
+
 // 16 bytes to a lane's own place, or zeros there.
 __device__ __forceinline__ void rot_copy16(uint32_t to, const uint4* from, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
 }
 
-constexpr int kRotAhead = 3;                    // heads of a lane in its ring
-constexpr int kRotSlot = 4 * kRotThreads * 16;  // bytes of a head of every lane: two runs of x, two of g
+// A CTA's units: heads of blocks of GROUPS tokens, in this order, all of queries or all
+// of keys.
+struct RotDeal {
+  bool is_q;
+  int cta, block, h, left;  // number among its tensor's CTAs; the first unit; their count
+  __device__ __forceinline__ RotDeal(const RotaryArgs& a, const RotarySplit& sp, int groups) {
+    const bool big = static_cast<int>(blockIdx.x) < sp.big_q + sp.big_k;
+    const int x = big ? blockIdx.x : blockIdx.x - sp.big_q - sp.big_k, qs = big ? sp.big_q : sp.small_q;
+    is_q = x < qs;
+    const int bigs = is_q ? sp.big_q : sp.big_k, smalls = is_q ? sp.small_q : sp.small_k, H = is_q ? a.q.H : a.k.H;
+    cta = (is_q ? x : x - qs) + (big ? 0 : bigs);
+    auto before = [&](int c) { return min(c, bigs) * (kRotBig - 1) + c; };
+    const long long units = (a.tokens + groups - 1) / groups * H, u0 = units * before(cta) / before(bigs + smalls);
+    left = static_cast<int>(units * before(cta + 1) / before(bigs + smalls) - u0);
+    block = static_cast<int>(u0 / H);
+    h = static_cast<int>(u0 - static_cast<long long>(block) * H);
+  }
+};
+
+// The same for calls of middle size, with a norm for large ones too: each lane copies its
+// pieces of the next two heads' rows into its own places of shared memory while it works
+// on one, and units are dealt evenly to two CTAs for each SM. Where units are many, six
+// sevenths of them, and the last seventh to as many small CTAs, which go where a CTA
+// ends first. Measured in us, and by runs of heads as above: B = 16, 8/1 heads, N = 4096, d
+// = 64 with a norm 31 and 54, without 30 and 40; B = 8, 16/4 heads, N = 2048, d = 128 with a
+// norm 29 and 37; 1.07 GB with a norm 165 and 167. The other way round: B = 1, 32/8 heads,
+// N = 512, two units for a token's sines, 5.1 and 4.5; and without a norm, where runs of
+// heads are at the copy rate, 537 MB 91 and 81, 1.07 GB 175 and 157. (Five heads ahead:
+// 1.07 GB 175 with a norm. Three CTAs per SM: the same.)
+template <int D, bool BF16, bool NORM>
+__global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_ring_kernel(const RotaryArgs a, const RotarySplit sp) {
+  using C = RotCfg<D>;
+  constexpr int U = kRotAhead;
+  extern __shared__ __align__(16) uint4 s_ring[];
+  __shared__ unsigned long long s_turn[D / 2];
+  grid_dependency_wait();
+  rot_turns(a, s_turn);
+  const RotLane ln = rot_lane(threadIdx.x % C::LANES, D, a.r, a.interleaved);
+  const RotDeal deal(a, sp, C::GROUPS);
+  const RotarySide& s = deal.is_q ? a.q : a.k;
+  int left = deal.left, h = deal.h;
+  const long long x_step = s.x.sh / 8, y_step = s.y.sh / 8;
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+  long long tt = static_cast<long long>(deal.block) * C::GROUPS + threadIdx.x / C::LANES, ct = tt;
+  int ch = h, copies = left, put = 0, take = 0;  // token ct, head ch are copied next
+  const uint4* xs = nullptr;
+  auto token = [&](long long x, int* b, int* n) {
+    const int t = x < a.tokens ? static_cast<int>(x) : 0;
+    *b = div_by(t, a.fN);
+    *n = t - *b * a.N;
+    return t;
+  };
+  auto seek = [&]() {
+    int b, n;
+    (void)token(ct, &b, &n);
+    xs = row_at(s.x, b, ch, n);
+  };
+  auto copy = [&]() {
+    if (copies > 0) {
+      const bool in = ct < a.tokens;
+      const uint32_t to = ring + put * (kRotSlot / 2);
+      rot_copy16(to, xs + ln.e0 / 8, in);
+      rot_copy16(to + kRotThreads * 16, xs + ln.e1 / 8, in);
+      put = put + 1 == U ? 0 : put + 1;
+      xs += x_step;
+      --copies;
+      if (++ch == s.H) {
+        ch = 0;
+        ct += C::GROUPS;
+        seek();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  seek();
+#pragma unroll 1
+  for (int i = 0; i < U - 1; ++i) copy();
+  float2 w[8];
+  if constexpr (NORM) load_weight<BF16>(s.weight, a.weight_fp32, ln, w);
+  __syncthreads();
+  RotTurn tn;
+  for (; left > 0; tt += C::GROUPS, h = 0) {
+    const bool on = tt < a.tokens;
+    int b, n;
+    const int t = token(tt, &b, &n);
+    uint4* dst = row_at(s.y, b, h, n);
+    tn.set(s_turn, ln, rot_position(a, t, b, n), a.amplitude, a.sign);
+    const int heads = min(left, s.H - h);
+    left -= heads;
+#pragma unroll 1
+    for (int i = 0; i < heads; ++i, dst += y_step) {
+      copy();
+      asm volatile("cp.async.wait_group %0;" ::"n"(U - 1) : "memory");
+      const uint4* at = s_ring + take * (kRotSlot / 32) + threadIdx.x;
+      take = take + 1 == U ? 0 : take + 1;
+      const uint4 v[2] = {at[0], at[kRotThreads]};
+      float2 x[8];
+      unpack16<BF16>(v, x);
+      if constexpr (NORM) {
+        const float2 inv = both(rsqrtf(row_squares<D>(x) * (1.f / D) + a.eps));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = f2_mul(f2_mul(x[j], inv), w[j]);
+      }
+      tn.apply(x, ln, a.interleaved);
+      if (on) {
+        const bool same = !NORM && !ln.turned;  // passed through, a NaN's bits too
+        dst[ln.e0 / 8] = same ? v[0] : pack8<BF16>(x);
+        dst[ln.e1 / 8] = same ? v[1] : pack8<BF16>(x + 4);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
 // Backward with a norm. A CTA's rows are all of queries or all of keys, so that a lane's
 // 16 sums of the weights' gradients stay in registers; at its end the CTA adds up its
@@ -239,10 +353,8 @@ constexpr int kRotSlot = 4 * kRotThreads * 16;  // bytes of a head of every lane
 // KiB in flight, which took 50 us for 252 MB (B = 8, 16/4 heads, N = 2048, d = 128). So
 // rows are copied to shared memory, two heads ahead of the one in work, where they need no
 // registers: 44 us with the sum of the CTAs' parts, 5.7 TB/s (three heads ahead the same),
-// and 239 for 1.61 GB (B = 4, 32 + 32 heads, N = 8192), the copy rate. Units of a head of
-// 32 (d = 128) or 64 tokens are dealt evenly, two CTAs for each SM; where units are many, six
-// sevenths of them, and the last seventh in as many small CTAs, which go where a CTA
-// ends first (1.61 GB: 264 without).
+// and 239 for 1.61 GB (B = 4, 32 + 32 heads, N = 8192), the copy rate; 264 without the small
+// CTAs at the end.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(const RotaryArgs a, const RotarySplit sp) {
   using C = RotCfg<D>;
@@ -255,18 +367,9 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
   rot_turns(a, s_turn);
   __syncthreads();
   const RotLane ln = rot_lane(threadIdx.x % C::LANES, D, a.r, a.interleaved);
-  // The CTA's units: heads of blocks of GROUPS tokens, in this order.
-  const bool big = static_cast<int>(blockIdx.x) < sp.big_q + sp.big_k;
-  const int x = big ? blockIdx.x : blockIdx.x - sp.big_q - sp.big_k, qs = big ? sp.big_q : sp.small_q;
-  const bool is_q = x < qs;
-  const RotarySide& s = is_q ? a.q : a.k;
-  const int bigs = is_q ? sp.big_q : sp.big_k, smalls = is_q ? sp.small_q : sp.small_k;
-  const int cta = (is_q ? x : x - qs) + (big ? 0 : bigs);
-  auto before = [&](int c) { return min(c, bigs) * (kRotBig - 1) + c; };
-  const long long units = (a.tokens + C::GROUPS - 1) / C::GROUPS * s.H, u0 = units * before(cta) / before(bigs + smalls);
-  int left = static_cast<int>(units * before(cta + 1) / before(bigs + smalls) - u0);
-  const int block0 = static_cast<int>(u0 / s.H);
-  int h = static_cast<int>(u0 - static_cast<long long>(block0) * s.H);
+  const RotDeal deal(a, sp, C::GROUPS);
+  const RotarySide& s = deal.is_q ? a.q : a.k;
+  int left = deal.left, h = deal.h;
   float2 w[8], dw[8];
   load_weight<BF16>(s.weight, a.weight_fp32, ln, w);
 #pragma unroll
@@ -275,7 +378,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
   // Each lane copies its pieces of the next rows, from one token to the next, into its own
   // places of shared memory; it alone reads them.
   const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
-  long long tt = static_cast<long long>(block0) * C::GROUPS + threadIdx.x / C::LANES, ct = tt;
+  long long tt = static_cast<long long>(deal.block) * C::GROUPS + threadIdx.x / C::LANES, ct = tt;
   int ch = h, copies = left, put = 0, take = 0;  // token ct, head ch are copied next
   const uint4 *xs = nullptr, *gs = nullptr;
   auto token = [&](long long x, int* b, int* n) {
@@ -370,7 +473,7 @@ __global__ void __launch_bounds__(kRotThreads, 2) fa2_rotary_norm_bwd_kernel(con
     float x = 0.f;
 #pragma unroll
     for (int y = 0; y < WARPS; ++y) x += s_dw[y][threadIdx.x];
-    a.part[static_cast<size_t>((is_q ? 0 : sp.big_q + sp.small_q) + cta) * D + threadIdx.x] = x;
+    a.part[static_cast<size_t>((deal.is_q ? 0 : sp.big_q + sp.small_q) + deal.cta) * D + threadIdx.x] = x;
   }
 }
 
@@ -403,12 +506,22 @@ __global__ void __launch_bounds__(32 * kRotSumRows) fa2_rotary_weight_kernel(con
   else static_cast<uint16_t*>(s.weight_grad)[e] = static_cast<uint16_t>(pack_x2<BF16>(y, 0.f) & 0xffffu);
 }
 
+template <int D, bool BF16, bool NORM>
+static cudaError_t launch_rotary_n(const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream) {
+  if (sp.big_q == 0) {
+    const long long items = a.tokens * a.chunks;
+    const dim3 grid(static_cast<unsigned>((items + RotCfg<D>::GROUPS - 1) / RotCfg<D>::GROUPS));
+    return launch_dependent(fa2_rotary_kernel<D, BF16, NORM>, grid, dim3(kRotThreads), 0, stream, a);
+  }
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(fa2_rotary_ring_kernel<D, BF16, NORM>, kRotAhead * kRotSlot / 2, done, true);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa2_rotary_ring_kernel<D, BF16, NORM>, dim3(sp.big_q + sp.big_k + sp.small_q + sp.small_k),
+                          dim3(kRotThreads), kRotAhead * kRotSlot / 2, stream, a, sp);
+}
 template <int D, bool BF16>
-static cudaError_t launch_rotary_t(const RotaryArgs& a, bool norm, cudaStream_t stream) {
-  const long long items = a.tokens * a.chunks;
-  const dim3 grid(static_cast<unsigned>((items + RotCfg<D>::GROUPS - 1) / RotCfg<D>::GROUPS));
-  return launch_dependent(norm ? fa2_rotary_kernel<D, BF16, true> : fa2_rotary_kernel<D, BF16, false>, grid,
-                          dim3(kRotThreads), 0, stream, a);
+static cudaError_t launch_rotary_t(const RotaryArgs& a, bool norm, const RotarySplit& sp, cudaStream_t stream) {
+  return norm ? launch_rotary_n<D, BF16, true>(a, sp, stream) : launch_rotary_n<D, BF16, false>(a, sp, stream);
 }
 
 template <int D, bool BF16>
@@ -424,9 +537,10 @@ static cudaError_t launch_rotary_bwd_t(const RotaryArgs& a, const RotarySplit& s
                           dim3(32 * kRotSumRows), 0, stream, a, ctas_q, ctas);
 }
 
-cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, cudaStream_t stream) {
-  if (d == 64) return bf16 ? launch_rotary_t<64, true>(a, norm, stream) : launch_rotary_t<64, false>(a, norm, stream);
-  return bf16 ? launch_rotary_t<128, true>(a, norm, stream) : launch_rotary_t<128, false>(a, norm, stream);
+// By units if sp has CTAs, else by runs of heads.
+cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream) {
+  if (d == 64) return bf16 ? launch_rotary_t<64, true>(a, norm, sp, stream) : launch_rotary_t<64, false>(a, norm, sp, stream);
+  return bf16 ? launch_rotary_t<128, true>(a, norm, sp, stream) : launch_rotary_t<128, false>(a, norm, sp, stream);
 }
 
 cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream) {

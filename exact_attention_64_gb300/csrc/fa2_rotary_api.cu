@@ -10,15 +10,17 @@
 #include "fa2_rotary.cuh"
 
 namespace fa2 {
-cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, cudaStream_t stream);
+cudaError_t launch_rotary(int d, bool bf16, bool norm, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream);
 cudaError_t launch_rotary_norm_bwd(int d, bool bf16, const RotaryArgs& a, const RotarySplit& sp, cudaStream_t stream);
 }  // namespace fa2
 
 namespace {
 
 constexpr long long kMaxItems = (1LL << 31) - 1;
-constexpr int kBwdCtas = 304;  // CTAs of the backward with a norm at most: two on each of 152 SMs
-constexpr long long kBwdSmall = 304 * 24;  // units from which as many small CTAs follow
+constexpr int kRotCtas = 304;  // CTAs that run at once: two on each of 152 SMs
+constexpr long long kRotSmall = 24 * kRotCtas;  // units from which as many small CTAs follow
+// Units from which the turn is dealt by them, and, without a norm, up to which.
+constexpr long long kRotUnits = 5 * kRotCtas, kRotMaxUnits = 64 * kRotCtas;
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -171,21 +173,31 @@ void set_chunks(fa2::RotaryArgs& a, int chunk) {
   a.chunks = a.chunks_q + chunks_of(a.k.H, chunk);
 }
 
-// The CTAs of the backward with a norm: a tensor's share is as its heads, and each has at
-// least a head of a block of tokens.
-fa2::RotarySplit bwd_split(long long tokens, int Hq, int Hk, int d) {
+// The CTAs of a launch by units, heads of blocks of tokens: a tensor's share is as its heads,
+// and each has at least a unit.
+fa2::RotarySplit split(long long tokens, int Hq, int Hk, int d) {
   const int groups = fa2::kRotThreads / (d / 16);
   const long long blocks = (tokens + groups - 1) / groups;
-  const int share = std::clamp((kBwdCtas * Hq + (Hq + Hk) / 2) / (Hq + Hk), 1, Hk > 0 ? kBwdCtas - 1 : kBwdCtas);
+  const int share = std::clamp((kRotCtas * Hq + (Hq + Hk) / 2) / (Hq + Hk), 1, Hk > 0 ? kRotCtas - 1 : kRotCtas);
   fa2::RotarySplit s{};
   s.big_q = static_cast<int>(std::min<long long>(share, blocks * Hq));
-  s.big_k = static_cast<int>(std::min<long long>(kBwdCtas - share, blocks * Hk));
-  if (blocks * (Hq + Hk) >= kBwdSmall) {
+  s.big_k = static_cast<int>(std::min<long long>(kRotCtas - share, blocks * Hk));
+  if (blocks * (Hq + Hk) >= kRotSmall) {
     s.small_q = s.big_q;
     s.small_k = s.big_k;
   }
   return s;
 }
+
+// The turn: by units, or by runs of heads (none in the split).
+fa2::RotarySplit turn_split(fa2::RotaryArgs& a, int Hq, int Hk, int d, bool norm) {
+  const int groups = fa2::kRotThreads / (d / 16);
+  const long long units = (a.tokens + groups - 1) / groups * (Hq + Hk);
+  if (units >= kRotUnits && (norm || units <= kRotMaxUnits)) return split(a.tokens, Hq, Hk, d);
+  set_chunks(a, turn_chunk(a.tokens, Hq + Hk, d));
+  return fa2::RotarySplit{};
+}
+
 int ctas_of(const fa2::RotarySplit& s) { return s.big_q + s.big_k + s.small_q + s.small_k; }
 
 bool bwd_sizes_ok(int B, int Hq, int Hk, int N, int d) {
@@ -239,16 +251,16 @@ int fa2_rotary_fwd(const void* q, const void* k, const double* freqs, const int*
   }
   fill(a, z, freqs, positions, rotary_dim, position_mode, interleaved, eps, amplitude, weight_dtype);
   a.sign = 1.f;
-  set_chunks(a, turn_chunk(a.tokens, Hq + Hk, d));
+  const fa2::RotarySplit sp = turn_split(a, Hq, Hk, d, norm);
   (void)cudaGetLastError();
-  const cudaError_t e = fa2::launch_rotary(d, dtype == FA2_BF16, norm, a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = fa2::launch_rotary(d, dtype == FA2_BF16, norm, a, sp, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
 }
 
 size_t fa2_rotary_bwd_workspace_size(int B, int Hq, int Hk, int N, int d, int norm) {
   if (!bwd_sizes_ok(B, Hq, Hk, N, d)) return 0;
   if (!norm) return 256;
-  return static_cast<size_t>(ctas_of(bwd_split(static_cast<long long>(B) * N, Hq, Hk, d))) * d * 4;
+  return static_cast<size_t>(ctas_of(split(static_cast<long long>(B) * N, Hq, Hk, d))) * d * 4;
 }
 
 int fa2_rotary_bwd(const void* dq, const void* dk, const void* q, const void* k, const double* freqs,
@@ -332,10 +344,10 @@ int fa2_rotary_bwd(const void* dq, const void* dk, const void* q, const void* k,
   cudaError_t e;
   if (norm) {
     a.part = static_cast<float*>(workspace);
-    e = fa2::launch_rotary_norm_bwd(d, dtype == FA2_BF16, a, bwd_split(a.tokens, Hq, Hk, d), static_cast<cudaStream_t>(stream));
+    e = fa2::launch_rotary_norm_bwd(d, dtype == FA2_BF16, a, split(a.tokens, Hq, Hk, d), static_cast<cudaStream_t>(stream));
   } else {
-    set_chunks(a, turn_chunk(a.tokens, Hq + Hk, d));
-    e = fa2::launch_rotary(d, dtype == FA2_BF16, false, a, static_cast<cudaStream_t>(stream));
+    const fa2::RotarySplit sp = turn_split(a, Hq, Hk, d, false);
+    e = fa2::launch_rotary(d, dtype == FA2_BF16, false, a, sp, static_cast<cudaStream_t>(stream));
   }
   return e == cudaSuccess ? FA2_OK : fa2::host_cuda_fail(e);
 }

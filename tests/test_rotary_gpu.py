@@ -162,6 +162,30 @@ def test_nothing_else_is_touched(cuda_device, fa2_lib, inter):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("case", [
+    (3, 61, 7, 2301, 64, 32, BF16, False, F32, "first", True),
+    (2, 20, 4, 1111, 128, 96, FP16, True, None, "each", False),
+    (1, 40, 0, 2500, 64, 48, BF16, False, None, "none", True),
+    (5, 9, 8, 601, 128, 128, FP16, False, "same", "first", False),
+], ids=lambda c: "-".join(str(x).replace("torch.", "") for x in c))
+def test_turns_dealt_by_units(cuda_device, fa2_lib, case):
+    test_forward(cuda_device, fa2_lib, case)
+    test_backward(cuda_device, fa2_lib, case)
+
+
+def test_nothing_else_is_touched_by_units(cuda_device, fa2_lib):
+    """The same of a call that is dealt by units; also rows with gaps around the outputs."""
+    x = torch.randn(2, 30, 1700, 128).to(BF16).cuda()
+    x[1, 29, 1699, 5], x[0, 0, 0, 100], x[0, 7, 900, 127] = float("inf"), float("nan"), float("nan")
+    buf = torch.full((2, 1700, 32, 128), 3.0, dtype=BF16, device="cuda")
+    y = buf[:, :, 1:31].transpose(1, 2)
+    fa2_lib.rotary_forward(x, None, fa2_lib.rotary_frequencies(32).cuda(), q_out=y)
+    assert torch.equal(y[..., 32:].contiguous().view(torch.int16), x[..., 32:].contiguous().view(torch.int16))
+    assert (buf[:, :, 0] == 3).all() and (buf[:, :, 31] == 3).all()
+    bad = (~torch.isfinite(y[..., :32])).nonzero().tolist()
+    assert bad == [[1, 29, 1699, 5], [1, 29, 1699, 21]]
+
+
 def test_rows_of_zeros_and_eps(cuda_device, fa2_lib):
     x = torch.zeros(1, 2, 5, 64, dtype=FP16, device="cuda")
     w = torch.ones(64, device="cuda")
