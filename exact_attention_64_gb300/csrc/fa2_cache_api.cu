@@ -32,6 +32,9 @@ constexpr int kPrefixCtas = 152;  // most CTAs of a shared prefix
 constexpr int kKwCtas = 152;      // most CTAs of the key weights
 constexpr long long kMaxRows = (1LL << 31) - 1;
 constexpr long long kMaxSlots = 1LL << 30;  // slots that a table row can name
+// Entries of a table that a resize can change: it numbers its releases and takes in 31
+// bits, and a number may pass their count by a step of its loops, 16 CTAs x 512 threads.
+constexpr long long kMaxEntries = (1LL << 31) - (1 << 14);
 
 struct Buf {
   const void* p;
@@ -471,7 +474,7 @@ int fa2_cache_evict(void* k_cache, void* v_cache, const int* table, const int* l
 
 size_t fa2_cache_resize_workspace_size(int B, int num_pages, int page_size, int max_pages) {
   if (check_cache(B, 1, 64, 1, page_size, max_pages, FA2_BF16) != FA2_OK || num_pages < 1) return 0;
-  if (static_cast<long long>(B) * max_pages > kMaxRows) return 0;
+  if (static_cast<long long>(B) * max_pages > kMaxEntries) return 0;
   return align_up(static_cast<size_t>(num_pages) * 4, 256) + align_up(static_cast<size_t>(B) * max_pages * 4, 256);
 }
 
@@ -482,7 +485,7 @@ int fa2_cache_resize(int* table, const int* lens, const int* new_lens, int* refs
   if (num_pages < 1) return FA2_ERR_INVALID_ARG;
   int st = check_cache(B, 1, 64, 1, page_size, max_pages, FA2_BF16);
   if (st != FA2_OK) return st;
-  if (static_cast<long long>(B) * max_pages > kMaxRows) return FA2_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * max_pages > kMaxEntries) return FA2_ERR_UNSUPPORTED;
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(new_lens, 4) || !aligned(refs, 4) ||
       !aligned(free_pages, 4) || !aligned(num_free, 4) || !aligned(lens_out, 4))
     return FA2_ERR_ALIGNMENT;

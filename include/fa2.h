@@ -433,8 +433,8 @@ size_t fa2_cache_evict_workspace_size(int B, int Hkv, int page_size, int max_pag
  *                 suffice. Not lens or new_lens.
  *   workspace   : device, >= fa2_cache_resize_workspace_size(...) bytes, 256-byte
  *                 aligned, scratch owned by the caller.
- * B * max_pages < 2^31. A page number that the cache does not have, or a page given
- * back more often than it was named, is not freed and sets FA2_ERR_PAGE; the pool's
+ * B * max_pages <= 2^31 - 2^14. A page number that the cache does not have, or a page
+ * given back more often than it was named, is not freed and sets FA2_ERR_PAGE; the pool's
  * contents are then undefined (but stay within it). Repeated calls give the same
  * bits. */
 int fa2_cache_resize(int* table, const int* lens, const int* new_lens, int* refs, int* free_pages, int* num_free,
