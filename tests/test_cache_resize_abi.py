@@ -36,7 +36,7 @@ def test_numbers_of_pages_stay_below_two_to_the_31(fa2_lib):
     size = lambda B, mp: lib.fa2_cache_resize_workspace_size(B, 100, 1, mp)  # noqa: E731
     most = 2 ** 31 - 2 ** 14
     assert size(2, most // 2) == 512 + most * 4
-    for B, mp in ((2, most // 2 + 1), (49981, 42966), (65535, 32768)):  # 42966 * 49981 = 2^31 - 2
+    for B, mp in ((2, most // 2 + 1), (49981, 42966), (3, 715827882)):  # the last two: 2^31 - 2
         assert most < B * mp < 2 ** 31 and size(B, mp) == 0
         p = [A + i * STEP * 16 for i in range(8)]
         assert lib.fa2_cache_resize(*p[:7], B, 100, 1, mp, p[7], 2 ** 40, None) == 2
