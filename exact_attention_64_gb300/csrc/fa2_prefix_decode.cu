@@ -580,8 +580,77 @@ __global__ void __maxnreg__(PfxCfg<D>::REGS)
 constexpr int kPjThreads = 256, kPjWarps = kPjThreads / 32;
 constexpr int kPjResident = 152 * 32;  // warps of the join that run at once
 
+// Infinite entries of V. A remainder of p may be negative or 0, and -1 * inf or 0 * inf
+// beside the first piece's product makes NaN in the prefix's kernel of what is infinite.
+// So where a row's sum is NaN and its l is a number, V's columns are looked through: an
+// infinite entry of a slot that weighs more than 0 makes the output infinite; both signs,
+// a NaN, or an infinite entry of a slot that weighs nothing make NaN. By one warp, 4 columns
+// a lane, once the row of o stands there. Its time (a page's and a row's latency for each 4
+// slots) counts for such rows only; the others pay 0.1 us a call, 0.4 at d = 64, for the
+// test of their sums (64 sequences, 32/8 heads, 8192 slots: 49.9 -> 50.0 and 35.6 -> 36.0;
+// as a function that is called, in the same registers, 50.1 and 36.2, and 1.2 more in fp16).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const PrefixArgs a, int per_row) {
+__device__ __forceinline__ void pfx_infinite(const DecodeArgs& d, long long row, float M, int lane) {
+  constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u, MAN = BF16 ? 0x7fu : 0x3ffu;
+  constexpr int U = 4;  // slots in flight
+  const CacheView& c = d.c;
+  const int b = static_cast<int>(div_pos(row, d.Hq)), x = static_cast<int>(row - static_cast<long long>(b) * d.Hq);
+  const int h = div_by(x, d.fg), len = seq_len(c, b), first = prefix_of(len, prefix_slots(d)), e = lane * 4;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(d.q + row * D);
+  auto halves = [](const uint2& v, uint32_t (&w)[4]) {
+    w[0] = v.x & 0xffffu, w[1] = v.x >> 16, w[2] = v.y & 0xffffu, w[3] = v.y >> 16;
+  };
+  auto is_nan = [](uint32_t w) { return (w & EXP) == EXP && (w & MAN) != 0u; };
+  uint32_t o[4] = {0u, 0u, 0u, 0u}, seen[4] = {0u, 0u, 0u, 0u};  // seen: 1: inf, 2: -inf, 4: NaN
+  if (e < D) halves(ld_global(reinterpret_cast<const uint2*>(d.o + row * D + e)), o);
+#pragma unroll 1
+  for (int j0 = 0; j0 < len; j0 += U) {
+    bool open = false;  // a column that may still change
+#pragma unroll
+    for (int i = 0; i < 4; ++i) open |= is_nan(o[i]) && seen[i] < 3u;
+    if (!__any_sync(0xffffffffu, open)) break;
+    uint2 v[U];
+    int at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u;
+      at[u] = -1;
+      v[u] = make_uint2(0u, 0u);
+      if (j >= len) continue;
+      const int p = div_by(j, c.ps);
+      const int page = ld_global(j < first ? d.prefix + p : c.table + static_cast<size_t>(b) * c.max_pages + p);
+      at[u] = page_row(c, page, h, j - p * c.ps.d);
+      if (at[u] >= 0 && e < D) v[u] = ld_global(reinterpret_cast<const uint2*>(d.v + static_cast<size_t>(at[u]) * D + e));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t w[4];
+      halves(v[u], w);
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) any |= is_nan(o[i]) && (w[i] & EXP) == EXP;
+      if (!any) continue;
+      const uint32_t* k = reinterpret_cast<const uint32_t*>(d.k + static_cast<size_t>(at[u]) * D);
+      float s = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < D / 2; ++i) {
+        const float2 y = unpack_x2<BF16>(ld_global(q + i)), z = unpack_x2<BF16>(ld_global(k + i));
+        s = fmaf(y.x, z.x, fmaf(y.y, z.y, s));
+      }
+      const bool weighs = ex2_approx(s * d.scale_log2 - M) > 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((w[i] & EXP) == EXP) seen[i] |= !weighs || is_nan(w[i]) ? 4u : w[i] >> 15 ? 2u : 1u;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (is_nan(o[i]) && (seen[i] == 1u || seen[i] == 2u)) d.o[row * D + e + i] = static_cast<uint16_t>(EXP | (seen[i] == 2u ? 0x8000u : 0u));
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPjThreads)
+    fa2_prefix_join_kernel(const PrefixArgs a, int per_row) {
   constexpr int LPR = D / 4, PPW = 32 / LPR, U = 4;
   __shared__ float2 s_ml[kPjWarps];
   __shared__ float4 s_acc[kPjWarps][LPR];
@@ -674,12 +743,17 @@ __global__ void __launch_bounds__(kPjThreads) fa2_prefix_join_kernel(const Prefi
     if (sub == 0 && lane < LPR)
       for (int y = 1; y < per_row; ++y) add(s_ml[warp + y].x, s_ml[warp + y].y, s_acc[warp + y][lane]);
   }
-  if (on && sub == 0 && lane < LPR) {
+  if (!on || sub != 0) return;
+  bool nan = false;
+  if (lane < LPR) {
     const float inv = S == 0.f ? 0.f : 1.f / S;
     *reinterpret_cast<uint2*>(d.o + row * D + lane * 4) =
         make_uint2(pack_x2<BF16>(acc.x * inv, acc.y * inv), pack_x2<BF16>(acc.z * inv, acc.w * inv));
     if (lane == 0) d.lse[row] = S == 0.f ? -INFINITY : (M + log2f(S)) * kLn2f;
+    const float all = (acc.x + acc.y) + (acc.z + acc.w);
+    nan = all != all && S > 0.f && S < INFINITY;
   }
+  if (__any_sync(0xffffffffu, nan)) pfx_infinite<D, BF16>(d, row, M, lane);
 }
 
 cudaError_t launch_decode_suffix(int d, bool bf16, int head_tile, const DecodeArgs& a, bool warps, int ctas,

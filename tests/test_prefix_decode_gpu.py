@@ -262,6 +262,70 @@ def test_infinite_values(cuda_device, fa2_lib):
         assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("B,Hq,Hkv,d,ps,P", [(3, 4, 2, 64, 16, 200), (30, 4, 2, 64, 16, 700), (40, 8, 2, 128, 5, 333),
+                                             (90, 12, 2, 128, 64, 1500), (300, 2, 2, 64, 16, 150)])
+def test_infinite_values_come_out_infinite(cuda_device, fa2_lib, B, Hq, Hkv, d, ps, P, dtype):
+    """A V entry of +-inf makes its element of o +-inf, as p * inf does, in the prefix and
+    behind it; both signs in one column, or NaN, make NaN; all other elements are as
+    without it, and so are those of sequences that do not have the prefix."""
+    lens = [P + b % 40 for b in range(B)]
+    lens[1], lens[-1] = P - 9, P + 7
+    c = Shared(B, Hkv, d, ps, P, lens, dtype, seed=B)
+    q, g = c.query(Hq), Hq // Hkv
+    bad = c.v.clone()
+
+    def put(j, col, x, b=B - 1):
+        bad[int(c.table[b, j // ps]), Hkv - 1, j % ps, col] = x
+
+    inf, nan = float("inf"), float("nan")
+    for j in (2, 17, 65, 99, P // 2 // ps * ps):    # whole pages of the prefix
+        put(j, 3, inf)
+        put(j, 9, -inf)
+    put(5, 20, inf)
+    put(101, 20, -inf)
+    put(33, 30, nan)
+    put(34, 30, inf)
+    put(70, d - 1, inf)
+    put(P + 3, d - 1, -inf)                        # the last sequence's own slot
+    put(P + 4, 40, -inf)
+    for room in (False, True):
+        a = c.args(q, room)
+        want, lse0 = (t.cpu() for t in fa2_lib.prefix_decode(*a))
+        a[2] = bad.cuda()
+        o, lse = (t.cpu() for t in fa2_lib.prefix_decode(*a))
+        assert fa2_lib.device_status() == 0
+        heads = slice(Hq - g, Hq)
+        on = torch.tensor([n >= P for n in lens])
+        for col, x in ((3, inf), (9, -inf), (20, nan), (30, nan), (d - 1, inf)):
+            part = want[on]
+            part[:, heads, col] = x
+            want[on] = part
+        want[-1, heads, d - 1], want[-1, heads, 40] = nan, -inf
+        assert torch.equal(o.isnan(), want.isnan())
+        assert torch.equal(o.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+        assert torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_infinite_values_of_slots_that_weigh_little(cuda_device, fa2_lib, dtype):
+    """2^-60 of the largest is a weight; a score of -inf is none, and 0 * inf is NaN."""
+    for B in (3, 40):
+        c = Shared(B, 1, 64, 16, 512, [512] * (B - 1) + [515], dtype, seed=7)
+        c.k.zero_()
+        c.k[int(c.table[-1, 20]), 0, 5, 0] = 1.0                 # the largest score, 60
+        c.k[int(c.table[-1, 3]), 0, 1, 0] = -float("inf")
+        c.v[int(c.table[-1, 9]), 0, 2, 11] = float("inf")        # score 0
+        c.v[int(c.table[-1, 3]), 0, 1, 12] = float("inf")
+        q = torch.zeros(B, 1, 64, dtype=dtype)
+        q[..., 0] = 60.0
+        for o, _ in (fa2_lib.prefix_decode(*c.args(q, B > 16), scale=float(np.log(2.0))),
+                     fa2_lib.paged_decode(*c.args(q)[:5], scale=float(np.log(2.0)))):
+            o = o.cpu()
+            assert (o[:, :, 11] == float("inf")).all() and o[:, :, 12].isnan().all()
+            assert int((~torch.isfinite(o)).sum()) == 2 * B
+
+
 @pytest.mark.parametrize("B", [6, 12])
 def test_graph_follows_lengths_prefix_and_tables(cuda_device, fa2_lib, B):
     ps = 16
