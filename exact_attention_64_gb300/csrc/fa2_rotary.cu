@@ -19,9 +19,11 @@
 // Inputs and outputs may have any strides: a projection's token-major rows become
 // the head-major ones of attention without a pass of their own.
 //
-// Angles: f / 2 pi is kept as a 64-bit fraction of a turn, and its product with the
-// position modulo 2^64 is exact, so that an angle is as exact at position 2^31 as at
-// 1: two integer multiplications instead of a reduction in 64-bit floating point.
+// Angles: f / 2 pi is formed in two pieces and kept as a 64-bit fraction of a turn, and
+// its product with the position modulo 2^64 is exact, so that an angle is right to 2^-31
+// turns at any position (|f| up to 2^40): two integer multiplications instead of a
+// reduction in 64-bit floating point. Its sine and cosine are taken of 24 bits of it, half
+// a turn or less: 2^-26 turns.
 #include "fa2_rotary.cuh"
 
 namespace fa2 {
@@ -88,11 +90,14 @@ __device__ __forceinline__ void load_weight(const void* w, int fp32, const RotLa
 }
 
 // The pairs' turns per position as 64-bit fractions, one pair per thread. (In
-// 64-bit floating point, which this GPU has little of: once per CTA.)
+// 64-bit floating point, which this GPU has little of: once per CTA.) 1 / 2 pi is kInv2Pi +
+// kInv2PiLow to 2^-110; what the product with the first rounds off is in the second.
+constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLow = -9.839338337591243e-18;
 __device__ __forceinline__ void rot_turns(const RotaryArgs& a, unsigned long long* s_turn) {
   for (int i = threadIdx.x; i < a.r / 2; i += kRotThreads) {
-    const double t = ld_global(a.freqs + i) * 0.15915494309189533577;
-    s_turn[i] = __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+    const double f = ld_global(a.freqs + i), t = f * kInv2Pi, low = fma(f, kInv2PiLow, fma(f, kInv2Pi, -t));
+    s_turn[i] = __double2ull_rz((t - floor(t)) * 18446744073709551616.0) +
+                static_cast<unsigned long long>(__double2ll_rn((low - rint(low)) * 18446744073709551616.0));
   }
 }
 

@@ -473,9 +473,10 @@ size_t fa2_key_weights_workspace_size(void);
  *   y_a = amplitude (u_a cos t - u_b sin t),  y_b = amplitude (u_b cos t + u_a sin t),
  *   t = p freqs[j]
  * for the pairs j < rotary_dim / 2, with (a, b) = (j, j + rotary_dim / 2), or
- * (2j, 2j + 1) if interleaved; y_i = u_i for i >= rotary_dim. Sums and angles are
- * not rounded below 32 bits (an angle is exact to 2^-31 turns at any position), y is
- * rounded once. The sum of squares of a row has to be finite in fp32.
+ * (2j, 2j + 1) if interleaved; y_i = u_i for i >= rotary_dim. Sums and products are fp32.
+ * An angle is formed to 2^-31 turns at any position, for frequencies up to 2^40, and
+ * rounded to 24 bits (at most 2^-26 turns) for its sine and cosine. y is rounded once.
+ * The sum of squares of a row has to be finite in fp32.
  *   q, k          : device [B][Hq][N][d], [B][Hk][N][d] dtype, rows of d contiguous
  *                   elements, 16-byte aligned, other strides below. k may be NULL
  *                   (Hk = 0, and nothing that belongs to it).

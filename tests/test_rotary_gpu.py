@@ -1,5 +1,7 @@
 """Rotary positions and the per-head norm against the definition in 64 bits."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -144,6 +146,33 @@ def test_backward(cuda_device, fa2_lib, case):
 ], ids=["large-and-small-ctas", "cuts-inside-tokens", "one-head-of-a-block-each"])
 def test_backward_with_norm_dealt_to_many_ctas(cuda_device, fa2_lib, case):
     test_backward(cuda_device, fa2_lib, case)
+
+
+# 1 / 2 pi, to 60 digits
+TURN = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
+
+
+@pytest.mark.parametrize("N", [40, 1800])
+def test_angles_at_far_positions_and_high_frequencies(cuda_device, fa2_lib, N):
+    """An angle is right to 2^-31 turns for frequencies up to 2^40 at any position: against
+    angles in exact arithmetic (an fp64 product of the two is off by up to 2^18 there). With
+    half a step of fp16 and the bound that all turns are held to; N = 1800: by units."""
+    d, H = 64, 60
+    f = torch.tensor([2.0 ** 40 * 10 ** (-0.55 * j) for j in range(d // 2)], dtype=torch.float64)
+    g = torch.Generator().manual_seed(N)
+    p = torch.randint(-(2 ** 31), 2 ** 31 - 1, (1, N), generator=g, dtype=torch.int64)
+    p[0, :4] = torch.tensor([2 ** 31 - 1, -(2 ** 31), 1, 0])
+    x = torch.randn(1, H, N, d, generator=g).to(FP16)
+    check = list(range(0, N, max(1, N // 40)))
+    t = np.array([[float((int(pos) * Fraction(w) * TURN) % 1) for w in f.tolist()] for pos in p[0, check].tolist()])
+    c, s = np.cos(2 * np.pi * t), np.sin(2 * np.pi * t)
+    a, b = orc.pairs(d, False)
+    u = bits64(x)[:, :, check]
+    ref = np.empty_like(u)
+    ref[..., a], ref[..., b] = u[..., a] * c - u[..., b] * s, u[..., b] * c + u[..., a] * s
+    y, _ = fa2_lib.rotary_forward(x.cuda(), None, f.cuda(), p.int().cuda())
+    tol = _bound(u, ref, f, p.numpy(), d, False, 1.0, FP16, False)
+    assert (np.abs(bits64(y)[:, :, check] - ref) <= tol).all()
 
 
 @pytest.mark.parametrize("inter", [False, True])
