@@ -79,7 +79,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 // Whether two outputs share an element. Two views of one buffer whose heads stand
-// side by side in a token's row (a packed projection) do not.
+// side by side, in a token's row (a packed projection) or head by head, do not.
 bool outputs_clash(const Rows& x, const Rows& y, const Sizes& z) {
   if (!overlap(x.p, span(x, z) * 2, y.p, span(y, z) * 2)) return false;
   const Rows &lo = x.p < y.p ? x : y, &hi = x.p < y.p ? y : x;
@@ -87,12 +87,19 @@ bool outputs_clash(const Rows& x, const Rows& y, const Sizes& z) {
   const long long bytes = static_cast<const char*>(hi.p) - static_cast<const char*>(lo.p);
   if (bytes % 2 != 0) return true;
   const long long off = bytes / 2;
-  // The heads of one token, then the tokens.
+  long long below = 0;
+  // Together they are the heads of one tensor: the upper ones begin whole head strides on.
+  const long long head = lo.H > 1 ? lo.st[1] : hi.H > 1 ? hi.st[1] : off;
+  if (head > 0 && (hi.H == 1 || hi.st[1] == head) && off % head == 0 && off / head >= lo.H && off / head <= 65535) {
+    const int all[3] = {z.B, static_cast<int>(off / head) + hi.H, z.N};
+    const long long st[3] = {x.st[0], head, x.st[2]};
+    if (disjoint(all, st, 3, z.d, &below)) return false;
+  }
+  // Or all heads of one token come before those of the next.
   if (off < (lo.H > 1 ? (lo.H - 1) * lo.st[1] : 0) + z.d) return true;
   const long long row = off + (hi.H > 1 ? (hi.H - 1) * hi.st[1] : 0) + z.d;
   const int n[2] = {z.B, z.N};
   const long long st[2] = {x.st[0], x.st[2]};
-  long long below = 0;
   return !disjoint(n, st, 2, row, &below);
 }
 

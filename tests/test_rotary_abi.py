@@ -2,6 +2,7 @@
 with made-up addresses, and the binding with host tensors."""
 
 import ctypes
+import random
 
 import pytest
 import torch
@@ -54,6 +55,47 @@ def test_forward_rejects(fa2_lib):
     assert _fwd(lib, {"ko": _p(6) + 7 * D * 2}, st=(CQ, CK, packed, packed)) == 8  # runs into the next token
     other = (N * 8 * D, D, 16 * D)
     assert _fwd(lib, {"ko": _p(6) + 4 * D * 2}, st=(CQ, CK, packed, other)) == 8
+
+
+def _layout(lib, ko, sq, sk, B, Hq, Hk, N, d=64):
+    """Status of outputs at these offsets and strides; 3 (the weights' alignment, which is
+    checked next) if they do not clash."""
+    ptr = {"qo": _p(6), "ko": _p(6) + 2 * ko, "qw": _p(50) + 8}
+    return _fwd(lib, ptr, ((Hq * N * d, N * d, d), (Hk * N * d, N * d, d), sq, sk), B, Hq, Hk, N, d)
+
+
+def test_outputs_side_by_side(fa2_lib):
+    """Heads of one buffer in a token's row or head by head, in any order and with room
+    around them; never rows that share elements (against a count of the elements)."""
+    lib = fa2_lib.load_library()
+    d = 64
+    for B in (1, 3):
+        for Hq, Hk, N in ((4, 2, 10), (1, 1, 7), (8, 1, 1), (1, 5, 3)):
+            H = Hq + Hk + 1  # a head of room behind
+            token, head = (N * H * d, d, H * d), (H * N * d, N * d, d)
+            for st in (token, head):
+                assert _layout(lib, Hq * st[1], st, st, B, Hq, Hk, N) == 3, (B, Hq, Hk, N, st)
+                swapped = {"qo": _p(6) + 2 * Hk * st[1], "ko": _p(6), "qw": _p(50) + 8}
+                assert _fwd(lib, swapped, ((Hq * N * d, N * d, d), (Hk * N * d, N * d, d), st, st), B, Hq, Hk, N, d) == 3
+                if Hq > 1:
+                    assert _layout(lib, (Hq - 1) * st[1], st, st, B, Hq, Hk, N) == 8
+    r = random.Random(3)
+    seen = {3: 0, 8: 0}
+    for _ in range(4000):
+        B, Hq, Hk, N = (r.choice([1, 2, 3]) for _ in range(4))
+        steps = sorted(d * r.choice([1, 1, 2, 3, 4, 6, 9]) for _ in range(3))
+        order = r.sample(range(3), 3)
+        sq = tuple(steps[i] for i in order)
+        sk = sq if r.random() < 0.8 else tuple(r.sample(steps, 3))
+        ko = r.choice([d * r.randint(0, 30), 8 * r.randint(0, 240)])
+        rows = lambda off, st, H: [off + b * st[0] + h * st[1] + n * st[2]  # noqa: E731
+                                   for b in range(B) for h in range(H) for n in range(N)]
+        at = sorted(rows(0, sq, Hq) + rows(ko, sk, Hk))
+        apart = all(y - x >= d for x, y in zip(at, at[1:]))
+        got = _layout(lib, ko, sq, sk, B, Hq, Hk, N)
+        assert got == 8 or (got == 3 and apart), (B, Hq, Hk, N, sq, sk, ko)
+        seen[got] += 1
+    assert seen[3] > 300
 
 
 def test_backward_rejects(fa2_lib):
