@@ -14,6 +14,7 @@ bfloat16 (``d`` in {64, 128}); the logsumexp is float32 ``[B, H, N]``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from pathlib import Path
 
@@ -445,6 +446,42 @@ def bwd_block_work(block_x: int, N: int, d: int, causal: bool):
     return a.value, b.value, c.value, e.value
 
 
+class _NoSecondGradient(torch.autograd.Function):
+    """Gradients as they are, after the n tensors that they depend on; a gradient of
+    theirs, which the kernels do not have, raises."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[n:]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("gradients of exact_attention_64_gb300 cannot be differentiated again")
+
+
+def _differentiable_once(backward):
+    """A Function's backward whose results raise when they are differentiated
+    (create_graph=True), if they depend on anything that wants a gradient: without this
+    they would pass for constants."""
+
+    @functools.wraps(backward)
+    def once(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        of = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
+        at = [i for i, t in enumerate(out) if t is not None]
+        if not of or not at:
+            return out
+        out = list(out)
+        for i, t in zip(at, _NoSecondGradient.apply(len(of), *of, *(out[i] for i in at))):
+            out[i] = t
+        return tuple(out)
+
+    return once
+
+
 class _FA2Function(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal, scale):
@@ -667,6 +704,7 @@ class _RotaryFunction(torch.autograd.Function):
         return rotary_forward(q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude)
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, *grads):
         freqs, positions, *rest = ctx.saved_tensors
         weights, inputs = rest[:2], rest[2:]
@@ -696,5 +734,8 @@ class _RotaryFunction(torch.autograd.Function):
 
 def rotary(q, k, freqs, positions=None, interleaved: bool = False, q_weight=None, k_weight=None,
            eps: float = 1e-6, amplitude: float = 1.0):
-    """Differentiable ``rotary_forward``: gradients of q, k and the weights."""
+    """Differentiable ``rotary_forward``: gradients of q, k and the weights (first
+    ones: a second one raises). freqs has none."""
+    if torch.is_grad_enabled() and getattr(freqs, "requires_grad", False):
+        raise ValueError("freqs has no gradient: detach it")
     return _RotaryFunction.apply(q, k, freqs, positions, interleaved, q_weight, k_weight, eps, amplitude)

@@ -295,6 +295,35 @@ def test_autograd_of_one_tensor(cuda_device, fa2_lib):
         assert torch.equal(q.grad, want[0]) and (w is None or torch.equal(w.grad, want[2]))
 
 
+@pytest.mark.parametrize("norm", [False, True])
+def test_a_second_gradient_raises(cuda_device, fa2_lib, norm):
+    """create_graph gives the same first gradients; what depends on the norm's inputs or on
+    gradients that want one raises when it is differentiated again, and a gradient that is a
+    constant stays one. freqs, which has no gradient, must not want one."""
+    q0, k0, g = _inputs(1, 2, 2, 9, 64, BF16, seed=7)
+    f = fa2_lib.rotary_frequencies(64).cuda()
+    w = [torch.rand(64, generator=g).cuda().requires_grad_() for _ in range(2)] if norm else [None, None]
+    q, k = q0.detach().clone().requires_grad_(), k0.detach().clone().requires_grad_()
+    leaves = [t for t in (q, k, *w) if t is not None]
+    turn = lambda: fa2_lib.rotary(q, k, f, q_weight=w[0], k_weight=w[1])  # noqa: E731
+    loss = lambda y: (y[0].float().square() + y[1].float() * q.detach().float()).sum()  # noqa: E731
+    want = torch.autograd.grad(loss(turn()), leaves)
+    got = torch.autograd.grad(loss(turn()), leaves, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # beside a term that can be differentiated
+    with pytest.raises(RuntimeError, match="differentiated"):
+        torch.autograd.grad(got[0].float().square().sum() + q.float().square().sum(), q)
+    got = torch.autograd.grad(turn()[1].float().sum(), k, create_graph=True)
+    assert got[0].requires_grad == norm
+    for t in leaves[1::2] if norm else ():
+        with pytest.raises(RuntimeError, match="differentiated"):
+            torch.autograd.grad(got[0].float().square().sum() + t.float().square().sum(), t, retain_graph=True)
+    with pytest.raises(ValueError, match="freqs"):
+        fa2_lib.rotary(q, k, f.clone().requires_grad_())
+    with torch.no_grad():
+        fa2_lib.rotary(q, k, f.clone().requires_grad_())
+
+
 def test_gradient_against_differences(cuda_device, fa2_lib):
     """Differences of the forward itself along the gradient's signs, in its own 16 bits:
     both sides of a step h are rounded by a half step of y, over 2 h. x is on a grid
