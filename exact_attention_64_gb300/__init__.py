@@ -491,6 +491,7 @@ class _FA2Function(torch.autograd.Function):
         return o
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
         dq, dk, dv = backward(q, k, v, o, lse, do.contiguous(), causal=ctx.causal,
@@ -499,7 +500,8 @@ class _FA2Function(torch.autograd.Function):
 
 
 def attention(q, k, v, causal: bool = False, scale: float | None = None):
-    """Differentiable FlashAttention-2 (forward and backward in libfa2)."""
+    """Differentiable FlashAttention-2 (forward and backward in libfa2): first
+    gradients; a second one raises."""
     return _FA2Function.apply(q, k, v, causal, scale)
 
 
