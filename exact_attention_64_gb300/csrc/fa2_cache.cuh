@@ -170,7 +170,7 @@ struct DecodeArgs {
   long long* starts;      // workspace [B + 3]: units before those of each sequence, the prefix's CTAs, uneven_shares
   int rows;               // query rows of a key head, B * g: row R is head R % g of sequence R / g
   FastDiv fg;
-  int early;              // SHARED: CTAs that begin beside the prefix's kernel; 0: all alike
+  int early;              // by warps: CTAs that begin beside the prefix's kernel; 0: all alike
   int prefix_items;       // with `early`: items of that kernel
   int row_tiles;          // tiles of query rows whose prefix this kernel attends to itself, per key head, or 0
   FastDiv ft;             // row_tiles

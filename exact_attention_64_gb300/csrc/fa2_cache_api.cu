@@ -352,7 +352,12 @@ int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, c
   const long long longest = std::max(static_cast<long long>(c.c.L), inside ? static_cast<long long>(c.prefix_cap) : 0LL);
   const long long units = items * ((longest + fa2::decode_unit(d) - 1) / fa2::decode_unit(d));
   a.tail_ctas = static_cast<int>(std::min<long long>(units, std::min(2 * sms, kDecodeCtas)));
-  if (!inside && a.tail_ctas == 2 * sms) {
+  // By warps half of the CTAs begin beside the prefix's; by CTAs (115200 bytes of shared
+  // memory at d = 128, where 68608 of an SM's are left) none has room there, and uneven
+  // shares help or harm by chance: 64 sequences, 8/1 heads, 8192 slots and up to 1024 (4000)
+  // own ones 26.7 us (35.3) even and 27.2 (36.8) uneven; 20 of 64/4 heads 40.2 and 42.1; 40
+  // of 16/2 heads the other way, 29.6 and 28.2.
+  if (!inside && a.tail_warps && a.tail_ctas == 2 * sms) {
     c.early = sms;
     c.prefix_items = a.items;
   }

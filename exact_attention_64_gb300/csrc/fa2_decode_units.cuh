@@ -158,18 +158,20 @@ struct UnitDeal {
   }
 };
 
-// k of a call whose prefix has a kernel of its own: five times the time that the early
+// k of a call whose workers are warps and whose prefix has a kernel of its own: five times the time that the early
 // workers have alone (about 4 us of its start and end, and 4.8, or 3.4 at d = 64, per slot
 // tile of two row tiles) by the time that all units take, as far as every worker then has a
-// unit. 64 sequences behind 8192 slots, 32/8 heads, d = 128, up to 1024 own slots: 47.6 us
-// and 50.6 with equal shares; up to 4000: 110.6 and 111.7 (117.7 with the first case's k);
-// up to 300, all of which are read beside the prefix: 34.7 and 34.0.
+// unit. 64 sequences behind 8192 slots, 32/8 heads, d = 128, up to 1024 own slots: 50.1 us
+// and 53.4 with equal shares; up to 4000: 118.3 and 121.4; up to 300: 37.0 and 36.9; d = 64,
+// fp16, up to 1024: 37.2 and 42.0. The other way round: d = 128 in fp16, whose own slots'
+// products take longer than the rule's time for them, 61.6 and 56.6; and 16 sequences of
+// 128/4 heads behind 16384 slots, 52.9 and 49.3.
 template <int D>
-__device__ __forceinline__ int uneven_shares(const DecodeArgs& a, int cut, int G, int first, long long T, bool warps) {
+__device__ __forceinline__ int uneven_shares(const DecodeArgs& a, int cut, int G, int first, long long T) {
   if (a.early == 0 || G < 2 * first || cut == 0) return 0;
   const float tiles = static_cast<float>(a.prefix_items) * static_cast<float>((cut + 127) / 128);
   const float alone = 4000.f + __fdividef(tiles * (D == 128 ? 4800.f : 3400.f), static_cast<float>(a.early));  // ns
-  const int k = static_cast<int>(fminf(__fdividef(5.f * alone, static_cast<float>(T) * (warps ? 2.f : 7.f)) + 0.5f, kMaxUneven));
+  const int k = static_cast<int>(fminf(__fdividef(5.f * alone, static_cast<float>(T) * 2.f) + 0.5f, kMaxUneven));
   return (kShares - k) * T >= (kShares + k) * first + (kShares - k) * (G - first) ? k : 0;
 }
 

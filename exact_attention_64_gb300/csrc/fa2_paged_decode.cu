@@ -288,10 +288,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) fa2_paged_decode_kernel(con
     if (blockIdx.x == 0 && warp == 0)
       for (int b = lane; b < c.B; b += 32)
         if (ld_global(c.lens + b) != seq_len(c, b)) report_page(c.status);
-    const int first = SHARED ? a.early * (WARPS ? kDecWarps : 1) : 0;
+    const int first = WARPS ? a.early * kDecWarps : 0;
     int uneven = 0;
     if constexpr (SHARED) {
-      uneven = uneven_shares<D>(a, P.cut, static_cast<int>(G), first, T, WARPS);
+      if constexpr (WARPS) uneven = uneven_shares<D>(a, P.cut, static_cast<int>(G), first, T);
       if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[c.B + 2] = uneven;  // for the join
       if (blockIdx.x == 0 && warp == 1) map.write_starts(a.starts, PU);  // for the join
       if (blockIdx.x == 0 && threadIdx.x == 0 && a.row_tiles > 0 && ld_global(a.prefix_len) != P.len) report_page(c.status);
