@@ -34,7 +34,7 @@
 //
 // Per CTA and slot tile of two row tiles about 4300 clocks at d = 128, of which the 48
 // products are about 3070 at the tensor core's best. B = 256, 32/8 heads, 16384 slots and up to
-// 200 own ones: 104 us, of which the prefix's kernel takes about 80.
+// 200 own ones: 106 us, of which the prefix's kernel takes about 80.
 #include "fa2_common.cuh"
 #include "fa2_decode_units.cuh"
 
@@ -585,14 +585,15 @@ constexpr int kPjResident = 152 * 32;  // warps of the join that run at once
 // So where a row's sum is NaN and its l is a number, V's columns are looked through: an
 // infinite entry of a slot that weighs more than 0 makes the output infinite; both signs,
 // a NaN, or an infinite entry of a slot that weighs nothing make NaN. By one warp, 4 columns
-// a lane, once the row of o stands there. Its time (a page's and a row's latency for each 4
-// slots) counts for such rows only; the others pay 0.1 us a call, 0.4 at d = 64, for the
-// test of their sums (64 sequences, 32/8 heads, 8192 slots: 49.9 -> 50.0 and 35.6 -> 36.0;
-// as a function that is called, in the same registers, 50.1 and 36.2, and 1.2 more in fp16).
+// a lane, once the row of o stands there. Its time, a row's latency for each 8 slots, counts
+// for such rows only: 0.13 us a slot, 2 ms for 64 sequences of 16384 slots with one such
+// entry. The others pay for the test of their sums 0.1 us a call, 0.4 at d = 64 (64
+// sequences, 32/8 heads, 8192 slots: 49.8 -> 50.0 and 35.6 -> 36.0; as a function that is
+// called, in the same registers, 50.1 and 36.2, and 1.2 more in fp16).
 template <int D, bool BF16>
 __device__ __forceinline__ void pfx_infinite(const DecodeArgs& d, long long row, float M, int lane) {
   constexpr uint32_t EXP = BF16 ? 0x7f80u : 0x7c00u, MAN = BF16 ? 0x7fu : 0x3ffu;
-  constexpr int U = 4;  // slots in flight
+  constexpr int U = 8;  // slots in flight (with 16 the join has too many registers: 1 us a call)
   const CacheView& c = d.c;
   const int b = static_cast<int>(div_pos(row, d.Hq)), x = static_cast<int>(row - static_cast<long long>(b) * d.Hq);
   const int h = div_by(x, d.fg), len = seq_len(c, b), first = prefix_of(len, prefix_slots(d)), e = lane * 4;
@@ -603,44 +604,52 @@ __device__ __forceinline__ void pfx_infinite(const DecodeArgs& d, long long row,
   auto is_nan = [](uint32_t w) { return (w & EXP) == EXP && (w & MAN) != 0u; };
   uint32_t o[4] = {0u, 0u, 0u, 0u}, seen[4] = {0u, 0u, 0u, 0u};  // seen: 1: inf, 2: -inf, 4: NaN
   if (e < D) halves(ld_global(reinterpret_cast<const uint2*>(d.o + row * D + e)), o);
+  // A lane looks up the page of one of 32 slots; then all read their columns of each.
+  auto look_up = [&](int j) {
+    if (j >= len) return -1;
+    const int p = div_by(j, c.ps);
+    const int page = ld_global(j < first ? d.prefix + p : c.table + static_cast<size_t>(b) * c.max_pages + p);
+    return page_row(c, page, h, j - p * c.ps.d);
+  };
+  int next = look_up(lane);
 #pragma unroll 1
-  for (int j0 = 0; j0 < len; j0 += U) {
+  for (int j0 = 0; j0 < len; j0 += 32) {
     bool open = false;  // a column that may still change
 #pragma unroll
     for (int i = 0; i < 4; ++i) open |= is_nan(o[i]) && seen[i] < 3u;
     if (!__any_sync(0xffffffffu, open)) break;
-    uint2 v[U];
-    int at[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u;
-      at[u] = -1;
-      v[u] = make_uint2(0u, 0u);
-      if (j >= len) continue;
-      const int p = div_by(j, c.ps);
-      const int page = ld_global(j < first ? d.prefix + p : c.table + static_cast<size_t>(b) * c.max_pages + p);
-      at[u] = page_row(c, page, h, j - p * c.ps.d);
-      if (at[u] >= 0 && e < D) v[u] = ld_global(reinterpret_cast<const uint2*>(d.v + static_cast<size_t>(at[u]) * D + e));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t w[4];
-      halves(v[u], w);
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) any |= is_nan(o[i]) && (w[i] & EXP) == EXP;
-      if (!any) continue;
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(d.k + static_cast<size_t>(at[u]) * D);
-      float s = 0.f;
+    const int rows = next;
+    next = look_up(j0 + 32 + lane);
 #pragma unroll 1
-      for (int i = 0; i < D / 2; ++i) {
-        const float2 y = unpack_x2<BF16>(ld_global(q + i)), z = unpack_x2<BF16>(ld_global(k + i));
-        s = fmaf(y.x, z.x, fmaf(y.y, z.y, s));
-      }
-      const bool weighs = ex2_approx(s * d.scale_log2 - M) > 0.f;
+    for (int u0 = 0; u0 < 32; u0 += U) {
+      uint2 v[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((w[i] & EXP) == EXP) seen[i] |= !weighs || is_nan(w[i]) ? 4u : w[i] >> 15 ? 2u : 1u;
+      for (int u = 0; u < U; ++u) {
+        const int at = __shfl_sync(0xffffffffu, rows, u0 + u);
+        v[u] = make_uint2(0u, 0u);
+        if (open && at >= 0) v[u] = ld_global(reinterpret_cast<const uint2*>(d.v + static_cast<size_t>(at) * D + e));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = __shfl_sync(0xffffffffu, rows, u0 + u);
+        uint32_t w[4];
+        halves(v[u], w);
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= is_nan(o[i]) && (w[i] & EXP) == EXP;
+        if (!any) continue;
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(d.k + static_cast<size_t>(at) * D);
+        float s = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < D / 2; ++i) {
+          const float2 y = unpack_x2<BF16>(ld_global(q + i)), z = unpack_x2<BF16>(ld_global(k + i));
+          s = fmaf(y.x, z.x, fmaf(y.y, z.y, s));
+        }
+        const bool weighs = ex2_approx(s * d.scale_log2 - M) > 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((w[i] & EXP) == EXP) seen[i] |= !weighs || is_nan(w[i]) ? 4u : w[i] >> 15 ? 2u : 1u;
+      }
     }
   }
 #pragma unroll

@@ -354,9 +354,11 @@ size_t fa2_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_s
  * Prefix slots past the last multiple of 16 (or of the largest power of two that
  * divides page_size, if that is less) are read for each sequence by its own table. In
  * the prefix P enters its product with a relative error of 2^-16 (bf16), or 2^-22 and
- * 2^-36 of the row's largest (fp16). An infinite V entry gives what it gives in
- * fa2_paged_decode; a call that meets one in the prefix may take longer. The result does
- * not depend on timing: repeated calls give the same bits. */
+ * 2^-36 of the row's largest (fp16), or as in fa2_paged_decode where its kernel attends
+ * to the prefix too, which goes by B * Hq / Hkv, Hkv, d and prefix_pages * page_size. An
+ * infinite V entry gives what it gives in fa2_paged_decode; where that makes NaN of a
+ * product in the prefix the call takes longer, about 0.13 us for each slot. The result
+ * does not depend on timing: repeated calls give the same bits. */
 int fa2_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int* table, const int* lens,
                       const int* prefix, const int* prefix_len, void* o, float* lse, int B, int Hq, int Hkv, int d,
                       int num_pages, int page_size, int max_pages, int prefix_pages, float scale, int dtype,
