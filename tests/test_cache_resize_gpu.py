@@ -185,3 +185,22 @@ def test_refusals(cuda_device, fa2_lib):
             fa2_lib.cache_resize(**{**a, **bad})
         assert e.value.code == code
     p.check()
+
+
+def test_many_releases_of_pages_named_twice(cuda_device, fa2_lib):
+    """More than 2^18 releases, over 32 to a lane, in which a page's last one counts."""
+    B, width = 1600, 400
+    r = random.Random(1)
+    p = Pool([0] * B, 1, width, spare=B // 2 * width)
+    p.step(fa2_lib, [width] * (B // 2) + [0] * (B // 2))
+    for b in range(B // 2, B):
+        n = r.randint(0, width)
+        p.table[b][:n] = p.table[b - B // 2][:n]
+        p.lens[b] = n
+        for q in p.table[b][:n]:
+            p.refs[q] += 1
+    p.g["table"].copy_(torch.tensor(p.table, dtype=torch.int32))
+    p.g["refs"].copy_(torch.tensor(p.refs, dtype=torch.int32))
+    assert sum(p.lens) > 2 ** 18
+    p.step(fa2_lib, [0] * B)
+    assert len(p.free) == len(p.refs) and not any(p.refs)
