@@ -554,7 +554,9 @@ def prefix_decode(q, k_cache, v_cache, table, lens, prefix, prefix_len, scale: f
     ``[1]``: how many slots. Sequences of at least prefix_len slots have the prefix in
     their first slots (their tables name the same pages; where it ends inside a page
     that page may be a copy); shorter ones are read by their own table alone. Other
-    arguments and results as in ``paged_decode``; weights are not gathered.
+    arguments and results as in ``paged_decode``; weights are not gathered. By the
+    batch's size and the list's room the prefix is attended to by one of two kernels,
+    whose bits differ (include/fa2.h says to what P is kept).
     """
     return (_native_mod or _native()).prefix_decode(q, k_cache, v_cache, table, lens, prefix, prefix_len, scale, out,
                                                     lse, workspace)

@@ -22,8 +22,8 @@
 
 namespace fa2 {
 
-// A step of 256 sequences and back takes 7.7 us with 512 threads, 10.8 with 1024 and 7.1
-// with 256; 512 sequences, three quarters of which change by up to 1024 pages, and back
+// A step of 256 sequences and back takes 7.7 us with 512 threads (8.0 to 8.2 on other
+// boards), 10.8 with 1024 and 7.1 with 256; 512 sequences, three quarters of which change by up to 1024 pages, and back
 // 77, 72 and 114.
 constexpr int kRszThreads = 512;
 constexpr int kRszWarps = kRszThreads / 32;
